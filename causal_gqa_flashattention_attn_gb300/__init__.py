@@ -17,6 +17,10 @@ Entry points (names as in the C ABI):
   attn_decode_paged_splitk_fp8     the same over an fp8 e4m3 row-wise cache
   attn_decode_paged_splitk_static  the same decode with no workspace argument
   attn_decode_paged_fused   the decode with the LSE merge inside the same launch
+  attn_kv_append            new keys and values into a bf16 paged cache, q and k rotated on the way
+  attn_kv_append_fp8_block  the same into an e4m3 cache with a scale per block of tokens and KV head
+  attn_decode_paged_fp8_block   decode over that cache (1..16 queries per sequence), merge included
+  attn_prefill_paged_fp8_block  ragged prefill over it
   attn_lse_merge            LSE-weighted merge of split partials
   attn_lse_merge_bwd        its gradient
   attn_status_string
@@ -38,11 +42,14 @@ ATTN_DEV_PAGE_OUT_OF_RANGE = 0x1
 ATTN_DEV_SEQ_TOO_LONG = 0x2
 ATTN_DEV_WAIT_TIMEOUT = 0x4
 ATTN_DEV_WORKSPACE_STATE = 0x8
+ATTN_DEV_POSITION_OUT_OF_RANGE = 0x10
 
 EXPORTED = ("attn_prefill_fwd", "attn_prefill_workspace_bytes", "attn_prefill_plan", "attn_prefill_plan_sms", "attn_prefill_fwd_ws", "attn_prefill_host_workspace_bytes", "attn_prefill_fwd_host", "attn_prefill_paged_varlen", "attn_prefill_varlen_workspace_bytes",
             "attn_prefill_paged_varlen_ws", "attn_decode_workspace_bytes", "attn_decode_split_tokens", "attn_decode_split_tokens_for", "attn_decode_split_tokens_balanced_for", "attn_decode_paged_splitk", "attn_decode_paged_splitk_mq",
             "attn_decode_paged_splitk_fp8", "attn_decode_paged_fused", "attn_decode_fused_workspace_bytes", "attn_decode_cooperative",
-            "attn_decode_paged_splitk_static", "attn_lse_merge", "attn_lse_merge_bwd", "attn_selftest_wait_timeout",
+            "attn_decode_paged_splitk_static", "attn_kv_append", "attn_kv_append_fp8_block",
+            "attn_decode_fp8_block_workspace_bytes", "attn_decode_paged_fp8_block",
+            "attn_prefill_fp8_block_workspace_bytes", "attn_prefill_paged_fp8_block", "attn_lse_merge", "attn_lse_merge_bwd", "attn_selftest_wait_timeout",
             "attn_status_string", "attn_abi_version")
 ATTN_DECODE_STATIC_SCRATCH_BYTES = 32 << 20
 
@@ -112,6 +119,22 @@ def lib():
     L.attn_decode_paged_splitk_static.argtypes = [vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32,
                                                   i32, i32, i32, f32, vp, vp, vp, vp]
     L.attn_decode_paged_splitk_static.restype = i32
+    i64 = ctypes.c_longlong
+    append = [vp, vp, vp, i64, i64, i64, vp, i32, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, vp]
+    L.attn_kv_append.argtypes = append + [i32, i32, i32, i32, i32, i32, i32, vp, vp]
+    L.attn_kv_append.restype = i32
+    L.attn_kv_append_fp8_block.argtypes = append + [vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, vp, vp]
+    L.attn_kv_append_fp8_block.restype = i32
+    L.attn_decode_fp8_block_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    L.attn_decode_fp8_block_workspace_bytes.restype = sz
+    L.attn_decode_paged_fp8_block.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32,
+                                              i32, f32, vp, sz, vp, vp, vp, vp]
+    L.attn_decode_paged_fp8_block.restype = i32
+    L.attn_prefill_fp8_block_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.attn_prefill_fp8_block_workspace_bytes.restype = sz
+    L.attn_prefill_paged_fp8_block.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32,
+                                               i32, i32, i32, f32, vp, sz, vp, vp, vp, vp]
+    L.attn_prefill_paged_fp8_block.restype = i32
     L.attn_lse_merge.argtypes = [vp, vp, i32, i32, i32, vp, vp, i32, vp]
     L.attn_lse_merge.restype = i32
     L.attn_lse_merge_bwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, vp]
@@ -521,6 +544,238 @@ def attn_decode_paged_splitk_static(q, k_cache, v_cache, block_table, seq_lens, 
         _ptr(dev_status), _stream_ptr(stream))
     _check("attn_decode_paged_splitk_static", st)
     return o, lse
+
+
+def _expect(name, t, device, shape, *dtypes):
+    """Checks a dense CUDA tensor (None passes): its device, its shape (-1: any size) and its type."""
+    if t is None:
+        return None
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on {device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if t.dim() != len(shape) or any(w not in (-1, n) for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have the shape {tuple(shape)} (-1: any), not {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, device):
+    """The handle of ``stream``, or of the current stream of ``device``, which must be the current device."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current CUDA device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream.device != device:
+        raise ValueError("stream must belong to the tensors' device")
+    return stream.cuda_stream
+
+
+def _allocate(stream, make):
+    """What ``make`` allocates, on ``stream`` if one is given: the memory belongs to the stream that uses it."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _pages(block_table, kv_indptr, bsz, device):
+    """(pages, indptr, entries per row) of a block table [B, max_pages], or of a CSR list."""
+    if kv_indptr is None:
+        return _expect("block_table", block_table, device, (bsz, -1), torch.int32), None, block_table.shape[1]
+    return (_expect("block_table (with kv_indptr)", block_table, device, (-1,), torch.int32),
+            _expect("kv_indptr", kv_indptr, device, (bsz + 1,), torch.int32), 0)
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _block_cache(k_cache, v_cache, k_scale, v_scale, device):
+    """Pointers and (num_pages, page_size, Hkv, D, block_tokens) of a block-scaled e4m3 cache."""
+    kp = _expect("k_cache", k_cache, device, (-1, -1, -1, -1), *_CODES)
+    vp = _expect("v_cache", v_cache, device, k_cache.shape, *_CODES)
+    num_pages, page_size, hkv, d = k_cache.shape
+    sp = _expect("k_scale", k_scale, device, (num_pages, -1, hkv), torch.float32)
+    blocks = k_scale.shape[1]
+    if blocks == 0 or page_size % blocks:
+        raise ValueError(f"k_scale has {blocks} blocks for pages of {page_size} tokens")
+    wp = _expect("v_scale", v_scale, device, (num_pages, blocks, hkv), torch.float32)
+    return (kp, vp, sp, wp), (num_pages, page_size, hkv, d, page_size // blocks)
+
+
+def _token_rows(name, x, device):
+    """(pointer, elements from token to token) of ``x [T, H, D]`` bf16 whose tokens are dense rows."""
+    if x.device != device or x.dtype != torch.bfloat16 or x.dim() != 3:
+        raise ValueError(f"{name} must be a bfloat16 tensor [tokens, heads, D] on {device}")
+    t, h, d = x.shape
+    s = x.stride()
+    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    return x.data_ptr(), s[0] if t > 1 else h * d
+
+
+def _append_args(q, k, v, block_table, seq_lens, cos_sin, qo_indptr, kv_indptr, positions, interleaved, q_out, stream):
+    """The arguments that both appends share, in the order of the C ABI, and the output."""
+    device = k.device
+    raw = _raw_stream(stream, device)
+    kp, ks = _token_rows("k", k, device)
+    vp, vs = _token_rows("v", v, device)
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    total, hkv, d = k.shape
+    qp = qop = None
+    qs, hq = 0, hkv
+    if q is not None:
+        qp, qs = _token_rows("q", q, device)
+        hq = q.shape[1]
+        if q.shape[0] != total or q.shape[2] != d:
+            raise ValueError("q, k and v must have the same tokens and head dimension")
+        if q_out is None:
+            q_out = _allocate(stream, lambda: torch.empty(total, hq, d, dtype=torch.bfloat16, device=device))
+        qop = _expect("q_out", q_out, device, (total, hq, d), torch.bfloat16)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    bsz = seq_lens.numel()
+    lp = _expect("seq_lens", seq_lens, device, (bsz,), torch.int32)
+    table, indptr, width = _pages(block_table, kv_indptr, bsz, device)
+    cp = _expect("cos_sin", cos_sin, device, (-1, -1), torch.float32)
+    max_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
+    args = (qp, kp, vp, qs, ks, vs, cp, max_pos, rot, int(interleaved),
+            _expect("positions", positions, device, (total,), torch.int32),
+            _expect("qo_indptr", qo_indptr, device, (bsz + 1,), torch.int32), lp, table, indptr, width, qop)
+    return args, (bsz, total, hq, hkv, d), q_out, raw
+
+
+def attn_kv_append(q, k, v, k_cache, v_cache, block_table, seq_lens, cos_sin=None, qo_indptr=None, kv_indptr=None,
+                   positions=None, interleaved=False, q_out=None, dev_status=None, stream=None):
+    """Write new keys and values into a bf16 paged cache, rotating queries and
+    keys by their positions.
+
+    ``q [T, Hq, D]`` (or None), ``k, v [T, Hkv, D]`` bf16, a token's heads
+    dense, tokens any multiple of 8 elements apart (parts of one projection's
+    output as they are); caches ``[num_pages, page_size, Hkv, D]`` bf16.
+    ``seq_lens [B]`` are the lengths after the append; ``qo_indptr [B + 1]``
+    gives each sequence's new tokens (None: one each).  ``block_table [B,
+    max_pages]``, or with ``kv_indptr [B + 1]`` a CSR page list.  ``cos_sin
+    [max_pos, R]`` float32 holds R/2 cosines and R/2 sines per position (None:
+    no rotation), e.g. ``a = pos[:, None] / base ** (arange(0, R, 2) / R)`` in
+    float64, then ``cat([a.cos(), a.sin()], 1).float()``; pairs are ``(i, i +
+    R/2)`` or, with ``interleaved``, ``(2i, 2i + 1)``.  ``positions [T]``
+    replaces the tokens' indices.  Returns the rotated ``q [T, Hq, D]``.
+    """
+    args, (bsz, total, hq, hkv, d), q_out, raw = _append_args(q, k, v, block_table, seq_lens, cos_sin, qo_indptr,
+                                                              kv_indptr, positions, interleaved, q_out, stream)
+    kcp = _expect("k_cache", k_cache, k.device, (-1, -1, hkv, d), torch.bfloat16)
+    vcp = _expect("v_cache", v_cache, k.device, k_cache.shape, torch.bfloat16)
+    sp = _expect("dev_status", dev_status, k.device, (1,), torch.int32)
+    st = lib().attn_kv_append(*args, kcp, vcp, bsz, total, hq, hkv, d, k_cache.shape[0], k_cache.shape[1], sp, raw)
+    _check("attn_kv_append", st)
+    return q_out
+
+
+def attn_kv_append_fp8_block(q, k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cos_sin=None,
+                             qo_indptr=None, kv_indptr=None, positions=None, interleaved=False, q_out=None,
+                             dev_status=None, stream=None):
+    """:func:`attn_kv_append` into an e4m3 cache (uint8 or float8_e4m3fn
+    ``[num_pages, page_size, Hkv, D]``) with float32 scales ``[num_pages,
+    page_size / block_tokens, Hkv]``: value = code * scale.  Scales are powers
+    of two; a block that takes more tokens keeps its scale or grows it."""
+    args, (bsz, total, hq, hkv, d), q_out, raw = _append_args(q, k, v, block_table, seq_lens, cos_sin, qo_indptr,
+                                                              kv_indptr, positions, interleaved, q_out, stream)
+    ptrs, (num_pages, page_size, cache_hkv, cache_d, block) = _block_cache(k_cache, v_cache, k_scale, v_scale, k.device)
+    if (cache_hkv, cache_d) != (hkv, d):
+        raise ValueError("the cache's heads must be those of k and v")
+    sp = _expect("dev_status", dev_status, k.device, (1,), torch.int32)
+    st = lib().attn_kv_append_fp8_block(*args, *ptrs, bsz, total, hq, hkv, d, num_pages, page_size, block, sp, raw)
+    _check("attn_kv_append_fp8_block", st)
+    return q_out
+
+
+def attn_decode_fp8_block_workspace_bytes(B, q_len, Hq, Hkv, D=128):
+    """Bytes of the zeroed workspace attn_decode_paged_fp8_block takes on the current device."""
+    return int(lib().attn_decode_fp8_block_workspace_bytes(B, q_len, Hq, Hkv, D))
+
+
+def attn_decode_paged_fp8_block(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, kv_indptr=None,
+                                scale=None, workspace=None, o=None, lse=None, dev_status=None, stream=None):
+    """Decode over the cache that :func:`attn_kv_append_fp8_block` writes.
+
+    ``q [B, Hq, D]`` (one query per sequence) or ``[B, q_len, Hq, D]`` bf16,
+    token-major; query i of a sequence sees tokens ``t <= len - q_len + i``.
+    ``workspace``: a uint8 tensor of attn_decode_fp8_block_workspace_bytes()
+    bytes, zeroed once and reusable (None allocates one).  Returns ``(o, lse,
+    workspace)``, ``lse [B, Hq]`` or ``[B, q_len, Hq]``.
+    """
+    device = q.device
+    raw = _raw_stream(stream, device)
+    single = q.dim() == 3
+    _expect("q", q, device, (-1,) * (3 if single else 4), torch.bfloat16)
+    bsz, nq, hq, d = (q.shape[0], 1, q.shape[1], q.shape[2]) if single else q.shape
+    ptrs, (num_pages, page_size, hkv, cache_d, block) = _block_cache(k_cache, v_cache, k_scale, v_scale, device)
+    if cache_d != d:
+        raise ValueError("q and the cache must have the same head dimension")
+    table, indptr, width = _pages(block_table, kv_indptr, bsz, device)
+    lp = _expect("seq_lens", seq_lens, device, (bsz,), torch.int32)
+    if workspace is None:
+        need = attn_decode_fp8_block_workspace_bytes(bsz, nq, hq, hkv, d)
+        workspace = _allocate(stream, lambda: torch.zeros(max(need, 16), dtype=torch.uint8, device=device))
+    if o is None:
+        o = _allocate(stream, lambda: torch.empty_like(q))
+    if lse is None:
+        lse = _allocate(stream, lambda: torch.empty(q.shape[:-1], dtype=torch.float32, device=device))
+    st = lib().attn_decode_paged_fp8_block(
+        q.data_ptr(), *ptrs, table, indptr, width, lp, bsz, nq, hq, hkv, d, num_pages, page_size, block,
+        1.0 / math.sqrt(d) if scale is None else float(scale), _expect("workspace", workspace, device, (-1,), torch.uint8),
+        workspace.numel(), _expect("o", o, device, q.shape, torch.bfloat16),
+        _expect("lse", lse, device, q.shape[:-1], torch.float32),
+        _expect("dev_status", dev_status, device, (1,), torch.int32), raw)
+    _check("attn_decode_paged_fp8_block", st)
+    return o, lse, workspace
+
+
+def attn_prefill_fp8_block_workspace_bytes(B, max_kv_rows, Hkv, D=128):
+    """Bytes of workspace attn_prefill_paged_fp8_block takes."""
+    return int(lib().attn_prefill_fp8_block_workspace_bytes(B, max_kv_rows, Hkv, D))
+
+
+def attn_prefill_paged_fp8_block(q, k_cache, v_cache, k_scale, v_scale, qo_indptr, block_table, seq_lens,
+                                 kv_indptr=None, max_kv_rows=None, scale=None, workspace=None, o=None, lse=None,
+                                 dev_status=None, stream=None):
+    """Ragged causal prefill over the cache that :func:`attn_kv_append_fp8_block`
+    writes: ``q [total_q, Hq, D]`` bf16, rows ``qo_indptr[b]`` up to
+    ``qo_indptr[b+1]`` being the last positions of sequence b's ``seq_lens[b]``
+    cached tokens.  ``max_kv_rows``: at least the sum of ``seq_lens`` (by
+    default the pool's row count, which holds it unless sequences share pages).
+    ``workspace``: a uint8 tensor of attn_prefill_fp8_block_workspace_bytes()
+    bytes.  Returns ``(o [total_q, Hq, D], lse [total_q, Hq], workspace)``.
+    """
+    device = q.device
+    raw = _raw_stream(stream, device)
+    _expect("q", q, device, (-1, -1, -1), torch.bfloat16)
+    total, hq, d = q.shape
+    ptrs, (num_pages, page_size, hkv, cache_d, block) = _block_cache(k_cache, v_cache, k_scale, v_scale, device)
+    if cache_d != d:
+        raise ValueError("q and the cache must have the same head dimension")
+    bsz = seq_lens.numel()
+    lp = _expect("seq_lens", seq_lens, device, (bsz,), torch.int32)
+    qip = _expect("qo_indptr", qo_indptr, device, (bsz + 1,), torch.int32)
+    table, indptr, width = _pages(block_table, kv_indptr, bsz, device)
+    if max_kv_rows is None:
+        max_kv_rows = num_pages * page_size
+    if workspace is None:
+        need = attn_prefill_fp8_block_workspace_bytes(bsz, max_kv_rows, hkv, d)
+        workspace = _allocate(stream, lambda: torch.empty(max(need, 16), dtype=torch.uint8, device=device))
+    if o is None:
+        o = _allocate(stream, lambda: torch.empty_like(q))
+    if lse is None:
+        lse = _allocate(stream, lambda: torch.empty(total, hq, dtype=torch.float32, device=device))
+    st = lib().attn_prefill_paged_fp8_block(
+        q.data_ptr(), *ptrs, qip, table, indptr, width, lp, bsz, total, hq, hkv, d, num_pages, page_size, block,
+        int(max_kv_rows), 1.0 / math.sqrt(d) if scale is None else float(scale),
+        _expect("workspace", workspace, device, (-1,), torch.uint8), workspace.numel(),
+        _expect("o", o, device, q.shape, torch.bfloat16), _expect("lse", lse, device, (total, hq), torch.float32),
+        _expect("dev_status", dev_status, device, (1,), torch.int32), raw)
+    _check("attn_prefill_paged_fp8_block", st)
+    return o, lse, workspace
 
 
 def decode_partials_view(workspace, B, Hq, max_kv_len, split_tokens, D):

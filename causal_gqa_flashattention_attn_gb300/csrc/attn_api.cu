@@ -196,8 +196,60 @@ attn_status_t varlen_impl(const void* q, const void* k_cache, const void* v_cach
     if (total_q == 0) return ATTN_OK;
     VarlenArgs a{q,  k_cache, v_cache, qo_indptr, kv_indptr, kv_indices, kv_last_page_len, o,      lse,
                  B,  Hq,      Hkv,     D,         total_q,   num_pages,  page_size,        scale,  dev_status,
-                 kv_ws, max_kv_rows};
+                 kv_ws, max_kv_rows, false};
     return from_cuda(launch_prefill_varlen_tc(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+namespace {
+
+// The page list and pool sizes that the cache's writers and the readers of its
+// block-scaled form share.
+attn_status_t paged_check(const void* k_cache, const void* v_cache, const int32_t* block_table,
+                          const int32_t* kv_indptr, int max_pages, const int32_t* seq_lens, int B, int Hq, int Hkv,
+                          int D, int num_pages, int page_size) {
+    if (k_cache == nullptr || v_cache == nullptr || block_table == nullptr || seq_lens == nullptr)
+        return ATTN_ERR_INVALID_ARG;
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || num_pages <= 0 || page_size <= 0) return ATTN_ERR_INVALID_ARG;
+    if (kv_indptr == nullptr && max_pages <= 0) return ATTN_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache)) return ATTN_ERR_INVALID_ARG;
+    if (D != 128) return ATTN_ERR_UNSUPPORTED;
+    if (static_cast<long long>(num_pages) * page_size >= (1LL << 31) - 1) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+attn_status_t block_check(const float* k_scale, const float* v_scale, int page_size, int block_tokens) {
+    if (k_scale == nullptr || v_scale == nullptr) return ATTN_ERR_INVALID_ARG;
+    if (block_tokens <= 0 || page_size % block_tokens != 0) return ATTN_ERR_INVALID_ARG;
+    if (block_tokens % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+// The checks of both writers; `a` holds the arguments, a.k_scale NULL for bf16.
+attn_status_t append_impl(const AppendArgs& a, int D, void* stream) {
+    if (a.k == nullptr || a.v == nullptr || (a.q == nullptr) != (a.q_out == nullptr)) return ATTN_ERR_INVALID_ARG;
+    const attn_status_t st = paged_check(a.k_cache, a.v_cache, a.block_table, a.kv_indptr, a.max_pages, a.seq_lens,
+                                         a.B, a.Hq, a.Hkv, D, a.num_pages, a.page_size);
+    if (st != ATTN_OK) return st;
+    if (a.total_q < 0 || (a.qo_indptr == nullptr && a.total_q != a.B)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(a.k) || !aligned16(a.v) || (a.q != nullptr && (!aligned16(a.q) || !aligned16(a.q_out))))
+        return ATTN_ERR_INVALID_ARG;
+    if (a.k_stride % 8 != 0 || a.v_stride % 8 != 0 || a.k_stride < static_cast<long long>(a.Hkv) * D ||
+        a.v_stride < static_cast<long long>(a.Hkv) * D)
+        return ATTN_ERR_INVALID_ARG;
+    if (a.q != nullptr && (a.q_stride % 8 != 0 || a.q_stride < static_cast<long long>(a.Hq) * D))
+        return ATTN_ERR_INVALID_ARG;
+    if (a.q != nullptr && a.q == a.q_out && a.q_stride != static_cast<long long>(a.Hq) * D) return ATTN_ERR_INVALID_ARG;
+    if (a.rot_dim < 0 || a.rot_dim > D || (a.interleaved != 0 && a.interleaved != 1)) return ATTN_ERR_INVALID_ARG;
+    if (a.rot_dim > 0 && (a.cos_sin == nullptr || a.max_pos <= 0 || !aligned16(a.cos_sin))) return ATTN_ERR_INVALID_ARG;
+    if (a.rot_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+    if (static_cast<long long>(a.Hq) + 2LL * a.Hkv >= (1LL << 24)) return ATTN_ERR_UNSUPPORTED;
+    // one CTA per token and, for a block-scaled cache, per block
+    if (static_cast<long long>(a.total_q) + a.total_q / 16 + 2LL * a.B >= (1LL << 31)) return ATTN_ERR_UNSUPPORTED;
+    if (a.total_q == 0) return ATTN_OK;
+    return from_cuda(launch_kv_append(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -519,6 +571,108 @@ attn_status_t attn_prefill_paged_varlen_ws(const void* q, const void* k_cache, c
     if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
     return varlen_impl(q, k_cache, v_cache, qo_indptr, kv_indptr, kv_indices, kv_last_page_len, o, lse, B, Hq, Hkv,
                        D, total_q, num_pages, page_size, scale, dev_status, stream, workspace, max_kv_rows);
+}
+
+attn_status_t attn_kv_append(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                             long long v_stride, const float* cos_sin, int max_pos, int rot_dim, int interleaved,
+                             const int32_t* positions, const int32_t* qo_indptr, const int32_t* seq_lens,
+                             const int32_t* block_table, const int32_t* kv_indptr, int max_pages_per_seq,
+                             void* q_out, void* k_cache, void* v_cache, int B, int total_q, int Hq, int Hkv, int D,
+                             int num_pages, int page_size, int32_t* dev_status, void* stream) {
+    const AppendArgs a{q,       k,       v,       q_stride,    k_stride,  v_stride,          cos_sin,
+                       max_pos, rot_dim, interleaved, positions, qo_indptr, seq_lens,        block_table,
+                       kv_indptr, max_pages_per_seq, q_out, k_cache, v_cache, nullptr,       nullptr,
+                       B,       total_q, Hq,      Hkv,         num_pages, page_size,         1,
+                       dev_status};
+    return append_impl(a, D, stream);
+}
+
+attn_status_t attn_kv_append_fp8_block(const void* q, const void* k, const void* v, long long q_stride,
+                                       long long k_stride, long long v_stride, const float* cos_sin, int max_pos,
+                                       int rot_dim, int interleaved, const int32_t* positions,
+                                       const int32_t* qo_indptr, const int32_t* seq_lens, const int32_t* block_table,
+                                       const int32_t* kv_indptr, int max_pages_per_seq, void* q_out, void* k_cache,
+                                       void* v_cache, float* k_scale, float* v_scale, int B, int total_q, int Hq,
+                                       int Hkv, int D, int num_pages, int page_size, int block_tokens,
+                                       int32_t* dev_status, void* stream) {
+    const attn_status_t st = block_check(k_scale, v_scale, page_size, block_tokens);
+    if (st != ATTN_OK) return st;
+    const AppendArgs a{q,       k,       v,       q_stride,    k_stride,  v_stride,          cos_sin,
+                       max_pos, rot_dim, interleaved, positions, qo_indptr, seq_lens,        block_table,
+                       kv_indptr, max_pages_per_seq, q_out, k_cache, v_cache, k_scale,       v_scale,
+                       B,       total_q, Hq,      Hkv,         num_pages, page_size,         block_tokens,
+                       dev_status};
+    return append_impl(a, D, stream);
+}
+
+size_t attn_decode_fp8_block_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D) {
+    if (B <= 0 || q_len <= 0 || q_len > 16 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D != 128) return 0;
+    const int sms = device_sm_count();
+    return sms > 0 ? decode_fp8_block_workspace(q_len, Hq, Hkv, sms) : 0;
+}
+
+attn_status_t attn_decode_paged_fp8_block(const void* q, const void* k_cache, const void* v_cache,
+                                          const float* k_scale, const float* v_scale, const int32_t* block_table,
+                                          const int32_t* kv_indptr, int max_pages_per_seq, const int32_t* seq_lens,
+                                          int B, int q_len, int Hq, int Hkv, int D, int num_pages, int page_size,
+                                          int block_tokens, float scale, void* workspace, size_t workspace_bytes,
+                                          void* o, float* lse, int32_t* dev_status, void* stream) {
+    if (q == nullptr || o == nullptr || q_len <= 0) return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = paged_check(k_cache, v_cache, block_table, kv_indptr, max_pages_per_seq, seq_lens, B, Hq, Hkv,
+                                   D, num_pages, page_size);
+    if (st == ATTN_OK) st = block_check(k_scale, v_scale, page_size, block_tokens);
+    if (st != ATTN_OK) return st;
+    if (!std::isfinite(scale) || !aligned16(q) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
+    if (q_len > 16 || B > decode_fp8_block_max_seqs()) return ATTN_ERR_UNSUPPORTED;
+    if (static_cast<long long>(Hq) * q_len >= (1LL << 20)) return ATTN_ERR_UNSUPPORTED;
+    // tiles of 32 tokens are counted in int
+    if (kv_indptr == nullptr &&
+        (static_cast<long long>(max_pages_per_seq) * page_size / 32 + 1) * B >= (1LL << 31))
+        return ATTN_ERR_UNSUPPORTED;
+    if (workspace == nullptr || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
+    const int sms = device_sm_count();
+    if (sms <= 0) return ATTN_ERR_CUDA;
+    if (workspace_bytes < decode_fp8_block_workspace(q_len, Hq, Hkv, sms)) return ATTN_ERR_WORKSPACE;
+    const DecodeBlockArgs a{q,       k_cache, v_cache, k_scale, v_scale,   block_table, kv_indptr, max_pages_per_seq,
+                            seq_lens, B,      q_len,   Hq,      Hkv,       num_pages,   page_size, block_tokens,
+                            scale,   workspace, o,     lse,     dev_status};
+    return from_cuda(launch_decode_fp8_block(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_prefill_fp8_block_workspace_bytes(int B, int max_kv_rows, int Hkv, int D) {
+    if (B <= 0 || max_kv_rows <= 0 || Hkv <= 0 || D != 128) return 0;
+    return prefill_fp8_block_workspace(B, max_kv_rows, Hkv);
+}
+
+attn_status_t attn_prefill_paged_fp8_block(const void* q, const void* k_cache, const void* v_cache,
+                                           const float* k_scale, const float* v_scale, const int32_t* qo_indptr,
+                                           const int32_t* block_table, const int32_t* kv_indptr,
+                                           int max_pages_per_seq, const int32_t* seq_lens, int B, int total_q, int Hq,
+                                           int Hkv, int D, int num_pages, int page_size, int block_tokens,
+                                           int max_kv_rows, float scale, void* workspace, size_t workspace_bytes,
+                                           void* o, float* lse, int32_t* dev_status, void* stream) {
+    if (q == nullptr || o == nullptr || qo_indptr == nullptr || total_q < 0 || max_kv_rows <= 0)
+        return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = paged_check(k_cache, v_cache, block_table, kv_indptr, max_pages_per_seq, seq_lens, B, Hq, Hkv,
+                                   D, num_pages, page_size);
+    if (st == ATTN_OK) st = block_check(k_scale, v_scale, page_size, block_tokens);
+    if (st != ATTN_OK) return st;
+    if (!std::isfinite(scale) || !aligned16(q) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
+    if (Hq / Hkv > 128 || B > varlen_max_seqs()) return ATTN_ERR_UNSUPPORTED;
+    // as attn_prefill_paged_varlen: items and query blocks are counted in int and 21 bits
+    if (total_q >= (1 << 22) || (static_cast<long long>(total_q) + B) * Hkv >= (1LL << 31)) return ATTN_ERR_UNSUPPORTED;
+    // rows of the copy, each sequence's up to the next multiple of 128, are counted in int
+    if (static_cast<long long>(max_kv_rows) + 128LL * B >= (1LL << 31) ||
+        (static_cast<long long>(max_kv_rows) + 128LL * B) * Hkv >= (1LL << 33))
+        return ATTN_ERR_UNSUPPORTED;
+    if (workspace == nullptr || !aligned16(workspace) ||
+        workspace_bytes < prefill_fp8_block_workspace(B, max_kv_rows, Hkv))
+        return ATTN_ERR_WORKSPACE;
+    if (total_q == 0) return ATTN_OK;
+    const PrefillBlockArgs a{q,        k_cache, v_cache, k_scale, v_scale, qo_indptr, block_table, kv_indptr,
+                             max_pages_per_seq, seq_lens, B, total_q, Hq, Hkv, num_pages, page_size, block_tokens,
+                             max_kv_rows, scale, workspace, o, lse, dev_status};
+    return from_cuda(launch_prefill_fp8_block(a, static_cast<cudaStream_t>(stream)));
 }
 
 attn_status_t attn_lse_merge(const float* o_part, const float* lse_part, int N, int S, int D, void* o, float* lse,

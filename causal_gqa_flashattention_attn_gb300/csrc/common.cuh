@@ -135,7 +135,75 @@ struct VarlenArgs {
     int32_t* dev_status;
     void* kv_ws;            // NULL: gather rows inside the kernel; else contiguous K then V copy
     int max_kv_rows;        // rows the copy holds (>= kv_indptr[B] * page_size)
+    bool copied;            // the caller has made the copy: no gather is launched
 };
+// A paged cache's new tokens (kv_append.cu).
+struct AppendArgs {
+    const void* q;          // [total_q, Hq, D] bf16, rows q_stride elements apart; NULL: no queries
+    const void* k;          // [total_q, Hkv, D] bf16
+    const void* v;
+    long long q_stride, k_stride, v_stride;
+    const float* cos_sin;   // [max_pos, rot_dim]
+    int max_pos, rot_dim, interleaved;
+    const int32_t* positions;     // [total_q], may be NULL
+    const int32_t* qo_indptr;     // [B + 1], may be NULL
+    const int32_t* seq_lens;      // [B], after the append
+    const int32_t* block_table;   // [B, max_pages], or with kv_indptr a CSR list
+    const int32_t* kv_indptr;
+    int max_pages;
+    void* q_out;            // [total_q, Hq, D]
+    void* k_cache;          // [num_pages, page_size, Hkv, D]
+    void* v_cache;
+    float* k_scale;         // NULL: bf16 cache; else [num_pages, page_size / block_tokens, Hkv]
+    float* v_scale;
+    int B, total_q, Hq, Hkv, num_pages, page_size, block_tokens;
+    int32_t* dev_status;
+};
+cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
+
+// The readers of the block-scaled e4m3 cache (decode_fp8_block.cu, prefill_fp8_block.cu).
+struct DecodeBlockArgs {
+    const void* q;          // [B, q_len, Hq, D] bf16
+    const void* k_cache;    // [num_pages, page_size, Hkv, D] e4m3
+    const void* v_cache;
+    const float* k_scale;   // [num_pages, page_size / block_tokens, Hkv]
+    const float* v_scale;
+    const int32_t* block_table;
+    const int32_t* kv_indptr;   // may be NULL
+    int max_pages;
+    const int32_t* seq_lens;
+    int B, q_len, Hq, Hkv, num_pages, page_size, block_tokens;
+    float scale;
+    void* workspace;
+    void* o;                // as q
+    float* lse;             // [B, q_len, Hq] or NULL
+    int32_t* dev_status;
+};
+int decode_fp8_block_max_seqs();
+size_t decode_fp8_block_workspace(int q_len, int Hq, int Hkv, int sms);
+cudaError_t launch_decode_fp8_block(const DecodeBlockArgs& a, cudaStream_t stream);
+
+struct PrefillBlockArgs {
+    const void* q;          // [total_q, Hq, D] bf16
+    const void* k_cache;
+    const void* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* qo_indptr;   // [B + 1]
+    const int32_t* block_table;
+    const int32_t* kv_indptr;   // may be NULL
+    int max_pages;
+    const int32_t* seq_lens;
+    int B, total_q, Hq, Hkv, num_pages, page_size, block_tokens, max_kv_rows;
+    float scale;
+    void* workspace;
+    void* o;                // as q
+    float* lse;             // [total_q, Hq] or NULL
+    int32_t* dev_status;
+};
+size_t prefill_fp8_block_workspace(int B, int max_kv_rows, int Hkv);
+cudaError_t launch_prefill_fp8_block(const PrefillBlockArgs& a, cudaStream_t stream);
+
 int varlen_max_seqs();
 cudaError_t launch_prefill_varlen_tc(const VarlenArgs& a, cudaStream_t stream);
 

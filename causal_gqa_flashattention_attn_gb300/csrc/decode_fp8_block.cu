@@ -1,0 +1,590 @@
+// decode_fp8_block.cu - paged decode over an e4m3 KV cache with one scale per
+// block of tokens and KV head, one to sixteen causal queries per sequence.
+//
+// Mathematics, per query row r of a KV head, with codes k_t, v_t and the
+// scales a_t, b_t of their blocks:
+//   s_t = scale a_t (q_r . k_t),  O_r = sum_t p_t b_t v_t / sum_t p_t,
+//   p_t = 2^(log2e s_t - m),  over the visible tokens t <= len - q_len + i.
+// The codes enter m16n8k16 fp16 MMAs exactly (every e4m3 number is a half); q
+// is taken in fp16 after a power of two that brings its row's largest element
+// to [1, 2), so any bf16 magnitude fits.  a_t multiplies the fp32 score.  b_t
+// multiplies p_t before p_t b_t is rounded to fp16 for the value MMA, against
+// a running power M with p_t b_t 2^(m - M) <= 2^8 of its own: blocks whose
+// scales are far apart do not push each other's weights into fp16's
+// subnormals.  Sums and running maxima are fp32.
+//
+// Work: a column is a KV head with a group of up to 8 or 16 (query, head)
+// rows; every warp of the grid takes one column and an equal share of the
+// 32-token tiles of all sequences, so a ragged batch is balanced whatever its
+// lengths, which only the device knows.  A share that holds a whole sequence
+// writes its output; the pieces of a sequence that is cut between warps go to
+// the workspace and a second kernel joins them.
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace gb300 {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kTile = 32;       // tokens per step of a warp
+constexpr int kWarps = 8;       // per CTA
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxSeqs = 4096;  // tile counts before each sequence, in shared memory
+constexpr int kMergeThreads = 128;
+
+struct Params {
+    const __nv_bfloat16* q;   // [B, q_len, Hq, D]
+    const uint8_t* k_cache;   // [num_pages, page_size, Hkv, D]
+    const uint8_t* v_cache;
+    const float* k_scale;     // [num_pages, page_size / block, Hkv]
+    const float* v_scale;
+    PageList list;
+    const int32_t* seq_lens;
+    int B, Hq, Hkv, G, nq, block;
+    int cols;       // KV heads x row groups
+    int workers;    // shares per column
+    float scale_log2;
+    __nv_bfloat16* o;
+    float* lse;     // may be NULL
+    float* part_o;  // [2 workers][cols][rows][D]
+    float* part_l;  // [2 workers][cols][rows], log2
+    int32_t* status;
+};
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Transpose of an 8x8 matrix of 16-bit elements held in fragment layout.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Sequence b's cached tokens: its length within what its page list holds.
+__device__ __forceinline__ int length_of(const Params& p, int b, bool flag) {
+    const int len = p.seq_lens[b];
+    const long long cap = static_cast<long long>(page_count(p.list, b)) * p.list.page_size;
+    if (len < 0 || len > cap) {
+        if (flag) flag_status(p.status, ATTN_DEV_SEQ_TOO_LONG);
+        return len < 0 ? 0 : static_cast<int>(cap);
+    }
+    return len;
+}
+
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+
+// Whether a CSR list holds so many tokens that tiles do not count in int (the
+// host has checked block tables).
+__device__ __forceinline__ bool too_many_tiles(const Params& p) {
+    if (p.list.indptr == nullptr) return false;
+    return static_cast<long long>(p.list.indptr[p.B]) * p.list.page_size / kTile + p.B >= (1LL << 31);
+}
+
+// before[b] = tiles of the sequences before b (before[B] = all), by the whole
+// CTA: each thread sums a run of sequences.
+__device__ __forceinline__ void count_tiles(const Params& p, int* before, int* warp_sum, bool flag) {
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = threadIdx.x * per, b1 = min(b0 + per, p.B);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) sum += tiles_of(length_of(p, b, flag));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int base = incl - sum;
+    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    for (int b = b0; b < b1; ++b) {
+        before[b] = base;
+        base += tiles_of(length_of(p, b, false));
+    }
+    if (threadIdx.x == 0) {
+        int all = 0;
+        for (int w = 0; w < kWarps; ++w) all += warp_sum[w];
+        before[p.B] = all;
+    }
+    __syncthreads();
+}
+
+// Shares of `total` tiles in use, the first tile of share w, and the share of tile x.
+__device__ __forceinline__ int shares_of(int workers, int total) { return min(workers, total); }
+__device__ __forceinline__ int share_start(int total, int n, int w) {
+    return static_cast<int>(static_cast<long long>(total) * w / n);
+}
+__device__ __forceinline__ int share_of(int total, int n, int x) {
+    return static_cast<int>((static_cast<long long>(x + 1) * n - 1) / total);
+}
+
+// Per-warp state of the online softmax and the O^T accumulators of NB x 8 rows
+// (row 2t4 + j of block n): m for the sums, M for the values.
+template <int NB>
+struct State {
+    float o[NB][8][4];   // m-tile mt: elements 16g + 2mt (c0, c1) and + 1 (c2, c3)
+    float m[NB][2], M[NB][2], l[NB][2];
+};
+
+template <int NB>
+__device__ __forceinline__ void reset(State<NB>& st) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) st.o[n][i][0] = st.o[n][i][1] = st.o[n][i][2] = st.o[n][i][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            st.m[n][j] = st.M[n][j] = -INFINITY;
+            st.l[n][j] = 0.f;
+        }
+    }
+}
+
+// The query rows of a column in fp16 as B fragments: column g of block n is
+// row n * 8 + g, k pairs of k-step ks are elements 32t4 + 4ks + {0, 1}, {2, 3};
+// mul = log2e * scale over the row's power of two; lim = last visible token.
+template <int NB>
+struct Queries {
+    uint32_t f[NB][8][2];
+    float mul[NB][2];
+    int lim[NB][2];
+};
+
+template <int NB>
+__device__ __forceinline__ void load_queries(const Params& p, int b, int kvh, int row0, int n_rows, int len, int lane,
+                                             Queries<NB>& qs) {
+    const int g = lane >> 2, t4 = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        const int r = row0 + 8 * n + g;
+        const bool real = r < n_rows;
+        const int i = real ? r / p.G : 0, h = real ? r % p.G : 0;
+        const __nv_bfloat16* src =
+            p.q + ((static_cast<size_t>(b) * p.nq + i) * p.Hq + static_cast<size_t>(kvh) * p.G + h) * kD + 32 * t4;
+        float x[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+            if (real) raw = __ldg(reinterpret_cast<const uint4*>(src) + c);
+            const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[8 * c + 2 * k] = __uint_as_float(u[k] << 16);
+                x[8 * c + 2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+            }
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) top = fmaxf(top, fabsf(x[k]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^-e of the row's largest element (clamped so that both factors stay normal)
+        int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+        e = top == 0.f ? 0 : (e < -120 ? -120 : (e > 120 ? 120 : e));
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+            qs.f[n][ks][0] = pack_f16x2(x[4 * ks] * down, x[4 * ks + 1] * down);
+            qs.f[n][ks][1] = pack_f16x2(x[4 * ks + 2] * down, x[4 * ks + 3] * down);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int col = 2 * t4 + j, rr = row0 + 8 * n + col;
+            qs.mul[n][j] = __shfl_sync(0xffffffffu, up, 4 * col) * p.scale_log2;
+            qs.lim[n][j] = rr < n_rows ? len - p.nq + rr / p.G : -1;
+        }
+    }
+}
+
+// A bit for each of the four e4m3 bytes of a word that is NaN (bit 7 of the byte).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// Values that are NaN in a tile whose tokens some rows do not see: a weight of
+// 0 times NaN is NaN, so the code leaves the value MMA (as 0) and its element of
+// O becomes NaN in the rows that do see the token.  Lanes of a quad hold chunk g
+// of different tokens and O^T of different rows.
+template <int NB>
+__device__ __forceinline__ void take_nans(State<NB>& st, const Queries<NB>& qs, uint4 (&vx)[2][4], int tok0, int lane) {
+    const float nan = __int_as_float(0x7FFFFFFF);
+#pragma unroll
+    for (int sb = 0; sb < 2; ++sb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t* words = &vx[sb][i].x;
+#pragma unroll 1
+            for (int src = 0; src < 4; ++src) {
+                const int t = tok0 + 16 * sb + 2 * src + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t bad = nan_bytes(__shfl_sync(0xffffffffu, words[w], (lane & 28) + src));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)   // element 16g + 4w + e: m-tile 2w + e / 2, row half e mod 2
+                        if ((bad >> (8 * e)) & 0x80u) {
+#pragma unroll
+                            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                                for (int j = 0; j < 2; ++j)
+                                    if (t <= qs.lim[n][j]) st.o[n][2 * w + (e >> 1)][2 * (e & 1) + j] = nan;
+                        }
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) words[w] &= ~((nan_bytes(words[w]) >> 7) * 0xFFu);
+        }
+}
+
+// One 32-token tile of a warp as two 16-token sub-tiles.  kPartial: some token
+// is past the piece, its page is missing, or some row does not see it; tokens
+// whose bit of `valid` is not set may hold anything.  kx, vx: the code words,
+// [sub-tile][chunk]; ka, vb: the scales of the sub-tiles.
+template <int NB, bool kPartial>
+__device__ __forceinline__ void tile_step(State<NB>& st, const Queries<NB>& qs, const uint4 (&kx)[2][4],
+                                          uint4 (&vx)[2][4], const float (&ka)[2], const float (&vb)[2], int tok0,
+                                          uint32_t valid, int lane) {
+    const int g = lane >> 2, t4 = lane & 3;
+    float s[NB][2][4];
+#pragma unroll
+    for (int sb = 0; sb < 2; ++sb) {
+        const uint32_t wg[8] = {kx[sb][0].x, kx[sb][0].y, kx[sb][0].z, kx[sb][0].w,
+                                kx[sb][1].x, kx[sb][1].y, kx[sb][1].z, kx[sb][1].w};
+        const uint32_t w8[8] = {kx[sb][2].x, kx[sb][2].y, kx[sb][2].z, kx[sb][2].w,
+                                kx[sb][3].x, kx[sb][3].y, kx[sb][3].z, kx[sb][3].w};
+        float acc[NB][4];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+            const uint32_t a0 = e4m3x2_to_f16x2(wg[ks]), a1 = e4m3x2_to_f16x2(w8[ks]);
+            const uint32_t a2 = e4m3x2_to_f16x2(wg[ks] >> 16), a3 = e4m3x2_to_f16x2(w8[ks] >> 16);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) mma_f16_16816(acc[n], a0, a1, a2, a3, qs.f[n][ks][0], qs.f[n][ks][1]);
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[n][sb][e] = acc[n][e] * (ka[sb] * qs.mul[n][e & 1]);
+                if constexpr (kPartial) {
+                    const int t = 16 * sb + g + 8 * (e >> 1);
+                    if (!((valid >> t) & 1u) || tok0 + t > qs.lim[n][e & 1]) s[n][sb][e] = -INFINITY;
+                }
+            }
+        if constexpr (kPartial) {
+            // a weight of 0 times NaN is not 0: zero the codes
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = 16 * sb + 2 * t4 + (i & 1) + 8 * (i >> 1);
+                if (!((valid >> t) & 1u)) vx[sb][i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    }
+    if constexpr (kPartial) {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int sb = 0; sb < 2; ++sb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                bad |= nan_bytes(vx[sb][i].x) | nan_bytes(vx[sb][i].y) | nan_bytes(vx[sb][i].z) | nan_bytes(vx[sb][i].w);
+        if (__any_sync(0xffffffffu, bad != 0u)) take_nans<NB>(st, qs, vx, tok0, lane);
+    }
+    const float lb[2] = {__log2f(vb[0]), __log2f(vb[1])};   // -inf for a scale of 0
+    // running maxima, raised (and the sums rescaled) only when a score passes them by 2^8
+    bool over = false;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int sb = 0; sb < 2; ++sb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float x = fmaxf(s[n][sb][j], s[n][sb][2 + j]);
+                over |= x > st.m[n][j] + 8.f || x + lb[sb] > st.M[n][j] + 8.f;
+            }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float x0 = fmaxf(s[n][0][j], s[n][0][2 + j]), x1 = fmaxf(s[n][1][j], s[n][1][2 + j]);
+                float mx = fmaxf(x0, x1), Mx = fmaxf(x0 + lb[0], x1 + lb[1]);
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                    Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, off));
+                }
+                if (mx > st.m[n][j]) {
+                    st.l[n][j] *= ex2(st.m[n][j] - mx);
+                    st.m[n][j] = mx;
+                }
+                if (Mx > st.M[n][j]) {
+                    const float alpha = ex2(st.M[n][j] - Mx);
+                    st.M[n][j] = Mx;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        st.o[n][i][j] *= alpha;
+                        st.o[n][i][2 + j] *= alpha;
+                    }
+                }
+            }
+    }
+#pragma unroll
+    for (int sb = 0; sb < 2; ++sb) {
+        uint32_t w0[NB], w1[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            float w[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float m = st.m[n][j] == -INFINITY ? 0.f : st.m[n][j];
+                const float M = st.M[n][j] == -INFINITY ? 0.f : st.M[n][j];
+                st.l[n][j] += ex2(s[n][sb][j] - m) + ex2(s[n][sb][2 + j] - m);
+                // an exponential of its own: 2^(s - m) may be 0 where this is not
+                w[j] = ex2(s[n][sb][j] + (lb[sb] - M));
+                w[2 + j] = ex2(s[n][sb][2 + j] + (lb[sb] - M));
+            }
+            w0[n] = movmatrix_trans(pack_f16x2(w[0], w[1]));
+            w1[n] = movmatrix_trans(pack_f16x2(w[2], w[3]));
+        }
+        const uint32_t* xa = &vx[sb][0].x;
+        const uint32_t* xb = &vx[sb][1].x;
+        const uint32_t* xc = &vx[sb][2].x;
+        const uint32_t* xd = &vx[sb][3].x;
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+            const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;   // the two tokens' bytes of two elements
+            const uint32_t ab = __byte_perm(xa[mt >> 1], xb[mt >> 1], sel);
+            const uint32_t cd = __byte_perm(xc[mt >> 1], xd[mt >> 1], sel);
+            const uint32_t a0 = e4m3x2_to_f16x2(ab), a1 = e4m3x2_to_f16x2(ab >> 16);
+            const uint32_t a2 = e4m3x2_to_f16x2(cd), a3 = e4m3x2_to_f16x2(cd >> 16);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) mma_f16_16816(st.o[n][mt], a0, a1, a2, a3, w0[n], w1[n]);
+        }
+    }
+}
+
+template <int NB>
+__global__ void __launch_bounds__(kThreads, 1) decode_fp8_block_kernel(const Params p) {
+    extern __shared__ int before[];
+    __shared__ int warp_sum[kWarps];
+    if (too_many_tiles(p)) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) flag_status(p.status, ATTN_DEV_SEQ_TOO_LONG);
+        return;
+    }
+    count_tiles(p, before, warp_sum, blockIdx.x == 0);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const int total = before[p.B];
+    const int shares = shares_of(p.workers, total);
+    const int n_rows = p.G * p.nq;
+    const int n_warps = gridDim.x * kWarps;
+
+    for (int unit = blockIdx.x * kWarps + warp; unit < p.workers * p.cols; unit += n_warps) {
+        const int w = unit / p.cols, col = unit % p.cols;
+        const int kvh = col % p.Hkv, row0 = (col / p.Hkv) * 8 * NB;
+        const int rows = min(8 * NB, n_rows - row0);
+        auto out_row = [&](int b, int r) -> size_t {   // row of [B, q_len, Hq]
+            const int rr = row0 + r;
+            return (static_cast<size_t>(b) * p.nq + rr / p.G) * p.Hq + static_cast<size_t>(kvh) * p.G + rr % p.G;
+        };
+        // sequences without tokens: nothing is visible
+        for (int b = w; b < p.B; b += p.workers) {
+            if (before[b + 1] != before[b]) continue;
+            for (int r = 0; r < rows; ++r) {
+                const size_t row = out_row(b, r);
+                reinterpret_cast<uint2*>(p.o + row * kD)[lane] = make_uint2(0u, 0u);
+                if (p.lse != nullptr && lane == 0) p.lse[row] = -INFINITY;
+            }
+        }
+        if (w >= shares) continue;
+        int x = share_start(total, shares, w);
+        const int x_end = share_start(total, shares, w + 1);
+        int b = warp_rank(p.B, x, lane, [&](int i) { return before[i]; });
+        while (x < x_end) {
+            while (before[b + 1] <= x) ++b;
+            const int t_lo = x - before[b], n_tiles = before[b + 1] - before[b];
+            const int t_hi = min(n_tiles, t_lo + (x_end - x));
+            x += t_hi - t_lo;
+            const int len = length_of(p, b, false);
+            const int n_pages = page_count(p.list, b);
+            Queries<NB> qs;
+            load_queries<NB>(p, b, kvh, row0, n_rows, len, lane, qs);
+            State<NB> st;
+            reset<NB>(st);
+            const int lim_min = len - p.nq + row0 / p.G;   // the first row's limit, the smallest
+            for (int t = t_lo; t < t_hi; ++t) {
+                // lane i finds token i of the tile
+                const int tok0 = t * kTile, tok = tok0 + lane;
+                long long slot = -1;
+                if (tok < len) {
+                    const int page = page_at(p.list, b, tok / p.list.page_size, n_pages, p.status);
+                    if (page >= 0) slot = static_cast<long long>(page) * p.list.page_size + tok % p.list.page_size;
+                }
+                const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0);
+                float sk = 0.f, sv = 0.f;   // the scales of the token's block
+                if (slot >= 0) {
+                    const size_t at = static_cast<size_t>(slot / p.block) * p.Hkv + kvh;
+                    sk = __ldg(p.k_scale + at);
+                    sv = __ldg(p.v_scale + at);
+                }
+                const float ka[2] = {__shfl_sync(0xffffffffu, sk, 0), __shfl_sync(0xffffffffu, sk, 16)};
+                const float vb[2] = {__shfl_sync(0xffffffffu, sv, 0), __shfl_sync(0xffffffffu, sv, 16)};
+                uint4 kx[2][4], vx[2][4];
+                const size_t off = slot >= 0 ? (static_cast<size_t>(slot) * p.Hkv + kvh) * kD : 0;
+#pragma unroll
+                for (int sb = 0; sb < 2; ++sb)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        // K: chunks 2t4, 2t4 + 1 of tokens g, g + 8; V: chunk g of tokens 2t4, 2t4 + 1, + 8, + 9
+                        const size_t ko = __shfl_sync(0xffffffffu, off, 16 * sb + g + 8 * (i >> 1));
+                        const size_t vo = __shfl_sync(0xffffffffu, off, 16 * sb + 2 * t4 + (i & 1) + 8 * (i >> 1));
+                        kx[sb][i] = __ldg(reinterpret_cast<const uint4*>(p.k_cache + ko) + 2 * t4 + (i & 1));
+                        vx[sb][i] = __ldg(reinterpret_cast<const uint4*>(p.v_cache + vo) + g);
+                    }
+                if (valid == 0xffffffffu && tok0 + kTile - 1 <= lim_min)
+                    tile_step<NB, false>(st, qs, kx, vx, ka, vb, tok0, valid, lane);
+                else
+                    tile_step<NB, true>(st, qs, kx, vx, ka, vb, tok0, valid, lane);
+            }
+            // the piece's rows: normalised O and log2 of the sum
+            const bool whole = t_lo == 0 && t_hi == n_tiles;
+            const size_t part = (static_cast<size_t>(2 * w + (t_lo == 0 ? 1 : 0)) * p.cols + col) * (8 * NB);
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float l = st.l[n][j];
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                    const int r = 8 * n + 2 * t4 + j;
+                    if (r >= rows) continue;
+                    // O = 2^(M - m) sum p b v / l; rows that saw nothing have l = 0
+                    const float m = st.m[n][j], M = st.M[n][j];
+                    const float f = l == 0.f || M == -INFINITY ? 0.f : ex2(M - m) / l;
+                    const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+                    if (whole) {
+                        const size_t row = out_row(b, r);
+                        uint32_t u[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) u[i] = pack_bf16x2(st.o[n][i][j] * f, st.o[n][i][2 + j] * f);
+                        uint4* dst = reinterpret_cast<uint4*>(p.o + row * kD + 16 * g);
+                        dst[0] = make_uint4(u[0], u[1], u[2], u[3]);
+                        dst[1] = make_uint4(u[4], u[5], u[6], u[7]);
+                        if (p.lse != nullptr && g == 0) p.lse[row] = lse2 * kLn2;
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(p.part_o + (part + r) * kD + 16 * g);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            dst[i] = make_float4(st.o[n][2 * i][j] * f, st.o[n][2 * i][2 + j] * f,
+                                                 st.o[n][2 * i + 1][j] * f, st.o[n][2 * i + 1][2 + j] * f);
+                        if (g == 0) p.part_l[part + r] = lse2;
+                    }
+                }
+        }
+    }
+}
+
+// Joins the pieces of the sequences that were cut: a CTA per (sequence, query
+// row), a thread per element.  O = sum_s 2^(L_s - L) O_s / sum_s 2^(L_s - L).
+__global__ void __launch_bounds__(kMergeThreads) decode_fp8_block_merge_kernel(const Params p, int rows_per_col) {
+    __shared__ int part_sum[2][kMergeThreads / 32];
+    if (too_many_tiles(p)) return;
+    const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // tiles before the sequence, and of all of them
+    int pre = 0, all = 0;
+    for (int i = threadIdx.x; i < p.B; i += kMergeThreads) {
+        const int t = tiles_of(length_of(p, i, false));
+        all += t;
+        if (i < b) pre += t;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        pre += __shfl_xor_sync(0xffffffffu, pre, off);
+        all += __shfl_xor_sync(0xffffffffu, all, off);
+    }
+    if (lane == 0) part_sum[0][warp] = pre, part_sum[1][warp] = all;
+    __syncthreads();
+    pre = all = 0;
+#pragma unroll
+    for (int i = 0; i < kMergeThreads / 32; ++i) pre += part_sum[0][i], all += part_sum[1][i];
+    const int n_tiles = tiles_of(length_of(p, b, false));
+    if (n_tiles == 0) return;
+    const int shares = shares_of(p.workers, all);
+    const int w0 = share_of(all, shares, pre), w1 = share_of(all, shares, pre + n_tiles - 1);
+    if (w0 == w1) return;   // one share held it all
+    const int row = blockIdx.x;                       // of [q_len, Hq]
+    const int kvh = (row % p.Hq) / p.G, r = (row / p.Hq) * p.G + row % p.G;
+    const int col = (r / rows_per_col) * p.Hkv + kvh;
+    float top = -INFINITY;
+    auto at = [&](int w) -> size_t {   // the piece that starts the sequence is its share's second slot
+        return (static_cast<size_t>(2 * w + (w == w0 ? 1 : 0)) * p.cols + col) * rows_per_col + r % rows_per_col;
+    };
+    for (int w = w0; w <= w1; ++w) top = fmaxf(top, p.part_l[at(w)]);
+    float sum = 0.f, acc = 0.f;
+    for (int w = w0; w <= w1; ++w) {
+        const float l = p.part_l[at(w)];
+        if (l == -INFINITY) continue;
+        const float f = ex2(l - top);
+        sum += f;
+        acc = fmaf(f, p.part_o[at(w) * kD + threadIdx.x], acc);
+    }
+    const size_t out = static_cast<size_t>(b) * p.nq * p.Hq + row;
+    p.o[out * kD + threadIdx.x] = __float2bfloat16(sum == 0.f ? 0.f : acc / sum);
+    if (p.lse != nullptr && threadIdx.x == 0) p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+// Rows of a column: 8, or 16 where a KV head has more of them.
+int rows_per_column(int rows) { return rows <= 8 ? 8 : 16; }
+
+}  // namespace
+
+int decode_fp8_block_max_seqs() { return kMaxSeqs; }
+
+size_t decode_fp8_block_workspace(int q_len, int Hq, int Hkv, int sms) {
+    const int rows = (Hq / Hkv) * q_len, per = rows_per_column(rows);
+    const long long cols = static_cast<long long>(Hkv) * ((rows + per - 1) / per);
+    const long long warps = static_cast<long long>(sms) * kWarps;
+    const long long workers = warps / cols > 1 ? warps / cols : 1;
+    return static_cast<size_t>(2 * workers * cols * per) * (kD + 1) * sizeof(float);
+}
+
+cudaError_t launch_decode_fp8_block(const DecodeBlockArgs& a, cudaStream_t stream) {
+    const int sms = device_sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    Params p;
+    p.q = static_cast<const __nv_bfloat16*>(a.q);
+    p.k_cache = static_cast<const uint8_t*>(a.k_cache);
+    p.v_cache = static_cast<const uint8_t*>(a.v_cache);
+    p.k_scale = a.k_scale;
+    p.v_scale = a.v_scale;
+    p.list = PageList{a.block_table, a.kv_indptr, a.max_pages, a.num_pages, a.page_size};
+    p.seq_lens = a.seq_lens;
+    p.B = a.B;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.G = a.Hq / a.Hkv;
+    p.nq = a.q_len;
+    p.block = a.block_tokens;
+    const int rows = p.G * p.nq, per = rows_per_column(rows);
+    p.cols = a.Hkv * ((rows + per - 1) / per);
+    p.workers = sms * kWarps / p.cols > 1 ? sms * kWarps / p.cols : 1;
+    p.scale_log2 = a.scale * kLog2e;
+    p.o = static_cast<__nv_bfloat16*>(a.o);
+    p.lse = a.lse;
+    p.part_o = static_cast<float*>(a.workspace);
+    p.part_l = p.part_o + static_cast<size_t>(2) * p.workers * p.cols * per * kD;
+    p.status = a.dev_status;
+    const size_t smem = (static_cast<size_t>(a.B) + 1) * sizeof(int);
+    if (per == 8)
+        decode_fp8_block_kernel<1><<<sms, kThreads, smem, stream>>>(p);
+    else
+        decode_fp8_block_kernel<2><<<sms, kThreads, smem, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    decode_fp8_block_merge_kernel<<<dim3(a.q_len * a.Hq, a.B), kMergeThreads, 0, stream>>>(p, per);
+    return cudaGetLastError();
+}
+
+}  // namespace gb300

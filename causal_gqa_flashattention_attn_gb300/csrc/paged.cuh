@@ -1,0 +1,69 @@
+// paged.cuh - page lists, ragged batches and e4m3 conversions shared by the
+// kernels that write a paged KV cache and those that read its 8-bit form.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace gb300 {
+
+// Pages of the sequences: row b of a block table (indptr NULL), or entries
+// [indptr[b], indptr[b+1]) of a CSR list.
+struct PageList {
+    const int32_t* pages;
+    const int32_t* indptr;
+    int max_pages;   // entries per row of the block table
+    int num_pages, page_size;
+};
+
+// Entries of sequence b's list.
+__device__ __forceinline__ int page_count(const PageList& l, int b) {
+    return l.indptr != nullptr ? l.indptr[b + 1] - l.indptr[b] : l.max_pages;
+}
+
+// The pool page in entry e >= 0 of sequence b's list of n entries, or -1 (and
+// the status bit) past the list's end or outside the pool.
+__device__ __forceinline__ int page_at(const PageList& l, int b, int e, int n, int32_t* status) {
+    if (e >= n) {
+        flag_status(status, ATTN_DEV_SEQ_TOO_LONG);
+        return -1;
+    }
+    const size_t base = l.indptr != nullptr ? static_cast<size_t>(l.indptr[b])
+                                            : static_cast<size_t>(b) * static_cast<size_t>(l.max_pages);
+    const int page = l.pages[base + e];
+    if (page < 0 || page >= l.num_pages) {
+        flag_status(status, ATTN_DEV_PAGE_OUT_OF_RANGE);
+        return -1;
+    }
+    return page;
+}
+
+// Last b in [0, B) with key(b) <= x, for key(0) <= x and key not decreasing; a
+// whole warp counts together, 32 keys per round with independent loads.
+template <typename Key>
+__device__ __forceinline__ int warp_rank(int B, int x, int lane, Key key) {
+    int n = 0;
+#pragma unroll 4
+    for (int b0 = 0; b0 < B; b0 += 32)
+        n += __popc(__ballot_sync(0xffffffffu, b0 + lane < B && key(b0 + lane) <= x));
+    return n > 0 ? n - 1 : 0;
+}
+
+// Two floats to two e4m3 bytes (lo in the low byte), round to nearest even;
+// beyond +-448 (infinities too) becomes +-448, NaN stays NaN.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two e4m3 bytes to two halves (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
+    return r;
+}
+
+}  // namespace gb300

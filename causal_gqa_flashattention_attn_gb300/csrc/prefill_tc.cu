@@ -1412,7 +1412,7 @@ cudaError_t launch_prefill_varlen_tc(const VarlenArgs& a, cudaStream_t stream) {
                               CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
         const int row_vecs = static_cast<int>(row_bytes / 16);
-        gather_pages_kernel<<<sms * 8, 256, 0, stream>>>(
+        if (!a.copied) gather_pages_kernel<<<sms * 8, 256, 0, stream>>>(
             static_cast<const uint4*>(a.k_cache), static_cast<const uint4*>(a.v_cache), a.kv_indptr, a.kv_indices,
             a.B, a.page_size, a.num_pages, row_vecs, reinterpret_cast<uint4*>(k_ws), reinterpret_cast<uint4*>(v_ws),
             a.max_kv_rows, a.dev_status);

@@ -57,6 +57,7 @@ typedef enum {
 #define ATTN_DEV_SEQ_TOO_LONG      0x2  /* seq_lens[b] > max_kv_len or > max_pages_per_seq * page_size */
 #define ATTN_DEV_WAIT_TIMEOUT      0x4  /* a bounded mbarrier wait gave up */
 #define ATTN_DEV_WORKSPACE_STATE   0x8  /* attn_prefill_fwd_ws: the split counters were not zero */
+#define ATTN_DEV_POSITION_OUT_OF_RANGE 0x10  /* attn_kv_append: a position < 0 or >= max_pos */
 
 /*
  * attn_prefill_fwd - causal GQA prefill.
@@ -452,6 +453,157 @@ attn_status_t attn_decode_paged_splitk_static(const void* q, const void* k_cache
                                               void* o, float* lse, int32_t* dev_status, void* stream);
 
 /*
+ * attn_kv_append - writes new keys and values into a bf16 paged KV cache and
+ * rotates the new queries and keys by their positions on the way.
+ *
+ * The pages read paged caches and show no writer; this is the one that the
+ * paged decode and prefill entries of this library are fed by.  With (c, s) the
+ * cosine and sine of pair i at a token's position, a pair (a, b) of its first
+ * rot_dim elements becomes (a c - b s, a s + b c) in fp32 and is rounded once;
+ * the elements from rot_dim on, and v, are copied.
+ *
+ *   q            [total_q, Hq, D] bfloat16, token rows q_stride elements apart
+ *                (read; NULL: keys and values only)
+ *   k, v         [total_q, Hkv, D] bfloat16, k_stride and v_stride apart (read)
+ *   *_stride     multiples of 8, at least Hq * D or Hkv * D (q, k and v may be
+ *                parts of one projection's output)
+ *   cos_sin      float32 [max_pos, rot_dim]: rot_dim / 2 cosines, then as many
+ *                sines, of each position (read; NULL with rot_dim 0)
+ *   rot_dim      0 (no rotation) or a multiple of 16 up to D
+ *   interleaved  0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1)
+ *   positions    int32 [total_q], the table row of each token (read; NULL: its
+ *                index in its sequence)
+ *   qo_indptr    int32 [B + 1]: the new tokens of sequence b are rows
+ *                [qo_indptr[b], qo_indptr[b+1]); rows of no sequence are left
+ *                alone (read; NULL: one token per sequence, total_q = B)
+ *   seq_lens     int32 [B], the lengths AFTER the append, as the attention
+ *                that follows takes them (read): with n new tokens, the i-th
+ *                goes to index seq_lens[b] - n + i.  A token whose index would
+ *                be negative (a padded batch's entry of length 0) is left alone.
+ *   block_table  int32 [B, max_pages_per_seq] (kv_indptr NULL), or with
+ *                kv_indptr int32 [B + 1] a CSR list (the kv_indices of
+ *                attn_prefill_paged_varlen; max_pages_per_seq is not used):
+ *                entry t / page_size of a sequence's list is the pool page of
+ *                its token t (read)
+ *   q_out        [total_q, Hq, D] bfloat16, dense (written; may be q itself
+ *                where q is dense; NULL with q)
+ *   k_cache, v_cache  bfloat16 [num_pages, page_size, Hkv, D] (written)
+ *   D            128
+ * A missing page (ATTN_DEV_PAGE_OUT_OF_RANGE, or ATTN_DEV_SEQ_TOO_LONG past
+ * the list's end) leaves its tokens' keys and values unwritten; a position
+ * outside [0, max_pos) (ATTN_DEV_POSITION_OUT_OF_RANGE) leaves the whole token
+ * out.  Pages that take new tokens belong to one sequence each.
+ */
+attn_status_t attn_kv_append(const void* q, const void* k, const void* v,
+                             long long q_stride, long long k_stride, long long v_stride,
+                             const float* cos_sin, int max_pos, int rot_dim, int interleaved,
+                             const int32_t* positions, const int32_t* qo_indptr, const int32_t* seq_lens,
+                             const int32_t* block_table, const int32_t* kv_indptr, int max_pages_per_seq,
+                             void* q_out, void* k_cache, void* v_cache,
+                             int B, int total_q, int Hq, int Hkv, int D, int num_pages, int page_size,
+                             int32_t* dev_status, void* stream);
+
+/*
+ * attn_kv_append_fp8_block - attn_kv_append into an e4m3 cache with one scale
+ * per block of tokens and KV head.
+ *
+ * The cache holds value = e4m3(code) * scale of the code's block; a block is
+ * block_tokens tokens of one page (page_size is a multiple of it).  A block's
+ * scale becomes the smallest power of two 2^e >= 2^-126 with
+ * max |new value| / 2^e <= 448 (0 if all are 0), but no less than the scale
+ * that its earlier tokens have; if it grows, their codes are rescaled (exact
+ * but for codes that become e4m3 subnormals; a stored scale that is no power
+ * of two counts as the next one above).  New codes are value / scale rounded
+ * once, to nearest even, keys after their rotation: a value next to a border
+ * between two codes falls on the side that 64-bit arithmetic gives.  A NaN is
+ * stored as NaN and an infinity as the block's largest code; neither counts for
+ * the scale.  A block whose first new token is its first token starts afresh.
+ *
+ *   k_cache, v_cache  uint8 [num_pages, page_size, Hkv, D], e4m3 bytes (written)
+ *   k_scale, v_scale  float32 [num_pages, page_size / block_tokens, Hkv]
+ *                     (read and written)
+ *   block_tokens      a multiple of 16 that divides page_size
+ * Other arguments and errors as attn_kv_append.
+ */
+attn_status_t attn_kv_append_fp8_block(const void* q, const void* k, const void* v,
+                                       long long q_stride, long long k_stride, long long v_stride,
+                                       const float* cos_sin, int max_pos, int rot_dim, int interleaved,
+                                       const int32_t* positions, const int32_t* qo_indptr, const int32_t* seq_lens,
+                                       const int32_t* block_table, const int32_t* kv_indptr, int max_pages_per_seq,
+                                       void* q_out, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                       int B, int total_q, int Hq, int Hkv, int D, int num_pages, int page_size,
+                                       int block_tokens, int32_t* dev_status, void* stream);
+
+/*
+ * attn_decode_paged_fp8_block - decode over the cache that
+ * attn_kv_append_fp8_block writes, 1 to 16 causal queries per sequence, merge
+ * included.
+ *
+ * O = softmax(scale * q K^T + mask) V with K, V = code * scale of its block:
+ * query i of a sequence sees tokens t <= len - q_len + i.  A row that sees
+ * nothing gets O = 0 and LSE = -inf.  The work is cut evenly over the GPU on
+ * the device, whatever the lengths, so there is no split size to choose; the
+ * pieces of a sequence are joined by LSE weight in a fixed order, so results
+ * do not depend on timing.
+ *
+ *   q            [B, q_len, Hq, D] bfloat16: token-major, as attn_kv_append
+ *                writes q_out for q_len new tokens per sequence       (read)
+ *   k_cache, v_cache, k_scale, v_scale, block_table, kv_indptr, page_size,
+ *   block_tokens as attn_kv_append_fp8_block (read).  Scales are finite and
+ *                not negative; any such scale is taken, not only powers of two.
+ *   seq_lens     int32 [B] (read)
+ *   workspace    >= attn_decode_fp8_block_workspace_bytes() bytes, 16-byte
+ *                aligned (the current device's share count goes into it).
+ *                Zero it once; every call that completes leaves it ready for
+ *                the next.  Calls that may run at the same time need separate
+ *                workspaces.
+ *   o            as q (written); lse float32 [B, q_len, Hq], natural log
+ *                (written; may be NULL)
+ *   D = 128, q_len 1..16, any Hq % Hkv == 0, B <= 4096; with a block table
+ *   B * (max_pages_per_seq * page_size / 32 + 1) < 2^31.
+ * Bad pages are left out as in attn_decode_paged_splitk; a length past the
+ * page list sets ATTN_DEV_SEQ_TOO_LONG and is cut there.
+ */
+size_t attn_decode_fp8_block_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D);
+attn_status_t attn_decode_paged_fp8_block(const void* q, const void* k_cache, const void* v_cache,
+                                          const float* k_scale, const float* v_scale,
+                                          const int32_t* block_table, const int32_t* kv_indptr,
+                                          int max_pages_per_seq, const int32_t* seq_lens,
+                                          int B, int q_len, int Hq, int Hkv, int D, int num_pages, int page_size,
+                                          int block_tokens, float scale, void* workspace, size_t workspace_bytes,
+                                          void* o, float* lse, int32_t* dev_status, void* stream);
+
+/*
+ * attn_prefill_paged_fp8_block - causal prefill of a ragged batch over the
+ * same cache: what attn_prefill_paged_varlen_ws computes, with K and V =
+ * code * scale (rounded to bf16, which is exact for the power-of-two scales
+ * that attn_kv_append_fp8_block writes) and the sequences' lengths given
+ * directly.
+ *
+ *   q            [total_q, Hq, D] bfloat16; sequence b owns rows
+ *                [qo_indptr[b], qo_indptr[b+1])                       (read)
+ *   seq_lens     int32 [B], cached tokens, the new ones included      (read)
+ *   max_kv_rows  rows the workspace holds: at least the sum of seq_lens (more
+ *                sets ATTN_DEV_SEQ_TOO_LONG and is cut)
+ *   workspace    >= attn_prefill_fp8_block_workspace_bytes() bytes, 16-byte
+ *                aligned (scratch, overwritten)
+ *   o            [total_q, Hq, D]; lse float32 [total_q, Hq] or NULL (written)
+ * Cache and page-list arguments as attn_decode_paged_fp8_block; limits as
+ * attn_prefill_paged_varlen.  A token on a bad page is read as zeros.  A NaN
+ * among a sequence's values shows in every query of that sequence whose last
+ * visible token is in the same 128-token tile or later.
+ */
+size_t attn_prefill_fp8_block_workspace_bytes(int B, int max_kv_rows, int Hkv, int D);
+attn_status_t attn_prefill_paged_fp8_block(const void* q, const void* k_cache, const void* v_cache,
+                                           const float* k_scale, const float* v_scale, const int32_t* qo_indptr,
+                                           const int32_t* block_table, const int32_t* kv_indptr,
+                                           int max_pages_per_seq, const int32_t* seq_lens,
+                                           int B, int total_q, int Hq, int Hkv, int D, int num_pages, int page_size,
+                                           int block_tokens, int max_kv_rows, float scale,
+                                           void* workspace, size_t workspace_bytes,
+                                           void* o, float* lse, int32_t* dev_status, void* stream);
+
+/*
  * attn_lse_merge - LSE-weighted merge of split partials.
  *
  * Follows "splitk_kernels.py", _splitK_reduce: per row n,
@@ -516,7 +668,11 @@ const char* attn_status_string(attn_status_t status);
  * 109 32-token splits for the persistent int4 decode; the balanced split takes a tile.
  * 110 the tensor-core prefill takes any Hq / Hkv up to 128 (not only divisors of 128), and D = 64.
  * 111 the fused decode's workspace holds three more words (the cooperative grid merge).
- * 112 attn_decode_cooperative. */
+ * 112 attn_decode_cooperative.
+ * The entries of the paged cache's writers and of its block-scaled form
+ * (attn_kv_append, attn_kv_append_fp8_block, attn_decode_paged_fp8_block,
+ * attn_prefill_paged_fp8_block) came after it and changed nothing that was
+ * there: a caller that may meet an older library looks for the symbols. */
 int attn_abi_version(void);
 
 #ifdef __cplusplus
