@@ -30,6 +30,9 @@ constexpr int kTile = 32;       // tokens per step of a warp
 constexpr int kWarps = 8;       // per CTA
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxSeqs = 4096;  // tile counts before each sequence, in shared memory
+constexpr int kStages = 3;      // tiles in flight or in use per warp
+constexpr int kCodes = kTile * kD;                    // 4 KB: a tile's K (or V) codes of one head
+constexpr int kWarpBytes = kStages * 2 * kCodes;
 constexpr int kMergeThreads = 128;
 
 struct Params {
@@ -40,7 +43,8 @@ struct Params {
     const float* v_scale;
     PageList list;
     const int32_t* seq_lens;
-    int B, Hq, Hkv, G, nq, block;
+    Divisor page_div, block_div;
+    int B, Hq, Hkv, G, nq;
     int cols;       // KV heads x row groups
     int workers;    // shares per column
     float scale_log2;
@@ -239,21 +243,25 @@ __device__ __forceinline__ void take_nans(State<NB>& st, const Queries<NB>& qs, 
 }
 
 // One 32-token tile of a warp as two 16-token sub-tiles.  kPartial: some token
-// is past the piece, its page is missing, or some row does not see it; tokens
-// whose bit of `valid` is not set may hold anything.  kx, vx: the code words,
-// [sub-tile][chunk]; ka, vb: the scales of the sub-tiles.
+// is not there (its codes are zeros and its bit of `valid` is not set), or some
+// row does not see it.  codes: K, then V; k_at, v_at: this lane's chunks of the
+// first sub-tile, the second is 16 rows on; ka, vb: the scales of the sub-tiles.
 template <int NB, bool kPartial>
-__device__ __forceinline__ void tile_step(State<NB>& st, const Queries<NB>& qs, const uint4 (&kx)[2][4],
-                                          uint4 (&vx)[2][4], const float (&ka)[2], const float (&vb)[2], int tok0,
-                                          uint32_t valid, int lane) {
-    const int g = lane >> 2, t4 = lane & 3;
+__device__ __forceinline__ void tile_step(State<NB>& st, const Queries<NB>& qs, const uint8_t* codes,
+                                          const int (&k_at)[2], const int (&v_at)[2], const float (&ka)[2],
+                                          const float (&vb)[2], int tok0, uint32_t valid, int lane) {
+    const int g = lane >> 2;
     float s[NB][2][4];
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb) {
-        const uint32_t wg[8] = {kx[sb][0].x, kx[sb][0].y, kx[sb][0].z, kx[sb][0].w,
-                                kx[sb][1].x, kx[sb][1].y, kx[sb][1].z, kx[sb][1].w};
-        const uint32_t w8[8] = {kx[sb][2].x, kx[sb][2].y, kx[sb][2].z, kx[sb][2].w,
-                                kx[sb][3].x, kx[sb][3].y, kx[sb][3].z, kx[sb][3].w};
+        uint4 kx[4];   // chunks 2t4, 2t4 + 1 of token g, then of token g + 8
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            kx[i] = *reinterpret_cast<const uint4*>(codes + (16 * sb + 8 * (i >> 1)) * kD + k_at[i & 1]);
+        const uint32_t wg[8] = {kx[0].x, kx[0].y, kx[0].z, kx[0].w,
+                                kx[1].x, kx[1].y, kx[1].z, kx[1].w};
+        const uint32_t w8[8] = {kx[2].x, kx[2].y, kx[2].z, kx[2].w,
+                                kx[3].x, kx[3].y, kx[3].z, kx[3].w};
         float acc[NB][4];
 #pragma unroll
         for (int n = 0; n < NB; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
@@ -274,15 +282,13 @@ __device__ __forceinline__ void tile_step(State<NB>& st, const Queries<NB>& qs, 
                     if (!((valid >> t) & 1u) || tok0 + t > qs.lim[n][e & 1]) s[n][sb][e] = -INFINITY;
                 }
             }
-        if constexpr (kPartial) {
-            // a weight of 0 times NaN is not 0: zero the codes
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 16 * sb + 2 * t4 + (i & 1) + 8 * (i >> 1);
-                if (!((valid >> t) & 1u)) vx[sb][i] = make_uint4(0u, 0u, 0u, 0u);
-            }
-        }
     }
+    uint4 vx[2][4];   // chunk g of tokens 2t4, 2t4 + 1, 2t4 + 8, 2t4 + 9
+#pragma unroll
+    for (int sb = 0; sb < 2; ++sb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            vx[sb][i] = *reinterpret_cast<const uint4*>(codes + (16 * sb + 8 * (i >> 1)) * kD + v_at[i & 1]);
     if constexpr (kPartial) {
         uint32_t bad = 0;
 #pragma unroll
@@ -366,10 +372,81 @@ __device__ __forceinline__ void tile_step(State<NB>& st, const Queries<NB>& qs, 
     }
 }
 
+// What a tile's copies bring besides its codes.
+struct TileInfo {
+    float k[2], v[2];   // scales of the two sub-tiles
+    uint32_t valid;     // tokens that are there
+    uint32_t pad[3];
+};
+
+// Byte offset of 16-byte chunk c of row r of a tile's codes: the chunk is
+// XOR-ed with the row, so the eight lanes of a shared-memory phase, which read
+// one chunk of two rows' four or chunk pairs, meet eight different ones.
+__device__ __forceinline__ int chunk_off(int r, int c) { return r * kD + (((c ^ r) & 7) << 4); }
+
+// The tiles of a warp's share, fetched ahead: `x` is the next one, in sequence
+// b; the page of its token `lane` has been looked up one step before it is used.
+struct Feed {
+    int x, x_end, b, len;
+    int page, tok;   // tok: the lane's token, or -1 past the sequence's end
+};
+
+__device__ __forceinline__ void feed_look(const Params& p, const int* before, Feed& f, int lane) {
+    if (f.x >= f.x_end) return;
+    if (before[f.b + 1] <= f.x) {
+        do ++f.b;
+        while (before[f.b + 1] <= f.x);
+        f.len = length_of(p, f.b, false);
+    }
+    const int tok = (f.x - before[f.b]) * kTile + lane;
+    f.tok = tok < f.len ? tok : -1;
+    f.page = -1;
+    if (f.tok >= 0) {
+        const size_t base = p.list.indptr != nullptr ? static_cast<size_t>(p.list.indptr[f.b])
+                                                     : static_cast<size_t>(f.b) * static_cast<size_t>(p.list.max_pages);
+        f.page = __ldg(p.list.pages + base + p.page_div.div(tok));
+    }
+}
+
+// Issues the copies of tile f.x into a stage (zeros for tokens that are not
+// there), as one group, and looks at the next one.
+__device__ __forceinline__ void feed_tile(const Params& p, const int* before, Feed& f, uint8_t* stage, TileInfo* info,
+                                          int kvh, int lane) {
+    if (f.x < f.x_end) {
+        const bool there = f.tok >= 0 && f.page >= 0 && f.page < p.list.num_pages;
+        if (f.tok >= 0 && !there) flag_status(p.status, ATTN_DEV_PAGE_OUT_OF_RANGE);
+        const uint32_t valid = __ballot_sync(0xffffffffu, there);
+        const int o = there ? f.tok - p.page_div.div(f.tok) * p.list.page_size : 0;
+        const int page = there ? f.page : 0;
+        const size_t row_bytes = static_cast<size_t>(p.Hkv) * kD;
+        const size_t off = (static_cast<size_t>(page) * p.list.page_size + o) * row_bytes + static_cast<size_t>(kvh) * kD;
+        if ((lane & 15) == 0) {
+            const size_t at = (static_cast<size_t>(page) * (p.page_div.d / p.block_div.d) + p.block_div.div(o)) * p.Hkv + kvh;
+            cp_async4(&info->k[lane >> 4], p.k_scale + at, there ? 4 : 0);
+            cp_async4(&info->v[lane >> 4], p.v_scale + at, there ? 4 : 0);
+        }
+        if (lane == 0) info->valid = valid;
+        const int c = lane & 7, r0 = lane >> 3;
+#pragma unroll
+        for (int i = 0; i < kTile / 4; ++i) {
+            const int r = r0 + 4 * i;
+            const size_t src = __shfl_sync(0xffffffffu, off, r) + 16 * c;
+            const uint32_t n = (valid >> r) & 1u ? 16 : 0;
+            cp_async16(stage + chunk_off(r, c), p.k_cache + src, n);
+            cp_async16(stage + kCodes + chunk_off(r, c), p.v_cache + src, n);
+        }
+        ++f.x;
+        feed_look(p, before, f, lane);
+    }
+    cp_async_commit();
+}
+
 template <int NB>
 __global__ void __launch_bounds__(kThreads, 1) decode_fp8_block_kernel(const Params p) {
-    extern __shared__ int before[];
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ TileInfo infos[kWarps][kStages];
     __shared__ int warp_sum[kWarps];
+    int* before = reinterpret_cast<int*>(smem + kWarps * kWarpBytes);
     if (too_many_tiles(p)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) flag_status(p.status, ATTN_DEV_SEQ_TOO_LONG);
         return;
@@ -380,6 +457,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp8_block_kernel(const Par
     const int shares = shares_of(p.workers, total);
     const int n_rows = p.G * p.nq;
     const int n_warps = gridDim.x * kWarps;
+    uint8_t* ring = smem + warp * kWarpBytes;
+    TileInfo* info = infos[warp];
+    int k_at[2], v_at[2];   // K: chunks 2t4, 2t4 + 1 of row g; V: chunk g of rows 2t4, 2t4 + 1
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        k_at[i] = chunk_off(g, 2 * t4 + i);
+        v_at[i] = kCodes + chunk_off(2 * t4 + i, g);
+    }
 
     for (int unit = blockIdx.x * kWarps + warp; unit < p.workers * p.cols; unit += n_warps) {
         const int w = unit / p.cols, col = unit % p.cols;
@@ -402,51 +487,41 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp8_block_kernel(const Par
         int x = share_start(total, shares, w);
         const int x_end = share_start(total, shares, w + 1);
         int b = warp_rank(p.B, x, lane, [&](int i) { return before[i]; });
+        Feed f;
+        f.x = x;
+        f.x_end = x_end;
+        f.b = b;
+        f.len = length_of(p, b, false);
+        feed_look(p, before, f, lane);
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) feed_tile(p, before, f, ring + i * 2 * kCodes, info + i, kvh, lane);
+        int slot = 0;
         while (x < x_end) {
             while (before[b + 1] <= x) ++b;
             const int t_lo = x - before[b], n_tiles = before[b + 1] - before[b];
             const int t_hi = min(n_tiles, t_lo + (x_end - x));
             x += t_hi - t_lo;
             const int len = length_of(p, b, false);
-            const int n_pages = page_count(p.list, b);
             Queries<NB> qs;
             load_queries<NB>(p, b, kvh, row0, n_rows, len, lane, qs);
             State<NB> st;
             reset<NB>(st);
             const int lim_min = len - p.nq + row0 / p.G;   // the first row's limit, the smallest
             for (int t = t_lo; t < t_hi; ++t) {
-                // lane i finds token i of the tile
-                const int tok0 = t * kTile, tok = tok0 + lane;
-                long long slot = -1;
-                if (tok < len) {
-                    const int page = page_at(p.list, b, tok / p.list.page_size, n_pages, p.status);
-                    if (page >= 0) slot = static_cast<long long>(page) * p.list.page_size + tok % p.list.page_size;
-                }
-                const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0);
-                float sk = 0.f, sv = 0.f;   // the scales of the token's block
-                if (slot >= 0) {
-                    const size_t at = static_cast<size_t>(slot / p.block) * p.Hkv + kvh;
-                    sk = __ldg(p.k_scale + at);
-                    sv = __ldg(p.v_scale + at);
-                }
-                const float ka[2] = {__shfl_sync(0xffffffffu, sk, 0), __shfl_sync(0xffffffffu, sk, 16)};
-                const float vb[2] = {__shfl_sync(0xffffffffu, sv, 0), __shfl_sync(0xffffffffu, sv, 16)};
-                uint4 kx[2][4], vx[2][4];
-                const size_t off = slot >= 0 ? (static_cast<size_t>(slot) * p.Hkv + kvh) * kD : 0;
-#pragma unroll
-                for (int sb = 0; sb < 2; ++sb)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        // K: chunks 2t4, 2t4 + 1 of tokens g, g + 8; V: chunk g of tokens 2t4, 2t4 + 1, + 8, + 9
-                        const size_t ko = __shfl_sync(0xffffffffu, off, 16 * sb + g + 8 * (i >> 1));
-                        const size_t vo = __shfl_sync(0xffffffffu, off, 16 * sb + 2 * t4 + (i & 1) + 8 * (i >> 1));
-                        kx[sb][i] = __ldg(reinterpret_cast<const uint4*>(p.k_cache + ko) + 2 * t4 + (i & 1));
-                        vx[sb][i] = __ldg(reinterpret_cast<const uint4*>(p.v_cache + vo) + g);
-                    }
+                cp_async_wait_group<kStages - 2>();
+                __syncwarp();   // everyone's copies of this stage are there; the stage before it has been read
+                const int next = slot == 0 ? kStages - 1 : slot - 1;
+                feed_tile(p, before, f, ring + next * 2 * kCodes, info + next, kvh, lane);
+                const uint8_t* codes = ring + slot * 2 * kCodes;
+                const float ka[2] = {info[slot].k[0], info[slot].k[1]};
+                const float vb[2] = {info[slot].v[0], info[slot].v[1]};
+                const uint32_t valid = info[slot].valid;
+                const int tok0 = t * kTile;
                 if (valid == 0xffffffffu && tok0 + kTile - 1 <= lim_min)
-                    tile_step<NB, false>(st, qs, kx, vx, ka, vb, tok0, valid, lane);
+                    tile_step<NB, false>(st, qs, codes, k_at, v_at, ka, vb, tok0, valid, lane);
                 else
-                    tile_step<NB, true>(st, qs, kx, vx, ka, vb, tok0, valid, lane);
+                    tile_step<NB, true>(st, qs, codes, k_at, v_at, ka, vb, tok0, valid, lane);
+                slot = slot + 1 == kStages ? 0 : slot + 1;
             }
             // the piece's rows: normalised O and log2 of the sum
             const bool whole = t_lo == 0 && t_hi == n_tiles;
@@ -483,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp8_block_kernel(const Par
                     }
                 }
         }
+        __syncwarp();   // the ring may be filled for another unit
     }
 }
 
@@ -566,7 +642,8 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockArgs& a, cudaStream_t strea
     p.Hkv = a.Hkv;
     p.G = a.Hq / a.Hkv;
     p.nq = a.q_len;
-    p.block = a.block_tokens;
+    p.page_div = make_divisor(a.page_size);
+    p.block_div = make_divisor(a.block_tokens);
     const int rows = p.G * p.nq, per = rows_per_column(rows);
     p.cols = a.Hkv * ((rows + per - 1) / per);
     p.workers = sms * kWarps / p.cols > 1 ? sms * kWarps / p.cols : 1;
@@ -576,12 +653,12 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockArgs& a, cudaStream_t strea
     p.part_o = static_cast<float*>(a.workspace);
     p.part_l = p.part_o + static_cast<size_t>(2) * p.workers * p.cols * per * kD;
     p.status = a.dev_status;
-    const size_t smem = (static_cast<size_t>(a.B) + 1) * sizeof(int);
-    if (per == 8)
-        decode_fp8_block_kernel<1><<<sms, kThreads, smem, stream>>>(p);
-    else
-        decode_fp8_block_kernel<2><<<sms, kThreads, smem, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const size_t smem = kWarps * kWarpBytes + (static_cast<size_t>(a.B) + 1) * sizeof(int);
+    auto kern = per == 8 ? decode_fp8_block_kernel<1> : decode_fp8_block_kernel<2>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    kern<<<sms, kThreads, smem, stream>>>(p);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     decode_fp8_block_merge_kernel<<<dim3(a.q_len * a.Hq, a.B), kMergeThreads, 0, stream>>>(p, per);
     return cudaGetLastError();

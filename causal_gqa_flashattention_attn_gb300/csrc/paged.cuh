@@ -40,6 +40,24 @@ __device__ __forceinline__ int page_at(const PageList& l, int b, int e, int n, i
     return page;
 }
 
+// n / d for 0 <= n < 2^31 and a divisor fixed on the host: with s the least
+// power 2^s >= d and mul = ceil(2^(31+s) / d) < 2^32, mul d - 2^(31+s) < 2^s, so
+// the product's error stays below 1/d.
+struct Divisor {
+    uint32_t d, mul;
+    int shift;
+    __device__ __forceinline__ int div(int n) const {
+        return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> shift);
+    }
+};
+
+inline Divisor make_divisor(int d) {
+    int s = 0;
+    while ((1LL << s) < d) ++s;
+    const uint64_t one = 1ULL << (31 + s);
+    return Divisor{static_cast<uint32_t>(d), static_cast<uint32_t>((one + d - 1) / d), 31 + s};
+}
+
 // Last b in [0, B) with key(b) <= x, for key(0) <= x and key not decreasing; a
 // whole warp counts together, 32 keys per round with independent loads.
 template <typename Key>
