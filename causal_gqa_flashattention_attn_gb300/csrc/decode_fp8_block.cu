@@ -17,8 +17,9 @@
 // rows; every warp of the grid takes one column and an equal share of the
 // 32-token tiles of all sequences, so a ragged batch is balanced whatever its
 // lengths, which only the device knows.  A share that holds a whole sequence
-// writes its output; the pieces of a sequence that is cut between warps go to
-// the workspace and a second kernel joins them.
+// writes its output; the pieces of a sequence that is cut between shares go to
+// the workspace, and a second kernel, which is launched along with the first
+// and waits for it on the device, joins them.
 #include "paged.cuh"
 #include "ptx.cuh"
 
@@ -33,7 +34,8 @@ constexpr int kMaxSeqs = 4096;  // tile counts before each sequence, in shared m
 constexpr int kStages = 3;      // tiles in flight or in use per warp
 constexpr int kCodes = kTile * kD;                    // 4 KB: a tile's K (or V) codes of one head
 constexpr int kWarpBytes = kStages * 2 * kCodes;
-constexpr int kMergeThreads = 128;
+constexpr int kMergeWarps = 8;
+constexpr int kBatch = 16;      // pieces a merging warp has in flight
 
 struct Params {
     const __nv_bfloat16* q;   // [B, q_len, Hq, D]
@@ -117,14 +119,21 @@ __device__ __forceinline__ void count_tiles(const Params& p, int* before, int* w
     __syncthreads();
 }
 
-// Shares of `total` tiles in use, the first tile of share w, and the share of tile x.
-__device__ __forceinline__ int shares_of(int workers, int total) { return min(workers, total); }
-__device__ __forceinline__ int share_start(int total, int n, int w) {
-    return static_cast<int>(static_cast<long long>(total) * w / n);
-}
-__device__ __forceinline__ int share_of(int total, int n, int x) {
-    return static_cast<int>((static_cast<long long>(x + 1) * n - 1) / total);
-}
+// The cut of `total` tiles into shares: the first `extra` shares take each + 1
+// tiles, the others `each`.
+struct Cut {
+    int shares, each, extra;
+    __device__ __forceinline__ Cut(int workers, int total) {
+        shares = max(1, min(workers, total));
+        each = total / shares;
+        extra = total - each * shares;
+    }
+    __device__ __forceinline__ int start(int w) const { return w * each + min(w, extra); }
+    __device__ __forceinline__ int share_of(int x) const {
+        const int big = extra * (each + 1);
+        return x < big ? x / (each + 1) : extra + (x - big) / each;
+    }
+};
 
 // Per-warp state of the online softmax and the O^T accumulators of NB x 8 rows
 // (row 2t4 + j of block n): m for the sums, M for the values.
@@ -442,8 +451,10 @@ __device__ __forceinline__ void feed_tile(const Params& p, const int* before, Fe
 }
 
 template <int NB>
-__global__ void __launch_bounds__(kThreads, 1) decode_fp8_block_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 1) decode_fp8_block_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(128) uint8_t smem[];
+    // the merge kernel's CTAs may come in as soon as there is room: they wait for this grid's end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ TileInfo infos[kWarps][kStages];
     __shared__ int warp_sum[kWarps];
     int* before = reinterpret_cast<int*>(smem + kWarps * kWarpBytes);
@@ -454,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp8_block_kernel(const Par
     count_tiles(p, before, warp_sum, blockIdx.x == 0);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int total = before[p.B];
-    const int shares = shares_of(p.workers, total);
+    const Cut cut(p.workers, total);
     const int n_rows = p.G * p.nq;
     const int n_warps = gridDim.x * kWarps;
     uint8_t* ring = smem + warp * kWarpBytes;
@@ -483,9 +494,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp8_block_kernel(const Par
                 if (p.lse != nullptr && lane == 0) p.lse[row] = -INFINITY;
             }
         }
-        if (w >= shares) continue;
-        int x = share_start(total, shares, w);
-        const int x_end = share_start(total, shares, w + 1);
+        if (w >= cut.shares) continue;
+        int x = cut.start(w);
+        const int x_end = cut.start(w + 1);
+        if (x >= x_end) continue;
         int b = warp_rank(p.B, x, lane, [&](int i) { return before[i]; });
         Feed f;
         f.x = x;
@@ -493,17 +505,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp8_block_kernel(const Par
         f.b = b;
         f.len = length_of(p, b, false);
         feed_look(p, before, f, lane);
+        // the queries' loads go ahead of the codes'
+        Queries<NB> qs;
+        load_queries<NB>(p, b, kvh, row0, n_rows, f.len, lane, qs);
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) feed_tile(p, before, f, ring + i * 2 * kCodes, info + i, kvh, lane);
         int slot = 0;
-        while (x < x_end) {
+        for (bool first = true; x < x_end; first = false) {
             while (before[b + 1] <= x) ++b;
             const int t_lo = x - before[b], n_tiles = before[b + 1] - before[b];
             const int t_hi = min(n_tiles, t_lo + (x_end - x));
             x += t_hi - t_lo;
             const int len = length_of(p, b, false);
-            Queries<NB> qs;
-            load_queries<NB>(p, b, kvh, row0, n_rows, len, lane, qs);
+            if (!first) load_queries<NB>(p, b, kvh, row0, n_rows, len, lane, qs);
             State<NB> st;
             reset<NB>(st);
             const int lim_min = len - p.nq + row0 / p.G;   // the first row's limit, the smallest
@@ -562,15 +576,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp8_block_kernel(const Par
     }
 }
 
-// Joins the pieces of the sequences that were cut: a CTA per (sequence, query
-// row), a thread per element.  O = sum_s 2^(L_s - L) O_s / sum_s 2^(L_s - L).
-__global__ void __launch_bounds__(kMergeThreads) decode_fp8_block_merge_kernel(const Params p, int rows_per_col) {
-    __shared__ int part_sum[2][kMergeThreads / 32];
-    if (too_many_tiles(p)) return;
-    const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Joins the pieces of the sequences that were cut: `per_row` warps (1, 4 or 8)
+// per output row, four elements a lane.  O = sum_s 2^(L_s - L) O_s / sum_s
+// 2^(L_s - L); each warp takes every per_row-th piece, kBatch at a time.
+__global__ void __launch_bounds__(32 * kMergeWarps) decode_fp8_block_merge_kernel(const __grid_constant__ Params p,
+                                                                                  int rows_per_col, int per_row) {
+    __shared__ int sums[2][kMergeWarps];
+    __shared__ float4 warp_acc[kMergeWarps][32];
+    __shared__ float warp_top[kMergeWarps], warp_sum[kMergeWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rows = p.nq * p.Hq;
+    const int rows_per_cta = kMergeWarps / per_row;
+    const int cta_per_seq = (rows + rows_per_cta - 1) / rows_per_cta;
+    const int b = blockIdx.x / cta_per_seq, row = blockIdx.x % cta_per_seq * rows_per_cta + warp / per_row;
     // tiles before the sequence, and of all of them
     int pre = 0, all = 0;
-    for (int i = threadIdx.x; i < p.B; i += kMergeThreads) {
+    const bool bad = too_many_tiles(p);
+    for (int i = threadIdx.x; i < p.B && !bad; i += 32 * kMergeWarps) {
         const int t = tiles_of(length_of(p, i, false));
         all += t;
         if (i < b) pre += t;
@@ -580,35 +602,79 @@ __global__ void __launch_bounds__(kMergeThreads) decode_fp8_block_merge_kernel(c
         pre += __shfl_xor_sync(0xffffffffu, pre, off);
         all += __shfl_xor_sync(0xffffffffu, all, off);
     }
-    if (lane == 0) part_sum[0][warp] = pre, part_sum[1][warp] = all;
+    if (lane == 0) sums[0][warp] = pre, sums[1][warp] = all;
     __syncthreads();
     pre = all = 0;
 #pragma unroll
-    for (int i = 0; i < kMergeThreads / 32; ++i) pre += part_sum[0][i], all += part_sum[1][i];
+    for (int i = 0; i < kMergeWarps; ++i) pre += sums[0][i], all += sums[1][i];
     const int n_tiles = tiles_of(length_of(p, b, false));
-    if (n_tiles == 0) return;
-    const int shares = shares_of(p.workers, all);
-    const int w0 = share_of(all, shares, pre), w1 = share_of(all, shares, pre + n_tiles - 1);
+    const Cut cut(p.workers, all);
+    // the first kernel is done and its writes are here; CTAs without work wait
+    // too, so that this grid never ends before that one
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (n_tiles == 0 || bad) return;
+    const int w0 = cut.share_of(pre), w1 = cut.share_of(pre + n_tiles - 1);
     if (w0 == w1) return;   // one share held it all
-    const int row = blockIdx.x;                       // of [q_len, Hq]
-    const int kvh = (row % p.Hq) / p.G, r = (row / p.Hq) * p.G + row % p.G;
-    const int col = (r / rows_per_col) * p.Hkv + kvh;
-    float top = -INFINITY;
+    const int r = (row / p.Hq) * p.G + row % p.G;
+    const int col = (r / rows_per_col) * p.Hkv + row % p.Hq / p.G;
     auto at = [&](int w) -> size_t {   // the piece that starts the sequence is its share's second slot
         return (static_cast<size_t>(2 * w + (w == w0 ? 1 : 0)) * p.cols + col) * rows_per_col + r % rows_per_col;
     };
-    for (int w = w0; w <= w1; ++w) top = fmaxf(top, p.part_l[at(w)]);
-    float sum = 0.f, acc = 0.f;
-    for (int w = w0; w <= w1; ++w) {
-        const float l = p.part_l[at(w)];
-        if (l == -INFINITY) continue;
-        const float f = ex2(l - top);
-        sum += f;
-        acc = fmaf(f, p.part_o[at(w) * kD + threadIdx.x], acc);
+    float top = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = w0 + warp % per_row; row < rows && w <= w1; w += per_row * kBatch) {
+        const int m = min(kBatch, (w1 - w) / per_row + 1);
+        const float l = lane < m ? __ldcg(p.part_l + at(w + lane * per_row)) : -INFINITY;
+        float4 v[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (i < m) v[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at(w + i * per_row) * kD) + lane);
+        float high = l;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, off));
+        high = fmaxf(high, top);
+        const float back = top == -INFINITY ? 0.f : ex2(top - high);
+        top = high;
+        sum *= back;
+        acc.x *= back, acc.y *= back, acc.z *= back, acc.w *= back;
+        const float f = l == -INFINITY ? 0.f : ex2(l - top);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const float fi = __shfl_sync(0xffffffffu, f, i);
+            if (i < m && fi != 0.f) {
+                sum += fi;
+                acc.x = fmaf(fi, v[i].x, acc.x);
+                acc.y = fmaf(fi, v[i].y, acc.y);
+                acc.z = fmaf(fi, v[i].z, acc.z);
+                acc.w = fmaf(fi, v[i].w, acc.w);
+            }
+        }
     }
-    const size_t out = static_cast<size_t>(b) * p.nq * p.Hq + row;
-    p.o[out * kD + threadIdx.x] = __float2bfloat16(sum == 0.f ? 0.f : acc / sum);
-    if (p.lse != nullptr && threadIdx.x == 0) p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    if (per_row > 1) {   // the row's warps, in order
+        warp_acc[warp][lane] = acc;
+        if (lane == 0) warp_top[warp] = top, warp_sum[warp] = sum;
+        __syncthreads();
+        if (warp % per_row != 0) return;
+        for (int i = 0; i < per_row; ++i) top = fmaxf(top, warp_top[warp + i]);
+        sum = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < per_row; ++i) {
+            if (warp_sum[warp + i] == 0.f) continue;
+            const float f = ex2(warp_top[warp + i] - top);
+            const float4 a = warp_acc[warp + i][lane];
+            sum = fmaf(f, warp_sum[warp + i], sum);
+            acc.x = fmaf(f, a.x, acc.x);
+            acc.y = fmaf(f, a.y, acc.y);
+            acc.z = fmaf(f, a.z, acc.z);
+            acc.w = fmaf(f, a.w, acc.w);
+        }
+    }
+    if (row >= rows) return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const size_t out = static_cast<size_t>(b) * rows + row;
+    reinterpret_cast<uint2*>(p.o + out * kD)[lane] =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (p.lse != nullptr && lane == 0) p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 // Rows of a column: 8, or 16 where a KV head has more of them.
@@ -659,9 +725,20 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockArgs& a, cudaStream_t strea
     if (e != cudaSuccess) return e;
     kern<<<sms, kThreads, smem, stream>>>(p);
     e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    decode_fp8_block_merge_kernel<<<dim3(a.q_len * a.Hq, a.B), kMergeThreads, 0, stream>>>(p, per);
-    return cudaGetLastError();
+    if (e != cudaSuccess || p.workers == 1) return e;   // one share per column: no sequence is cut
+    // a sequence has about workers / B pieces, one that is longer than the others more
+    const int per_row = p.workers > 16LL * a.B ? 8 : (p.workers > 4LL * a.B ? 4 : 1);
+    const int rows_per_cta = kMergeWarps / per_row;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.B) * ((a.q_len * a.Hq + rows_per_cta - 1) / rows_per_cta));
+    cfg.blockDim = dim3(32 * kMergeWarps);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, decode_fp8_block_merge_kernel, p, per, per_row);
 }
 
 }  // namespace gb300
