@@ -2,7 +2,9 @@
 
 This module only marshals arguments: it takes torch tensors that already live
 on the GPU, passes their device pointers and sizes to the C ABI declared in
-``include/attn.h`` and raises on a non-OK status.  Every step of the
+``include/attn.h`` (through ctypes, or for the paged cache's writers and the
+block-scaled cache's readers through the compiled ``_binding``) and raises on a
+non-OK status.  Every step of the
 computation runs in the library's CUDA kernels; there is no fallback of any
 kind, and importing a function of this module fails loudly when the library
 has not been built.
@@ -546,103 +548,30 @@ def attn_decode_paged_splitk_static(q, k_cache, v_cache, block_table, seq_lens, 
     return o, lse
 
 
-def _expect(name, t, device, shape, *dtypes):
-    """Checks a dense CUDA tensor (None passes): its device, its shape (-1: any size) and its type."""
-    if t is None:
-        return None
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on {device}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if t.dim() != len(shape) or any(w not in (-1, n) for w, n in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have the shape {tuple(shape)} (-1: any), not {tuple(t.shape)}")
-    return t.data_ptr()
+_native_module = None
 
 
-def _raw_stream(stream, device):
-    """The handle of ``stream``, or of the current stream of ``device``, which must be the current device."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError("tensors must be on the current CUDA device")
+def _native():
+    """The compiled binding (csrc/binding.cpp), which checks the tensors of the
+    paged cache's entries (``ValueError``), allocates the outputs that are not
+    given and calls the C ABI on the current stream."""
+    global _native_module
+    if _native_module is None:
+        lib()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("_binding.so is missing or does not load: build it with __graft_entry__.build()") from e
+        _native_module = _binding
+    return _native_module
+
+
+def _run(stream, call, *args):
+    """``call(*args)`` on ``stream``: what it allocates belongs to that stream too."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    if stream.device != device:
-        raise ValueError("stream must belong to the tensors' device")
-    return stream.cuda_stream
-
-
-def _allocate(stream, make):
-    """What ``make`` allocates, on ``stream`` if one is given: the memory belongs to the stream that uses it."""
-    if stream is None:
-        return make()
+        return call(*args)
     with torch.cuda.stream(stream):
-        return make()
-
-
-def _pages(block_table, kv_indptr, bsz, device):
-    """(pages, indptr, entries per row) of a block table [B, max_pages], or of a CSR list."""
-    if kv_indptr is None:
-        return _expect("block_table", block_table, device, (bsz, -1), torch.int32), None, block_table.shape[1]
-    return (_expect("block_table (with kv_indptr)", block_table, device, (-1,), torch.int32),
-            _expect("kv_indptr", kv_indptr, device, (bsz + 1,), torch.int32), 0)
-
-
-_CODES = (torch.uint8, torch.float8_e4m3fn)
-
-
-def _block_cache(k_cache, v_cache, k_scale, v_scale, device):
-    """Pointers and (num_pages, page_size, Hkv, D, block_tokens) of a block-scaled e4m3 cache."""
-    kp = _expect("k_cache", k_cache, device, (-1, -1, -1, -1), *_CODES)
-    vp = _expect("v_cache", v_cache, device, k_cache.shape, *_CODES)
-    num_pages, page_size, hkv, d = k_cache.shape
-    sp = _expect("k_scale", k_scale, device, (num_pages, -1, hkv), torch.float32)
-    blocks = k_scale.shape[1]
-    if blocks == 0 or page_size % blocks:
-        raise ValueError(f"k_scale has {blocks} blocks for pages of {page_size} tokens")
-    wp = _expect("v_scale", v_scale, device, (num_pages, blocks, hkv), torch.float32)
-    return (kp, vp, sp, wp), (num_pages, page_size, hkv, d, page_size // blocks)
-
-
-def _token_rows(name, x, device):
-    """(pointer, elements from token to token) of ``x [T, H, D]`` bf16 whose tokens are dense rows."""
-    if x.device != device or x.dtype != torch.bfloat16 or x.dim() != 3:
-        raise ValueError(f"{name} must be a bfloat16 tensor [tokens, heads, D] on {device}")
-    t, h, d = x.shape
-    s = x.stride()
-    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
-        raise ValueError(f"{name}: the heads of a token must be dense")
-    return x.data_ptr(), s[0] if t > 1 else h * d
-
-
-def _append_args(q, k, v, block_table, seq_lens, cos_sin, qo_indptr, kv_indptr, positions, interleaved, q_out, stream):
-    """The arguments that both appends share, in the order of the C ABI, and the output."""
-    device = k.device
-    raw = _raw_stream(stream, device)
-    kp, ks = _token_rows("k", k, device)
-    vp, vs = _token_rows("v", v, device)
-    if v.shape != k.shape:
-        raise ValueError("k and v must have the same shape")
-    total, hkv, d = k.shape
-    qp = qop = None
-    qs, hq = 0, hkv
-    if q is not None:
-        qp, qs = _token_rows("q", q, device)
-        hq = q.shape[1]
-        if q.shape[0] != total or q.shape[2] != d:
-            raise ValueError("q, k and v must have the same tokens and head dimension")
-        if q_out is None:
-            q_out = _allocate(stream, lambda: torch.empty(total, hq, d, dtype=torch.bfloat16, device=device))
-        qop = _expect("q_out", q_out, device, (total, hq, d), torch.bfloat16)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    bsz = seq_lens.numel()
-    lp = _expect("seq_lens", seq_lens, device, (bsz,), torch.int32)
-    table, indptr, width = _pages(block_table, kv_indptr, bsz, device)
-    cp = _expect("cos_sin", cos_sin, device, (-1, -1), torch.float32)
-    max_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
-    args = (qp, kp, vp, qs, ks, vs, cp, max_pos, rot, int(interleaved),
-            _expect("positions", positions, device, (total,), torch.int32),
-            _expect("qo_indptr", qo_indptr, device, (bsz + 1,), torch.int32), lp, table, indptr, width, qop)
-    return args, (bsz, total, hq, hkv, d), q_out, raw
+        return call(*args)
 
 
 def attn_kv_append(q, k, v, k_cache, v_cache, block_table, seq_lens, cos_sin=None, qo_indptr=None, kv_indptr=None,
@@ -662,14 +591,8 @@ def attn_kv_append(q, k, v, k_cache, v_cache, block_table, seq_lens, cos_sin=Non
     R/2)`` or, with ``interleaved``, ``(2i, 2i + 1)``.  ``positions [T]``
     replaces the tokens' indices.  Returns the rotated ``q [T, Hq, D]``.
     """
-    args, (bsz, total, hq, hkv, d), q_out, raw = _append_args(q, k, v, block_table, seq_lens, cos_sin, qo_indptr,
-                                                              kv_indptr, positions, interleaved, q_out, stream)
-    kcp = _expect("k_cache", k_cache, k.device, (-1, -1, hkv, d), torch.bfloat16)
-    vcp = _expect("v_cache", v_cache, k.device, k_cache.shape, torch.bfloat16)
-    sp = _expect("dev_status", dev_status, k.device, (1,), torch.int32)
-    st = lib().attn_kv_append(*args, kcp, vcp, bsz, total, hq, hkv, d, k_cache.shape[0], k_cache.shape[1], sp, raw)
-    _check("attn_kv_append", st)
-    return q_out
+    return _run(stream, _native().kv_append, q, k, v, k_cache, v_cache, None, None, block_table, seq_lens, cos_sin, qo_indptr,
+                kv_indptr, positions, interleaved, q_out, dev_status)
 
 
 def attn_kv_append_fp8_block(q, k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cos_sin=None,
@@ -679,15 +602,10 @@ def attn_kv_append_fp8_block(q, k, v, k_cache, v_cache, k_scale, v_scale, block_
     ``[num_pages, page_size, Hkv, D]``) with float32 scales ``[num_pages,
     page_size / block_tokens, Hkv]``: value = code * scale.  Scales are powers
     of two; a block that takes more tokens keeps its scale or grows it."""
-    args, (bsz, total, hq, hkv, d), q_out, raw = _append_args(q, k, v, block_table, seq_lens, cos_sin, qo_indptr,
-                                                              kv_indptr, positions, interleaved, q_out, stream)
-    ptrs, (num_pages, page_size, cache_hkv, cache_d, block) = _block_cache(k_cache, v_cache, k_scale, v_scale, k.device)
-    if (cache_hkv, cache_d) != (hkv, d):
-        raise ValueError("the cache's heads must be those of k and v")
-    sp = _expect("dev_status", dev_status, k.device, (1,), torch.int32)
-    st = lib().attn_kv_append_fp8_block(*args, *ptrs, bsz, total, hq, hkv, d, num_pages, page_size, block, sp, raw)
-    _check("attn_kv_append_fp8_block", st)
-    return q_out
+    if k_scale is None or v_scale is None:
+        raise ValueError("k_scale and v_scale must be tensors")
+    return _run(stream, _native().kv_append, q, k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cos_sin,
+                qo_indptr, kv_indptr, positions, interleaved, q_out, dev_status)
 
 
 def attn_decode_fp8_block_workspace_bytes(B, q_len, Hq, Hkv, D=128):
@@ -705,31 +623,8 @@ def attn_decode_paged_fp8_block(q, k_cache, v_cache, k_scale, v_scale, block_tab
     bytes, zeroed once and reusable (None allocates one).  Returns ``(o, lse,
     workspace)``, ``lse [B, Hq]`` or ``[B, q_len, Hq]``.
     """
-    device = q.device
-    raw = _raw_stream(stream, device)
-    single = q.dim() == 3
-    _expect("q", q, device, (-1,) * (3 if single else 4), torch.bfloat16)
-    bsz, nq, hq, d = (q.shape[0], 1, q.shape[1], q.shape[2]) if single else q.shape
-    ptrs, (num_pages, page_size, hkv, cache_d, block) = _block_cache(k_cache, v_cache, k_scale, v_scale, device)
-    if cache_d != d:
-        raise ValueError("q and the cache must have the same head dimension")
-    table, indptr, width = _pages(block_table, kv_indptr, bsz, device)
-    lp = _expect("seq_lens", seq_lens, device, (bsz,), torch.int32)
-    if workspace is None:
-        need = attn_decode_fp8_block_workspace_bytes(bsz, nq, hq, hkv, d)
-        workspace = _allocate(stream, lambda: torch.zeros(max(need, 16), dtype=torch.uint8, device=device))
-    if o is None:
-        o = _allocate(stream, lambda: torch.empty_like(q))
-    if lse is None:
-        lse = _allocate(stream, lambda: torch.empty(q.shape[:-1], dtype=torch.float32, device=device))
-    st = lib().attn_decode_paged_fp8_block(
-        q.data_ptr(), *ptrs, table, indptr, width, lp, bsz, nq, hq, hkv, d, num_pages, page_size, block,
-        1.0 / math.sqrt(d) if scale is None else float(scale), _expect("workspace", workspace, device, (-1,), torch.uint8),
-        workspace.numel(), _expect("o", o, device, q.shape, torch.bfloat16),
-        _expect("lse", lse, device, q.shape[:-1], torch.float32),
-        _expect("dev_status", dev_status, device, (1,), torch.int32), raw)
-    _check("attn_decode_paged_fp8_block", st)
-    return o, lse, workspace
+    return _run(stream, _native().decode_fp8_block, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, kv_indptr,
+                scale, workspace, o, lse, dev_status)
 
 
 def attn_prefill_fp8_block_workspace_bytes(B, max_kv_rows, Hkv, D=128):
@@ -748,34 +643,8 @@ def attn_prefill_paged_fp8_block(q, k_cache, v_cache, k_scale, v_scale, qo_indpt
     ``workspace``: a uint8 tensor of attn_prefill_fp8_block_workspace_bytes()
     bytes.  Returns ``(o [total_q, Hq, D], lse [total_q, Hq], workspace)``.
     """
-    device = q.device
-    raw = _raw_stream(stream, device)
-    _expect("q", q, device, (-1, -1, -1), torch.bfloat16)
-    total, hq, d = q.shape
-    ptrs, (num_pages, page_size, hkv, cache_d, block) = _block_cache(k_cache, v_cache, k_scale, v_scale, device)
-    if cache_d != d:
-        raise ValueError("q and the cache must have the same head dimension")
-    bsz = seq_lens.numel()
-    lp = _expect("seq_lens", seq_lens, device, (bsz,), torch.int32)
-    qip = _expect("qo_indptr", qo_indptr, device, (bsz + 1,), torch.int32)
-    table, indptr, width = _pages(block_table, kv_indptr, bsz, device)
-    if max_kv_rows is None:
-        max_kv_rows = num_pages * page_size
-    if workspace is None:
-        need = attn_prefill_fp8_block_workspace_bytes(bsz, max_kv_rows, hkv, d)
-        workspace = _allocate(stream, lambda: torch.empty(max(need, 16), dtype=torch.uint8, device=device))
-    if o is None:
-        o = _allocate(stream, lambda: torch.empty_like(q))
-    if lse is None:
-        lse = _allocate(stream, lambda: torch.empty(total, hq, dtype=torch.float32, device=device))
-    st = lib().attn_prefill_paged_fp8_block(
-        q.data_ptr(), *ptrs, qip, table, indptr, width, lp, bsz, total, hq, hkv, d, num_pages, page_size, block,
-        int(max_kv_rows), 1.0 / math.sqrt(d) if scale is None else float(scale),
-        _expect("workspace", workspace, device, (-1,), torch.uint8), workspace.numel(),
-        _expect("o", o, device, q.shape, torch.bfloat16), _expect("lse", lse, device, (total, hq), torch.float32),
-        _expect("dev_status", dev_status, device, (1,), torch.int32), raw)
-    _check("attn_prefill_paged_fp8_block", st)
-    return o, lse, workspace
+    return _run(stream, _native().prefill_fp8_block, q, k_cache, v_cache, k_scale, v_scale, qo_indptr, block_table, seq_lens,
+                kv_indptr, max_kv_rows, scale, workspace, o, lse, dev_status)
 
 
 def decode_partials_view(workspace, B, Hq, max_kv_len, split_tokens, D):

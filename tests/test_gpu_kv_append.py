@@ -321,3 +321,63 @@ def test_append_flags_bad_pages_and_positions():
                 assert there == [int(lists.rows[1][0]) * 16 + 3], (fp8, what)
             assert bool(torch.all(q_out[0] == 9.0)) == (what == "position")
             assert not bool(torch.all(q_out[1] == 9.0))
+
+
+def test_binding_refuses_wrong_tensors():
+    """Types, shapes, strides and devices that a call does not take raise ValueError, statuses AttnError; nothing is written."""
+    dev = gpu_or_skip()
+    import causal_gqa_flashattention_attn_gb300 as attn
+    i32 = dict(dtype=torch.int32, device=dev)
+    q, k = (torch.ones(2, h, D, dtype=torch.bfloat16, device=dev) for h in (4, 2))
+    c8 = torch.zeros(3, 32, 2, D, dtype=torch.uint8, device=dev)
+    cb = torch.zeros(3, 32, 2, D, dtype=torch.bfloat16, device=dev)
+    sc = torch.ones(3, 2, 2, device=dev)
+    table, lens, ptr = torch.zeros(2, 1, **i32), torch.ones(2, **i32), torch.tensor([0, 1, 2], **i32)
+
+    def append(match, error=ValueError, fp8=True, **kw):
+        a = dict(q=q, k=k, v=k, k_cache=c8 if fp8 else cb, v_cache=c8 if fp8 else cb, block_table=table, seq_lens=lens)
+        if fp8:
+            a.update(k_scale=sc, v_scale=sc)
+        a.update(kw)
+        with pytest.raises(error, match=match):
+            (attn.attn_kv_append_fp8_block if fp8 else attn.attn_kv_append)(**a)
+
+    for fp8 in (False, True):
+        append("seq_lens", fp8=fp8, seq_lens=lens.long())
+        append("block_table", fp8=fp8, seq_lens=torch.ones(3, **i32))
+        append("block_table", fp8=fp8, block_table=table.cpu())
+        append("bfloat16", fp8=fp8, k=k.float())
+        append("bfloat16", fp8=fp8, q=q.half())
+        append("dense", fp8=fp8, q=torch.zeros(2, D, 4, dtype=torch.bfloat16, device=dev).transpose(1, 2))
+        append("same shape", fp8=fp8, v=q)
+        append("same tokens", fp8=fp8, q=q[:1])
+        append("q_out", fp8=fp8, q_out=q[:, :2].contiguous())
+        append("q_out without q", fp8=fp8, q=None, q_out=q)
+        append("qo_indptr", fp8=fp8, qo_indptr=lens)
+        append("kv_indptr", fp8=fp8, block_table=lens, kv_indptr=lens)
+        append("positions", fp8=fp8, positions=ptr)
+        append("cos_sin", fp8=fp8, cos_sin=torch.zeros(9, 16, dtype=torch.float64, device=dev))
+        append("unsupported", attn.AttnError, fp8=fp8, cos_sin=torch.zeros(9, 18, device=dev))
+        append("invalid", attn.AttnError, fp8=fp8, cos_sin=torch.zeros(9, 144, device=dev))
+        append("invalid", attn.AttnError, fp8=fp8, k=k[:1].expand(2, 2, D))
+        append("invalid", attn.AttnError, fp8=fp8, k=torch.zeros(2 * 2 * D + 4, dtype=torch.bfloat16, device=dev)[4:].view(2, 2, D))
+        append("dev_status", fp8=fp8, dev_status=lens)
+    append("k_cache", k_cache=cb)
+    append("v_cache", v_cache=c8[:2])
+    append("contiguous", k_cache=c8.transpose(1, 2).contiguous().transpose(1, 2))
+    append("blocks", k_scale=torch.ones(3, 5, 2, device=dev))
+    append("v_scale", v_scale=torch.ones(3, 1, 2, device=dev))
+    append("heads", k=q, v=q)
+    append("k_cache", fp8=False, k_cache=c8)
+    append("unsupported", attn.AttnError, k_scale=torch.ones(3, 4, 2, device=dev), v_scale=torch.ones(3, 4, 2, device=dev))
+    for f, extra in ((attn.attn_decode_paged_fp8_block, ()), (attn.attn_prefill_paged_fp8_block, (ptr,))):
+        with pytest.raises(ValueError, match="q must"):
+            f(q[0], c8, c8, sc, sc, *extra, table, lens)
+        with pytest.raises(ValueError, match="head dimension"):
+            f(q[..., :64].contiguous(), c8, c8, sc, sc, *extra, table, lens)
+        with pytest.raises(attn.AttnError, match="workspace"):
+            f(q, c8, c8, sc, sc, *extra, table, lens, workspace=torch.zeros(16, dtype=torch.uint8, device=dev))
+        with pytest.raises(ValueError, match="lse"):
+            f(q, c8, c8, sc, sc, *extra, table, lens, lse=torch.zeros(2, 4, dtype=torch.float64, device=dev))
+    torch.cuda.synchronize()
+    assert not torch.any(c8) and not torch.any(cb) and bool(torch.all(sc == 1)) and bool(torch.all(q == 1))
