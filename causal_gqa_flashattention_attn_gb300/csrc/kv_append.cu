@@ -15,10 +15,11 @@
 // divided by the growth.  Powers of two make every product and quotient with
 // a scale exact, so code * scale is off from x by one e4m3 rounding alone, old
 // codes change only where they fall into e4m3's subnormals, and code * scale
-// is a bf16 number.  A key's code is that of its 64-bit rotation: fp32 decides
+// is a bf16 number.  A key's code is that of its exact rotation: fp32 decides
 // unless the value lies within a few units of a border, where it is computed
-// again in 64 bits (about one value in 10^4).
+// again in twice the precision.
 #include "paged.cuh"
+#include "ptx.cuh"
 
 namespace gb300 {
 namespace {
@@ -26,7 +27,6 @@ namespace {
 constexpr int kD = 128;
 constexpr int kThreads = 256;   // of a CTA that takes tokens
 constexpr int kBatch = 3;       // rows that a lane has in flight
-constexpr int kHeld = 2;        // rows of a block that a lane holds in registers
 
 struct Params {
     const __nv_bfloat16* q;   // NULL: no queries
@@ -44,18 +44,53 @@ struct Params {
     float* k_scale;   // NULL: bf16 cache
     float* v_scale;
     int max_pos, rot, B, total_q, Hq, Hkv, block;
-    int n_units, slices;   // block kernel: units of tokens, CTAs per unit
+    Divisor page_div, block_div;
+    int n_units;   // ragged batches into 8-bit blocks: blocks of tokens, and spare ones
     int32_t* status;
 };
 
-// Sixteen elements of a row as eight pairs.
+// Two fp32 numbers that one instruction works on.
+struct Two {
+    float x, y;
+};
+
+__device__ __forceinline__ uint64_t bits_of(Two v) {
+    return static_cast<uint64_t>(__float_as_uint(v.x)) | (static_cast<uint64_t>(__float_as_uint(v.y)) << 32);
+}
+__device__ __forceinline__ Two two_of(uint64_t b) {
+    return Two{__uint_as_float(static_cast<uint32_t>(b)), __uint_as_float(static_cast<uint32_t>(b >> 32))};
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits_of(a)), "l"(bits_of(b)));
+    return two_of(d);
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits_of(a)), "l"(bits_of(b)));
+    return two_of(d);
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits_of(a)), "l"(bits_of(b)), "l"(bits_of(c)));
+    return two_of(d);
+}
+__device__ __forceinline__ Two minus(Two a) { return Two{-a.x, -a.y}; }
+// max(m, |v.x|, |v.y|); NaN does not count.
+__device__ __forceinline__ float max_size(float m, Two v) {
+    float d;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(v.x), "f"(v.y));
+    return d;
+}
+
+// Sixteen elements of a row as eight pairs (a, b), two by two.
 struct Pairs {
-    float a[8], b[8];
+    Two a[4], b[4];
 };
 
 // Cosines and sines of a lane's eight pairs.
 struct Angles {
-    float c[8], s[8];
+    Two c[4], s[4];
 };
 
 __device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
@@ -78,13 +113,13 @@ template <bool kInter>
 __device__ __forceinline__ void unpack(uint4 x, uint4 y, Pairs& z) {
     const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
         if constexpr (kInter) {
-            z.a[i] = lo_bf16(u[i]);
-            z.b[i] = hi_bf16(u[i]);
+            z.a[i] = Two{lo_bf16(u[2 * i]), lo_bf16(u[2 * i + 1])};
+            z.b[i] = Two{hi_bf16(u[2 * i]), hi_bf16(u[2 * i + 1])};
         } else {
-            z.a[i] = (i & 1) ? hi_bf16(u[i >> 1]) : lo_bf16(u[i >> 1]);
-            z.b[i] = (i & 1) ? hi_bf16(u[4 + (i >> 1)]) : lo_bf16(u[4 + (i >> 1)]);
+            z.a[i] = Two{lo_bf16(u[i]), hi_bf16(u[i])};
+            z.b[i] = Two{lo_bf16(u[4 + i]), hi_bf16(u[4 + i])};
         }
     }
 }
@@ -94,32 +129,44 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <bool kInter>
-__device__ __forceinline__ void pack(const Pairs& z, uint4& x, uint4& y) {
-    if constexpr (kInter) {
-        x = make_uint4(pack2(z.a[0], z.b[0]), pack2(z.a[1], z.b[1]), pack2(z.a[2], z.b[2]), pack2(z.a[3], z.b[3]));
-        y = make_uint4(pack2(z.a[4], z.b[4]), pack2(z.a[5], z.b[5]), pack2(z.a[6], z.b[6]), pack2(z.a[7], z.b[7]));
-    } else {
-        x = make_uint4(pack2(z.a[0], z.a[1]), pack2(z.a[2], z.a[3]), pack2(z.a[4], z.a[5]), pack2(z.a[6], z.a[7]));
-        y = make_uint4(pack2(z.b[0], z.b[1]), pack2(z.b[2], z.b[3]), pack2(z.b[4], z.b[5]), pack2(z.b[6], z.b[7]));
+// Word i of the two chunks from its two elements, by `join`.
+template <bool kInter, typename Join>
+__device__ __forceinline__ void pack(const Pairs& z, uint4& x, uint4& y, Join join) {
+    uint32_t u[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (kInter) {
+            u[2 * i] = join(z.a[i].x, z.b[i].x);
+            u[2 * i + 1] = join(z.a[i].y, z.b[i].y);
+        } else {
+            u[i] = join(z.a[i].x, z.a[i].y);
+            u[4 + i] = join(z.b[i].x, z.b[i].y);
+        }
     }
+    x = make_uint4(u[0], u[1], u[2], u[3]);
+    y = make_uint4(u[4], u[5], u[6], u[7]);
 }
 
 // Table row `pos`, pairs 8l .. 8l + 7.
 __device__ __forceinline__ void load_angles(const Params& p, int pos, int l, Angles& t) {
     const float4* row = reinterpret_cast<const float4*>(p.cos_sin + static_cast<size_t>(pos) * p.rot + 8 * l);
     const float4* srow = row + (p.rot >> 3);
-    const float4 c0 = __ldg(row), c1 = __ldg(row + 1), s0 = __ldg(srow), s1 = __ldg(srow + 1);
-    t.c[0] = c0.x, t.c[1] = c0.y, t.c[2] = c0.z, t.c[3] = c0.w, t.c[4] = c1.x, t.c[5] = c1.y, t.c[6] = c1.z, t.c[7] = c1.w;
-    t.s[0] = s0.x, t.s[1] = s0.y, t.s[2] = s0.z, t.s[3] = s0.w, t.s[4] = s1.x, t.s[5] = s1.y, t.s[6] = s1.z, t.s[7] = s1.w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 c = __ldg(row + i), s = __ldg(srow + i);
+        t.c[2 * i] = Two{c.x, c.y};
+        t.c[2 * i + 1] = Two{c.z, c.w};
+        t.s[2 * i] = Two{s.x, s.y};
+        t.s[2 * i + 1] = Two{s.z, s.w};
+    }
 }
 
 __device__ __forceinline__ void rotate(Pairs& z, const Angles& t) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float a = z.a[i], b = z.b[i];
-        z.a[i] = fmaf(a, t.c[i], -(b * t.s[i]));
-        z.b[i] = fmaf(a, t.s[i], b * t.c[i]);
+    for (int i = 0; i < 4; ++i) {
+        const Two a = z.a[i], b = z.b[i];
+        z.a[i] = fma(b, minus(t.s[i]), mul(a, t.c[i]));
+        z.b[i] = fma(a, t.s[i], mul(b, t.c[i]));
     }
 }
 
@@ -142,21 +189,23 @@ __device__ __forceinline__ float old_scale_of(float s) {
     if (!(s > 0.f) || s > 3.0e38f) return 0.f;
     const uint32_t u = __float_as_uint(s);
     const int e = static_cast<int>(u >> 23) - 127 + ((u & 0x7FFFFFu) != 0u ? 1 : 0);
-    return pow2(e < -126 ? -126 : (e > 127 ? 127 : e));
+    return pow2(e < -126 ? -126 : (e > 126 ? 126 : e));
 }
 
-// a c - b s within 1.5 units in the last place, also where the products cancel.
-__device__ __forceinline__ float cross(float a, float c, float b, float s) {
-    const float w = b * s;
-    return fmaf(a, c, -w) - fmaf(b, s, -w);
+// 1 / s for s = 0 (0) or a power of two from 2^-126 to 2^126.
+__device__ __forceinline__ float inverse_of(float s) {
+    return s > 0.f ? __uint_as_float(0x7F000000u - __float_as_uint(s)) : 0.f;
 }
 
+// The rotation within 1.5 units in the last place, also where the products
+// cancel: one product rounded, the sum with the other, and the rounding taken
+// back, each sum in one operation.
 __device__ __forceinline__ void rotate_closely(Pairs& z, const Angles& t) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float a = z.a[i], b = z.b[i];
-        z.a[i] = cross(a, t.c[i], b, t.s[i]);
-        z.b[i] = cross(a, t.s[i], -b, t.c[i]);
+    for (int i = 0; i < 4; ++i) {
+        const Two a = z.a[i], b = z.b[i], c = t.c[i], s = t.s[i], ns = minus(s);
+        z.a[i] = add(fma(a, c, mul(b, ns)), fma(b, ns, mul(b, s)));
+        z.b[i] = add(fma(b, c, mul(a, s)), fma(a, s, mul(a, ns)));
     }
 }
 
@@ -164,33 +213,41 @@ __device__ __forceinline__ void rotate_closely(Pairs& z, const Angles& t) {
 __device__ __forceinline__ float size_of(const Pairs& z) {
     float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(fmaxf(top, fabsf(z.a[i])), fabsf(z.b[i]));
+    for (int i = 0; i < 4; ++i) top = max_size(max_size(top, z.a[i]), z.b[i]);
     return top;
 }
 
 // Whether fp32's maximum does not settle a block's scale: it is within a few
-// units of 1.75 * 2^e (and the values are rotated), or infinite.
-__device__ __forceinline__ bool doubtful(float top, bool rotated) {
+// units of 1.75 * 2^e and comes from a rotated row, or infinite.  own: the
+// lane's own maximum, of rotated values or not.
+__device__ __forceinline__ bool doubtful(float top, float own, bool rotated) {
     const int edge = static_cast<int>(__float_as_uint(top) & 0x7FFFFFu) - 0x600000;
-    return (rotated && edge >= -4 && edge <= 4) || !(top < 3.0e38f);
+    const bool lanes = rotated && __float_as_uint(own) + 8u >= __float_as_uint(top);
+    return (lanes && edge >= -4 && edge <= 4) || !(top < 3.0e38f);
 }
 
 // Whether fp32's value v of a rotated element (2 units off at most, scaled by
 // a power of two) may lie on the other side of a border between two e4m3
-// codes: its 20 dropped bits are near one half, or it is among e4m3's
-// subnormals (or 0), where other bits are dropped, or above 448 or NaN.
-__device__ __forceinline__ bool near_border(float v) {
-    const uint32_t u = __float_as_uint(v);
-    return (u & 0xFFFFFu) - 0x7FFFCu <= 8u || (u & 0x7FFFFFFFu) - 0x3C800000u > 0x43E00000u - 0x3C800000u;
+// codes: its 20 dropped bits are near one half (of a code that is normal).
+__device__ __forceinline__ bool near_half(float v) {
+    return __float_as_uint(v) * 4096u + (0x80000000u + 4u * 4096u) <= 8u * 4096u;   // the 20 bits moved to the top
 }
-
-// a c - b s in 64 bits, times a power of two, rounded towards zero to fp32 with
-// the last bit set if anything was lost: the e4m3 rounding of it is that of the
-// 64-bit value.
-__device__ __noinline__ float cross_exact(float a, float c, float b, float s, float inv) {
-    const double x = (static_cast<double>(a) * c - static_cast<double>(b) * s) * static_cast<double>(inv);
-    const float f = __double2float_rz(x);
-    return static_cast<double>(f) == x || !(fabsf(f) < 1e30f) ? f : __uint_as_float(__float_as_uint(f) | 1u);
+// a c - b s in twice fp32's precision (each product and the difference with
+// its error), rounded towards zero to fp32 with the last bit set if anything
+// was lost: the e4m3 rounding of it is that of the exact value.  fp64 would do
+// the same at a sixty-fourth of the rate.
+__device__ __forceinline__ float cross_exact(float a, float c, float b, float s) {
+    const float p = a * c, q = b * s;
+    const float r = p - q, back = r - p;
+    const float err = (p - (r - back)) - (q + back);             // of the difference
+    const float low = (fmaf(a, c, -p) - fmaf(b, s, -q)) + err;   // with the products' own
+    const float h = r + low;
+    const float rest = low - (h - r);
+    if (!(fabsf(h) < 3.0e38f)) return p - q;                     // infinities and NaN as they come
+    if (rest == 0.f) return h;
+    const uint32_t u = __float_as_uint(h);
+    // towards zero: one unit back where the rest points inwards
+    return __uint_as_float((((h < 0.f) != (rest < 0.f)) && h != 0.f ? u - 1u : u) | 1u);
 }
 
 __device__ __forceinline__ float finite_size(float x) {
@@ -204,64 +261,91 @@ struct Source {
     int c0, c1, pos;
 };
 
-// The largest finite size of a row in 64 bits (rounded to fp32 so that its
-// scale is that of the 64-bit value), from memory.
+// The largest finite size of a row's sixteenth, rotated values in twice fp32's
+// precision (past fp32's range: its largest number, which has the same scale).
 template <bool kInter>
 __device__ __noinline__ float size_again(const Params& p, const Source r, int l) {
     Pairs z;
     unpack<kInter>(r.x[r.c0], r.x[r.c1], z);
-    Angles t;
-    if (r.pos >= 0) load_angles(p, r.pos, l, t);
+    if (r.pos >= 0) {
+        Angles t;
+        load_angles(p, r.pos, l, t);
+        auto turned = [&](float a, float c, float b, float s) {
+            const float x = cross_exact(a, c, b, s);
+            return !(fabsf(x) < 3.0e38f) && fabsf(a) <= 3.4e38f && fabsf(b) <= 3.4e38f ? 3.402823466e38f : x;
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const Two a = z.a[i], b = z.b[i], c = t.c[i], s = t.s[i];
+            z.a[i] = Two{turned(a.x, c.x, b.x, s.x), turned(a.y, c.y, b.y, s.y)};
+            z.b[i] = Two{turned(a.x, s.x, -b.x, c.x), turned(a.y, s.y, -b.y, c.y)};
+        }
+    }
     float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float x = r.pos >= 0 ? cross_exact(z.a[i], t.c[i], z.b[i], t.s[i], 1.f) : z.a[i];
-        const float y = r.pos >= 0 ? cross_exact(z.a[i], t.s[i], -z.b[i], t.c[i], 1.f) : z.b[i];
-        top = fmaxf(top, fmaxf(finite_size(x), finite_size(y)));
-    }
+    for (int i = 0; i < 4; ++i)
+        top = fmaxf(fmaxf(fmaxf(top, finite_size(z.a[i].x)), finite_size(z.a[i].y)),
+                    fmaxf(finite_size(z.b[i].x), finite_size(z.b[i].y)));
     return top;
+}
+
+// Sixteen values as codes, the first chunk's eight in the first two words.
+template <bool kInter>
+__device__ __forceinline__ uint4 to_codes(const Pairs& z) {
+    uint4 x, y;   // two codes a word
+    pack<kInter>(z, x, y, [](float lo, float hi) { return to_e4m3x2(lo, hi); });
+    return make_uint4(x.x | (x.y << 16), x.z | (x.w << 16), y.x | (y.y << 16), y.z | (y.w << 16));
+}
+
+// The codes of a rotated row's sixteenth in twice fp32's precision, from memory.
+template <bool kInter>
+__device__ __noinline__ uint4 codes_again(const Params& p, const Source r, float inv, int l) {
+    Pairs z;
+    unpack<kInter>(r.x[r.c0], r.x[r.c1], z);
+    Angles t;
+    load_angles(p, r.pos, l, t);
+    const Two inv2{inv, inv};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const Two a = mul(z.a[i], inv2), b = mul(z.b[i], inv2), c = t.c[i], s = t.s[i];
+        z.a[i] = Two{cross_exact(a.x, c.x, b.x, s.x), cross_exact(a.y, c.y, b.y, s.y)};
+        z.b[i] = Two{cross_exact(a.x, s.x, -b.x, c.x), cross_exact(a.y, s.y, -b.y, c.y)};
+    }
+    return to_codes<kInter>(z);
 }
 
 // A lane's sixteen values over the scale to codes: z holds the values (fp32's
 // of rotated ones), inv = 1 / scale.
 template <bool kInter>
 __device__ __forceinline__ void store_codes(const Params& p, Pairs& z, float inv, const Source& r, uint8_t* row, int l) {
+    const Two inv2{inv, inv};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        z.a[i] *= inv;
-        z.b[i] *= inv;
+    for (int i = 0; i < 4; ++i) {
+        z.a[i] = mul(z.a[i], inv2);
+        z.b[i] = mul(z.b[i], inv2);
     }
+    uint4 codes = to_codes<kInter>(z);
     if (r.pos >= 0) {
+        // the row's smallest size stands for the subnormals, 0 * value for NaN and infinities
         bool near = false;
+        float least = 1.f;
+        Two none{0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) near |= near_border(z.a[i]) || near_border(z.b[i]);
-        if (near) {
-            Pairs w;
-            unpack<kInter>(r.x[r.c0], r.x[r.c1], w);
-            Angles t;
-            load_angles(p, r.pos, l, t);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                // 0 of finite factors is exact
-                if (near_border(z.a[i]) && z.a[i] != 0.f) z.a[i] = cross_exact(w.a[i], t.c[i], w.b[i], t.s[i], inv);
-                if (near_border(z.b[i]) && z.b[i] != 0.f) z.b[i] = cross_exact(w.a[i], t.s[i], -w.b[i], t.c[i], inv);
-            }
+        for (int i = 0; i < 4; ++i) {
+            near |= near_half(z.a[i].x) | near_half(z.a[i].y) | near_half(z.b[i].x) | near_half(z.b[i].y);
+            least = fminf(fminf(fminf(least, fabsf(z.a[i].x)), fminf(fabsf(z.a[i].y), fabsf(z.b[i].x))), fabsf(z.b[i].y));
+            none = fma(z.a[i], Two{0.f, 0.f}, fma(z.b[i], Two{0.f, 0.f}, none));
         }
+        if (least < 0.015625f) {
+            // subnormal codes have the borders that 2^-6 above them has
+            auto low = [](float v) { return near_half(fabsf(v) < 0.015625f ? fabsf(v) + 0.015625f : v); };
+#pragma unroll
+            for (int i = 0; i < 4; ++i) near |= low(z.a[i].x) | low(z.a[i].y) | low(z.b[i].x) | low(z.b[i].y);
+        }
+        if (near || none.x != 0.f || none.y != 0.f) codes = codes_again<kInter>(p, r, inv, l);
     }
-    uint2 x, y;
-    if constexpr (kInter) {
-        x = make_uint2(to_e4m3x2(z.a[0], z.b[0]) | (to_e4m3x2(z.a[1], z.b[1]) << 16),
-                       to_e4m3x2(z.a[2], z.b[2]) | (to_e4m3x2(z.a[3], z.b[3]) << 16));
-        y = make_uint2(to_e4m3x2(z.a[4], z.b[4]) | (to_e4m3x2(z.a[5], z.b[5]) << 16),
-                       to_e4m3x2(z.a[6], z.b[6]) | (to_e4m3x2(z.a[7], z.b[7]) << 16));
-    } else {
-        x = make_uint2(to_e4m3x2(z.a[0], z.a[1]) | (to_e4m3x2(z.a[2], z.a[3]) << 16),
-                       to_e4m3x2(z.a[4], z.a[5]) | (to_e4m3x2(z.a[6], z.a[7]) << 16));
-        y = make_uint2(to_e4m3x2(z.b[0], z.b[1]) | (to_e4m3x2(z.b[2], z.b[3]) << 16),
-                       to_e4m3x2(z.b[4], z.b[5]) | (to_e4m3x2(z.b[6], z.b[7]) << 16));
-    }
-    reinterpret_cast<uint2*>(row)[r.c0] = x;
-    reinterpret_cast<uint2*>(row)[r.c1] = y;
+    reinterpret_cast<uint2*>(row)[r.c0] = make_uint2(codes.x, codes.y);
+    reinterpret_cast<uint2*>(row)[r.c1] = make_uint2(codes.z, codes.w);
 }
 
 // The codes of a row that is there, times ratio.
@@ -318,18 +402,18 @@ __device__ __forceinline__ bool find_token(const Params& p, int i, int lane, int
 }
 
 // The rows of new token i by `warps` warps, `warp` being one of them: queries,
-// and with kKv its keys and values, into a bf16 cache or (kFp8) as the one new
-// token of an 8-bit block.  The rows' loads are issued before the token's
+// keys and values, into a bf16 cache or (kFp8) as the one new token of an 8-bit
+// block.  The rows' loads are issued before the token's
 // place, which takes three loads in a row, is known.
-template <bool kInter, bool kKv, bool kFp8>
+template <bool kInter, bool kFp8>
 __device__ __forceinline__ void token_rows(const Params& p, int i, int warp, int warps) {
     const int lane = threadIdx.x & 31, l = lane & 7;
     const int n_q = p.q != nullptr ? p.Hq : 0;
-    const int n = n_q + (kKv ? 2 * p.Hkv : 0);
+    const int n = n_q + 2 * p.Hkv;
     const int c0 = first_chunk<kInter>(p, l), c1 = second_chunk<kInter>(p, l);
     auto source = [&](int r) -> const uint4* {
         const __nv_bfloat16* x;
-        if (!kKv || r < n_q)
+        if (r < n_q)
             x = p.q + i * p.q_stride + r * kD;
         else if (r < n_q + p.Hkv)
             x = p.k + i * p.k_stride + (r - n_q) * kD;
@@ -337,7 +421,7 @@ __device__ __forceinline__ void token_rows(const Params& p, int i, int warp, int
             x = p.v + i * p.v_stride + (r - n_q - p.Hkv) * kD;
         return reinterpret_cast<const uint4*>(x);
     };
-    int b = 0, t = 0, pos = 0, slot_in_page = 0;
+    int b = 0, t = 0, pos = 0;
     long long slot = -1;
     Angles turn;
     for (int r0 = warp * 4 + (lane >> 3), step = 4 * warps, first = 1; first || r0 < n; r0 += kBatch * step, first = 0) {
@@ -352,25 +436,22 @@ __device__ __forceinline__ void token_rows(const Params& p, int i, int warp, int
         if (first) {
             if (!find_token(p, i, lane, b, t, pos)) return;
             if (l < (p.rot >> 4)) load_angles(p, pos, l, turn);
-            if constexpr (kKv) {
-                const int page = page_at(p.list, b, t / p.list.page_size, page_count(p.list, b),
-                                         warp == 0 && lane == 0 ? p.status : nullptr);
-                slot_in_page = t % p.list.page_size;
-                if (page >= 0) slot = static_cast<long long>(page) * p.list.page_size + slot_in_page;
-            }
+            const int entry = p.page_div.div(t);
+            const int page = page_at(p.list, b, entry, page_count(p.list, b), warp == 0 && lane == 0 ? p.status : nullptr);
+            if (page >= 0) slot = static_cast<long long>(page) * p.list.page_size + (t - entry * p.list.page_size);
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int r = r0 + k * step;
             if (r >= n) break;
-            const bool query = !kKv || r < n_q, key = kKv && !query && r < n_q + p.Hkv;
+            const bool query = r < n_q, key = !query && r < n_q + p.Hkv;
             const bool turns = (query || key) && l < (p.rot >> 4);
             Pairs z;
             if (query || !kFp8) {
                 if (turns) {
                     unpack<kInter>(x[k], y[k], z);
                     rotate(z, turn);
-                    pack<kInter>(z, x[k], y[k]);
+                    pack<kInter>(z, x[k], y[k], pack2);
                 }
                 uint4* dst;
                 if (query) {
@@ -387,17 +468,18 @@ __device__ __forceinline__ void token_rows(const Params& p, int i, int warp, int
                 // one new row of a block: eight lanes settle its scale
                 const unsigned eight = 0xFFu << (lane & 24);
                 const int h = key ? r - n_q : r - n_q - p.Hkv;
-                const int there = t % p.block;   // rows of the block before it
-                float* scale = (key ? p.k_scale : p.v_scale) + static_cast<size_t>(slot / p.block) * p.Hkv + h;
+                const int there = t - p.block_div.div(t) * p.block;   // rows of the block before it
+                float* scale = (key ? p.k_scale : p.v_scale) + static_cast<size_t>(p.block_div.div(static_cast<int>(slot))) * p.Hkv + h;
                 uint8_t* row = static_cast<uint8_t*>(key ? p.k_cache : p.v_cache) + (static_cast<size_t>(slot) * p.Hkv + h) * kD;
                 const float was = there > 0 ? *scale : 0.f;
                 const Source src{source(r), c0, c1, turns ? pos : -1};
                 unpack<kInter>(x[k], y[k], z);
                 if (turns) rotate_closely(z, turn);
-                float top = size_of(z);
+                const float own = size_of(z);
+                float top = own;
 #pragma unroll
                 for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(eight, top, off));
-                if (doubtful(top, key && p.rot > 0)) {
+                if (__any_sync(eight, doubtful(top, own, turns))) {
                     top = size_again<kInter>(p, src, l);
 #pragma unroll
                     for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(eight, top, off));
@@ -408,7 +490,7 @@ __device__ __forceinline__ void token_rows(const Params& p, int i, int warp, int
                 if (l == 0 && !(there > 0 && now == was)) *scale = now;
                 if (ratio != 1.f)
                     for (int j = 1; j <= there; ++j) rescale_row(row - static_cast<size_t>(j) * p.Hkv * kD, ratio, l);
-                store_codes<kInter>(p, z, now > 0.f ? 1.f / now : 0.f, src, row, l);
+                store_codes<kInter>(p, z, inverse_of(now), src, row, l);
             }
         }
     }
@@ -419,162 +501,322 @@ template <bool kInter, bool kFp8>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ Params p, int warps_per_token) {
     const int warp = threadIdx.x >> 5;
     const int i = blockIdx.x * (kThreads / 32 / warps_per_token) + warp / warps_per_token;
-    if (i < p.total_q) token_rows<kInter, true, kFp8>(p, i, warp % warps_per_token, warps_per_token);
+    if (i < p.total_q) token_rows<kInter, kFp8>(p, i, warp % warps_per_token, warps_per_token);
 }
 
-// 8-bit blocks of ragged batches.  CTAs [0, n_units * slices): a unit is one
-// block of tokens of one sequence; groups of 4 * block threads (at most 512)
-// take one head's keys or values of it at a time, a lane holding kHeld rows'
-// sixteenths in registers from the load over the block's maximum to the codes,
-// and the next head's rows in flight meanwhile.  The other CTAs take queries, two
-// warps a token.  Sequence b's blocks are the units from S_b = qo_indptr[b] /
-// block + 2b on: n new tokens touch at most n / block + 2 blocks, and S_{b+1} -
-// S_b is at least that, so no prefix sum is needed; the units left over do
-// nothing.
-template <bool kInter>
-__global__ void __launch_bounds__(512) kv_append_blocks_kernel(const __grid_constant__ Params p, int group_threads) {
-    __shared__ float tops[2][16];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 7;
-    if (static_cast<int>(blockIdx.x) >= p.n_units * p.slices) {
-        const int tokens = blockDim.x >> 6;
-        const int i = (blockIdx.x - p.n_units * p.slices) * tokens + (warp >> 1);
-        if (warp < 2 * tokens && i < p.total_q) token_rows<kInter, false, false>(p, i, warp & 1, 2);
-        return;
+// Ragged batches into 8-bit blocks.  Every warp copies kRows rows into shared
+// memory, all of them in flight at once, and works on them there, eight lanes a
+// row, four rows at a time.  17k tokens of 32 + 2 x 8 heads (378 MB): 68 us, 83 %
+// of the copy rate; alone the queries take 47 us (their bytes 44) and the blocks
+// 40, bound by their instructions and the angles' latency.  Tried: unrolled over
+// rows in registers 120 us (a quarter of it waiting for instructions, 12 warps an
+// SM), a CTA of 8 lanes per row and a round per head 105-118 us (what a head
+// costs a warp beside its four rows), 6 CTAs an SM 80 us (80 registers spill),
+// queries by token instead of by 8 tokens x 4 heads 79 us, the two kinds mixed 70.
+constexpr int kTaskWarps = 4;
+constexpr int kRows = 32;
+constexpr int kRowBytes = 2 * kD;
+
+struct TaskMemory {
+    uint4 rows[kTaskWarps][kRows * kRowBytes / 16];
+    float top[2][kTaskWarps];
+    int doubt[kTaskWarps];
+};
+
+// Copies rows t0 .. of `n` into the warp's buffer; `row` gives a row's source.
+template <typename Row>
+__device__ __forceinline__ void copy_rows(uint4* buf, int n, int lane, Row row) {
+    const int l = lane & 7;
+#pragma unroll
+    for (int k = 0; k < kRows / 4; ++k) {
+        const int r = 4 * k + (lane >> 3);
+        if (r < n) {
+            const uint4* src = row(r);
+            cp_async16(buf + r * 16 + l, src + l, 16);
+            cp_async16(buf + r * 16 + l + 8, src + l + 8, 16);
+        }
     }
-    const int u = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
-    const int b = warp_rank(p.B, u, lane, [&](int x) { return p.qo_indptr[x] / p.block + 2 * x; });
+}
+
+// A rotated sixteenth in 16 bits each: bf16 rounded to odd (towards zero, the
+// last bit set if anything was lost).  Eight significant bits, two more than
+// the four of a code and its rounding need, give the code of the exact value
+// whatever the power of two it is divided by later.  fp32's bits decide unless
+// the 16 dropped ones are within a few units of 0.  z: the lane's raw pairs.
+template <bool kInter>
+__device__ __forceinline__ void rotate_to_odd(const Angles& t, Pairs& z, float& own, uint4& x, uint4& y) {
+    Pairs r = z;
+    rotate_closely(r, t);
+    own = fmaxf(own, size_of(r));
+    auto near_zero = [](float v) { return __float_as_uint(v) * 65536u + 4u * 65536u <= 8u * 65536u; };
+    bool near = false;
+    Two none{0.f, 0.f};   // 0 * value: NaN for NaN and infinities
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        near |= near_zero(r.a[i].x) | near_zero(r.a[i].y) | near_zero(r.b[i].x) | near_zero(r.b[i].y);
+        none = fma(r.a[i], Two{0.f, 0.f}, fma(r.b[i], Two{0.f, 0.f}, none));
+    }
+    uint32_t odd = 0x00010001u;
+    if (near || none.x != 0.f || none.y != 0.f) {
+        odd = 0;
+        auto exactly = [](float a, float c, float b, float s) {
+            const uint32_t u = __float_as_uint(cross_exact(a, c, b, s));
+            return __uint_as_float((u & 0xFFFFu) != 0u ? u | 0x10000u : u);
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const Two a = z.a[i], b = z.b[i], c = t.c[i], s = t.s[i];
+            r.a[i] = Two{exactly(a.x, c.x, b.x, s.x), exactly(a.y, c.y, b.y, s.y)};
+            r.b[i] = Two{exactly(a.x, s.x, -b.x, c.x), exactly(a.y, s.y, -b.y, c.y)};
+        }
+    }
+    pack<kInter>(r, x, y, [&](float lo, float hi) {
+        return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632) | odd;
+    });
+}
+
+// The largest size among two chunks of bf16, infinite if one is not finite.
+__device__ __forceinline__ float size_of(uint4 x, uint4 y) {
+    const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, u[i] & 0x7FFF7FFFu);
+    m = max(m & 0xFFFFu, m >> 16);
+    return m > 0x7F7Fu ? INFINITY : __uint_as_float(m << 16);
+}
+
+// Eight bf16 times inv as codes.
+__device__ __forceinline__ uint2 codes_of(uint4 w, float inv) {
+    const Two inv2{inv, inv};
+    const Two a = mul(Two{lo_bf16(w.x), hi_bf16(w.x)}, inv2), b = mul(Two{lo_bf16(w.y), hi_bf16(w.y)}, inv2);
+    const Two c = mul(Two{lo_bf16(w.z), hi_bf16(w.z)}, inv2), d = mul(Two{lo_bf16(w.w), hi_bf16(w.w)}, inv2);
+    return make_uint2(to_e4m3x2(a.x, a.y) | (to_e4m3x2(b.x, b.y) << 16), to_e4m3x2(c.x, c.y) | (to_e4m3x2(d.x, d.y) << 16));
+}
+
+// kPartHeads heads of kPartTokens consecutive new tokens: queries.  Eight lanes
+// keep a token's angles for all of its heads; lane j finds token j's place while
+// the rows are on their way.
+constexpr int kPartTokens = 8;
+constexpr int kPartHeads = kRows / kPartTokens;
+
+template <bool kInter>
+__device__ __forceinline__ void query_task(const Params& p, int tile, int h0, uint4* buf, int lane) {
+    const int l = lane & 7, base = tile * kPartTokens;
+    const int heads = min(kPartHeads, p.Hq - h0);
+    // buffer row 4k + (lane / 8): token 4 (k & 1) + lane / 8, head k / 2
+#pragma unroll
+    for (int k = 0; k < kRows / 4; ++k) {
+        const int i = base + 4 * (k & 1) + (lane >> 3), h = k >> 1;
+        if (i < p.total_q && h < heads) {
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + i * p.q_stride + (h0 + h) * kD);
+            uint4* dst = buf + (4 * k + (lane >> 3)) * 16;
+            cp_async16(dst + l, src + l, 16);
+            cp_async16(dst + l + 8, src + l + 8, 16);
+        }
+    }
+    const int i = base + lane;
+    int pos = -1;
+    bool there = lane < kPartTokens && i < p.total_q && i >= p.qo_indptr[0] && i < p.qo_indptr[p.B];
+    if (there) {
+        int lo = 0, hi = p.B;   // last b with qo_indptr[b] <= i
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (p.qo_indptr[mid] <= i) lo = mid; else hi = mid;
+        }
+        const int t = p.seq_lens[lo] - (p.qo_indptr[lo + 1] - i);
+        there = t >= 0 && position_ok(p, i, t, pos);
+    }
+    const uint32_t mask = __ballot_sync(0xffffffffu, there);
+    const int c0 = first_chunk<kInter>(p, l), c1 = second_chunk<kInter>(p, l);
+    const bool turns = l < (p.rot >> 4);
+    Angles t[kPartTokens / 4];
+#pragma unroll
+    for (int k = 0; k < kPartTokens / 4; ++k) {
+        const int r = 4 * k + (lane >> 3);
+        const int at = __shfl_sync(0xffffffffu, pos, r);
+        if (turns && ((mask >> r) & 1u)) load_angles(p, at, l, t[k]);
+    }
+    cp_async_wait_all();
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kPartTokens / 4; ++k) {
+        const int r = 4 * k + (lane >> 3);
+        if (!((mask >> r) & 1u)) continue;
+        uint4* dst = reinterpret_cast<uint4*>(p.q_out + (static_cast<size_t>(base + r) * p.Hq + h0) * kD);
+        const uint4* src = buf + r * 16;
+#pragma unroll 2
+        for (int h = 0; h < heads; ++h, dst += 16, src += kPartTokens * 16) {
+            uint4 x = src[c0], y = src[c1];
+            if (turns) {
+                Pairs z;
+                unpack<kInter>(x, y, z);
+                rotate(z, t[k]);
+                pack<kInter>(z, x, y, pack2);
+            }
+            dst[c0] = x;
+            dst[c1] = y;
+        }
+    }
+}
+
+// One head's keys or values of one block of one sequence, by a group of `warps`
+// warps (this one is number `w` of them), kRows rows each: up to kRows * warps
+// new rows stay in shared memory between the maximum and the codes, rotated
+// ones in 16 bits rounded to odd; more are read and rotated again.
+template <bool kInter>
+__device__ __forceinline__ void block_task(const Params& p, int u, int pair, TaskMemory& mem, int w, int warps, int lane) {
+    const int l = lane & 7, warp = threadIdx.x >> 5, group = warp / warps;
+    uint4* buf = mem.rows[warp];
+    const int b = warp_rank(p.B, u, lane, [&](int x) { return p.block_div.div(p.qo_indptr[x]) + 2 * x; });
     const int i0 = p.qo_indptr[b], n = p.qo_indptr[b + 1] - i0;
-    const int j = u - (i0 / p.block + 2 * b);
+    const int j = u - (p.block_div.div(i0) + 2 * b);
     if (i0 < 0 || n <= 0 || j < 0 || i0 + n > p.total_q) return;
     const int len = p.seq_lens[b];
     const int start = len - n;                         // tokens below 0: left alone
     const int from = start > 0 ? start : 0;
-    const long long j0l = (static_cast<long long>(from / p.block) + j) * p.block;   // the block's first token
+    const long long j0l = (static_cast<long long>(p.block_div.div(from)) + j) * p.block;   // the block's first token
     if (j0l >= len) return;
     const int j0 = static_cast<int>(j0l);
-    const int lo = from > j0 ? from : j0;
+    const int lo = from > j0 ? from : j0;              // rows [lo, hi) of the block are new, [j0, lo) were there
     const int hi = len - j0 < p.block ? len : j0 + p.block;
-    const int page = page_at(p.list, b, j0 / p.list.page_size, page_count(p.list, b),
-                             threadIdx.x == 0 && slice == 0 ? p.status : nullptr);
-    if (page < 0) return;
-    const size_t row0 = static_cast<size_t>(page) * p.list.page_size + j0 % p.list.page_size;
+    const bool key = pair < p.Hkv;
+    const int h = key ? pair : pair - p.Hkv;
+    const __nv_bfloat16* x0 = (key ? p.k : p.v) + h * kD;
+    const long long stride = key ? p.k_stride : p.v_stride;
+    const int t_first = lo + w * kRows, t_step = warps * kRows;
+    const bool held = hi - lo <= t_step;
+    auto source = [&](int t) { return reinterpret_cast<const uint4*>(x0 + (i0 + (t - start)) * stride); };
+    auto copy = [&](int t0) { copy_rows(buf, min(kRows, hi - t0), lane, [&](int r) { return source(t0 + r); }); };
+    copy(t_first);
+    const int entry = p.page_div.div(j0);
+    const int page = page_at(p.list, b, entry, page_count(p.list, b), lane == 0 && w == 0 && pair == 0 ? p.status : nullptr);
+    if (page < 0) {
+        cp_async_wait_all();
+        return;
+    }
+    const size_t row0 = static_cast<size_t>(page) * p.list.page_size + (j0 - entry * p.list.page_size);
     const size_t row_bytes = static_cast<size_t>(p.Hkv) * kD;
-    const int group = threadIdx.x / group_threads, groups = blockDim.x / group_threads;
-    const int row_in_group = (threadIdx.x - group * group_threads) >> 3, rows = group_threads >> 3;
-    const int warps_per_group = group_threads >> 5, warp0 = group * warps_per_group;
-    const bool held = p.block <= kHeld * rows;
+    uint8_t* cells = static_cast<uint8_t*>(key ? p.k_cache : p.v_cache) + (row0 * p.Hkv + h) * kD;
+    float* scale = (key ? p.k_scale : p.v_scale) + p.block_div.div(static_cast<int>(row0)) * static_cast<size_t>(p.Hkv) + h;
+    const float was = lo > j0 ? *scale : 0.f;
     const int c0 = first_chunk<kInter>(p, l), c1 = second_chunk<kInter>(p, l);
-    const bool lane_turns = l < (p.rot >> 4);
-
-    // row `t` of the sequence for keys or values of head h, if it is new (and its position is good)
-    auto source = [&](int t, int pair, Source& s) -> bool {
-        if (t < lo || t >= hi) return false;
-        const int i = i0 + (t - start);
-        int pos;
-        if (!position_ok(p, i, t, pos)) return false;
-        const bool key = pair < p.Hkv;
-        const __nv_bfloat16* x = key ? p.k + i * p.k_stride + pair * kD : p.v + i * p.v_stride + (pair - p.Hkv) * kD;
-        s = Source{reinterpret_cast<const uint4*>(x), c0, c1, key && lane_turns ? pos : -1};
-        return true;
-    };
-    auto load = [&](int pair, uint4 (&x)[kHeld], uint4 (&y)[kHeld]) {
-#pragma unroll
-        for (int k = 0; k < kHeld; ++k) {
-            Source s;
-            if (pair < 2 * p.Hkv && source(j0 + row_in_group + k * rows, pair, s)) {
-                x[k] = s.x[c0];
-                y[k] = s.x[c1];
-            }
-        }
-    };
-    auto value = [&](const Source& s, uint4 x, uint4 y, Pairs& z) {
-        unpack<kInter>(x, y, z);
-        if (s.pos >= 0) {
-            Angles t;
-            load_angles(p, s.pos, l, t);
-            rotate_closely(z, t);
-        }
-    };
-    // the largest of every lane of the group
-    auto group_max = [&](float top, int buffer) -> float {
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        if (lane == 0) tops[buffer][warp] = top;
-        __syncthreads();
-        for (int w = 0; w < warps_per_group; ++w) top = fmaxf(top, tops[buffer][warp0 + w]);
-        return top;
-    };
-
-    const int per_round = p.slices * groups;
-    int buffer = 0;
-    uint4 x[kHeld], y[kHeld];
-    int pair = slice * groups + group;
-    if (held) load(pair, x, y);
-    for (int round = 0; round * per_round < 2 * p.Hkv; ++round, pair += per_round) {
-        const bool live = pair < 2 * p.Hkv, key = pair < p.Hkv;
-        const int h = key ? pair : pair - p.Hkv;
-        float* scale = nullptr;
-        uint8_t* cells = nullptr;
-        float was = 0.f, top = 0.f;
-        if (live) {
-            scale = (key ? p.k_scale : p.v_scale) + row0 / p.block * p.Hkv + h;
-            cells = static_cast<uint8_t*>(key ? p.k_cache : p.v_cache) + (row0 * p.Hkv + h) * kD;
-            if (lo > j0) was = *scale;
-        }
-        Pairs z[kHeld];
-        if (held) {
-#pragma unroll
-            for (int k = 0; k < kHeld; ++k) {
-                Source s;
-                if (live && source(j0 + row_in_group + k * rows, pair, s)) {
-                    value(s, x[k], y[k], z[k]);
-                    top = fmaxf(top, size_of(z[k]));
-                }
-            }
-            load(pair + per_round, x, y);
-        } else {
-            for (int t = j0 + row_in_group; live && t < hi; t += rows) {
-                Source s;
-                if (!source(t, pair, s)) continue;
-                value(s, s.x[c0], s.x[c1], z[0]);
-                top = fmaxf(top, size_of(z[0]));
-            }
-        }
-        top = group_max(top, buffer);
-        buffer ^= 1;
-        // every group of the CTA decides together: the barrier is the CTA's
-        if (__syncthreads_or(live && doubtful(top, key && p.rot > 0))) {
-            float again = 0.f;
-            for (int t = j0 + row_in_group; live && t < hi; t += rows) {
-                Source s;
-                if (source(t, pair, s)) again = fmaxf(again, size_again<kInter>(p, s, l));
-            }
-            top = group_max(again, buffer);
-            buffer ^= 1;
-        }
-        if (!live) continue;
-        float ratio;
-        const float now = join_scales(scale_of(top), lo > j0, was, ratio);
-        const float inv = now > 0.f ? 1.f / now : 0.f;
-        // (every lane read the old scale before the barrier)
-        if (threadIdx.x == group * group_threads && !(lo > j0 && now == was)) *scale = now;
-        if (ratio != 1.f)
-            for (int t = j0 + row_in_group; t < lo; t += rows) rescale_row(cells + (t - j0) * row_bytes, ratio, l);
-        if (held) {
-#pragma unroll
-            for (int k = 0; k < kHeld; ++k) {
-                Source s;
-                const int t = j0 + row_in_group + k * rows;
-                if (source(t, pair, s)) store_codes<kInter>(p, z[k], inv, s, cells + (t - j0) * row_bytes, l);
+    const bool turns = key && l < (p.rot >> 4);
+    // whether row t is to be written, and its row of the table
+    auto is_there = [&](int t, int& pos) { return t < hi && position_ok(p, i0 + (t - start), t, pos); };
+    float own = 0.f;
+    // rotates the rows in the buffer, from t0 on, where they are, and takes their maximum
+    auto turn_rows = [&](int t0) {
+        cp_async_wait_all();
+        __syncwarp();
+        const int m = min(kRows, hi - t0);
+        if (turns) {
+            Angles next;
+            int pos;
+            bool ok = (lane >> 3) < m && is_there(t0 + (lane >> 3), pos);
+            if (ok) load_angles(p, pos, l, next);
+#pragma unroll 1
+            for (int r = lane >> 3; r < m; r += 4) {
+                const Angles t = next;
+                const bool now_ok = ok;
+                ok = r + 4 < m && is_there(t0 + r + 4, pos);
+                if (ok) load_angles(p, pos, l, next);   // ahead of their use
+                if (!now_ok) continue;
+                Pairs z;
+                unpack<kInter>(buf[r * 16 + c0], buf[r * 16 + c1], z);
+                uint4 x, y;
+                rotate_to_odd<kInter>(t, z, own, x, y);
+                buf[r * 16 + c0] = x;
+                buf[r * 16 + c1] = y;
             }
         } else {
-            for (int t = j0 + row_in_group; t < hi; t += rows) {
-                Source s;
-                if (!source(t, pair, s)) continue;
-                value(s, s.x[c0], s.x[c1], z[0]);
-                store_codes<kInter>(p, z[0], inv, s, cells + (t - j0) * row_bytes, l);
+#pragma unroll 2
+            for (int r = lane >> 3; r < m; r += 4) {
+                int pos;
+                if (is_there(t0 + r, pos)) own = fmaxf(own, size_of(buf[r * 16 + c0], buf[r * 16 + c1]));
             }
         }
+        __syncwarp();
+    };
+    // the group's warps meet (the barrier's number as a constant, so that the CTA takes few of them)
+    auto meet = [&] {
+        if (warps == 1) __syncwarp();
+        else if (warps == 4) __syncthreads();
+        else if (group == 0) named_barrier_sync(1, 64);
+        else named_barrier_sync(2, 64);
+    };
+    // the largest of every lane of the group (non-negative: bits are ordered as numbers)
+    auto group_max = [&](float x, int turn) {
+        x = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+        if (lane == 0) mem.top[turn][warp] = x;
+        meet();
+        for (int i = 0; i < warps; ++i) x = fmaxf(x, mem.top[turn][group * warps + i]);
+        return x;
+    };
+    for (int t0 = t_first; t0 < hi; t0 += t_step) {
+        if (t0 > t_first) copy(t0);
+        turn_rows(t0);
+    }
+    float top = group_max(own, 0);
+    const bool doubt = __any_sync(0xffffffffu, doubtful(top, own, turns));
+    if (lane == 0) mem.doubt[warp] = doubt;
+    meet();   // (and every warp of the group has read the old scale)
+    int any = 0;
+    for (int i = 0; i < warps; ++i) any |= mem.doubt[group * warps + i];
+    if (any != 0) {
+        own = 0.f;
+        for (int t0 = t_first; t0 < hi; t0 += t_step)
+            for (int t = t0 + (lane >> 3); t < min(t0 + kRows, hi); t += 4) {
+                int pos;
+                if (is_there(t, pos))
+                    own = fmaxf(own, size_again<kInter>(p, Source{source(t), c0, c1, turns ? pos : -1}, l));
+            }
+        top = group_max(own, 1);
+    }
+    float ratio;
+    const float now = join_scales(scale_of(top), lo > j0, was, ratio);
+    const float inv = inverse_of(now);
+    if (lane == 0 && w == 0 && !(lo > j0 && now == was)) *scale = now;
+    if (ratio != 1.f)
+        for (int t = j0 + 4 * w + (lane >> 3); t < lo; t += 4 * warps) rescale_row(cells + (t - j0) * row_bytes, ratio, l);
+    for (int t0 = t_first; t0 < hi; t0 += t_step) {
+        if (!held) {
+            copy(t0);
+            turn_rows(t0);
+        }
+        const int m = min(kRows, hi - t0);
+#pragma unroll 2
+        for (int r = lane >> 3; r < m; r += 4) {
+            int pos;
+            if (!is_there(t0 + r, pos)) continue;
+            uint2* row = reinterpret_cast<uint2*>(cells + (t0 + r - j0) * row_bytes);
+            row[c0] = codes_of(buf[r * 16 + c0], inv);
+            row[c1] = codes_of(buf[r * 16 + c1], inv);
+        }
+        __syncwarp();
+    }
+}
+
+// The first block_ctas CTAs take blocks, group_warps warps one head's keys or
+// values, neighbouring groups neighbouring heads; the others take queries.
+// Sequence b's blocks are the units from S_b = qo_indptr[b] / block + 2b on: n
+// new tokens touch at most n / block + 2 blocks, and S_{b+1} - S_b is at least
+// that, so no prefix sum is needed; the units left over do nothing.
+template <bool kInter>
+__global__ void __launch_bounds__(32 * kTaskWarps, 4) kv_append_blocks_kernel(const __grid_constant__ Params p,
+                                                                             int group_warps, int block_ctas) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    TaskMemory& mem = *reinterpret_cast<TaskMemory*>(smem);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (static_cast<int>(blockIdx.x) < block_ctas) {
+        const long long task = static_cast<long long>(blockIdx.x) * (kTaskWarps / group_warps) + warp / group_warps;
+        if (task < static_cast<long long>(p.n_units) * 2 * p.Hkv)
+            block_task<kInter>(p, static_cast<int>(task / (2 * p.Hkv)), static_cast<int>(task % (2 * p.Hkv)), mem,
+                               warp % group_warps, group_warps, lane);
+    } else {
+        const long long task = static_cast<long long>(blockIdx.x - block_ctas) * kTaskWarps + warp;
+        const int parts = (p.Hq + kPartHeads - 1) / kPartHeads;
+        if (task < static_cast<long long>((p.total_q + kPartTokens - 1) / kPartTokens) * parts)
+            query_task<kInter>(p, static_cast<int>(task / parts), static_cast<int>(task % parts) * kPartHeads, mem.rows[warp], lane);
     }
 }
 
@@ -607,30 +849,32 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
     p.Hq = a.Hq;
     p.Hkv = a.Hkv;
     p.block = a.block_tokens;
-    p.n_units = p.slices = 0;
+    p.page_div = make_divisor(a.page_size);
+    p.block_div = make_divisor(a.block_tokens);
+    p.n_units = 0;
     p.status = a.dev_status;
-    if (a.k_scale == nullptr || a.qo_indptr == nullptr) {
+    const bool fp8 = a.k_scale != nullptr;
+    if (!fp8 || a.qo_indptr == nullptr) {
         // all eight warps on a token while there are fewer tokens than CTAs fit at once, else two each
         const int per = a.total_q <= 4 * sms ? 8 : 2;
         const int tokens = kThreads / 32 / per;
         const int grid = (a.total_q + tokens - 1) / tokens;
-        auto kern = a.k_scale != nullptr ? (a.interleaved ? kv_append_kernel<true, true> : kv_append_kernel<false, true>)
-                                         : (a.interleaved ? kv_append_kernel<true, false> : kv_append_kernel<false, false>);
+        auto kern = fp8 ? (a.interleaved ? kv_append_kernel<true, true> : kv_append_kernel<false, true>)
+                        : (a.interleaved ? kv_append_kernel<true, false> : kv_append_kernel<false, false>);
         kern<<<grid, kThreads, 0, stream>>>(p, per);
         return cudaGetLastError();
     }
     p.n_units = a.total_q / a.block_tokens + 2 * a.B;
-    const int group = a.block_tokens < 128 ? 4 * a.block_tokens : 512;
-    const int groups = group < 256 ? 256 / group : 1;
-    const int rounds = (2 * a.Hkv + groups - 1) / groups;   // of one CTA that does the whole unit
-    // CTAs of four rounds each, where that still gives every SM eight of them
-    p.slices = static_cast<long long>(p.n_units) * rounds >= 32LL * sms ? (rounds + 3) / 4 : rounds;
-    const int tokens = group * groups / 64;
-    const int q_ctas = a.q != nullptr ? (a.total_q + tokens - 1) / tokens : 0;
-    if (static_cast<long long>(p.n_units) * p.slices + q_ctas >= (1LL << 31)) p.slices = 1;   // the caller has checked that this fits
-    const long long grid = static_cast<long long>(p.n_units) * p.slices + q_ctas;
+    const int group = a.block_tokens <= kRows ? 1 : (a.block_tokens <= 2 * kRows ? 2 : 4);
+    const long long block_ctas = (static_cast<long long>(p.n_units) * 2 * a.Hkv * group + kTaskWarps - 1) / kTaskWarps;
+    const long long queries =
+        a.q != nullptr ? static_cast<long long>((a.total_q + kPartTokens - 1) / kPartTokens) * ((a.Hq + kPartHeads - 1) / kPartHeads) : 0;
+    const long long grid = block_ctas + (queries + kTaskWarps - 1) / kTaskWarps;
+    if (grid >= (1LL << 31)) return cudaErrorInvalidConfiguration;
     auto kern = a.interleaved ? kv_append_blocks_kernel<true> : kv_append_blocks_kernel<false>;
-    kern<<<static_cast<unsigned>(grid), group * groups, 0, stream>>>(p, group);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    kern<<<static_cast<unsigned>(grid), 32 * kTaskWarps, sizeof(TaskMemory), stream>>>(p, group, static_cast<int>(block_ctas));
     return cudaGetLastError();
 }
 
