@@ -35,7 +35,7 @@ constexpr int kStages = 3;      // tiles in flight or in use per warp
 constexpr int kCodes = kTile * kD;                    // 4 KB: a tile's K (or V) codes of one head
 constexpr int kWarpBytes = kStages * 2 * kCodes;
 constexpr int kMergeWarps = 8;
-constexpr int kBatch = 16;      // pieces a merging warp has in flight
+constexpr int kBatch = 8;       // pieces a merging warp has in flight
 
 struct Params {
     const __nv_bfloat16* q;   // [B, q_len, Hq, D]
@@ -46,6 +46,7 @@ struct Params {
     PageList list;
     const int32_t* seq_lens;
     Divisor page_div, block_div;
+    bool tile_in_page;   // pages are multiples of a tile
     int B, Hq, Hkv, G, nq;
     int cols;       // KV heads x row groups
     int workers;    // shares per column
@@ -60,6 +61,16 @@ struct Params {
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// m16n8k16 fp16 MMA, fp32 accumulators; not volatile, so that independent ones
+// may be interleaved.
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // Transpose of an 8x8 matrix of 16-bit elements held in fragment layout.
@@ -260,38 +271,42 @@ __device__ __forceinline__ void tile_step(State<NB>& st, const Queries<NB>& qs, 
                                           const int (&k_at)[2], const int (&v_at)[2], const float (&ka)[2],
                                           const float (&vb)[2], int tok0, uint32_t valid, int lane) {
     const int g = lane >> 2;
+    // scores: the sub-tiles' MMA chains side by side
+    uint32_t wg[2][8], w8[2][8];   // chunks 2t4, 2t4 + 1 of token g, and of token g + 8
+#pragma unroll
+    for (int sb = 0; sb < 2; ++sb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 c = *reinterpret_cast<const uint4*>(codes + (16 * sb + 8 * (i >> 1)) * kD + k_at[i & 1]);
+            uint32_t* w = (i < 2 ? wg[sb] : w8[sb]) + 4 * (i & 1);
+            w[0] = c.x, w[1] = c.y, w[2] = c.z, w[3] = c.w;
+        }
     float s[NB][2][4];
 #pragma unroll
-    for (int sb = 0; sb < 2; ++sb) {
-        uint4 kx[4];   // chunks 2t4, 2t4 + 1 of token g, then of token g + 8
+    for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            kx[i] = *reinterpret_cast<const uint4*>(codes + (16 * sb + 8 * (i >> 1)) * kD + k_at[i & 1]);
-        const uint32_t wg[8] = {kx[0].x, kx[0].y, kx[0].z, kx[0].w,
-                                kx[1].x, kx[1].y, kx[1].z, kx[1].w};
-        const uint32_t w8[8] = {kx[2].x, kx[2].y, kx[2].z, kx[2].w,
-                                kx[3].x, kx[3].y, kx[3].z, kx[3].w};
-        float acc[NB][4];
+        for (int sb = 0; sb < 2; ++sb) s[n][sb][0] = s[n][sb][1] = s[n][sb][2] = s[n][sb][3] = 0.f;
 #pragma unroll
-        for (int n = 0; n < NB; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+    for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-            const uint32_t a0 = e4m3x2_to_f16x2(wg[ks]), a1 = e4m3x2_to_f16x2(w8[ks]);
-            const uint32_t a2 = e4m3x2_to_f16x2(wg[ks] >> 16), a3 = e4m3x2_to_f16x2(w8[ks] >> 16);
+        for (int sb = 0; sb < 2; ++sb) {
+            const uint32_t a0 = e4m3x2_to_f16x2(wg[sb][ks]), a1 = e4m3x2_to_f16x2(w8[sb][ks]);
+            const uint32_t a2 = e4m3x2_hi_to_f16x2(wg[sb][ks]), a3 = e4m3x2_hi_to_f16x2(w8[sb][ks]);
 #pragma unroll
-            for (int n = 0; n < NB; ++n) mma_f16_16816(acc[n], a0, a1, a2, a3, qs.f[n][ks][0], qs.f[n][ks][1]);
+            for (int n = 0; n < NB; ++n) mma16816(s[n][sb], a0, a1, a2, a3, qs.f[n][ks][0], qs.f[n][ks][1]);
         }
+#pragma unroll
+    for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                s[n][sb][e] = acc[n][e] * (ka[sb] * qs.mul[n][e & 1]);
+                s[n][sb][e] *= ka[sb] * qs.mul[n][e & 1];
                 if constexpr (kPartial) {
                     const int t = 16 * sb + g + 8 * (e >> 1);
                     if (!((valid >> t) & 1u) || tok0 + t > qs.lim[n][e & 1]) s[n][sb][e] = -INFINITY;
                 }
             }
-    }
     uint4 vx[2][4];   // chunk g of tokens 2t4, 2t4 + 1, 2t4 + 8, 2t4 + 9
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb)
@@ -373,10 +388,10 @@ __device__ __forceinline__ void tile_step(State<NB>& st, const Queries<NB>& qs, 
             const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;   // the two tokens' bytes of two elements
             const uint32_t ab = __byte_perm(xa[mt >> 1], xb[mt >> 1], sel);
             const uint32_t cd = __byte_perm(xc[mt >> 1], xd[mt >> 1], sel);
-            const uint32_t a0 = e4m3x2_to_f16x2(ab), a1 = e4m3x2_to_f16x2(ab >> 16);
-            const uint32_t a2 = e4m3x2_to_f16x2(cd), a3 = e4m3x2_to_f16x2(cd >> 16);
+            const uint32_t a0 = e4m3x2_to_f16x2(ab), a1 = e4m3x2_hi_to_f16x2(ab);
+            const uint32_t a2 = e4m3x2_to_f16x2(cd), a3 = e4m3x2_hi_to_f16x2(cd);
 #pragma unroll
-            for (int n = 0; n < NB; ++n) mma_f16_16816(st.o[n][mt], a0, a1, a2, a3, w0[n], w1[n]);
+            for (int n = 0; n < NB; ++n) mma16816(st.o[n][mt], a0, a1, a2, a3, w0[n], w1[n]);
         }
     }
 }
@@ -436,6 +451,24 @@ __device__ __forceinline__ void feed_tile(const Params& p, const int* before, Fe
         }
         if (lane == 0) info->valid = valid;
         const int c = lane & 7, r0 = lane >> 3;
+        if (p.tile_in_page && valid == 0xffffffffu) {
+            // the rows are row_bytes apart: a third of the instructions of finding each one's place
+            const size_t at = __shfl_sync(0xffffffffu, off, 0) + r0 * row_bytes + 16 * c;
+            const uint8_t* k = p.k_cache + at;
+            const uint8_t* v = p.v_cache + at;
+            uint8_t* even = stage + chunk_off(r0, c);       // rows r0, r0 + 8, ...
+            uint8_t* odd = stage + chunk_off(r0 + 4, c);    // rows r0 + 4, r0 + 12, ...
+#pragma unroll
+            for (int i = 0; i < kTile / 4; ++i, k += 4 * row_bytes, v += 4 * row_bytes) {
+                uint8_t* dst = (i & 1 ? odd : even) + (i >> 1) * 8 * kD;
+                cp_async16(dst, k, 16);
+                cp_async16(dst + kCodes, v, 16);
+            }
+            ++f.x;
+            feed_look(p, before, f, lane);
+            cp_async_commit();
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < kTile / 4; ++i) {
             const int r = r0 + 4 * i;
@@ -576,10 +609,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp8_block_kernel(const __g
     }
 }
 
-// Joins the pieces of the sequences that were cut: `per_row` warps (1, 4 or 8)
+// Joins the pieces of the sequences that were cut: `per_row` warps (1, 2, 4 or 8)
 // per output row, four elements a lane.  O = sum_s 2^(L_s - L) O_s / sum_s
 // 2^(L_s - L); each warp takes every per_row-th piece, kBatch at a time.
-__global__ void __launch_bounds__(32 * kMergeWarps) decode_fp8_block_merge_kernel(const __grid_constant__ Params p,
+__global__ void __launch_bounds__(32 * kMergeWarps, 4) decode_fp8_block_merge_kernel(const __grid_constant__ Params p,
                                                                                   int rows_per_col, int per_row) {
     __shared__ int sums[2][kMergeWarps];
     __shared__ float4 warp_acc[kMergeWarps][32];
@@ -710,6 +743,7 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockArgs& a, cudaStream_t strea
     p.nq = a.q_len;
     p.page_div = make_divisor(a.page_size);
     p.block_div = make_divisor(a.block_tokens);
+    p.tile_in_page = a.page_size % kTile == 0;
     const int rows = p.G * p.nq, per = rows_per_column(rows);
     p.cols = a.Hkv * ((rows + per - 1) / per);
     p.workers = sms * kWarps / p.cols > 1 ? sms * kWarps / p.cols : 1;
@@ -726,8 +760,13 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockArgs& a, cudaStream_t strea
     kern<<<sms, kThreads, smem, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.workers == 1) return e;   // one share per column: no sequence is cut
-    // a sequence has about workers / B pieces, one that is longer than the others more
-    const int per_row = p.workers > 16LL * a.B ? 8 : (p.workers > 4LL * a.B ? 4 : 1);
+    // a sequence has about workers / B pieces, one that is longer than the others
+    // more: as many warps to a row as there are pieces for, while the CTAs (four
+    // fit on an SM) fit at once
+    const long long all_rows = static_cast<long long>(a.B) * a.q_len * a.Hq;
+    int per_row = 1;
+    while (per_row < kMergeWarps && p.workers > 2LL * per_row * a.B && all_rows * 2 * per_row <= 4LL * sms * kMergeWarps)
+        per_row *= 2;
     const int rows_per_cta = kMergeWarps / per_row;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
