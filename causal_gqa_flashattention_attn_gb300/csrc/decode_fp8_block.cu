@@ -30,10 +30,11 @@ constexpr int kD = 128;
 constexpr int kTile = 32;       // tokens per step of a warp
 constexpr int kWarps = 8;       // per CTA
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxSeqs = 4096;  // tile counts before each sequence, in shared memory
+constexpr int kMaxSeqs = 4096;  // tile counts before each sequence, and lengths, in shared memory
 constexpr int kStages = 3;      // tiles in flight or in use per warp
 constexpr int kCodes = kTile * kD;                    // 4 KB: a tile's K (or V) codes of one head
 constexpr int kWarpBytes = kStages * 2 * kCodes;
+static_assert(kWarps * kWarpBytes + (2 * kMaxSeqs + 1) * 4 + 1024 <= 227 * 1024, "the tables fit beside the rings");
 constexpr int kMergeWarps = 8;
 constexpr int kBatch = 8;       // pieces a merging warp has in flight
 
@@ -45,7 +46,7 @@ struct Params {
     const float* v_scale;
     PageList list;
     const int32_t* seq_lens;
-    Divisor page_div, block_div;
+    Divisor page_div, block_div, cols_div, heads_div, group_div;
     bool tile_in_page;   // pages are multiples of a tile
     int B, Hq, Hkv, G, nq;
     int cols;       // KV heads x row groups
@@ -100,13 +101,16 @@ __device__ __forceinline__ bool too_many_tiles(const Params& p) {
     return static_cast<long long>(p.list.indptr[p.B]) * p.list.page_size / kTile + p.B >= (1LL << 31);
 }
 
-// before[b] = tiles of the sequences before b (before[B] = all), by the whole
-// CTA: each thread sums a run of sequences.
-__device__ __forceinline__ void count_tiles(const Params& p, int* before, int* warp_sum, bool flag) {
+// before[b] = tiles of the sequences before b (before[B] = all) and lens[b] =
+// their lengths, by the whole CTA: each thread takes a run of sequences.
+__device__ __forceinline__ void count_tiles(const Params& p, int* before, int* lens, int* warp_sum, bool flag) {
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = threadIdx.x * per, b1 = min(b0 + per, p.B);
     int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += tiles_of(length_of(p, b, flag));
+    for (int b = b0; b < b1; ++b) {
+        lens[b] = length_of(p, b, flag);
+        sum += tiles_of(lens[b]);
+    }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int incl = sum;
 #pragma unroll
@@ -120,13 +124,9 @@ __device__ __forceinline__ void count_tiles(const Params& p, int* before, int* w
     for (int w = 0; w < warp; ++w) base += warp_sum[w];
     for (int b = b0; b < b1; ++b) {
         before[b] = base;
-        base += tiles_of(length_of(p, b, false));
+        base += tiles_of(lens[b]);
     }
-    if (threadIdx.x == 0) {
-        int all = 0;
-        for (int w = 0; w < kWarps; ++w) all += warp_sum[w];
-        before[p.B] = all;
-    }
+    if (threadIdx.x == kThreads - 1) before[p.B] = base;   // the last run ends with the last sequence, or is empty
     __syncthreads();
 }
 
@@ -178,23 +178,33 @@ struct Queries {
     int lim[NB][2];
 };
 
+// Their loads, four 16-byte chunks of a lane's row (zeros past the rows).
 template <int NB>
-__device__ __forceinline__ void load_queries(const Params& p, int b, int kvh, int row0, int n_rows, int len, int lane,
-                                             Queries<NB>& qs) {
+__device__ __forceinline__ void fetch_queries(const Params& p, int b, int kvh, int row0, int n_rows, int lane,
+                                              uint4 (&raw)[NB][4]) {
     const int g = lane >> 2, t4 = lane & 3;
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
         const int r = row0 + 8 * n + g;
-        const bool real = r < n_rows;
-        const int i = real ? r / p.G : 0, h = real ? r % p.G : 0;
+        const int i = p.group_div.div(r), h = r - i * p.G;
         const __nv_bfloat16* src =
             p.q + ((static_cast<size_t>(b) * p.nq + i) * p.Hq + static_cast<size_t>(kvh) * p.G + h) * kD + 32 * t4;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            raw[n][c] = r < n_rows ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+template <int NB>
+__device__ __forceinline__ void take_queries(const Params& p, const uint4 (&raw)[NB][4], int row0, int n_rows, int len,
+                                             int lane, Queries<NB>& qs) {
+    const int t4 = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
         float x[32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-            if (real) raw = __ldg(reinterpret_cast<const uint4*>(src) + c);
-            const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+            const uint32_t u[4] = {raw[n][c].x, raw[n][c].y, raw[n][c].z, raw[n][c].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 x[8 * c + 2 * k] = __uint_as_float(u[k] << 16);
@@ -220,7 +230,7 @@ __device__ __forceinline__ void load_queries(const Params& p, int b, int kvh, in
         for (int j = 0; j < 2; ++j) {
             const int col = 2 * t4 + j, rr = row0 + 8 * n + col;
             qs.mul[n][j] = __shfl_sync(0xffffffffu, up, 4 * col) * p.scale_log2;
-            qs.lim[n][j] = rr < n_rows ? len - p.nq + rr / p.G : -1;
+            qs.lim[n][j] = rr < n_rows ? len - p.nq + p.group_div.div(rr) : -1;
         }
     }
 }
@@ -420,7 +430,7 @@ __device__ __forceinline__ void feed_look(const Params& p, const int* before, Fe
     if (before[f.b + 1] <= f.x) {
         do ++f.b;
         while (before[f.b + 1] <= f.x);
-        f.len = length_of(p, f.b, false);
+        f.len = before[p.B + 1 + f.b];   // the lengths follow the counts
     }
     const int tok = (f.x - before[f.b]) * kTile + lane;
     f.tok = tok < f.len ? tok : -1;
@@ -483,19 +493,22 @@ __device__ __forceinline__ void feed_tile(const Params& p, const int* before, Fe
     cp_async_commit();
 }
 
+// (192 registers leave room on the SM for a CTA of the merge kernel, which then
+// has its place and counts ready when this grid ends.)
 template <int NB>
-__global__ void __launch_bounds__(kThreads, 1) decode_fp8_block_kernel(const __grid_constant__ Params p) {
+__global__ void __maxnreg__(NB == 1 ? 192 : 255) decode_fp8_block_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(128) uint8_t smem[];
     // the merge kernel's CTAs may come in as soon as there is room: they wait for this grid's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ TileInfo infos[kWarps][kStages];
     __shared__ int warp_sum[kWarps];
     int* before = reinterpret_cast<int*>(smem + kWarps * kWarpBytes);
+    int* lens = before + p.B + 1;
     if (too_many_tiles(p)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) flag_status(p.status, ATTN_DEV_SEQ_TOO_LONG);
         return;
     }
-    count_tiles(p, before, warp_sum, blockIdx.x == 0);
+    count_tiles(p, before, lens, warp_sum, blockIdx.x == 0);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int total = before[p.B];
     const Cut cut(p.workers, total);
@@ -511,12 +524,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp8_block_kernel(const __g
     }
 
     for (int unit = blockIdx.x * kWarps + warp; unit < p.workers * p.cols; unit += n_warps) {
-        const int w = unit / p.cols, col = unit % p.cols;
-        const int kvh = col % p.Hkv, row0 = (col / p.Hkv) * 8 * NB;
+        const int w = p.cols_div.div(unit), col = unit - w * p.cols;
+        const int part_of_head = p.heads_div.div(col), kvh = col - part_of_head * p.Hkv, row0 = part_of_head * 8 * NB;
         const int rows = min(8 * NB, n_rows - row0);
         auto out_row = [&](int b, int r) -> size_t {   // row of [B, q_len, Hq]
-            const int rr = row0 + r;
-            return (static_cast<size_t>(b) * p.nq + rr / p.G) * p.Hq + static_cast<size_t>(kvh) * p.G + rr % p.G;
+            const int rr = row0 + r, i = p.group_div.div(rr);
+            return (static_cast<size_t>(b) * p.nq + i) * p.Hq + static_cast<size_t>(kvh) * p.G + (rr - i * p.G);
         };
         // sequences without tokens: nothing is visible
         for (int b = w; b < p.B; b += p.workers) {
@@ -536,11 +549,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp8_block_kernel(const __g
         f.x = x;
         f.x_end = x_end;
         f.b = b;
-        f.len = length_of(p, b, false);
+        f.len = lens[b];
         feed_look(p, before, f, lane);
-        // the queries' loads go ahead of the codes'
+        // the queries' loads go ahead of the codes', the page's is on its way
+        uint4 raw[NB][4];
+        fetch_queries<NB>(p, b, kvh, row0, n_rows, lane, raw);
         Queries<NB> qs;
-        load_queries<NB>(p, b, kvh, row0, n_rows, f.len, lane, qs);
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) feed_tile(p, before, f, ring + i * 2 * kCodes, info + i, kvh, lane);
         int slot = 0;
@@ -549,11 +563,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp8_block_kernel(const __g
             const int t_lo = x - before[b], n_tiles = before[b + 1] - before[b];
             const int t_hi = min(n_tiles, t_lo + (x_end - x));
             x += t_hi - t_lo;
-            const int len = length_of(p, b, false);
-            if (!first) load_queries<NB>(p, b, kvh, row0, n_rows, len, lane, qs);
+            const int len = lens[b];
+            if (!first) fetch_queries<NB>(p, b, kvh, row0, n_rows, lane, raw);
+            take_queries<NB>(p, raw, row0, n_rows, len, lane, qs);
             State<NB> st;
             reset<NB>(st);
-            const int lim_min = len - p.nq + row0 / p.G;   // the first row's limit, the smallest
+            const int lim_min = len - p.nq + p.group_div.div(row0);   // the first row's limit, the smallest
             for (int t = t_lo; t < t_hi; ++t) {
                 cp_async_wait_group<kStages - 2>();
                 __syncwarp();   // everyone's copies of this stage are there; the stage before it has been read
@@ -743,9 +758,12 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockArgs& a, cudaStream_t strea
     p.nq = a.q_len;
     p.page_div = make_divisor(a.page_size);
     p.block_div = make_divisor(a.block_tokens);
+    p.heads_div = make_divisor(a.Hkv);
+    p.group_div = make_divisor(p.G);
     p.tile_in_page = a.page_size % kTile == 0;
     const int rows = p.G * p.nq, per = rows_per_column(rows);
     p.cols = a.Hkv * ((rows + per - 1) / per);
+    p.cols_div = make_divisor(p.cols);
     p.workers = sms * kWarps / p.cols > 1 ? sms * kWarps / p.cols : 1;
     p.scale_log2 = a.scale * kLog2e;
     p.o = static_cast<__nv_bfloat16*>(a.o);
@@ -753,9 +771,15 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockArgs& a, cudaStream_t strea
     p.part_o = static_cast<float*>(a.workspace);
     p.part_l = p.part_o + static_cast<size_t>(2) * p.workers * p.cols * per * kD;
     p.status = a.dev_status;
-    const size_t smem = kWarps * kWarpBytes + (static_cast<size_t>(a.B) + 1) * sizeof(int);
+    const size_t smem = kWarps * kWarpBytes + (2 * static_cast<size_t>(a.B) + 1) * sizeof(int);
     auto kern = per == 8 ? decode_fp8_block_kernel<1> : decode_fp8_block_kernel<2>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // both kernels with the same division of L1, so that neither waits for it to change
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(decode_fp8_block_merge_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     kern<<<sms, kThreads, smem, stream>>>(p);
     e = cudaGetLastError();
