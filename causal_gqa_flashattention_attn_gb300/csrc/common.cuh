@@ -136,6 +136,10 @@ struct VarlenArgs {
     void* kv_ws;            // NULL: gather rows inside the kernel; else contiguous K then V copy
     int max_kv_rows;        // rows the copy holds (>= kv_indptr[B] * page_size)
     bool copied;            // the caller has made the copy: no gather is launched
+    // with `copied`, the (sequence, query block) pairs longest first,
+    // varlen_max_pairs() words of sequence << varlen_pair_bits() | query block
+    // (used if there are no more of them); NULL: every CTA sorts them itself
+    const uint32_t* order;
 };
 // A paged cache's new tokens (kv_append.cu).
 struct AppendArgs {
@@ -205,6 +209,8 @@ size_t prefill_fp8_block_workspace(int B, int max_kv_rows, int Hkv);
 cudaError_t launch_prefill_fp8_block(const PrefillBlockArgs& a, cudaStream_t stream);
 
 int varlen_max_seqs();
+int varlen_max_pairs();
+int varlen_pair_bits();
 cudaError_t launch_prefill_varlen_tc(const VarlenArgs& a, cudaStream_t stream);
 
 }  // namespace gb300

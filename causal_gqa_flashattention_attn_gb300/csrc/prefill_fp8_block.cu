@@ -9,6 +9,8 @@
 // rounds nothing; another scale's values are rounded once to bf16, as the
 // tensor cores' operands must be.  The copy costs 1 byte read and 2 written
 // per element once, against one read of the cache per query block otherwise.
+#include <algorithm>
+
 #include "paged.cuh"
 
 namespace gb300 {
@@ -25,70 +27,18 @@ struct Params {
     const float* v_scale;
     PageList list;
     const int32_t* seq_lens;
+    const int32_t* qo_indptr;
+    Divisor page_div, block_div;
     int B, Hkv, block, max_rows;
+    int q_block;      // query positions of a work item of the prefill
+    int max_pairs, pair_bits;
+    uint32_t* order;  // [max_pairs], work items' (sequence, query block) pairs, longest first
     int32_t* start;   // [B + 1], first pages of the copy
     int32_t* last;    // [B], rows in each sequence's last page
     uint4* k_copy;    // [copy rows, Hkv, D] bf16
     uint4* v_copy;
     int32_t* status;
 };
-
-// Each sequence's first page of the copy and the rows in its last page; one
-// CTA.  Sequences past max_rows tokens in all are cut there.
-__global__ void __launch_bounds__(1024) fp8_block_starts_kernel(const Params p) {
-    __shared__ long long warp_rows[32];
-    __shared__ int warp_pages[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long rows_before = 0;   // tokens and pages of the sequences of earlier rounds
-    int pages_before = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 1024) {
-        const int b = b0 + threadIdx.x;
-        int len = 0;
-        if (b < p.B) {
-            len = p.seq_lens[b];
-            const long long cap = static_cast<long long>(page_count(p.list, b)) * p.list.page_size;
-            if (len < 0 || len > cap) {
-                flag_status(p.status, ATTN_DEV_SEQ_TOO_LONG);
-                len = len < 0 ? 0 : static_cast<int>(cap);
-            }
-        }
-        long long rows = len;   // inclusive sums over the warp, then over the CTA
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, rows, off);
-            if (lane >= off) rows += v;
-        }
-        if (lane == 31) warp_rows[warp] = rows;
-        __syncthreads();
-        long long first = rows_before + rows - len;
-        for (int w = 0; w < warp; ++w) first += warp_rows[w];
-        if (first + len > p.max_rows) {
-            flag_status(p.status, ATTN_DEV_SEQ_TOO_LONG);
-            len = first < p.max_rows ? static_cast<int>(p.max_rows - first) : 0;
-        }
-        const int n = (len + kPage - 1) / kPage;
-        int pages = n;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, pages, off);
-            if (lane >= off) pages += v;
-        }
-        if (lane == 31) warp_pages[warp] = pages;
-        __syncthreads();
-        int start = pages_before + pages - n;
-        for (int w = 0; w < warp; ++w) start += warp_pages[w];
-        if (b < p.B) {
-            p.start[b] = start;
-            p.last[b] = n > 0 ? len - (n - 1) * kPage : 0;
-        }
-        for (int w = 0; w < 32; ++w) {
-            rows_before += warp_rows[w];
-            pages_before += warp_pages[w];
-        }
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) p.start[p.B] = pages_before;
-}
 
 // Sixteen codes times a scale as bf16.
 __device__ __forceinline__ void widen(uint4 w, float scale, uint4& lo, uint4& hi) {
@@ -105,38 +55,191 @@ __device__ __forceinline__ void widen(uint4 w, float scale, uint4& lo, uint4& hi
     hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// One warp per row of the copy; rows past a sequence's end or on a missing
-// page are zeros.
+constexpr int kWarps = kThreads / 32;
+constexpr int kKeys = 512;     // KV tiles of a work item's pair; 511 and more together
+constexpr int kMaxSeqs = 2048;
+constexpr int kCopyRows = 4;   // rows of the copy that a warp takes: they lie in one block of one page
+
+// The sum of `x` over the CTA's threads before this one, and over all of them.
+template <typename T>
+__device__ __forceinline__ T scan_cta(T x, T* warp_sums, T& all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    T incl = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const T v = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += v;
+    }
+    __syncthreads();   // the last scan's sums have been read
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    T before = incl - x;
+    all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += warp_sums[w];
+        all += warp_sums[w];
+    }
+    return before;
+}
+
+struct Shared {
+    int start[kMaxSeqs + 1];   // first pages of the copy
+    int len[kMaxSeqs];         // rows of each sequence, cut at max_rows in all
+    int count[kKeys];
+    long long row_sums[kWarps];
+    int sums[kWarps];
+};
+
+// The sequences' places in the copy, by the whole CTA.
+__device__ __forceinline__ void place_sequences(const Params& p, Shared& sh, bool flag) {
+    long long rows_before = 0;
+    int pages_before = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        int len = 0;
+        if (b < p.B) {
+            len = p.seq_lens[b];
+            const long long cap = static_cast<long long>(page_count(p.list, b)) * p.list.page_size;
+            if (len < 0 || len > cap) {
+                if (flag) flag_status(p.status, ATTN_DEV_SEQ_TOO_LONG);
+                len = len < 0 ? 0 : static_cast<int>(cap);
+            }
+        }
+        long long all_rows;
+        const long long first = rows_before + scan_cta<long long>(len, sh.row_sums, all_rows);
+        rows_before += all_rows;
+        if (first + len > p.max_rows) {
+            if (flag) flag_status(p.status, ATTN_DEV_SEQ_TOO_LONG);
+            len = first < p.max_rows ? static_cast<int>(p.max_rows - first) : 0;
+        }
+        int all_pages;
+        const int start = pages_before + scan_cta<int>((len + kPage - 1) / kPage, sh.sums, all_pages);
+        pages_before += all_pages;
+        if (b < p.B) {
+            sh.start[b] = start;
+            sh.len[b] = len;
+        }
+    }
+    if (threadIdx.x == 0) sh.start[p.B] = pages_before;
+    __syncthreads();
+}
+
+// One CTA, for the prefill: the places, and its work items longest first by a
+// counting sort over their KV tiles; items of one length come in any order, each
+// gives the same result wherever it runs.  (In the prefill's own CTAs, one warp
+// each, the same sort takes 15 us for 300 pairs.)
+__device__ __forceinline__ void sort_items(const Params& p, Shared& sh) {
+    for (int k = threadIdx.x; k < kKeys; k += kThreads) sh.count[k] = 0;
+    int pairs = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        int blocks = 0;
+        if (b < p.B) {
+            p.start[b] = sh.start[b];
+            p.last[b] = sh.len[b] > 0 ? sh.len[b] - (sh.len[b] - 1) / kPage * kPage : 0;
+            blocks = (p.qo_indptr[b + 1] - p.qo_indptr[b] + p.q_block - 1) / p.q_block;   // as the prefill counts
+        }
+        int all;
+        scan_cta<int>(blocks, sh.sums, all);
+        pairs += all;
+    }
+    if (threadIdx.x == 0) p.start[p.B] = sh.start[p.B];
+    if (pairs > p.max_pairs) return;   // too many to sort: taken in sequence order
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // every pair and its key, one warp a sequence, lanes its query blocks
+    auto each_pair = [&](auto use) {
+        for (int b = warp; b < p.B; b += kWarps) {
+            const int q_len = p.qo_indptr[b + 1] - p.qo_indptr[b], kv_len = sh.len[b];
+            for (int qb = lane; qb * p.q_block < q_len; qb += 32) {
+                const int end = min(kv_len, min((qb + 1) * p.q_block, q_len) + kv_len - q_len);   // keys the block sees
+                use(min(end > 0 ? (end + kPage - 1) / kPage : 0, kKeys - 1), b, qb);
+            }
+        }
+    };
+    each_pair([&](int key, int, int) { atomicAdd(&sh.count[key], 1); });
+    __syncthreads();
+    // first place of each key, from the longest down: two keys a thread
+    const int key = kKeys - 1 - 2 * static_cast<int>(threadIdx.x);
+    const int longer = sh.count[key], shorter = sh.count[key - 1];
+    int all;
+    const int at = scan_cta<int>(longer + shorter, sh.sums, all);
+    sh.count[key] = at;
+    sh.count[key - 1] = at + longer;
+    __syncthreads();
+    each_pair([&](int k, int b, int qb) {
+        const int to = atomicAdd(&sh.count[k], 1);
+        if (to < p.max_pairs) p.order[to] = (static_cast<uint32_t>(b) << p.pair_bits) | static_cast<uint32_t>(qb);
+    });
+}
+static_assert(kKeys == 2 * kThreads, "two keys a thread");
+
+// CTA (0, 0) sorts the prefill's work items; the others copy.  A warp takes
+// kCopyRows rows and 32 of their 16-byte vectors of codes, a row of both caches
+// ahead.  Rows past a sequence's end or on a missing page are zeros.  The loop
+// stays rolled: with eight rows unrolled the kernel took 23 us instead of 7 on a
+// short batch, most of it for fetching instructions that run once.
 __global__ void __launch_bounds__(kThreads) fp8_block_copy_kernel(const Params p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ Shared sh;
+    const bool sorts = blockIdx.x == 0;
+    if (sorts && blockIdx.y != 0) return;
+    place_sequences(p, sh, sorts);
+    if (sorts) {
+        sort_items(p, sh);
+        return;
+    }
     const int lane = threadIdx.x & 31;
     const int vecs = p.Hkv * (kD / 16);
-    const long long n_warps = static_cast<long long>(gridDim.x) * (kThreads / 32);
-    const long long end = static_cast<long long>(p.start[p.B]) * kPage;
+    const uint32_t chunks = (vecs + 31) / 32;
+    const uint32_t parts = static_cast<uint32_t>(sh.start[p.B]) * (kPage / kCopyRows);   // fewer than 2^31 rows
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    for (long long r = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); r < end; r += n_warps) {
-        const int page_row = static_cast<int>(r / kPage);
-        const int b = warp_rank(p.B, page_row, lane, [&](int i) { return p.start[i]; });
-        const int t = static_cast<int>(r - static_cast<long long>(p.start[b]) * kPage);
-        const int len = (p.start[b + 1] - p.start[b] - 1) * kPage + p.last[b];
-        long long slot = -1;
-        if (t < len) {
-            const int page = page_at(p.list, b, t / p.list.page_size, page_count(p.list, b),
-                                     lane == 0 ? p.status : nullptr);
-            if (page >= 0) slot = static_cast<long long>(page) * p.list.page_size + t % p.list.page_size;
-        }
-        for (int v = lane; v < vecs; v += 32) {
-            const size_t dst = (static_cast<size_t>(r) * vecs + v) * 2;
-            uint4 k0 = zero, k1 = zero, v0 = zero, v1 = zero;
-            if (slot >= 0) {
-                const size_t src = static_cast<size_t>(slot) * vecs + v;
-                const size_t at = static_cast<size_t>(slot / p.block) * p.Hkv + v / (kD / 16);
-                widen(__ldg(reinterpret_cast<const uint4*>(p.k_cache) + src), __ldg(p.k_scale + at), k0, k1);
-                widen(__ldg(reinterpret_cast<const uint4*>(p.v_cache) + src), __ldg(p.v_scale + at), v0, v1);
+    for (uint32_t part = (blockIdx.x - 1) * kWarps + (threadIdx.x >> 5); part < parts; part += (gridDim.x - 1) * kWarps) {
+        const int copy_page = static_cast<int>(part / (kPage / kCopyRows));
+        const int b = warp_rank(p.B, copy_page, lane, [&](int i) { return sh.start[i]; });
+        const int t0 = static_cast<int>(part - static_cast<uint32_t>(sh.start[b]) * (kPage / kCopyRows)) * kCopyRows;
+        const int len = sh.len[b];
+        const int entry = p.page_div.div(t0);
+        const int page = t0 < len ? page_at(p.list, b, entry, page_count(p.list, b), lane == 0 ? p.status : nullptr) : -1;
+        const int n = page >= 0 ? min(kCopyRows, len - t0) : 0;
+        const int o = t0 - entry * p.list.page_size;
+        const size_t slot = static_cast<size_t>(page >= 0 ? page : 0) * p.list.page_size + o;
+        const size_t block = static_cast<size_t>(page >= 0 ? page : 0) * (p.page_div.d / p.block_div.d) + p.block_div.div(o);
+        for (uint32_t c = blockIdx.y; c < chunks; c += gridDim.y) {
+            const int v = static_cast<int>(c) * 32 + lane;
+            if (v >= vecs) continue;
+            float ks = 0.f, vs = 0.f;
+            const uint4* k_in = reinterpret_cast<const uint4*>(p.k_cache) + slot * vecs + v;
+            const uint4* v_in = reinterpret_cast<const uint4*>(p.v_cache) + slot * vecs + v;
+            uint4* k_out = p.k_copy + (static_cast<size_t>(part) * kCopyRows * vecs + v) * 2;
+            uint4* v_out = p.v_copy + (static_cast<size_t>(part) * kCopyRows * vecs + v) * 2;
+            uint4 kx = zero, vx = zero;
+            if (n > 0) {
+                kx = __ldg(k_in);
+                vx = __ldg(v_in);
+                ks = __ldg(p.k_scale + block * p.Hkv + v / (kD / 16));
+                vs = __ldg(p.v_scale + block * p.Hkv + v / (kD / 16));
             }
-            p.k_copy[dst] = k0;
-            p.k_copy[dst + 1] = k1;
-            p.v_copy[dst] = v0;
-            p.v_copy[dst + 1] = v1;
+#pragma unroll 1
+            for (int r = 0; r < kCopyRows; ++r) {
+                uint4 k_next = zero, v_next = zero;
+                if (r + 1 < n) {
+                    k_in += vecs;
+                    v_in += vecs;
+                    k_next = __ldg(k_in);
+                    v_next = __ldg(v_in);
+                }
+                uint4 lo, hi;
+                widen(kx, ks, lo, hi);
+                k_out[0] = lo;
+                k_out[1] = hi;
+                widen(vx, vs, lo, hi);
+                v_out[0] = lo;
+                v_out[1] = hi;
+                k_out += 2 * vecs;
+                v_out += 2 * vecs;
+                kx = k_next;
+                vx = v_next;
+            }
         }
     }
 }
@@ -150,14 +253,17 @@ size_t copy_bytes(int B, int max_kv_rows, int Hkv) { return copy_rows(B, max_kv_
 
 }  // namespace
 
-// K copy, V copy, then the sequences' first pages and the rows in their last.
+// K copy, V copy, the work items' order, then the sequences' first pages and the
+// rows in their last.
 size_t prefill_fp8_block_workspace(int B, int max_kv_rows, int Hkv) {
-    return 2 * copy_bytes(B, max_kv_rows, Hkv) + ((2 * static_cast<size_t>(B) + 1) * sizeof(int32_t) + 15) / 16 * 16;
+    return 2 * copy_bytes(B, max_kv_rows, Hkv) + varlen_max_pairs() * sizeof(uint32_t) +
+           ((2 * static_cast<size_t>(B) + 1) * sizeof(int32_t) + 15) / 16 * 16;
 }
 
 cudaError_t launch_prefill_fp8_block(const PrefillBlockArgs& a, cudaStream_t stream) {
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
+    if (a.B > kMaxSeqs) return cudaErrorInvalidValue;
     uint8_t* w = static_cast<uint8_t*>(a.workspace);
     Params p;
     p.k_cache = static_cast<const uint8_t*>(a.k_cache);
@@ -168,19 +274,24 @@ cudaError_t launch_prefill_fp8_block(const PrefillBlockArgs& a, cudaStream_t str
     p.seq_lens = a.seq_lens;
     p.B = a.B;
     p.Hkv = a.Hkv;
+    p.qo_indptr = a.qo_indptr;
+    p.page_div = make_divisor(a.page_size);
+    p.block_div = make_divisor(a.block_tokens);
     p.block = a.block_tokens;
+    p.q_block = 2 * (128 / (a.Hq / a.Hkv));
     p.max_rows = a.max_kv_rows;
     p.k_copy = reinterpret_cast<uint4*>(w);
     const size_t bytes = copy_bytes(a.B, a.max_kv_rows, a.Hkv);
     p.v_copy = reinterpret_cast<uint4*>(w + bytes);
-    p.start = reinterpret_cast<int32_t*>(w + 2 * bytes);
+    p.order = reinterpret_cast<uint32_t*>(w + 2 * bytes);
+    p.max_pairs = varlen_max_pairs();
+    p.pair_bits = varlen_pair_bits();
+    p.start = reinterpret_cast<int32_t*>(p.order + p.max_pairs);
     p.last = p.start + a.B + 1;
     p.status = a.dev_status;
-    fp8_block_starts_kernel<<<1, 1024, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    fp8_block_copy_kernel<<<sms * 8, kThreads, 0, stream>>>(p);
-    e = cudaGetLastError();
+    // gridDim.x: the sorting CTA and the copying ones
+    fp8_block_copy_kernel<<<dim3(1 + sms * 4, std::min((a.Hkv * (kD / 16) + 31) / 32, 64)), kThreads, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // the copy as a cache of kPage-token pages in list order
     const size_t rows = copy_rows(a.B, a.max_kv_rows);
@@ -206,6 +317,7 @@ cudaError_t launch_prefill_fp8_block(const PrefillBlockArgs& a, cudaStream_t str
     v.kv_ws = a.workspace;
     v.max_kv_rows = static_cast<int>(rows);
     v.copied = true;
+    v.order = p.order;
     return launch_prefill_varlen_tc(v, stream);
 }
 

@@ -103,6 +103,7 @@ struct Params {
     const __nv_bfloat16* v_pool;
     int page_size, pool_rows;
     int gathered;   // K/V come by TMA from a contiguous copy in page-list order
+    const uint32_t* order_in;   // the sorted pairs, kMaxOrder words (NULL: every CTA sorts them)
     // split schedule (dense only): the (item, KV tile) steps in item order
     // (batch, KV head, query block), cut into gridDim.x equal ranges
     long long sk_total;   // KV tile steps of all items
@@ -456,10 +457,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int n_items = p.n_items;
     if constexpr (kVarlen) {
+        // a launch that may start before the copy's grid has ended waits for it
+        // here (any other is not held up)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         if (warp == 0) {
             varlen_prefix(p, prefix, lane);
             __syncwarp();
-            if (prefix[p.B] / p.Hkv <= kMaxOrder) varlen_sort_pairs(p, order, bucket, lane);
+            if (p.order_in == nullptr && prefix[p.B] / p.Hkv <= kMaxOrder) varlen_sort_pairs(p, order, bucket, lane);
+        } else if (p.order_in != nullptr) {
+            for (int k = threadIdx.x - 32; k < kMaxOrder; k += kThreads - 32) order[k] = p.order_in[k];
         }
     }
     if constexpr (kSplit) {
@@ -1321,6 +1327,7 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, cudaStream_t stream) {
     p.k_pool = p.v_pool = nullptr;
     p.page_size = p.pool_rows = 0;
     p.gathered = 0;
+    p.order_in = nullptr;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     p.sec_bh = section_pairs(a, p.n_qb, p.n_items < sms ? p.n_items : sms);
@@ -1352,6 +1359,8 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, cudaStream_t stream) {
 }
 
 int varlen_max_seqs() { return kMaxVarlenSeqs; }
+int varlen_max_pairs() { return kMaxOrder; }
+int varlen_pair_bits() { return kPairQbBits; }
 
 cudaError_t launch_prefill_varlen_tc(const VarlenArgs& a, cudaStream_t stream) {
     const int G = a.Hq / a.Hkv;
@@ -1390,6 +1399,7 @@ cudaError_t launch_prefill_varlen_tc(const VarlenArgs& a, cudaStream_t stream) {
     p.k_pool = static_cast<const __nv_bfloat16*>(a.k_cache);
     p.v_pool = static_cast<const __nv_bfloat16*>(a.v_cache);
     p.gathered = a.kv_ws != nullptr;
+    p.order_in = a.order;
     p.sk_total = p.sk_per_bh = 0;
     p.sk_zero_qb = 0;
     p.sk_count = nullptr;
@@ -1423,6 +1433,19 @@ cudaError_t launch_prefill_varlen_tc(const VarlenArgs& a, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
+    if (a.copied) {   // its launch and set-up overlap the copy's end
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(sms);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<true, false>, q_map, k_map, v_map, q_map, p);
+    }
     prefill_tc_kernel<true, false><<<sms, kThreads, smem, stream>>>(q_map, k_map, v_map, q_map, p);
     return cudaGetLastError();
 }

@@ -122,8 +122,8 @@ def test_prefill_validation(L):
     import causal_gqa_flashattention_attn_gb300 as attn
     need = attn.attn_prefill_fp8_block_workspace_bytes(2, 300, 8)
     # K and V copies of 300 rows, each of 2 sequences up to a multiple of 128: ceil((300 + 2 * 127) / 128) * 128 = 640 rows;
-    # 5 page words, rounded to 16 bytes
-    assert need == 2 * 640 * 8 * 128 * 2 + 32
+    # 4096 words of order; 5 page words, rounded to 16 bytes
+    assert need == 2 * 640 * 8 * 128 * 2 + 4096 * 4 + 32
     assert attn.attn_prefill_fp8_block_workspace_bytes(2, 0, 8) == 0
     assert _prefill(L, bytes=need) == 0
     assert _prefill(L, bytes=need - 1) == -3
