@@ -9,8 +9,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -78,6 +77,10 @@ void* expect(const char* name, const at::Tensor& t, at::Device device, std::init
                       shape_text(at::IntArrayRef(shape.begin(), shape.size())) + " (-1: any), not " +
                       shape_text(t.sizes()));
     return t.data_ptr();
+}
+
+at::Tensor make_empty(at::IntArrayRef shape, at::ScalarType type, at::Device device) {
+    return at::Tensor(at::detail::empty_cuda(shape, type, device, std::nullopt));
 }
 
 int small(const char* name, int64_t n) {
@@ -214,7 +217,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
             hq = q.size(1);
             if (q.size(0) != total || q.size(2) != d)
                 throw Refused("q, k and v must have the same tokens and head dimension");
-            if (args.none(14)) made = at::empty({total, hq, d}, k.options());
+            if (args.none(14)) made = make_empty({total, hq, d}, at::ScalarType::BFloat16, device);
             qop = expect("q_out", args.none(14) ? made : args.tensor("q_out", 14), device, {total, hq, d},
                          at::ScalarType::BFloat16);
         } else if (!args.none(14)) {
@@ -299,8 +302,8 @@ PyObject* decode_fp8_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
             const size_t need = attn_decode_fp8_block_workspace_bytes(b, i, h, c.hkv, c.d);
             ws = at::zeros({static_cast<int64_t>(std::max<size_t>(need, 16))}, q.options().dtype(at::ScalarType::Byte));
         }
-        if (args.none(10)) o = at::empty(q.sizes(), q.options());
-        if (args.none(11)) lse = at::empty(q.sizes().slice(0, q.dim() - 1), q.options().dtype(at::ScalarType::Float));
+        if (args.none(10)) o = make_empty(q.sizes(), bf16, device);
+        if (args.none(11)) lse = make_empty(q.sizes().slice(0, q.dim() - 1), at::ScalarType::Float, device);
         const at::Tensor& wt = args.none(9) ? ws : args.tensor("workspace", 9);
         const at::Tensor& ot = args.none(10) ? o : args.tensor("o", 10);
         const at::Tensor& lt = args.none(11) ? lse : args.tensor("lse", 11);
@@ -342,10 +345,10 @@ PyObject* prefill_fp8_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
         at::Tensor ws, o, lse;
         if (args.none(11)) {
             const size_t need = attn_prefill_fp8_block_workspace_bytes(s.count, max_rows, c.hkv, c.d);
-            ws = at::empty({static_cast<int64_t>(std::max<size_t>(need, 16))}, q.options().dtype(at::ScalarType::Byte));
+            ws = make_empty({static_cast<int64_t>(std::max<size_t>(need, 16))}, at::ScalarType::Byte, device);
         }
-        if (args.none(12)) o = at::empty(q.sizes(), q.options());
-        if (args.none(13)) lse = at::empty({total, hq}, q.options().dtype(at::ScalarType::Float));
+        if (args.none(12)) o = make_empty(q.sizes(), bf16, device);
+        if (args.none(13)) lse = make_empty({total, hq}, at::ScalarType::Float, device);
         const at::Tensor& wt = args.none(11) ? ws : args.tensor("workspace", 11);
         void* wp = expect("workspace", wt, device, {-1}, at::ScalarType::Byte);
         void* op = expect("o", args.none(12) ? o : args.tensor("o", 12), device, {total, hq, d}, bf16);

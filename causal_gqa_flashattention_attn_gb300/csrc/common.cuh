@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -88,6 +89,20 @@ cudaError_t ctas_per_sm(K kern, int threads, size_t smem, int* occ) {
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     return e == cudaSuccess ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(occ, kern, threads, smem) : e;
+}
+
+// Runs `set` (a kernel's attributes, which last) the first time it is asked on
+// the current device.
+template <typename Set>
+cudaError_t once_per_device(std::atomic<uint64_t>& done, Set set) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+    e = set();
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 cudaError_t launch_wait_timeout_selftest(int32_t* status, uint64_t limit_ns, cudaStream_t stream);

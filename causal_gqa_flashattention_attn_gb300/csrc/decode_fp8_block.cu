@@ -555,7 +555,7 @@ __global__ void __maxnreg__(NB == 1 ? 192 : 255) decode_fp8_block_kernel(const _
         uint4 raw[NB][4];
         fetch_queries<NB>(p, b, kvh, row0, n_rows, lane, raw);
         Queries<NB> qs;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < kStages - 1; ++i) feed_tile(p, before, f, ring + i * 2 * kCodes, info + i, kvh, lane);
         int slot = 0;
         for (bool first = true; x < x_end; first = false) {
@@ -773,13 +773,20 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockArgs& a, cudaStream_t strea
     p.status = a.dev_status;
     const size_t smem = kWarps * kWarpBytes + (2 * static_cast<size_t>(a.B) + 1) * sizeof(int);
     auto kern = per == 8 ? decode_fp8_block_kernel<1> : decode_fp8_block_kernel<2>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    // both kernels with the same division of L1, so that neither waits for it to change
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decode_fp8_block_merge_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                 cudaSharedmemCarveoutMaxShared);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = once_per_device(done, [] {
+        // both kernels with the same division of L1, so that neither waits for it to change
+        cudaError_t r = cudaFuncSetAttribute(decode_fp8_block_merge_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                             cudaSharedmemCarveoutMaxShared);
+        for (auto k : {decode_fp8_block_kernel<1>, decode_fp8_block_kernel<2>}) {
+            if (r == cudaSuccess)
+                r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kWarps * kWarpBytes + (2 * kMaxSeqs + 1) * static_cast<int>(sizeof(int)));
+            if (r == cudaSuccess)
+                r = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+        }
+        return r;
+    });
     if (e != cudaSuccess) return e;
     kern<<<sms, kThreads, smem, stream>>>(p);
     e = cudaGetLastError();

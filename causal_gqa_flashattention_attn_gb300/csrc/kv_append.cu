@@ -25,8 +25,8 @@ namespace gb300 {
 namespace {
 
 constexpr int kD = 128;
-constexpr int kThreads = 256;   // of a CTA that takes tokens
-constexpr int kBatch = 3;       // rows that a lane has in flight
+constexpr int kThreads = 256;    // of a CTA that takes several tokens
+constexpr int kMostThreads = 512;
 
 struct Params {
     const __nv_bfloat16* q;   // NULL: no queries
@@ -403,9 +403,9 @@ __device__ __forceinline__ bool find_token(const Params& p, int i, int lane, int
 
 // The rows of new token i by `warps` warps, `warp` being one of them: queries,
 // keys and values, into a bf16 cache or (kFp8) as the one new token of an 8-bit
-// block.  The rows' loads are issued before the token's
-// place, which takes three loads in a row, is known.
-template <bool kInter, bool kFp8>
+// block.  The rows' loads, kBatch a lane, are issued before the token's place,
+// which takes three loads in a row, is known.
+template <bool kInter, bool kFp8, int kBatch>
 __device__ __forceinline__ void token_rows(const Params& p, int i, int warp, int warps) {
     const int lane = threadIdx.x & 31, l = lane & 7;
     const int n_q = p.q != nullptr ? p.Hq : 0;
@@ -496,12 +496,32 @@ __device__ __forceinline__ void token_rows(const Params& p, int i, int warp, int
     }
 }
 
-// CTAs of kThreads threads, warps_per_token of whose warps take a token.
-template <bool kInter, bool kFp8>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ Params p, int warps_per_token) {
-    const int warp = threadIdx.x >> 5;
-    const int i = blockIdx.x * (kThreads / 32 / warps_per_token) + warp / warps_per_token;
-    if (i < p.total_q) token_rows<kInter, kFp8>(p, i, warp % warps_per_token, warps_per_token);
+// warps_per_token of a CTA's warps take a token.  With kBatch = 1 the CTA is one
+// token's, eight threads a row: each path's code is there once, and runs once
+// (64 tokens into 8-bit blocks: 3.3-4.0 us with three rows unrolled).
+template <bool kInter, bool kFp8, int kBatch>
+__global__ void __launch_bounds__(kMostThreads) kv_append_kernel(const __grid_constant__ Params p, int warps_per_token) {
+    const int warp = threadIdx.x >> 5, tokens = (blockDim.x >> 5) / warps_per_token;
+    const int i = blockIdx.x * tokens + warp / warps_per_token;
+    if (i < p.total_q) token_rows<kInter, kFp8, kBatch>(p, i, warp % warps_per_token, warps_per_token);
+}
+
+template <bool kFp8>
+cudaError_t launch_tokens(const Params& p, bool interleaved, int sms, cudaStream_t stream) {
+    // a CTA per token while they are at most about 768 threads an SM, or two
+    // CTAs, else two warps each.  32 + 2 x 8 heads, bf16 / 8 bits: 256 tokens 3.1
+    // / 5.2 us against 3.8 / 6.2, 400 tokens 4.5 / 7.8 against 3.8 / 6.2.
+    const int rows = (p.q != nullptr ? p.Hq : 0) + 2 * p.Hkv;
+    const int threads = std::min(kMostThreads, (rows * 8 + 31) / 32 * 32);
+    if (p.total_q <= sms * std::max(2, 768 / threads)) {
+        auto kern = interleaved ? kv_append_kernel<true, kFp8, 1> : kv_append_kernel<false, kFp8, 1>;
+        kern<<<p.total_q, threads, 0, stream>>>(p, threads / 32);
+    } else {
+        constexpr int kPer = 2, kTokens = kThreads / 32 / kPer;
+        auto kern = interleaved ? kv_append_kernel<true, kFp8, 3> : kv_append_kernel<false, kFp8, 3>;
+        kern<<<(p.total_q + kTokens - 1) / kTokens, kThreads, 0, stream>>>(p, kPer);
+    }
+    return cudaGetLastError();
 }
 
 // Ragged batches into 8-bit blocks.  Every warp copies kRows rows into shared
@@ -854,16 +874,8 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
     p.n_units = 0;
     p.status = a.dev_status;
     const bool fp8 = a.k_scale != nullptr;
-    if (!fp8 || a.qo_indptr == nullptr) {
-        // all eight warps on a token while there are fewer tokens than CTAs fit at once, else two each
-        const int per = a.total_q <= 4 * sms ? 8 : 2;
-        const int tokens = kThreads / 32 / per;
-        const int grid = (a.total_q + tokens - 1) / tokens;
-        auto kern = fp8 ? (a.interleaved ? kv_append_kernel<true, true> : kv_append_kernel<false, true>)
-                        : (a.interleaved ? kv_append_kernel<true, false> : kv_append_kernel<false, false>);
-        kern<<<grid, kThreads, 0, stream>>>(p, per);
-        return cudaGetLastError();
-    }
+    if (!fp8) return launch_tokens<false>(p, a.interleaved != 0, sms, stream);
+    if (a.qo_indptr == nullptr) return launch_tokens<true>(p, a.interleaved != 0, sms, stream);
     p.n_units = a.total_q / a.block_tokens + 2 * a.B;
     const int group = a.block_tokens <= kRows ? 1 : (a.block_tokens <= 2 * kRows ? 2 : 4);
     const long long block_ctas = (static_cast<long long>(p.n_units) * 2 * a.Hkv * group + kTaskWarps - 1) / kTaskWarps;
@@ -872,7 +884,15 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
     const long long grid = block_ctas + (queries + kTaskWarps - 1) / kTaskWarps;
     if (grid >= (1LL << 31)) return cudaErrorInvalidConfiguration;
     auto kern = a.interleaved ? kv_append_blocks_kernel<true> : kv_append_blocks_kernel<false>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = once_per_device(done, [] {
+        const cudaError_t r = cudaFuncSetAttribute(kv_append_blocks_kernel<true>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                   cudaSharedmemCarveoutMaxShared);
+        return r != cudaSuccess ? r
+                                : cudaFuncSetAttribute(kv_append_blocks_kernel<false>,
+                                                       cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                       cudaSharedmemCarveoutMaxShared);
+    });
     if (e != cudaSuccess) return e;
     kern<<<static_cast<unsigned>(grid), 32 * kTaskWarps, sizeof(TaskMemory), stream>>>(p, group, static_cast<int>(block_ctas));
     return cudaGetLastError();
