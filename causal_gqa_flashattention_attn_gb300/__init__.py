@@ -609,7 +609,7 @@ def attn_kv_append_fp8_block(q, k, v, k_cache, v_cache, k_scale, v_scale, block_
 
 
 def attn_decode_fp8_block_workspace_bytes(B, q_len, Hq, Hkv, D=128):
-    """Bytes of the zeroed workspace attn_decode_paged_fp8_block takes on the current device."""
+    """Bytes of workspace attn_decode_paged_fp8_block takes on the current device."""
     return int(lib().attn_decode_fp8_block_workspace_bytes(B, q_len, Hq, Hkv, D))
 
 
@@ -620,7 +620,7 @@ def attn_decode_paged_fp8_block(q, k_cache, v_cache, k_scale, v_scale, block_tab
     ``q [B, Hq, D]`` (one query per sequence) or ``[B, q_len, Hq, D]`` bf16,
     token-major; query i of a sequence sees tokens ``t <= len - q_len + i``.
     ``workspace``: a uint8 tensor of attn_decode_fp8_block_workspace_bytes()
-    bytes, zeroed once and reusable (None allocates one).  Returns ``(o, lse,
+    bytes, scratch (None allocates one).  Returns ``(o, lse,
     workspace)``, ``lse [B, Hq]`` or ``[B, q_len, Hq]``.
     """
     return _run(stream, _native().decode_fp8_block, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, kv_indptr,

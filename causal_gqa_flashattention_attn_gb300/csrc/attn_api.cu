@@ -229,13 +229,13 @@ attn_status_t block_check(const float* k_scale, const float* v_scale, int page_s
 
 // The checks of both writers; `a` holds the arguments, a.k_scale NULL for bf16.
 attn_status_t append_impl(const AppendArgs& a, int D, void* stream) {
-    if (a.k == nullptr || a.v == nullptr || (a.q == nullptr) != (a.q_out == nullptr)) return ATTN_ERR_INVALID_ARG;
     const attn_status_t st = paged_check(a.k_cache, a.v_cache, a.block_table, a.kv_indptr, a.max_pages, a.seq_lens,
                                          a.B, a.Hq, a.Hkv, D, a.num_pages, a.page_size);
     if (st != ATTN_OK) return st;
     if (a.total_q < 0 || (a.qo_indptr == nullptr && a.total_q != a.B)) return ATTN_ERR_INVALID_ARG;
-    if (!aligned16(a.k) || !aligned16(a.v) || (a.q != nullptr && (!aligned16(a.q) || !aligned16(a.q_out))))
+    if (a.total_q > 0 && (a.k == nullptr || a.v == nullptr || (a.q == nullptr) != (a.q_out == nullptr)))
         return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(a.k) || !aligned16(a.v) || !aligned16(a.q) || !aligned16(a.q_out)) return ATTN_ERR_INVALID_ARG;
     if (a.k_stride % 8 != 0 || a.v_stride % 8 != 0 || a.k_stride < static_cast<long long>(a.Hkv) * D ||
         a.v_stride < static_cast<long long>(a.Hkv) * D)
         return ATTN_ERR_INVALID_ARG;
@@ -246,8 +246,11 @@ attn_status_t append_impl(const AppendArgs& a, int D, void* stream) {
     if (a.rot_dim > 0 && (a.cos_sin == nullptr || a.max_pos <= 0 || !aligned16(a.cos_sin))) return ATTN_ERR_INVALID_ARG;
     if (a.rot_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
     if (static_cast<long long>(a.Hq) + 2LL * a.Hkv >= (1LL << 24)) return ATTN_ERR_UNSUPPORTED;
-    // one CTA per token and, for a block-scaled cache, per block
-    if (static_cast<long long>(a.total_q) + a.total_q / 16 + 2LL * a.B >= (1LL << 31)) return ATTN_ERR_UNSUPPORTED;
+    // CTAs: at most one per token, per 8 tokens' 16 heads of queries, and per
+    // block's head of keys or values
+    const long long ctas = static_cast<long long>(a.total_q) + (a.total_q / 8 + 1LL) * (a.Hq / 16 + 1LL) +
+                           (a.total_q / 16 + 2LL * a.B) * 2 * a.Hkv;
+    if (ctas >= (1LL << 31)) return ATTN_ERR_UNSUPPORTED;
     if (a.total_q == 0) return ATTN_OK;
     return from_cuda(launch_kv_append(a, static_cast<cudaStream_t>(stream)));
 }
@@ -652,7 +655,7 @@ attn_status_t attn_prefill_paged_fp8_block(const void* q, const void* k_cache, c
                                            int Hkv, int D, int num_pages, int page_size, int block_tokens,
                                            int max_kv_rows, float scale, void* workspace, size_t workspace_bytes,
                                            void* o, float* lse, int32_t* dev_status, void* stream) {
-    if (q == nullptr || o == nullptr || qo_indptr == nullptr || total_q < 0 || max_kv_rows <= 0)
+    if (qo_indptr == nullptr || total_q < 0 || max_kv_rows <= 0 || (total_q > 0 && (q == nullptr || o == nullptr)))
         return ATTN_ERR_INVALID_ARG;
     attn_status_t st = paged_check(k_cache, v_cache, block_table, kv_indptr, max_pages_per_seq, seq_lens, B, Hq, Hkv,
                                    D, num_pages, page_size);

@@ -10,7 +10,6 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
-#include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -145,6 +144,15 @@ int32_t* optional_int(const Args& args, const char* name, int i, int64_t count, 
     return static_cast<int32_t*>(expect(name, args.tensor(name, i), device, {count}, at::ScalarType::Int));
 }
 
+// The device's status word: any int32 tensor's first element.
+int32_t* status_word(const Args& args, int i, at::Device device) {
+    if (args.none(i)) return nullptr;
+    const at::Tensor& t = args.tensor("dev_status", i);
+    if (t.device() != device || t.scalar_type() != at::ScalarType::Int || t.numel() < 1 || !t.is_contiguous())
+        throw Refused("dev_status must be a contiguous int32 tensor on " + device.str());
+    return static_cast<int32_t*>(t.data_ptr());
+}
+
 // Rows of bf16 heads: dense within a token, any distance from token to token.
 void* token_rows(const char* name, const at::Tensor& x, at::Device device, long long& stride) {
     if (x.device() != device || x.scalar_type() != at::ScalarType::BFloat16 || x.dim() != 3)
@@ -234,7 +242,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         const int32_t* qo = optional_int(args, "qo_indptr", 10, s.count + 1, device);
         const int32_t* pos = optional_int(args, "positions", 12, total, device);
-        int32_t* status = optional_int(args, "dev_status", 15, 1, device);
+        int32_t* status = status_word(args, 15, device);
         const int t = small("k", total), h = small("q", hq), hk = small("k", hkv), dd = small("k", d);
         const int mp = small("cos_sin", max_pos), r = small("cos_sin", rot);
         if (args.none(5)) {
@@ -300,7 +308,7 @@ PyObject* decode_fp8_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
         at::Tensor ws, o, lse;
         if (args.none(9)) {
             const size_t need = attn_decode_fp8_block_workspace_bytes(b, i, h, c.hkv, c.d);
-            ws = at::zeros({static_cast<int64_t>(std::max<size_t>(need, 16))}, q.options().dtype(at::ScalarType::Byte));
+            ws = make_empty({static_cast<int64_t>(std::max<size_t>(need, 16))}, at::ScalarType::Byte, device);
         }
         if (args.none(10)) o = make_empty(q.sizes(), bf16, device);
         if (args.none(11)) lse = make_empty(q.sizes().slice(0, q.dim() - 1), at::ScalarType::Float, device);
@@ -315,7 +323,7 @@ PyObject* decode_fp8_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
               attn_decode_paged_fp8_block(qp, c.k, c.v, c.k_scale, c.v_scale, s.table, s.indptr, s.width, s.lens, b, i, h,
                                           c.hkv, c.d, c.pages, c.page_size, c.block, scale_or_default(args, 8, c.d), wp,
                                           static_cast<size_t>(wt.numel()), op, lp,
-                                          optional_int(args, "dev_status", 12, 1, device), stream_of(device)));
+                                          status_word(args, 12, device), stream_of(device)));
         return three(wrap_or(args, 10, o), wrap_or(args, 11, lse), wrap_or(args, 9, ws));
     });
 }
@@ -359,7 +367,7 @@ PyObject* prefill_fp8_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                            s.count, small("q", total), small("q", hq), c.hkv, c.d, c.pages, c.page_size,
                                            c.block, max_rows, scale_or_default(args, 10, c.d), wp,
                                            static_cast<size_t>(wt.numel()), op, lp,
-                                           optional_int(args, "dev_status", 14, 1, device), stream_of(device)));
+                                           status_word(args, 14, device), stream_of(device)));
         return three(wrap_or(args, 12, o), wrap_or(args, 13, lse), wrap_or(args, 11, ws));
     });
 }

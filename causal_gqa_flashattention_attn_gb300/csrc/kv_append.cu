@@ -44,6 +44,7 @@ struct Params {
     float* k_scale;   // NULL: bf16 cache
     float* v_scale;
     int max_pos, rot, B, total_q, Hq, Hkv, block;
+    bool wide;   // every row starts on 32 bytes
     Divisor page_div, block_div;
     int n_units;   // ragged batches into 8-bit blocks: blocks of tokens, and spare ones
     int32_t* status;
@@ -106,6 +107,32 @@ __device__ __forceinline__ int first_chunk(const Params& p, int l) {
 template <bool kInter>
 __device__ __forceinline__ int second_chunk(const Params& p, int l) {
     return !kInter && l < (p.rot >> 4) ? l + (p.rot >> 4) : 2 * l + 1;
+}
+
+// A lane's two chunks of a row.  Where they lie side by side (pairs of
+// neighbours) and rows start on 32 bytes (p.wide), one access takes them: two
+// would each touch half of every 32-byte sector.
+template <bool kInter>
+__device__ __forceinline__ void load_chunks(const Params& p, const uint4* row, int c0, int c1, uint4& x, uint4& y) {
+    if (kInter && p.wide) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w), "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                     : "l"(row + c0));
+    } else {
+        x = row[c0];
+        y = row[c1];
+    }
+}
+template <bool kInter>
+__device__ __forceinline__ void store_chunks(const Params& p, uint4* row, int c0, int c1, uint4 x, uint4 y) {
+    if (kInter && p.wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + c0), "r"(x.x), "r"(x.y),
+                     "r"(x.z), "r"(x.w), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                     : "memory");
+    } else {
+        row[c0] = x;
+        row[c1] = y;
+    }
 }
 
 // Two chunks of eight bf16 <-> eight pairs: neighbour by neighbour, or chunk by chunk.
@@ -191,6 +218,10 @@ __device__ __forceinline__ float old_scale_of(float s) {
     const int e = static_cast<int>(u >> 23) - 127 + ((u & 0x7FFFFFu) != 0u ? 1 : 0);
     return pow2(e < -126 ? -126 : (e > 126 ? 126 : e));
 }
+
+// Values below this make fp32's products subnormal; a block whose largest one is
+// there has its rotated codes computed from scaled inputs.
+constexpr float kTiny = 7.8886090522101181e-31f;   // 2^-100
 
 // 1 / s for s = 0 (0) or a power of two from 2^-126 to 2^126.
 __device__ __forceinline__ float inverse_of(float s) {
@@ -317,7 +348,8 @@ __device__ __noinline__ uint4 codes_again(const Params& p, const Source r, float
 // A lane's sixteen values over the scale to codes: z holds the values (fp32's
 // of rotated ones), inv = 1 / scale.
 template <bool kInter>
-__device__ __forceinline__ void store_codes(const Params& p, Pairs& z, float inv, const Source& r, uint8_t* row, int l) {
+__device__ __forceinline__ void store_codes(const Params& p, Pairs& z, float inv, bool tiny, const Source& r, uint8_t* row,
+                                            int l) {
     const Two inv2{inv, inv};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -342,7 +374,7 @@ __device__ __forceinline__ void store_codes(const Params& p, Pairs& z, float inv
 #pragma unroll
             for (int i = 0; i < 4; ++i) near |= low(z.a[i].x) | low(z.a[i].y) | low(z.b[i].x) | low(z.b[i].y);
         }
-        if (near || none.x != 0.f || none.y != 0.f) codes = codes_again<kInter>(p, r, inv, l);
+        if (near || tiny || none.x != 0.f || none.y != 0.f) codes = codes_again<kInter>(p, r, inv, l);
     }
     reinterpret_cast<uint2*>(row)[r.c0] = make_uint2(codes.x, codes.y);
     reinterpret_cast<uint2*>(row)[r.c1] = make_uint2(codes.z, codes.w);
@@ -429,9 +461,7 @@ __device__ __forceinline__ void token_rows(const Params& p, int i, int warp, int
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
             if (r0 + k * step < n) {
-                const uint4* src = source(r0 + k * step);
-                x[k] = src[c0];
-                y[k] = src[c1];
+                load_chunks<kInter>(p, source(r0 + k * step), c0, c1, x[k], y[k]);
             }
         if (first) {
             if (!find_token(p, i, lane, b, t, pos)) return;
@@ -462,8 +492,7 @@ __device__ __forceinline__ void token_rows(const Params& p, int i, int warp, int
                     dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(key ? p.k_cache : p.v_cache) +
                                                    (static_cast<size_t>(slot) * p.Hkv + h) * kD);
                 }
-                dst[c0] = x[k];
-                dst[c1] = y[k];
+                store_chunks<kInter>(p, dst, c0, c1, x[k], y[k]);
             } else if (slot >= 0) {
                 // one new row of a block: eight lanes settle its scale
                 const unsigned eight = 0xFFu << (lane & 24);
@@ -490,7 +519,7 @@ __device__ __forceinline__ void token_rows(const Params& p, int i, int warp, int
                 if (l == 0 && !(there > 0 && now == was)) *scale = now;
                 if (ratio != 1.f)
                     for (int j = 1; j <= there; ++j) rescale_row(row - static_cast<size_t>(j) * p.Hkv * kD, ratio, l);
-                store_codes<kInter>(p, z, inverse_of(now), src, row, l);
+                store_codes<kInter>(p, z, inverse_of(now), top < kTiny, src, row, l);
             }
         }
     }
@@ -498,7 +527,7 @@ __device__ __forceinline__ void token_rows(const Params& p, int i, int warp, int
 
 // warps_per_token of a CTA's warps take a token.  With kBatch = 1 the CTA is one
 // token's, eight threads a row: each path's code is there once, and runs once
-// (64 tokens into 8-bit blocks: 3.3-4.0 us with three rows unrolled).
+// (64 tokens into 8-bit blocks 3.3 us; 3.5-4.1 with three rows unrolled).
 template <bool kInter, bool kFp8, int kBatch>
 __global__ void __launch_bounds__(kMostThreads) kv_append_kernel(const __grid_constant__ Params p, int warps_per_token) {
     const int warp = threadIdx.x >> 5, tokens = (blockDim.x >> 5) / warps_per_token;
@@ -518,7 +547,7 @@ cudaError_t launch_tokens(const Params& p, bool interleaved, int sms, cudaStream
         kern<<<p.total_q, threads, 0, stream>>>(p, threads / 32);
     } else {
         constexpr int kPer = 2, kTokens = kThreads / 32 / kPer;
-        auto kern = interleaved ? kv_append_kernel<true, kFp8, 3> : kv_append_kernel<false, kFp8, 3>;
+        auto kern = interleaved ? kv_append_kernel<true, kFp8, 2> : kv_append_kernel<false, kFp8, 2>;
         kern<<<(p.total_q + kTokens - 1) / kTokens, kThreads, 0, stream>>>(p, kPer);
     }
     return cudaGetLastError();
@@ -673,8 +702,7 @@ __device__ __forceinline__ void query_task(const Params& p, int tile, int h0, ui
                 rotate(z, t[k]);
                 pack<kInter>(z, x, y, pack2);
             }
-            dst[c0] = x;
-            dst[c1] = y;
+            store_chunks<kInter>(p, dst, c0, c1, x, y);
         }
     }
 }
@@ -809,8 +837,14 @@ __device__ __forceinline__ void block_task(const Params& p, int u, int pair, Tas
             int pos;
             if (!is_there(t0 + r, pos)) continue;
             uint2* row = reinterpret_cast<uint2*>(cells + (t0 + r - j0) * row_bytes);
-            row[c0] = codes_of(buf[r * 16 + c0], inv);
-            row[c1] = codes_of(buf[r * 16 + c1], inv);
+            uint2 x = codes_of(buf[r * 16 + c0], inv), y = codes_of(buf[r * 16 + c1], inv);
+            if (turns && top < kTiny) {   // 16 bits rounded to odd do not hold such values' last bits
+                const uint4 codes = codes_again<kInter>(p, Source{source(t0 + r), c0, c1, pos}, inv, l);
+                x = make_uint2(codes.x, codes.y);
+                y = make_uint2(codes.z, codes.w);
+            }
+            row[c0] = x;
+            row[c1] = y;
         }
         __syncwarp();
     }
@@ -862,6 +896,10 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
     p.v_cache = a.v_cache;
     p.k_scale = a.k_scale;
     p.v_scale = a.v_scale;
+    const uintptr_t starts = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.q_out) |
+                             reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+                             reinterpret_cast<uintptr_t>(a.k_cache) | reinterpret_cast<uintptr_t>(a.v_cache);
+    p.wide = ((starts | static_cast<uintptr_t>(2 * (a.q_stride | a.k_stride | a.v_stride))) & 31u) == 0;
     p.max_pos = a.max_pos;
     p.rot = a.rot_dim;
     p.B = a.B;

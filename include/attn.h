@@ -515,9 +515,9 @@ attn_status_t attn_kv_append(const void* q, const void* k, const void* v,
  * but for codes that become e4m3 subnormals; a stored scale that is no power
  * of two counts as the next one above).  New codes are value / scale rounded
  * once, to nearest even, keys after their rotation: a value next to a border
- * between two codes falls on the side that 64-bit arithmetic gives.  A NaN is
- * stored as NaN and an infinity as the block's largest code; neither counts for
- * the scale.  A block whose first new token is its first token starts afresh.
+ * between two codes falls on the side that exact arithmetic gives.  A NaN is
+ * stored as NaN and an infinity as the largest code (NaN where the scale is 0);
+ * neither counts for the scale.  A block whose first new token is its first token starts afresh.
  *
  *   k_cache, v_cache  uint8 [num_pages, page_size, Hkv, D], e4m3 bytes (written)
  *   k_scale, v_scale  float32 [num_pages, page_size / block_tokens, Hkv]
@@ -553,10 +553,9 @@ attn_status_t attn_kv_append_fp8_block(const void* q, const void* k, const void*
  *                not negative; any such scale is taken, not only powers of two.
  *   seq_lens     int32 [B] (read)
  *   workspace    >= attn_decode_fp8_block_workspace_bytes() bytes, 16-byte
- *                aligned (the current device's share count goes into it).
- *                Zero it once; every call that completes leaves it ready for
- *                the next.  Calls that may run at the same time need separate
- *                workspaces.
+ *                aligned: scratch for the pieces, nothing in it outlasts a
+ *                call.  (The size goes by the current device's SM count.)
+ *                Calls that may run at the same time need separate workspaces.
  *   o            as q (written); lse float32 [B, q_len, Hq], natural log
  *                (written; may be NULL)
  *   D = 128, q_len 1..16, any Hq % Hkv == 0, B <= 4096; with a block table

@@ -159,7 +159,7 @@ def test_decode_same_bits_again_and_workspace_reuse():
     big, small = Cache([9000, 50, 3000], 4, 64, 64, rng), Cache([40, 2000], 4, 16, 16, rng, csr=True)
     qb, qs = bc.bf16(rng.standard_normal((3, 16, D))).to(dev), bc.bf16(rng.standard_normal((2, 4, 16, D))).to(dev)
     need = max(attn.attn_decode_fp8_block_workspace_bytes(3, 1, 16, 4), attn.attn_decode_fp8_block_workspace_bytes(2, 4, 16, 4))
-    ws = torch.zeros(need, dtype=torch.uint8, device=dev)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=dev)   # scratch: whatever it holds (NaN here)
     first = decode(attn, qb, big, dev, workspace=ws)
     decode(attn, qs, small, dev, workspace=ws)
     again = decode(attn, qb, big, dev, workspace=ws)
@@ -316,6 +316,63 @@ def test_prefill_flags():
     assert call([100, 40], 139)[2] == attn.ATTN_DEV_SEQ_TOO_LONG
     assert call([100, 49], 149)[2] == attn.ATTN_DEV_SEQ_TOO_LONG
     assert call([100, 48], 148)[2] == 0
+
+
+@pytest.mark.parametrize("n,new,hq", [(2048, 1, 4), (900, 18, 64)])
+def test_prefill_many_sequences(n, new, hq):
+    """The most sequences a batch may have, and more work items than are sorted (5 query blocks of 4 positions each)."""
+    dev = gpu_or_skip()
+    import causal_gqa_flashattention_attn_gb300 as attn
+    rng = np.random.default_rng(n)
+    lens = rng.integers(new, new + 20, n).tolist()
+    cache = Cache(lens, 1, 16, 16, rng)
+    q = bc.bf16(rng.standard_normal((n * new, hq, D)))
+    pages, _ = cache.lists.tensors(dev)
+    ptr = torch.arange(n + 1, dtype=torch.int32, device=dev) * new
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    o, lse, _ = attn.attn_prefill_paged_fp8_block(q.to(dev), *cache.device(dev), ptr, pages,
+                                                  torch.tensor(lens, dtype=torch.int32, device=dev), max_kv_rows=sum(lens),
+                                                  dev_status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0 and bool(torch.isfinite(o.float()).all()) and bool(torch.isfinite(lse).all())
+    for b in [0, 1, n // 2, n - 2, n - 1] + rng.integers(0, n, 8).tolist():
+        rows = slice(b * new, (b + 1) * new)
+        bc.check_attention(o[rows], lse[rows], bc.attend(q[rows].double().numpy(), *cache.values(b), weight_step=2.0 ** -8, small=0.0))
+
+
+def test_calls_on_two_streams_at_once():
+    """Decodes and prefills of two batches on two streams, each with its own workspace, give what they give alone."""
+    dev = gpu_or_skip()
+    import causal_gqa_flashattention_attn_gb300 as attn
+    rng = np.random.default_rng(14)
+    jobs = []
+    for lens in ([3000, 700, 40], [100, 5000]):
+        cache = Cache(lens, 2, 64, 32, rng)
+        n = len(lens)
+        pages, _ = cache.lists.tensors(dev)
+        d = dict(q=bc.bf16(rng.standard_normal((n, 3, 8, D))).to(dev), cache=cache.device(dev), pages=pages,
+                 lens=torch.tensor(lens, dtype=torch.int32, device=dev),
+                 ptr=torch.arange(n + 1, dtype=torch.int32, device=dev) * 3, stream=torch.cuda.Stream(dev))
+        d["ws"] = torch.empty(attn.attn_decode_fp8_block_workspace_bytes(n, 3, 8, 2), dtype=torch.uint8, device=dev)
+        d["pws"] = torch.empty(attn.attn_prefill_fp8_block_workspace_bytes(n, sum(lens), 2), dtype=torch.uint8, device=dev)
+        d["rows"] = sum(lens)
+        jobs.append(d)
+
+    def run(d, stream):
+        o, lse, _ = attn.attn_decode_paged_fp8_block(d["q"], *d["cache"], d["pages"], d["lens"], workspace=d["ws"], stream=stream)
+        po, plse, _ = attn.attn_prefill_paged_fp8_block(d["q"].view(-1, 8, D), *d["cache"], d["ptr"], d["pages"], d["lens"],
+                                                        max_kv_rows=d["rows"], workspace=d["pws"], stream=stream)
+        return o, lse, po, plse
+
+    alone = []
+    for d in jobs:
+        alone.append(run(d, None))
+        torch.cuda.synchronize()
+    for _ in range(5):
+        got = [run(d, d["stream"]) for d in jobs]
+        torch.cuda.synchronize()
+        for a, g in zip(alone, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, g))
 
 
 def test_prefill_nan_stays_in_its_sequence():

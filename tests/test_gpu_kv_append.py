@@ -110,6 +110,84 @@ def test_append_bf16(old, new, hq, hkv, page, rot, inter, csr, one):
     assert np.array_equal(v_cache.float().cpu().numpy(), want["v"].astype(np.float32))   # copied, the rest untouched
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("n,hq,hkv,ragged", [(3, 4, 1, False), (400, 8, 2, False), (700, 2, 1, False), (40, 8, 2, True),
+                                             (9, 72, 3, False)])
+def test_append_dense_rows(n, hq, hkv, ragged, inter):
+    """Rows that start on 32 bytes, from a few tokens to more than get a CTA each, more heads than a CTA has rows; both caches."""
+    dev = gpu_or_skip()
+    import causal_gqa_flashattention_attn_gb300 as attn
+    rng = np.random.default_rng(n + hq)
+    page = block = 16
+    old = rng.integers(0, 14, n).tolist()
+    new = rng.integers(0, 5, n).tolist() if ragged else [1] * n
+    new = [min(a, 16 - o) for a, o in zip(new, old)]
+    batch = Batch(old, new, hq, hkv, rng)
+    lists = bc.Lists([16] * n, page, rng)
+    pages, _ = lists.tensors(dev)
+    table = bc.rope_table(16, 96)
+    cs = torch.from_numpy(table).to(dev)
+    q, k, v = (x.contiguous().to(dev) for x in (batch.q, batch.k, batch.v))
+    t = batch.indices()
+    turned_q, turned_k = (bc.rotate(x.double().numpy(), table, t, inter) for x in (batch.q, batch.k))
+    slack = [bc.rotate_slack(x.double().numpy(), table, t, inter) for x in (batch.q, batch.k)]
+    shape = (lists.num_pages, page, hkv, D)
+    ptr = batch.indptr(dev) if ragged else None
+    caches = [torch.zeros(shape, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    out = attn.attn_kv_append(q, k, v, *caches, pages, batch.lens(dev), cos_sin=cs, qo_indptr=ptr, interleaved=inter)
+    codes = [np.full(shape, 0x38, np.uint8) for _ in range(2)]
+    scales = [np.full((lists.num_pages, 1, hkv), 2.0 ** -8, np.float32) for _ in range(2)]
+    dc = [torch.from_numpy(x.copy()).to(dev) for x in codes]
+    ds = [torch.from_numpy(x.copy()).to(dev) for x in scales]
+    out8 = attn.attn_kv_append_fp8_block(q, k, v, *dc, *ds, pages, batch.lens(dev), cos_sin=cs, qo_indptr=ptr,
+                                         interleaved=inter)
+    torch.cuda.synchronize()
+    check_bf16(out, turned_q, slack[0])
+    assert torch.equal(out, out8)
+    rows = torch.tensor([lists.rows[b][0] for b in range(n) for _ in range(new[b])], device=dev).long()
+    at = torch.from_numpy(t).to(dev)
+    check_bf16(caches[0][rows, at], turned_k, slack[1])
+    assert torch.equal(caches[1][rows, at], v)
+    for b in range(n):
+        if new[b]:
+            bc.append_blocks(codes[0], scales[0], lists, block, b, old[b], turned_k[batch.rows(b)])
+            bc.append_blocks(codes[1], scales[1], lists, block, b, old[b], batch.v[batch.rows(b)].double().numpy())
+    for w in range(2):
+        assert np.array_equal(ds[w].cpu().numpy(), scales[w])
+        assert np.array_equal(dc[w].cpu().numpy(), codes[w])
+
+
+@pytest.mark.parametrize("size", [2.0 ** -133, 2.0 ** -126, 2.0 ** -118, 2.0 ** -101, 2.0 ** 126])
+def test_append_fp8_block_rotated_far_from_one(size):
+    """Keys at the ends of bf16's range, where fp32's products are subnormal or overflow: codes as from exact rotations."""
+    dev = gpu_or_skip()
+    import causal_gqa_flashattention_attn_gb300 as attn
+    rng = np.random.default_rng(17)
+    table = bc.rope_table(40, 64)
+    cs = torch.from_numpy(table).to(dev)
+    for new, ragged in (([1, 1, 1], False), ([20, 3, 33], True)):
+        batch = Batch([0, 0, 0], new, 1, 2, rng, scale=size)
+        batch.k[:, :, 5] = 0.0
+        lists = bc.Lists([64] * 3, 64, rng)
+        pages, _ = lists.tensors(dev)
+        shape, blocks = (lists.num_pages, 64, 2, D), (lists.num_pages, 2, 2)
+        codes, scales = [np.zeros(shape, np.uint8) for _ in range(2)], [np.zeros(blocks, np.float32) for _ in range(2)]
+        dc = [torch.from_numpy(x.copy()).to(dev) for x in codes]
+        ds = [torch.from_numpy(x.copy()).to(dev) for x in scales]
+        k, v = batch.k.contiguous(), batch.v.contiguous()
+        attn.attn_kv_append_fp8_block(None, k.to(dev), v.to(dev), *dc, *ds, pages, batch.lens(dev), cos_sin=cs,
+                                      qo_indptr=batch.indptr(dev) if ragged else None)
+        torch.cuda.synchronize()
+        turned = bc.rotate(k.double().numpy(), table, batch.indices(), False)
+        for b in range(3):
+            bc.append_blocks(codes[0], scales[0], lists, 32, b, 0, turned[batch.rows(b)])
+            bc.append_blocks(codes[1], scales[1], lists, 32, b, 0, v[batch.rows(b)].double().numpy())
+        for w in range(2):
+            assert np.array_equal(ds[w].cpu().numpy(), scales[w])
+            got = dc[w].cpu().numpy()
+            assert np.array_equal(bc.E4M3[got], bc.E4M3[codes[w]]), (new, "kv"[w])
+
+
 def test_append_positions_in_place_padding_and_keys_only():
     """Positions of the caller's, q rotated in place, padded entries of length 0 and rows of no sequence left alone, no q."""
     dev = gpu_or_skip()
@@ -361,7 +439,7 @@ def test_binding_refuses_wrong_tensors():
         append("invalid", attn.AttnError, fp8=fp8, cos_sin=torch.zeros(9, 144, device=dev))
         append("invalid", attn.AttnError, fp8=fp8, k=k[:1].expand(2, 2, D))
         append("invalid", attn.AttnError, fp8=fp8, k=torch.zeros(2 * 2 * D + 4, dtype=torch.bfloat16, device=dev)[4:].view(2, 2, D))
-        append("dev_status", fp8=fp8, dev_status=lens)
+        append("dev_status", fp8=fp8, dev_status=lens.long())
     append("k_cache", k_cache=cb)
     append("v_cache", v_cache=c8[:2])
     append("contiguous", k_cache=c8.transpose(1, 2).contiguous().transpose(1, 2))

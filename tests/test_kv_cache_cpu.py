@@ -37,12 +37,13 @@ def _append(L, fp8, **kw):
 @pytest.mark.parametrize("fp8", [False, True])
 def test_append_validation(L, fp8):
     assert _append(L, fp8) == 0                              # no new tokens: nothing to do
+    assert _append(L, fp8, q=None, k=None, v=None, qout=None) == 0
     for name in ("k", "v", "kc", "vc", "table", "lens"):
-        assert _append(L, fp8, **{name: None}) == -1, name
+        assert _append(L, fp8, T=2, **{name: None}) == -1, name
     for name in ("q", "k", "v", "kc", "vc", "cs", "qout"):
         assert _append(L, fp8, **{name: ODD}) == -1, name    # misaligned
-    assert _append(L, fp8, q=None) == -1                     # q_out without q
-    assert _append(L, fp8, qout=None) == -1
+    assert _append(L, fp8, T=2, q=None) == -1                # q_out without q
+    assert _append(L, fp8, T=2, qout=None) == -1
     assert _append(L, fp8, q=None, qout=None) == 0
     assert _append(L, fp8, qs=4100) == -1                    # rows that are not 16-byte aligned
     assert _append(L, fp8, ks=1016) == -1                    # rows that overlap
@@ -130,7 +131,8 @@ def test_prefill_validation(L):
     assert _prefill(L, ws=None) == -3
     assert _prefill(L, ws=ODD) == -3
     for name in ("q", "k", "v", "ks", "vs", "qo", "table", "lens", "o"):
-        assert _prefill(L, **{name: None}) == -1, name
+        assert _prefill(L, T=2, **{name: None}) == -1, name
+    assert _prefill(L, q=None, o=None) == 0
     for name in ("q", "k", "v", "o"):
         assert _prefill(L, **{name: ODD}) == -1, name
     assert _prefill(L, T=-1) == -1
