@@ -638,8 +638,8 @@ def attn_prefill_paged_fp8_block(q, k_cache, v_cache, k_scale, v_scale, qo_indpt
     """Ragged causal prefill over the cache that :func:`attn_kv_append_fp8_block`
     writes: ``q [total_q, Hq, D]`` bf16, rows ``qo_indptr[b]`` up to
     ``qo_indptr[b+1]`` being the last positions of sequence b's ``seq_lens[b]``
-    cached tokens.  ``max_kv_rows``: at least the sum of ``seq_lens`` (by
-    default the pool's row count, which holds it unless sequences share pages).
+    cached tokens.  ``max_kv_rows``: at least the sum of ``seq_lens``, which
+    sizes the workspace (by default all that the page lists can hold).
     ``workspace``: a uint8 tensor of attn_prefill_fp8_block_workspace_bytes()
     bytes.  Returns ``(o [total_q, Hq, D], lse [total_q, Hq], workspace)``.
     """

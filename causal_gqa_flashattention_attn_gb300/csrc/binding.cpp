@@ -262,7 +262,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                            s.indptr, s.width, qop, c.k, c.v, c.k_scale, c.v_scale, s.count, t, h, hk, dd,
                                            c.pages, c.page_size, c.block, status, stream_of(device)));
         }
-        if (qp == nullptr) Py_RETURN_NONE;
+        if (args.none(0)) Py_RETURN_NONE;
         return wrap_or(args, 14, made);
     });
 }
@@ -344,7 +344,9 @@ PyObject* prefill_fp8_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor& qo = args.tensor("qo_indptr", 5);
         const int32_t* qop = static_cast<const int32_t*>(
             expect("qo_indptr", qo, device, {static_cast<int64_t>(s.count) + 1}, at::ScalarType::Int));
-        long long rows = static_cast<long long>(c.pages) * c.page_size;
+        // by default all that the page lists hold: sequences that share pages may have more rows than the pool
+        long long rows = (s.indptr != nullptr ? args.tensor("block_table", 6).numel()
+                                              : static_cast<long long>(s.count) * s.width) * c.page_size;
         if (!args.none(9)) {
             rows = PyLong_AsLongLong(args.a[9]);
             if (rows == -1 && PyErr_Occurred()) throw 0;

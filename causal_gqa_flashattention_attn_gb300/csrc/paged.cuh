@@ -18,9 +18,9 @@ struct PageList {
     int num_pages, page_size;
 };
 
-// Entries of sequence b's list.
+// Entries of sequence b's list (none where the CSR offsets fall).
 __device__ __forceinline__ int page_count(const PageList& l, int b) {
-    return l.indptr != nullptr ? l.indptr[b + 1] - l.indptr[b] : l.max_pages;
+    return l.indptr != nullptr ? max(l.indptr[b + 1] - l.indptr[b], 0) : l.max_pages;
 }
 
 // The pool page in entry e >= 0 of sequence b's list of n entries, or -1 (and

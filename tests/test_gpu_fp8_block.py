@@ -104,6 +104,25 @@ def test_decode(lens, nq, hq, hkv, page, block, csr, scales):
     bc.check_attention(o, lse, reference(q.double().numpy(), cache))
 
 
+def test_decode_csr_offsets_that_fall():
+    """A sequence whose CSR offsets fall has an empty list: flagged, nothing of it read, the others as they are."""
+    dev = gpu_or_skip()
+    import causal_gqa_flashattention_attn_gb300 as attn
+    rng = np.random.default_rng(23)
+    cache = Cache([40, 70, 33], 2, 16, 16, rng, csr=True)     # lists of 3, 5 and 3 pages
+    pages, _ = cache.lists.tensors(dev)
+    indptr = torch.tensor([3, 8, 8, 0], dtype=torch.int32, device=dev)   # the second list, none, falling
+    lens = torch.tensor([70, 5, 5], dtype=torch.int32, device=dev)
+    q = bc.bf16(rng.standard_normal((3, 1, 4, D)))
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    o, lse, _ = attn.attn_decode_paged_fp8_block(q.to(dev), *cache.device(dev), pages, lens, kv_indptr=indptr, dev_status=status)
+    torch.cuda.synchronize()
+    assert status.item() == attn.ATTN_DEV_SEQ_TOO_LONG
+    ref = bc.attend(q[0].double().numpy(), *cache.values(1))
+    bc.check_attention(o[:1], lse[:1], tuple(x[None] for x in ref))
+    assert not o[1:].any() and torch.isneginf(lse[1:]).all()
+
+
 @pytest.mark.parametrize("size", [2.0 ** -120, 2.0 ** -20, 2.0 ** 20, 2.0 ** 100])
 def test_decode_queries_of_any_size(size):
     """q beyond fp16's range on either side, with a scale that brings the scores back."""
@@ -316,6 +335,34 @@ def test_prefill_flags():
     assert call([100, 40], 139)[2] == attn.ATTN_DEV_SEQ_TOO_LONG
     assert call([100, 49], 149)[2] == attn.ATTN_DEV_SEQ_TOO_LONG
     assert call([100, 48], 148)[2] == 0
+
+
+def test_shared_pages():
+    """Sequences that read the same pages: together more tokens than the pool has, with the default workspace."""
+    dev = gpu_or_skip()
+    import causal_gqa_flashattention_attn_gb300 as attn
+    rng = np.random.default_rng(21)
+    cache = Cache([250], 2, 64, 32, rng)
+    lens, new = [250, 180, 250, 9, 200], [250, 20, 3, 9, 1]
+    table = torch.from_numpy(np.tile(cache.lists.rows[0], (5, 1))).to(dev)
+    seq = torch.tensor(lens, dtype=torch.int32, device=dev)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    k, v = cache.values(0)
+    q = bc.bf16(rng.standard_normal((sum(new), 4, D)))
+    at = np.cumsum([0] + new)
+    ptr = torch.tensor(at, dtype=torch.int32, device=dev)
+    o, lse, _ = attn.attn_prefill_paged_fp8_block(q.to(dev), *cache.device(dev), ptr, table, seq, dev_status=status)
+    torch.cuda.synchronize()
+    parts = [bc.attend(q[at[b]:at[b + 1]].double().numpy(), k[:lens[b]], v[:lens[b]], weight_step=2.0 ** -8, small=0.0)
+             for b in range(5)]
+    assert status.item() == 0
+    bc.check_attention(o, lse, [np.concatenate([p[i] for p in parts]) for i in range(4)])
+    q = bc.bf16(rng.standard_normal((5, 1, 4, D)))
+    o, lse, _ = attn.attn_decode_paged_fp8_block(q.to(dev), *cache.device(dev), table, seq, dev_status=status)
+    torch.cuda.synchronize()
+    parts = [bc.attend(q[b].double().numpy(), k[:lens[b]], v[:lens[b]]) for b in range(5)]
+    assert status.item() == 0
+    bc.check_attention(o, lse, tuple(np.stack([p[i] for p in parts]) for i in range(4)))
 
 
 @pytest.mark.parametrize("n,new,hq", [(2048, 1, 4), (900, 18, 64)])

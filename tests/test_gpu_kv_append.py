@@ -401,6 +401,22 @@ def test_append_flags_bad_pages_and_positions():
             assert not bool(torch.all(q_out[1] == 9.0))
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_append_no_tokens(fp8):
+    """A step whose sequences all bring nothing: an empty result, the cache as it was."""
+    dev = gpu_or_skip()
+    import causal_gqa_flashattention_attn_gb300 as attn
+    caches = [torch.full((2, 16, 2, D), 7, dtype=torch.uint8 if fp8 else torch.bfloat16, device=dev) for _ in range(2)]
+    scales = [torch.full((2, 1, 2), 0.5, device=dev) for _ in range(2)] if fp8 else []
+    x = [torch.zeros(0, h, D, dtype=torch.bfloat16, device=dev) for h in (4, 2, 2)]
+    call = attn.attn_kv_append_fp8_block if fp8 else attn.attn_kv_append
+    out = call(*x, *caches, *scales, torch.zeros(2, 1, dtype=torch.int32, device=dev),
+               torch.tensor([3, 0], dtype=torch.int32, device=dev), qo_indptr=torch.zeros(3, dtype=torch.int32, device=dev))
+    torch.cuda.synchronize()
+    assert out.shape == x[0].shape and out.dtype == torch.bfloat16
+    assert all((c == 7).all() for c in caches) and all((s == 0.5).all() for s in scales)
+
+
 def test_binding_refuses_wrong_tensors():
     """Types, shapes, strides and devices that a call does not take raise ValueError, statuses AttnError; nothing is written."""
     dev = gpu_or_skip()
