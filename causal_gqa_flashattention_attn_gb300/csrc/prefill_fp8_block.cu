@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "paged.cuh"
+#include "ptx.cuh"
 
 namespace gb300 {
 namespace {
@@ -40,19 +41,18 @@ struct Params {
     int32_t* status;
 };
 
-// Sixteen codes times a scale as bf16.
-__device__ __forceinline__ void widen(uint4 w, float scale, uint4& lo, uint4& hi) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    uint32_t r[8];
+// Eight codes times a scale as bf16.
+__device__ __forceinline__ uint4 widen(uint2 w, float scale) {
+    const uint32_t u[2] = {w.x, w.y};
+    uint32_t r[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t f = e4m3x2_to_f16x2(u[i >> 1] >> (16 * (i & 1)));
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t f = (i & 1) != 0 ? e4m3x2_hi_to_f16x2(u[i >> 1]) : e4m3x2_to_f16x2(u[i >> 1]);
         const __half2 h = *reinterpret_cast<const __half2*>(&f);
         const __nv_bfloat162 b = __floats2bfloat162_rn(__low2float(h) * scale, __high2float(h) * scale);
         r[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    lo = make_uint4(r[0], r[1], r[2], r[3]);
-    hi = make_uint4(r[4], r[5], r[6], r[7]);
+    return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 constexpr int kWarps = kThreads / 32;
@@ -82,16 +82,24 @@ __device__ __forceinline__ T scan_cta(T x, T* warp_sums, T& all) {
     return before;
 }
 
+// A warp's rows on their way: kCopyRows of 32 vectors, keys and values.
+constexpr int kWarpBytes = 2 * kCopyRows * 32 * 16;
+
 struct Shared {
-    int start[kMaxSeqs + 1];   // first pages of the copy
-    int len[kMaxSeqs];         // rows of each sequence, cut at max_rows in all
+    uint8_t rows[kWarps * kWarpBytes];
     int count[kKeys];
     long long row_sums[kWarps];
     int sums[kWarps];
+    // behind it: int start[B + 1], first pages of the copy, and rows[B] of each sequence, cut at max_rows in all
+    __device__ __forceinline__ int* start() { return reinterpret_cast<int*>(this + 1); }
 };
+
+size_t shared_bytes(int B) { return sizeof(Shared) + (2 * static_cast<size_t>(B) + 1) * sizeof(int); }
 
 // The sequences' places in the copy, by the whole CTA.
 __device__ __forceinline__ void place_sequences(const Params& p, Shared& sh, bool flag) {
+    int* start_of = sh.start();
+    int* len_of = start_of + p.B + 1;
     long long rows_before = 0;
     int pages_before = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
@@ -116,11 +124,11 @@ __device__ __forceinline__ void place_sequences(const Params& p, Shared& sh, boo
         const int start = pages_before + scan_cta<int>((len + kPage - 1) / kPage, sh.sums, all_pages);
         pages_before += all_pages;
         if (b < p.B) {
-            sh.start[b] = start;
-            sh.len[b] = len;
+            start_of[b] = start;
+            len_of[b] = len;
         }
     }
-    if (threadIdx.x == 0) sh.start[p.B] = pages_before;
+    if (threadIdx.x == 0) start_of[p.B] = pages_before;
     __syncthreads();
 }
 
@@ -129,27 +137,29 @@ __device__ __forceinline__ void place_sequences(const Params& p, Shared& sh, boo
 // gives the same result wherever it runs.  (In the prefill's own CTAs, one warp
 // each, the same sort takes 15 us for 300 pairs.)
 __device__ __forceinline__ void sort_items(const Params& p, Shared& sh) {
+    const int* start_of = sh.start();
+    const int* len_of = start_of + p.B + 1;
     for (int k = threadIdx.x; k < kKeys; k += kThreads) sh.count[k] = 0;
     int pairs = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
         int blocks = 0;
         if (b < p.B) {
-            p.start[b] = sh.start[b];
-            p.last[b] = sh.len[b] > 0 ? sh.len[b] - (sh.len[b] - 1) / kPage * kPage : 0;
+            p.start[b] = start_of[b];
+            p.last[b] = len_of[b] > 0 ? len_of[b] - (len_of[b] - 1) / kPage * kPage : 0;
             blocks = (p.qo_indptr[b + 1] - p.qo_indptr[b] + p.q_block - 1) / p.q_block;   // as the prefill counts
         }
         int all;
         scan_cta<int>(blocks, sh.sums, all);
         pairs += all;
     }
-    if (threadIdx.x == 0) p.start[p.B] = sh.start[p.B];
+    if (threadIdx.x == 0) p.start[p.B] = start_of[p.B];
     if (pairs > p.max_pairs) return;   // too many to sort: taken in sequence order
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // every pair and its key, one warp a sequence, lanes its query blocks
     auto each_pair = [&](auto use) {
         for (int b = warp; b < p.B; b += kWarps) {
-            const int q_len = p.qo_indptr[b + 1] - p.qo_indptr[b], kv_len = sh.len[b];
+            const int q_len = p.qo_indptr[b + 1] - p.qo_indptr[b], kv_len = len_of[b];
             for (int qb = lane; qb * p.q_block < q_len; qb += 32) {
                 const int end = min(kv_len, min((qb + 1) * p.q_block, q_len) + kv_len - q_len);   // keys the block sees
                 use(min(end > 0 ? (end + kPage - 1) / kPage : 0, kKeys - 1), b, qb);
@@ -174,13 +184,16 @@ __device__ __forceinline__ void sort_items(const Params& p, Shared& sh) {
 static_assert(kKeys == 2 * kThreads, "two keys a thread");
 
 // CTA (0, 0) sorts the prefill's work items; the others copy.  A warp takes
-// kCopyRows rows and 32 of their 16-byte vectors of codes, a row of both caches
-// ahead.  Rows past a sequence's end or on a missing page are zeros.  The loop
-// stays rolled: with eight rows unrolled the kernel took 23 us instead of 7 on a
-// short batch, most of it for fetching instructions that run once.
+// kCopyRows rows and 32 of their 16-byte vectors of codes, both caches' all in
+// flight at once (24k rows of 4 heads: 6 us sooner done than with one row ahead
+// in registers), and writes 16 bytes a lane side by side.  Rows past a
+// sequence's end or on a missing page are zeros.  The loop over rows stays
+// rolled: with eight rows unrolled the kernel took 23 us instead of 7 on a short
+// batch, most of it for fetching instructions that run once.
 __global__ void __launch_bounds__(kThreads) fp8_block_copy_kernel(const Params p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ Shared sh;
+    extern __shared__ __align__(16) uint8_t smem[];
+    Shared& sh = *reinterpret_cast<Shared*>(smem);
     const bool sorts = blockIdx.x == 0;
     if (sorts && blockIdx.y != 0) return;
     place_sequences(p, sh, sorts);
@@ -188,16 +201,18 @@ __global__ void __launch_bounds__(kThreads) fp8_block_copy_kernel(const Params p
         sort_items(p, sh);
         return;
     }
-    const int lane = threadIdx.x & 31;
+    const int* start_of = sh.start();
+    const int* len_of = start_of + p.B + 1;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint8_t* buf = sh.rows + warp * kWarpBytes;
     const int vecs = p.Hkv * (kD / 16);
     const uint32_t chunks = (vecs + 31) / 32;
-    const uint32_t parts = static_cast<uint32_t>(sh.start[p.B]) * (kPage / kCopyRows);   // fewer than 2^31 rows
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    for (uint32_t part = (blockIdx.x - 1) * kWarps + (threadIdx.x >> 5); part < parts; part += (gridDim.x - 1) * kWarps) {
+    const uint32_t parts = static_cast<uint32_t>(start_of[p.B]) * (kPage / kCopyRows);   // fewer than 2^31 rows
+    for (uint32_t part = (blockIdx.x - 1) * kWarps + warp; part < parts; part += (gridDim.x - 1) * kWarps) {
         const int copy_page = static_cast<int>(part / (kPage / kCopyRows));
-        const int b = warp_rank(p.B, copy_page, lane, [&](int i) { return sh.start[i]; });
-        const int t0 = static_cast<int>(part - static_cast<uint32_t>(sh.start[b]) * (kPage / kCopyRows)) * kCopyRows;
-        const int len = sh.len[b];
+        const int b = warp_rank(p.B, copy_page, lane, [&](int i) { return start_of[i]; });
+        const int t0 = static_cast<int>(part - static_cast<uint32_t>(start_of[b]) * (kPage / kCopyRows)) * kCopyRows;
+        const int len = len_of[b];
         const int entry = p.page_div.div(t0);
         const int page = t0 < len ? page_at(p.list, b, entry, page_count(p.list, b), lane == 0 ? p.status : nullptr) : -1;
         const int n = page >= 0 ? min(kCopyRows, len - t0) : 0;
@@ -205,40 +220,42 @@ __global__ void __launch_bounds__(kThreads) fp8_block_copy_kernel(const Params p
         const size_t slot = static_cast<size_t>(page >= 0 ? page : 0) * p.list.page_size + o;
         const size_t block = static_cast<size_t>(page >= 0 ? page : 0) * (p.page_div.d / p.block_div.d) + p.block_div.div(o);
         for (uint32_t c = blockIdx.y; c < chunks; c += gridDim.y) {
-            const int v = static_cast<int>(c) * 32 + lane;
-            if (v >= vecs) continue;
-            float ks = 0.f, vs = 0.f;
-            const uint4* k_in = reinterpret_cast<const uint4*>(p.k_cache) + slot * vecs + v;
-            const uint4* v_in = reinterpret_cast<const uint4*>(p.v_cache) + slot * vecs + v;
-            uint4* k_out = p.k_copy + (static_cast<size_t>(part) * kCopyRows * vecs + v) * 2;
-            uint4* v_out = p.v_copy + (static_cast<size_t>(part) * kCopyRows * vecs + v) * 2;
-            uint4 kx = zero, vx = zero;
-            if (n > 0) {
-                kx = __ldg(k_in);
-                vx = __ldg(v_in);
-                ks = __ldg(p.k_scale + block * p.Hkv + v / (kD / 16));
-                vs = __ldg(p.v_scale + block * p.Hkv + v / (kD / 16));
+            const int v0 = static_cast<int>(c) * 32, m = min(32, vecs - v0);   // vectors [v0, v0 + m) of each row
+            const uint4* k_in = reinterpret_cast<const uint4*>(p.k_cache) + slot * vecs + v0 + lane;
+            const uint4* v_in = reinterpret_cast<const uint4*>(p.v_cache) + slot * vecs + v0 + lane;
+            __syncwarp();   // the rows before these have been read
+#pragma unroll
+            for (int r = 0; r < kCopyRows; ++r) {
+                const bool there = lane < m && r < n;
+                uint8_t* at = buf + r * 512 + lane * 16;
+                cp_async16(at, there ? static_cast<const void*>(k_in + static_cast<size_t>(r) * vecs) : p.k_cache, there ? 16 : 0);
+                cp_async16(at + kCopyRows * 512, there ? static_cast<const void*>(v_in + static_cast<size_t>(r) * vecs) : p.v_cache, there ? 16 : 0);
             }
+            // a lane writes vectors lane and lane + 32 of the 2 m of each row
+            float ks[2] = {0.f, 0.f}, vs[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (n > 0 && lane + 32 * i < 2 * m) {
+                    const size_t at = block * p.Hkv + (2 * v0 + lane + 32 * i) / (kD / 8);
+                    ks[i] = __ldg(p.k_scale + at);
+                    vs[i] = __ldg(p.v_scale + at);
+                }
+            uint4* k_out = p.k_copy + (static_cast<size_t>(part) * kCopyRows * vecs + v0) * 2 + lane;
+            uint4* v_out = p.v_copy + (static_cast<size_t>(part) * kCopyRows * vecs + v0) * 2 + lane;
+            cp_async_wait_all();
+            __syncwarp();
 #pragma unroll 1
             for (int r = 0; r < kCopyRows; ++r) {
-                uint4 k_next = zero, v_next = zero;
-                if (r + 1 < n) {
-                    k_in += vecs;
-                    v_in += vecs;
-                    k_next = __ldg(k_in);
-                    v_next = __ldg(v_in);
-                }
-                uint4 lo, hi;
-                widen(kx, ks, lo, hi);
-                k_out[0] = lo;
-                k_out[1] = hi;
-                widen(vx, vs, lo, hi);
-                v_out[0] = lo;
-                v_out[1] = hi;
+                const uint2* kr = reinterpret_cast<const uint2*>(buf + r * 512) + lane;
+                const uint2* vr = reinterpret_cast<const uint2*>(buf + (kCopyRows + r) * 512) + lane;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (lane + 32 * i < 2 * m) {
+                        k_out[32 * i] = widen(kr[32 * i], ks[i]);
+                        v_out[32 * i] = widen(vr[32 * i], vs[i]);
+                    }
                 k_out += 2 * vecs;
                 v_out += 2 * vecs;
-                kx = k_next;
-                vx = v_next;
             }
         }
     }
@@ -290,8 +307,14 @@ cudaError_t launch_prefill_fp8_block(const PrefillBlockArgs& a, cudaStream_t str
     p.last = p.start + a.B + 1;
     p.status = a.dev_status;
     // gridDim.x: the sorting CTA and the copying ones
-    fp8_block_copy_kernel<<<dim3(1 + sms * 4, std::min((a.Hkv * (kD / 16) + 31) / 32, 64)), kThreads, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = once_per_device(done, [] {
+        return cudaFuncSetAttribute(fp8_block_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(shared_bytes(kMaxSeqs)));
+    });
+    if (e != cudaSuccess) return e;
+    fp8_block_copy_kernel<<<dim3(1 + sms * 4, std::min((a.Hkv * (kD / 16) + 31) / 32, 64)), kThreads, shared_bytes(a.B), stream>>>(p);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // the copy as a cache of kPage-token pages in list order
     const size_t rows = copy_rows(a.B, a.max_kv_rows);
