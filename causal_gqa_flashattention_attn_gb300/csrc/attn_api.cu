@@ -629,9 +629,9 @@ attn_status_t attn_decode_paged_fp8_block(const void* q, const void* k_cache, co
     if (q_len > 16 || B > decode_fp8_block_max_seqs()) return ATTN_ERR_UNSUPPORTED;
     if (static_cast<long long>(Hq) * q_len >= (1LL << 20) || static_cast<long long>(Hq) * q_len * B >= (1LL << 31))
         return ATTN_ERR_UNSUPPORTED;
-    // tiles of 32 tokens are counted in int
+    // tiles of 32 tokens, and two more for each sequence's end, are counted in int
     if (kv_indptr == nullptr &&
-        (static_cast<long long>(max_pages_per_seq) * page_size / 32 + 1) * B >= (1LL << 31))
+        (static_cast<long long>(max_pages_per_seq) * page_size / 32 + 3) * B >= (1LL << 31))
         return ATTN_ERR_UNSUPPORTED;
     if (workspace == nullptr || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
     const int sms = device_sm_count();

@@ -19,7 +19,17 @@
 // lengths, which only the device knows.  A share that holds a whole sequence
 // writes its output; the pieces of a sequence that is cut between shares go to
 // the workspace, and a second kernel, which is launched along with the first
-// and waits for it on the device, joins them.
+// and waits for it on the device, joins them.  (The join by whichever CTA comes
+// last, inside the first kernel, was much slower: its fences and counters stand
+// between the last tile and the output.)
+//
+// Bound: one read of the codes from HBM.  64 ragged sequences of 512 to 32768
+// tokens, 32 heads over 8 (2.05 GB): 293 us, 7.0 TB/s; 16 of 16384 (537 MB): 88
+// us, 6.1 TB/s, 4 us of it the merge.  With 16 rows a column the loop is bound
+// by its own latency, 844 instructions a tile at two warps a scheduler (1.5 us
+// a tile): 24 sequences of up to 9000 tokens with 4 queries of 16 heads over 2
+// (57 MB) 35.7 us.  One sequence of 1000 tokens: 8.9 us for the two kernels,
+// latency alone.
 #include "paged.cuh"
 #include "ptx.cuh"
 
@@ -35,6 +45,10 @@ constexpr int kStages = 3;      // tiles in flight or in use per warp
 constexpr int kCodes = kTile * kD;                    // 4 KB: a tile's K (or V) codes of one head
 constexpr int kWarpBytes = kStages * 2 * kCodes;
 static_assert(kWarps * kWarpBytes + (2 * kMaxSeqs + 1) * 4 + 1024 <= 227 * 1024, "the tables fit beside the rings");
+// A sequence's end (a tile with a mask, the piece's rows, the next queries)
+// costs a warp about as much as two tiles more: counted as such in the cut,
+// 24 sequences of 4 queries take 35.7 us instead of 37.0.
+constexpr int kEnd = 2;
 constexpr int kMergeWarps = 8;
 constexpr int kBatch = 8;       // pieces a merging warp has in flight
 
@@ -93,15 +107,17 @@ __device__ __forceinline__ int length_of(const Params& p, int b, bool flag) {
 }
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+// What a sequence counts for in the cut: its tiles, and its end.
+__device__ __forceinline__ int span_of(int len) { return len > 0 ? tiles_of(len) + kEnd : 0; }
 
 // Whether a CSR list holds so many tokens that tiles do not count in int (the
 // host has checked block tables).
 __device__ __forceinline__ bool too_many_tiles(const Params& p) {
     if (p.list.indptr == nullptr) return false;
-    return static_cast<long long>(p.list.indptr[p.B]) * p.list.page_size / kTile + p.B >= (1LL << 31);
+    return static_cast<long long>(p.list.indptr[p.B]) * p.list.page_size / kTile + (1 + kEnd) * p.B >= (1LL << 31);
 }
 
-// before[b] = tiles of the sequences before b (before[B] = all) and lens[b] =
+// before[b] = spans of the sequences before b (before[B] = all) and lens[b] =
 // their lengths, by the whole CTA: each thread takes a run of sequences.
 __device__ __forceinline__ void count_tiles(const Params& p, int* before, int* lens, int* warp_sum, bool flag) {
     const int per = (p.B + kThreads - 1) / kThreads;
@@ -109,7 +125,7 @@ __device__ __forceinline__ void count_tiles(const Params& p, int* before, int* l
     int sum = 0;
     for (int b = b0; b < b1; ++b) {
         lens[b] = length_of(p, b, flag);
-        sum += tiles_of(lens[b]);
+        sum += span_of(lens[b]);
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int incl = sum;
@@ -124,13 +140,13 @@ __device__ __forceinline__ void count_tiles(const Params& p, int* before, int* l
     for (int w = 0; w < warp; ++w) base += warp_sum[w];
     for (int b = b0; b < b1; ++b) {
         before[b] = base;
-        base += tiles_of(lens[b]);
+        base += span_of(lens[b]);
     }
     if (threadIdx.x == kThreads - 1) before[p.B] = base;   // the last run ends with the last sequence, or is empty
     __syncthreads();
 }
 
-// The cut of `total` tiles into shares: the first `extra` shares take each + 1
+// The cut of `total` tiles (and ends) into shares: the first `extra` shares take each + 1
 // tiles, the others `each`.
 struct Cut {
     int shares, each, extra;
@@ -426,6 +442,7 @@ struct Feed {
 };
 
 __device__ __forceinline__ void feed_look(const Params& p, const int* before, Feed& f, int lane) {
+    if (f.x >= before[f.b + 1] - kEnd) f.x = before[f.b + 1];   // past the end
     if (f.x >= f.x_end) return;
     if (before[f.b + 1] <= f.x) {
         do ++f.b;
@@ -545,6 +562,9 @@ __global__ void __maxnreg__(NB == 1 ? 192 : 255) decode_fp8_block_kernel(const _
         const int x_end = cut.start(w + 1);
         if (x >= x_end) continue;
         int b = warp_rank(p.B, x, lane, [&](int i) { return before[i]; });
+        if (x >= before[b + 1] - kEnd) x = before[b + 1];   // only the end is left of it
+        if (x >= x_end) continue;
+        while (before[b + 1] <= x) ++b;
         Feed f;
         f.x = x;
         f.x_end = x_end;
@@ -560,9 +580,9 @@ __global__ void __maxnreg__(NB == 1 ? 192 : 255) decode_fp8_block_kernel(const _
         int slot = 0;
         for (bool first = true; x < x_end; first = false) {
             while (before[b + 1] <= x) ++b;
-            const int t_lo = x - before[b], n_tiles = before[b + 1] - before[b];
+            const int t_lo = x - before[b], n_tiles = before[b + 1] - before[b] - kEnd;
             const int t_hi = min(n_tiles, t_lo + (x_end - x));
-            x += t_hi - t_lo;
+            x = t_hi == n_tiles ? before[b + 1] : x_end;
             const int len = lens[b];
             if (!first) fetch_queries<NB>(p, b, kvh, row0, n_rows, lane, raw);
             take_queries<NB>(p, raw, row0, n_rows, len, lane, qs);
@@ -637,11 +657,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) decode_fp8_block_merge_ke
     const int rows_per_cta = kMergeWarps / per_row;
     const int cta_per_seq = (rows + rows_per_cta - 1) / rows_per_cta;
     const int b = blockIdx.x / cta_per_seq, row = blockIdx.x % cta_per_seq * rows_per_cta + warp / per_row;
-    // tiles before the sequence, and of all of them
+    // spans before the sequence, and of all of them
     int pre = 0, all = 0;
     const bool bad = too_many_tiles(p);
     for (int i = threadIdx.x; i < p.B && !bad; i += 32 * kMergeWarps) {
-        const int t = tiles_of(length_of(p, i, false));
+        const int t = span_of(length_of(p, i, false));
         all += t;
         if (i < b) pre += t;
     }

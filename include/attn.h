@@ -559,7 +559,7 @@ attn_status_t attn_kv_append_fp8_block(const void* q, const void* k, const void*
  *   o            as q (written); lse float32 [B, q_len, Hq], natural log
  *                (written; may be NULL)
  *   D = 128, q_len 1..16, any Hq % Hkv == 0, B <= 4096; with a block table
- *   B * (max_pages_per_seq * page_size / 32 + 1) < 2^31.
+ *   B * (max_pages_per_seq * page_size / 32 + 3) < 2^31.
  * Bad pages are left out as in attn_decode_paged_splitk; a length past the
  * page list sets ATTN_DEV_SEQ_TOO_LONG and is cut there.
  */
