@@ -104,6 +104,55 @@ def test_decode(lens, nq, hq, hkv, page, block, csr, scales):
     bc.check_attention(o, lse, reference(q.double().numpy(), cache))
 
 
+#  more than 16 rows a KV head
+MANY_ROWS = [
+    ([0, 1, 15, 16, 17, 63, 64, 65, 127, 129, 300], 4, 16, 2, 16, 16, True, "any"),   # 32 rows, ends around a tile's
+    ([500, 64], 3, 12, 2, 32, 32, False, "pow2"),             # 18 rows
+    ([3000, 7], 9, 7, 1, 48, 16, False, "any"),               # 63 rows, cut over many CTAs
+    ([2000, 0, 1, 70], 16, 8, 1, 64, 64, True, "pow2"),       # 128 rows
+    ([900, 33], 16, 27, 3, 32, 32, False, "any"),             # 144 rows: a column of 128 and one of 16
+    ([70, 200], 16, 320, 160, 16, 16, False, "any"),          # more columns than CTAs
+    ([8, 3] * 150, 2, 20, 1, 16, 16, True, "pow2"),           # 40 rows, many short sequences
+    ([500, 333], 4, 32, 4, 64, 16, True, "far"),
+    ([700, 90], 8, 16, 2, 128, 128, False, "far"),
+]
+
+
+@pytest.mark.parametrize("lens,nq,hq,hkv,page,block,csr,scales", MANY_ROWS)
+def test_decode_many_rows(lens, nq, hq, hkv, page, block, csr, scales):
+    test_decode(lens, nq, hq, hkv, page, block, csr, scales)
+
+
+@pytest.mark.parametrize("nq,hq,hkv", [(4, 16, 2), (16, 4, 2), (16, 8, 2), (16, 16, 2)])
+def test_decode_many_rows_far_queries_and_nans(nq, hq, hkv):
+    """Queries of any size, peaked scores, and NaNs that some rows see and others do not, 32 to 128 rows a KV head."""
+    dev = gpu_or_skip()
+    import causal_gqa_flashattention_attn_gb300 as attn
+    rng = np.random.default_rng(nq + hq)
+    lens = [1500, 100, 77]
+    cache = Cache(lens, hkv, 64, 16, rng, scales="any")
+    for size in (2.0 ** -120, 30.0, 2.0 ** 100):
+        q = bc.bf16(rng.standard_normal((3, nq, hq, D)) * size)
+        q[0, 0, 0] = 0.0
+        scale = D ** -0.5 / size if size != 30.0 else None
+        o, lse, status = decode(attn, q.to(dev), cache, dev, scale=scale)
+        assert status == 0
+        bc.check_attention(o, lse, reference(q.double().numpy(), cache, scale=None if scale is None else float(np.float32(scale))))
+    clean = o, lse
+    put = [(0, 0, 0, 1499, 5), (1, 1, 1, 99 - (nq - 2), 9), (2, 1, 0, 76, 127), (2, 1, 0, 60, 0), (1, 0, 1, 98, 64)]
+    for b, w, h, t, d in put:      # sequence, K or V, KV head, token, element
+        cache.codes[w][cache.lists.rows[b][t // 64], t % 64, h, d] = 0x7F
+    want = torch.zeros(3, nq, hq, D, dtype=torch.bool)
+    g = hq // hkv
+    for b, w, h, t, d in put:
+        first = max(0, t - (lens[b] - nq))        # the first query that sees the token
+        want[b, first:, h * g:(h + 1) * g, slice(None) if w == 0 else d] = True
+    o, lse, status = decode(attn, q.to(dev), cache, dev, scale=scale)
+    assert status == 0
+    assert torch.equal(torch.isnan(o).cpu(), want)
+    assert torch.equal(o.cpu()[~want], clean[0].cpu()[~want])
+
+
 def test_decode_csr_offsets_that_fall():
     """A sequence whose CSR offsets fall has an empty list: flagged, nothing of it read, the others as they are."""
     dev = gpu_or_skip()
