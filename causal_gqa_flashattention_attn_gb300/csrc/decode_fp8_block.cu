@@ -20,8 +20,7 @@
 // writes its output; the pieces of a sequence that is cut between shares go to
 // the workspace, and a second kernel, which is launched along with the first
 // and waits for it on the device, joins them.  (The join by whichever CTA comes
-// last, inside the first kernel, was much slower: its fences and counters stand
-// between the last tile and the output.)
+// last, inside the first kernel, was slower.)
 //
 // Bound: one read of the codes from HBM.  64 ragged sequences of 512 to 32768
 // tokens, 32 heads over 8 (2.05 GB): 293 us, 7.0 TB/s; 16 of 16384 (537 MB): 88
@@ -29,7 +28,11 @@
 // by its own latency, 844 instructions a tile at two warps a scheduler (1.5 us
 // a tile): 24 sequences of up to 9000 tokens with 4 queries of 16 heads over 2
 // (57 MB) 35.7 us.  One sequence of 1000 tokens: 8.9 us for the two kernels,
-// latency alone.
+// latency alone.  Tried: 12 warps with two stages each, 302 and 91 us for the
+// first two and 53 for the third (16 rows spill at 168 registers); a CTA that
+// widens a tile once into shared memory for its warps' groups of 16 rows, 43 us
+// for 24 sequences of 4500 tokens and 32 rows where the warps alone take 32, 57
+// for 57 at 64 rows and 85 for 98 only at 128.
 #include "paged.cuh"
 #include "ptx.cuh"
 

@@ -18,6 +18,11 @@
 // is a bf16 number.  A key's code is that of its exact rotation: fp32 decides
 // unless the value lies within a few units of a border, where it is computed
 // again in twice the precision.
+//
+// Bound: the bytes, on long batches: 9k tokens of 32 + 2 x 4 heads into a bf16
+// cache (185 MB) take 31.5 us, 5.9 TB/s; into 8-bit blocks see below.  A decode
+// step of 64 tokens of 32 + 2 x 8 heads takes 2.5 us (8-bit blocks 3.1), the
+// latency of a launch and of three loads that wait for one another.
 #include "paged.cuh"
 #include "ptx.cuh"
 
@@ -555,11 +560,12 @@ cudaError_t launch_tokens(const Params& p, bool interleaved, int sms, cudaStream
 
 // Ragged batches into 8-bit blocks.  Every warp copies kRows rows into shared
 // memory, all of them in flight at once, and works on them there, eight lanes a
-// row, four rows at a time.  17k tokens of 32 + 2 x 8 heads (378 MB): 68 us, 83 %
-// of the copy rate; alone the queries take 47 us (their bytes 44) and the blocks
-// 40, bound by their instructions and the angles' latency.  Tried: unrolled over
+// row, four rows at a time.  17k tokens of 32 + 2 x 8 heads (378 MB): 71 us, 79 %
+// of the copy rate; alone the queries take 47 us (their bytes 41) and the blocks
+// 40 (their bytes 15), bound by what a warp waits for at four warps a scheduler.  Tried: unrolled over
 // rows in registers 120 us (a quarter of it waiting for instructions, 12 warps an
-// SM), a CTA of 8 lanes per row and a round per head 105-118 us (what a head
+// SM), 5 CTAs an SM 70 us but 8.7 instead of 8.1 for 13 short chunks, the first
+// angles and the lengths loaded sooner 71.5, a CTA of 8 lanes per row and a round per head 105-118 us (what a head
 // costs a warp beside its four rows), 6 CTAs an SM 80 us (80 registers spill),
 // queries by token instead of by 8 tokens x 4 heads 79 us, the two kinds mixed 70.
 constexpr int kTaskWarps = 4;

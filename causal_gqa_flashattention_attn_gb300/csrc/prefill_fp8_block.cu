@@ -5,10 +5,16 @@
 // contiguous copy, every sequence from a 128-row border on with zeros up to the
 // next one, and the tensor-core prefill reads that copy by TMA as a cache of
 // 128-token pages in list order: no tile of a sequence holds another's rows, so
-// a NaN stays in its own sequence.  With a power-of-two scale the value is a bf16 number, so the copy
-// rounds nothing; another scale's values are rounded once to bf16, as the
-// tensor cores' operands must be.  The copy costs 1 byte read and 2 written
-// per element once, against one read of the cache per query block otherwise.
+// a NaN stays in its own sequence.  With a power-of-two scale the value is a
+// bf16 number, so the copy rounds nothing; another scale's values are rounded
+// once to bf16, as the tensor cores' operands must be.  The copy costs 1 byte
+// read and 2 written per element once, against one read of the cache per query
+// block otherwise.
+//
+// Bound: the tensor cores.  8 sequences, 9.7k queries of 32 heads over 23.8k
+// tokens of 4 KV heads (360 GFLOP): 314.5 us, 1143 TFLOP/s, about 15 us of it
+// the copy before the prefill's first tile.  Three short prompts: 19.6 us, the
+// latency of two launches and of five KV tiles one after another.
 #include <algorithm>
 
 #include "paged.cuh"
