@@ -640,6 +640,7 @@ def attn_prefill_paged_fp8_block(q, k_cache, v_cache, k_scale, v_scale, qo_indpt
     ``qo_indptr[b+1]`` being the last positions of sequence b's ``seq_lens[b]``
     cached tokens.  ``max_kv_rows``: at least the sum of ``seq_lens``, which
     sizes the workspace (by default all that the page lists can hold).
+    ``scale`` (by default ``D ** -0.5``) is positive.
     ``workspace``: a uint8 tensor of attn_prefill_fp8_block_workspace_bytes()
     bytes.  Returns ``(o [total_q, Hq, D], lse [total_q, Hq], workspace)``.
     """

@@ -662,7 +662,8 @@ attn_status_t attn_prefill_paged_fp8_block(const void* q, const void* k_cache, c
     if (st == ATTN_OK) st = block_check(k_scale, v_scale, page_size, block_tokens);
     if (st != ATTN_OK) return st;
     if (!std::isfinite(scale) || !aligned16(q) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
-    if (Hq / Hkv > 128 || B > varlen_max_seqs()) return ATTN_ERR_UNSUPPORTED;
+    // the prefill's maxima and masks are taken before the scale: it has to keep their order
+    if (Hq / Hkv > 128 || B > varlen_max_seqs() || scale <= 0.f) return ATTN_ERR_UNSUPPORTED;
     // as attn_prefill_paged_varlen: items and query blocks are counted in int and 21 bits
     if (total_q >= (1 << 22) || (static_cast<long long>(total_q) + B) * Hkv >= (1LL << 31)) return ATTN_ERR_UNSUPPORTED;
     // rows of the copy, each sequence's up to the next multiple of 128, are counted in int

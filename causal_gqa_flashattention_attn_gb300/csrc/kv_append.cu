@@ -562,12 +562,13 @@ cudaError_t launch_tokens(const Params& p, bool interleaved, int sms, cudaStream
 // memory, all of them in flight at once, and works on them there, eight lanes a
 // row, four rows at a time.  17k tokens of 32 + 2 x 8 heads (378 MB): 71 us, 79 %
 // of the copy rate; alone the queries take 47 us (their bytes 41) and the blocks
-// 40 (their bytes 15), bound by what a warp waits for at four warps a scheduler.  Tried: unrolled over
-// rows in registers 120 us (a quarter of it waiting for instructions, 12 warps an
-// SM), 5 CTAs an SM 70 us but 8.7 instead of 8.1 for 13 short chunks, the first
-// angles and the lengths loaded sooner 71.5, a CTA of 8 lanes per row and a round per head 105-118 us (what a head
-// costs a warp beside its four rows), 6 CTAs an SM 80 us (80 registers spill),
-// queries by token instead of by 8 tokens x 4 heads 79 us, the two kinds mixed 70.
+// 40 (their bytes 15), bound by what a warp waits for at four warps a scheduler.
+// Tried: unrolled over rows in registers 120 us (a quarter of it waiting for
+// instructions, 12 warps an SM), 5 CTAs an SM 70 us but 8.7 instead of 8.1 for 13
+// short chunks, the first angles and the lengths loaded sooner 71.5, a CTA of 8
+// lanes per row and a round per head 105-118 us (what a head costs a warp beside
+// its four rows), 6 CTAs an SM 80 us (80 registers spill), queries by token
+// instead of by 8 tokens x 4 heads 79 us, the two kinds mixed 70.
 constexpr int kTaskWarps = 4;
 constexpr int kRows = 32;
 constexpr int kRowBytes = 2 * kD;

@@ -36,7 +36,7 @@ struct Params {
     const int32_t* seq_lens;
     const int32_t* qo_indptr;
     Divisor page_div, block_div;
-    int B, Hkv, block, max_rows;
+    int B, Hkv, max_rows;
     int q_block;      // query positions of a work item of the prefill
     int max_pairs, pair_bits;
     uint32_t* order;  // [max_pairs], work items' (sequence, query block) pairs, longest first
@@ -300,7 +300,6 @@ cudaError_t launch_prefill_fp8_block(const PrefillBlockArgs& a, cudaStream_t str
     p.qo_indptr = a.qo_indptr;
     p.page_div = make_divisor(a.page_size);
     p.block_div = make_divisor(a.block_tokens);
-    p.block = a.block_tokens;
     p.q_block = 2 * (128 / (a.Hq / a.Hkv));
     p.max_rows = a.max_kv_rows;
     p.k_copy = reinterpret_cast<uint4*>(w);

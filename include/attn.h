@@ -587,6 +587,7 @@ attn_status_t attn_decode_paged_fp8_block(const void* q, const void* k_cache, co
  *   workspace    >= attn_prefill_fp8_block_workspace_bytes() bytes, 16-byte
  *                aligned (scratch, overwritten)
  *   o            [total_q, Hq, D]; lse float32 [total_q, Hq] or NULL (written)
+ *   scale        > 0
  * Cache and page-list arguments as attn_decode_paged_fp8_block; limits as
  * attn_prefill_paged_varlen.  A token on a bad page is read as zeros.  A NaN
  * among a sequence's values shows in every query of that sequence whose last

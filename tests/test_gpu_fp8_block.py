@@ -199,6 +199,20 @@ def test_decode_peaked_scores():
     bc.check_attention(o, lse, reference(q.double().numpy(), cache))
 
 
+@pytest.mark.parametrize("scale", [-0.05, 0.0])
+@pytest.mark.parametrize("nq,hq", [(1, 4), (3, 8)])
+def test_decode_any_scale(scale, nq, hq):
+    """Scores of the other sign, and all alike: the masks still hold."""
+    dev = gpu_or_skip()
+    import causal_gqa_flashattention_attn_gb300 as attn
+    rng = np.random.default_rng(5)
+    cache = Cache([400, 2, 33], 2, 32, 16, rng)
+    q = bc.bf16(rng.standard_normal((3, nq, hq, D)))
+    o, lse, status = decode(attn, q.to(dev), cache, dev, scale=scale)
+    assert status == 0
+    bc.check_attention(o, lse, reference(q.double().numpy(), cache, scale=float(np.float32(scale))))
+
+
 def test_decode_nan_shows():
     """A NaN in a key or value that a row sees comes out as NaN; rows that do not see it are clean."""
     dev = gpu_or_skip()

@@ -287,6 +287,36 @@ def test_append_fp8_block_steps(steps, hq, hkv, page, block, rot, inter, csr):
         old = [o + m for o, m in zip(old, new)]
 
 
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_fp8_block_many_heads_positions_and_type(inter):
+    """300 + 2 x 100 heads, positions of their own, tensors of the float8 type."""
+    dev = gpu_or_skip()
+    import causal_gqa_flashattention_attn_gb300 as attn
+    rng = np.random.default_rng(31)
+    hq, hkv, page, block, new = 300, 100, 32, 16, [40, 25]
+    lists = bc.Lists(new, page, rng)
+    pages, _ = lists.tensors(dev)
+    batch = Batch([0, 0], new, hq, hkv, rng)
+    table = bc.rope_table(900, 128)
+    pos = rng.permutation(65) * 13 % 900
+    shape, blocks = (lists.num_pages, page, hkv, D), (lists.num_pages, page // block, hkv)
+    dc = [torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2)]
+    ds = [torch.zeros(blocks, device=dev) for _ in range(2)]
+    q, k, v = strided(batch, dev)
+    out = attn.attn_kv_append_fp8_block(q, k, v, *dc, *ds, pages, batch.lens(dev), cos_sin=torch.from_numpy(table).to(dev),
+                                        interleaved=inter, qo_indptr=batch.indptr(dev),
+                                        positions=torch.tensor(pos, dtype=torch.int32, device=dev))
+    torch.cuda.synchronize()
+    x = batch.q.double().numpy()
+    check_bf16(out, bc.rotate(x, table, pos, inter), bc.rotate_slack(x, table, pos, inter))
+    for got, scale, want in zip(dc, ds, (bc.rotate(batch.k.double().numpy(), table, pos, inter), batch.v.double().numpy())):
+        codes, scales = np.zeros(shape, np.uint8), np.zeros(blocks, np.float32)
+        for b in range(2):
+            bc.append_blocks(codes, scales, lists, block, b, 0, want[batch.rows(b)])
+        assert np.array_equal(scale.cpu().numpy(), scales)
+        assert np.array_equal(got.view(torch.uint8).cpu().numpy(), codes)
+
+
 def test_append_fp8_block_borders():
     """Ties between codes, sizes at 448 * 2^e and one step beside it, zeros, subnormal and huge values, NaN and infinities."""
     dev = gpu_or_skip()

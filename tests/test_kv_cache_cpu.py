@@ -138,6 +138,7 @@ def test_prefill_validation(L):
     assert _prefill(L, T=-1) == -1
     assert _prefill(L, rows=0) == -1
     assert _prefill(L, scale=float("inf")) == -1
+    assert _prefill(L, scale=0.0) == -2 and _prefill(L, scale=-0.1) == -2
     assert _prefill(L, Hq=30) == -1
     assert _prefill(L, D=64) == -2
     assert _prefill(L, block=8) == -2
