@@ -33,6 +33,8 @@
 // widens a tile once into shared memory for its warps' groups of 16 rows, 43 us
 // for 24 sequences of 4500 tokens and 32 rows where the warps alone take 32, 57
 // for 57 at 64 rows and 85 for 98 only at 128.
+#include <algorithm>
+
 #include "paged.cuh"
 #include "ptx.cuh"
 
@@ -748,19 +750,48 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) decode_fp8_block_merge_ke
     if (p.lse != nullptr && lane == 0) p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
-// Rows of a column: 8, or 16 where a KV head has more of them.
-int rows_per_column(int rows) { return rows <= 8 ? 8 : 16; }
+// The grid's warps over columns of `per` rows.
+void set_columns(Params& p, int per, int sms) {
+    p.cols = p.Hkv * ((p.G * p.nq + per - 1) / per);
+    p.workers = std::max(1, sms * kWarps / p.cols);
+}
+
+// Rows of the workspace.
+size_t part_rows(const Params& p, int per) { return static_cast<size_t>(2) * p.workers * p.cols * per; }
+
+// Rows of a column: 16 where a KV head has more than 8, but 8 while the most
+// tokens that the lists can name make short shares of such columns.  A tile of
+// 8 rows costs a warp 0.7 of one of 16, all that runs once for a share less than
+// half, and its kernel leaves room for the merge's: 4 queries of 8 heads over 2,
+// 2400 tokens (1 tile a share) 11.6 us against 16.5; 8 sequences of 1000 and 64
+// rows (4) 15.7 against 17.6; 29 ragged ones of 12 rows, 32k tokens (13) 29.2
+// against 30.2; 24 of 4500 and 32 rows (22) 38.4 against 31.9.
+constexpr int kNarrowTiles = 12;
+int rows_per_column(Params& p, int sms) {
+    set_columns(p, 8, sms);
+    const long long listed = p.list.indptr != nullptr ? p.list.num_pages
+                                                      : std::min<long long>(p.list.num_pages, static_cast<long long>(p.B) * p.list.max_pages);
+    const long long tiles = listed * p.list.page_size / kTile + static_cast<long long>(kEnd) * p.B;
+    if (p.G * p.nq <= 8 || tiles <= static_cast<long long>(kNarrowTiles) * p.workers) return 8;
+    set_columns(p, 16, sms);
+    return 16;
+}
 
 }  // namespace
 
 int decode_fp8_block_max_seqs() { return kMaxSeqs; }
 
 size_t decode_fp8_block_workspace(int q_len, int Hq, int Hkv, int sms) {
-    const int rows = (Hq / Hkv) * q_len, per = rows_per_column(rows);
-    const long long cols = static_cast<long long>(Hkv) * ((rows + per - 1) / per);
-    const long long warps = static_cast<long long>(sms) * kWarps;
-    const long long workers = warps / cols > 1 ? warps / cols : 1;
-    return static_cast<size_t>(2 * workers * cols * per) * (kD + 1) * sizeof(float);
+    Params p{};
+    p.Hkv = Hkv;
+    p.G = Hq / Hkv;
+    p.nq = q_len;
+    size_t rows = 0;   // enough for columns of either height
+    for (int per : {8, 16}) {
+        set_columns(p, per, sms);
+        if (per == 8 || p.G * p.nq > 8) rows = std::max(rows, part_rows(p, per));
+    }
+    return rows * (kD + 1) * sizeof(float);
 }
 
 cudaError_t launch_decode_fp8_block(const DecodeBlockArgs& a, cudaStream_t stream) {
@@ -784,15 +815,13 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockArgs& a, cudaStream_t strea
     p.heads_div = make_divisor(a.Hkv);
     p.group_div = make_divisor(p.G);
     p.tile_in_page = a.page_size % kTile == 0;
-    const int rows = p.G * p.nq, per = rows_per_column(rows);
-    p.cols = a.Hkv * ((rows + per - 1) / per);
+    const int per = rows_per_column(p, sms);
     p.cols_div = make_divisor(p.cols);
-    p.workers = sms * kWarps / p.cols > 1 ? sms * kWarps / p.cols : 1;
     p.scale_log2 = a.scale * kLog2e;
     p.o = static_cast<__nv_bfloat16*>(a.o);
     p.lse = a.lse;
     p.part_o = static_cast<float*>(a.workspace);
-    p.part_l = p.part_o + static_cast<size_t>(2) * p.workers * p.cols * per * kD;
+    p.part_l = p.part_o + part_rows(p, per) * kD;
     p.status = a.dev_status;
     const size_t smem = kWarps * kWarpBytes + (2 * static_cast<size_t>(a.B) + 1) * sizeof(int);
     auto kern = per == 8 ? decode_fp8_block_kernel<1> : decode_fp8_block_kernel<2>;

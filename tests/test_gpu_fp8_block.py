@@ -115,6 +115,10 @@ MANY_ROWS = [
     ([8, 3] * 150, 2, 20, 1, 16, 16, True, "pow2"),           # 40 rows, many short sequences
     ([500, 333], 4, 32, 4, 64, 16, True, "far"),
     ([700, 90], 8, 16, 2, 128, 128, False, "far"),
+    # long enough for columns of 16 rows (more than 12 tiles of 32 tokens a share on 152 SMs)
+    ([2000, 0, 1, 15, 33, 1900, 70], 16, 64, 2, 64, 16, True, "any"),   # 512 rows
+    ([3000, 4500, 31], 16, 32, 4, 48, 16, False, "far"),
+    ([1200] * 24 + [0, 3], 4, 60, 10, 64, 64, True, "pow2"),            # 24 rows: a column of 16 and one of 8
 ]
 
 
@@ -123,16 +127,33 @@ def test_decode_many_rows(lens, nq, hq, hkv, page, block, csr, scales):
     test_decode(lens, nq, hq, hkv, page, block, csr, scales)
 
 
-@pytest.mark.parametrize("nq,hq,hkv", [(4, 16, 2), (16, 4, 2), (16, 8, 2), (16, 16, 2)])
-def test_decode_many_rows_far_queries_and_nans(nq, hq, hkv):
+@pytest.mark.parametrize("lens,nq,hq", [([0, 1, 15, 16, 17, 31, 32, 33, 64, 100], 4, 16), ([3, 4, 5, 200], 5, 14),
+                                        ([700, 3, 0, 2049], 3, 12)])
+def test_decode_many_rows_of_a_large_pool(lens, nq, hq):
+    """Short sequences in a pool of 64k tokens: the columns go by what the lists could name."""
+    dev = gpu_or_skip()
+    import causal_gqa_flashattention_attn_gb300 as attn
+    rng = np.random.default_rng(17)
+    cache = Cache(lens, 2, 32, 16, rng, True, "any")
+    for w in range(2):
+        cache.codes[w] = np.concatenate([cache.codes[w], np.full((2000, 32, 2, D), 0x7F, np.uint8)])
+        cache.scales[w] = np.concatenate([cache.scales[w], np.full((2000, 2, 2), np.nan, np.float32)])
+    q = bc.bf16(rng.standard_normal((len(lens), nq, hq, D)))
+    o, lse, status = decode(attn, q.to(dev), cache, dev)
+    assert status == 0
+    bc.check_attention(o, lse, reference(q.double().numpy(), cache))
+
+
+@pytest.mark.parametrize("nq,hq,hkv,more", [(4, 16, 2, 0), (16, 4, 2, 0), (16, 8, 2, 0), (16, 16, 2, 0), (16, 16, 2, 9)])
+def test_decode_many_rows_far_queries_and_nans(nq, hq, hkv, more):
     """Queries of any size, peaked scores, and NaNs that some rows see and others do not, 32 to 128 rows a KV head."""
     dev = gpu_or_skip()
     import causal_gqa_flashattention_attn_gb300 as attn
     rng = np.random.default_rng(nq + hq)
-    lens = [1500, 100, 77]
+    lens = [1500, 100, 77] + [1500] * more
     cache = Cache(lens, hkv, 64, 16, rng, scales="any")
     for size in (2.0 ** -120, 30.0, 2.0 ** 100):
-        q = bc.bf16(rng.standard_normal((3, nq, hq, D)) * size)
+        q = bc.bf16(rng.standard_normal((len(lens), nq, hq, D)) * size)
         q[0, 0, 0] = 0.0
         scale = D ** -0.5 / size if size != 30.0 else None
         o, lse, status = decode(attn, q.to(dev), cache, dev, scale=scale)
@@ -142,7 +163,7 @@ def test_decode_many_rows_far_queries_and_nans(nq, hq, hkv):
     put = [(0, 0, 0, 1499, 5), (1, 1, 1, 99 - (nq - 2), 9), (2, 1, 0, 76, 127), (2, 1, 0, 60, 0), (1, 0, 1, 98, 64)]
     for b, w, h, t, d in put:      # sequence, K or V, KV head, token, element
         cache.codes[w][cache.lists.rows[b][t // 64], t % 64, h, d] = 0x7F
-    want = torch.zeros(3, nq, hq, D, dtype=torch.bool)
+    want = torch.zeros(len(lens), nq, hq, D, dtype=torch.bool)
     g = hq // hkv
     for b, w, h, t, d in put:
         first = max(0, t - (lens[b] - nq))        # the first query that sees the token
