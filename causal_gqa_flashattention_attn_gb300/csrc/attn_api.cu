@@ -196,7 +196,7 @@ attn_status_t varlen_impl(const void* q, const void* k_cache, const void* v_cach
     if (total_q == 0) return ATTN_OK;
     VarlenArgs a{q,  k_cache, v_cache, qo_indptr, kv_indptr, kv_indices, kv_last_page_len, o,      lse,
                  B,  Hq,      Hkv,     D,         total_q,   num_pages,  page_size,        scale,  dev_status,
-                 kv_ws, max_kv_rows, false, nullptr};
+                 kv_ws, max_kv_rows, false, nullptr, nullptr};
     return from_cuda(launch_prefill_varlen_tc(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -155,6 +155,7 @@ struct VarlenArgs {
     // varlen_max_pairs() words of sequence << varlen_pair_bits() | query block
     // (used if there are no more of them); NULL: every CTA sorts them itself
     const uint32_t* order;
+    const int32_t* order_n;   // how many
 };
 // A paged cache's new tokens (kv_append.cu).
 struct AppendArgs {

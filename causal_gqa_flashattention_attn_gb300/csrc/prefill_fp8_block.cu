@@ -42,6 +42,7 @@ struct Params {
     uint32_t* order;  // [max_pairs], work items' (sequence, query block) pairs, longest first
     int32_t* start;   // [B + 1], first pages of the copy
     int32_t* last;    // [B], rows in each sequence's last page
+    int32_t* pairs;   // how many pairs there are
     uint4* k_copy;    // [copy rows, Hkv, D] bf16
     uint4* v_copy;
     int32_t* status;
@@ -159,7 +160,10 @@ __device__ __forceinline__ void sort_items(const Params& p, Shared& sh) {
         scan_cta<int>(blocks, sh.sums, all);
         pairs += all;
     }
-    if (threadIdx.x == 0) p.start[p.B] = start_of[p.B];
+    if (threadIdx.x == 0) {
+        p.start[p.B] = start_of[p.B];
+        *p.pairs = pairs;
+    }
     if (pairs > p.max_pairs) return;   // too many to sort: taken in sequence order
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // every pair and its key, one warp a sequence, lanes its query blocks
@@ -276,11 +280,11 @@ size_t copy_bytes(int B, int max_kv_rows, int Hkv) { return copy_rows(B, max_kv_
 
 }  // namespace
 
-// K copy, V copy, the work items' order, then the sequences' first pages and the
-// rows in their last.
+// K copy, V copy, the work items' order, then the sequences' first pages, the
+// rows in their last, and the number of pairs.
 size_t prefill_fp8_block_workspace(int B, int max_kv_rows, int Hkv) {
     return 2 * copy_bytes(B, max_kv_rows, Hkv) + varlen_max_pairs() * sizeof(uint32_t) +
-           ((2 * static_cast<size_t>(B) + 1) * sizeof(int32_t) + 15) / 16 * 16;
+           ((2 * static_cast<size_t>(B) + 2) * sizeof(int32_t) + 15) / 16 * 16;
 }
 
 cudaError_t launch_prefill_fp8_block(const PrefillBlockArgs& a, cudaStream_t stream) {
@@ -310,6 +314,7 @@ cudaError_t launch_prefill_fp8_block(const PrefillBlockArgs& a, cudaStream_t str
     p.pair_bits = varlen_pair_bits();
     p.start = reinterpret_cast<int32_t*>(p.order + p.max_pairs);
     p.last = p.start + a.B + 1;
+    p.pairs = p.last + a.B;
     p.status = a.dev_status;
     // gridDim.x: the sorting CTA and the copying ones
     static std::atomic<uint64_t> done{0};
@@ -346,6 +351,7 @@ cudaError_t launch_prefill_fp8_block(const PrefillBlockArgs& a, cudaStream_t str
     v.max_kv_rows = static_cast<int>(rows);
     v.copied = true;
     v.order = p.order;
+    v.order_n = p.pairs;
     return launch_prefill_varlen_tc(v, stream);
 }
 

@@ -103,7 +103,8 @@ struct Params {
     const __nv_bfloat16* v_pool;
     int page_size, pool_rows;
     int gathered;   // K/V come by TMA from a contiguous copy in page-list order
-    const uint32_t* order_in;   // the sorted pairs, kMaxOrder words (NULL: every CTA sorts them)
+    const uint32_t* order_in;   // the sorted pairs, *order_n of kMaxOrder words (NULL: every CTA sorts them)
+    const int32_t* order_n;
     // split schedule (dense only): the (item, KV tile) steps in item order
     // (batch, KV head, query block), cut into gridDim.x equal ranges
     long long sk_total;   // KV tile steps of all items
@@ -465,7 +466,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (p.order_in == nullptr && prefix[p.B] / p.Hkv <= kMaxOrder) varlen_sort_pairs(p, order, bucket, lane);
         } else if (p.order_in != nullptr) {
-            for (int k = threadIdx.x - 32; k < kMaxOrder; k += kThreads - 32) order[k] = p.order_in[k];
+            // (the first words come without waiting for how many there are)
+            const int n = *p.order_n;
+            int k = threadIdx.x - 32;
+            static_assert(kThreads - 32 <= kMaxOrder, "one word a thread");
+            order[k] = p.order_in[k];
+            for (k += kThreads - 32; k < min(n, kMaxOrder); k += kThreads - 32) order[k] = p.order_in[k];
         }
     }
     if constexpr (kSplit) {
@@ -1328,6 +1334,7 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, cudaStream_t stream) {
     p.page_size = p.pool_rows = 0;
     p.gathered = 0;
     p.order_in = nullptr;
+    p.order_n = nullptr;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     p.sec_bh = section_pairs(a, p.n_qb, p.n_items < sms ? p.n_items : sms);
@@ -1400,6 +1407,7 @@ cudaError_t launch_prefill_varlen_tc(const VarlenArgs& a, cudaStream_t stream) {
     p.v_pool = static_cast<const __nv_bfloat16*>(a.v_cache);
     p.gathered = a.kv_ws != nullptr;
     p.order_in = a.order;
+    p.order_n = a.order_n;
     p.sk_total = p.sk_per_bh = 0;
     p.sk_zero_qb = 0;
     p.sk_count = nullptr;
