@@ -316,18 +316,19 @@ cudaError_t launch_prefill_fp8_block(const PrefillBlockArgs& a, cudaStream_t str
     p.last = p.start + a.B + 1;
     p.pairs = p.last + a.B;
     p.status = a.dev_status;
-    // gridDim.x: the sorting CTA and the copying ones
+    // gridDim.x: the sorting CTA and the copying ones, no more than the copy has parts for
+    const size_t rows = copy_rows(a.B, a.max_kv_rows);
+    const unsigned copying = static_cast<unsigned>(std::min<size_t>(static_cast<size_t>(sms) * 4, rows / (kCopyRows * kWarps)));
     static std::atomic<uint64_t> done{0};
     cudaError_t e = once_per_device(done, [] {
         return cudaFuncSetAttribute(fp8_block_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(shared_bytes(kMaxSeqs)));
     });
     if (e != cudaSuccess) return e;
-    fp8_block_copy_kernel<<<dim3(1 + sms * 4, std::min((a.Hkv * (kD / 16) + 31) / 32, 64)), kThreads, shared_bytes(a.B), stream>>>(p);
+    fp8_block_copy_kernel<<<dim3(1 + copying, std::min((a.Hkv * (kD / 16) + 31) / 32, 64)), kThreads, shared_bytes(a.B), stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // the copy as a cache of kPage-token pages in list order
-    const size_t rows = copy_rows(a.B, a.max_kv_rows);
     VarlenArgs v{};
     v.q = a.q;
     v.k_cache = p.k_copy;
