@@ -558,7 +558,7 @@ cudaError_t launch_tokens(const Params& p, bool interleaved, int sms, cudaStream
     return cudaGetLastError();
 }
 
-// Ragged batches into 8-bit blocks.  Every warp copies kRows rows into shared
+// Ragged batches into 8-bit blocks.  Every warp copies up to kRows rows into shared
 // memory, all of them in flight at once, and works on them there, eight lanes a
 // row, four rows at a time.  17k tokens of 32 + 2 x 8 heads (378 MB): 71 us, 79 %
 // of the copy rate; alone the queries take 47 us (their bytes 41) and the blocks
@@ -572,6 +572,7 @@ cudaError_t launch_tokens(const Params& p, bool interleaved, int sms, cudaStream
 constexpr int kTaskWarps = 4;
 constexpr int kRows = 32;
 constexpr int kRowBytes = 2 * kD;
+constexpr int kTaskCtas = 4;   // an SM holds at once
 
 struct TaskMemory {
     uint4 rows[kTaskWarps][kRows * kRowBytes / 16];
@@ -715,11 +716,12 @@ __device__ __forceinline__ void query_task(const Params& p, int tile, int h0, ui
 }
 
 // One head's keys or values of one block of one sequence, by a group of `warps`
-// warps (this one is number `w` of them), kRows rows each: up to kRows * warps
-// new rows stay in shared memory between the maximum and the codes, rotated
-// ones in 16 bits rounded to odd; more are read and rotated again.
+// warps (this one is number `w` of them), n_rows rows each (at most kRows): up
+// to n_rows * warps new rows stay in shared memory between the maximum and the
+// codes, rotated ones in 16 bits rounded to odd; more are read and rotated again.
 template <bool kInter>
-__device__ __forceinline__ void block_task(const Params& p, int u, int pair, TaskMemory& mem, int w, int warps, int lane) {
+__device__ __forceinline__ void block_task(const Params& p, int u, int pair, TaskMemory& mem, int w, int warps, int n_rows,
+                                           int lane) {
     const int l = lane & 7, warp = threadIdx.x >> 5, group = warp / warps;
     uint4* buf = mem.rows[warp];
     const int b = warp_rank(p.B, u, lane, [&](int x) { return p.block_div.div(p.qo_indptr[x]) + 2 * x; });
@@ -738,10 +740,10 @@ __device__ __forceinline__ void block_task(const Params& p, int u, int pair, Tas
     const int h = key ? pair : pair - p.Hkv;
     const __nv_bfloat16* x0 = (key ? p.k : p.v) + h * kD;
     const long long stride = key ? p.k_stride : p.v_stride;
-    const int t_first = lo + w * kRows, t_step = warps * kRows;
+    const int t_first = lo + w * n_rows, t_step = warps * n_rows;
     const bool held = hi - lo <= t_step;
     auto source = [&](int t) { return reinterpret_cast<const uint4*>(x0 + (i0 + (t - start)) * stride); };
-    auto copy = [&](int t0) { copy_rows(buf, min(kRows, hi - t0), lane, [&](int r) { return source(t0 + r); }); };
+    auto copy = [&](int t0) { copy_rows(buf, min(n_rows, hi - t0), lane, [&](int r) { return source(t0 + r); }); };
     copy(t_first);
     const int entry = p.page_div.div(j0);
     const int page = page_at(p.list, b, entry, page_count(p.list, b), lane == 0 && w == 0 && pair == 0 ? p.status : nullptr);
@@ -763,7 +765,7 @@ __device__ __forceinline__ void block_task(const Params& p, int u, int pair, Tas
     auto turn_rows = [&](int t0) {
         cp_async_wait_all();
         __syncwarp();
-        const int m = min(kRows, hi - t0);
+        const int m = min(n_rows, hi - t0);
         if (turns) {
             Angles next;
             int pos;
@@ -820,7 +822,7 @@ __device__ __forceinline__ void block_task(const Params& p, int u, int pair, Tas
     if (any != 0) {
         own = 0.f;
         for (int t0 = t_first; t0 < hi; t0 += t_step)
-            for (int t = t0 + (lane >> 3); t < min(t0 + kRows, hi); t += 4) {
+            for (int t = t0 + (lane >> 3); t < min(t0 + n_rows, hi); t += 4) {
                 int pos;
                 if (is_there(t, pos))
                     own = fmaxf(own, size_again<kInter>(p, Source{source(t), c0, c1, turns ? pos : -1}, l));
@@ -838,7 +840,7 @@ __device__ __forceinline__ void block_task(const Params& p, int u, int pair, Tas
             copy(t0);
             turn_rows(t0);
         }
-        const int m = min(kRows, hi - t0);
+        const int m = min(n_rows, hi - t0);
 #pragma unroll 2
         for (int r = lane >> 3; r < m; r += 4) {
             int pos;
@@ -863,8 +865,8 @@ __device__ __forceinline__ void block_task(const Params& p, int u, int pair, Tas
 // new tokens touch at most n / block + 2 blocks, and S_{b+1} - S_b is at least
 // that, so no prefix sum is needed; the units left over do nothing.
 template <bool kInter>
-__global__ void __launch_bounds__(32 * kTaskWarps, 4) kv_append_blocks_kernel(const __grid_constant__ Params p,
-                                                                             int group_warps, int block_ctas) {
+__global__ void __launch_bounds__(32 * kTaskWarps, kTaskCtas) kv_append_blocks_kernel(const __grid_constant__ Params p,
+                                                                             int group_warps, int warp_rows, int block_ctas) {
     extern __shared__ __align__(128) uint8_t smem[];
     TaskMemory& mem = *reinterpret_cast<TaskMemory*>(smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -872,7 +874,7 @@ __global__ void __launch_bounds__(32 * kTaskWarps, 4) kv_append_blocks_kernel(co
         const long long task = static_cast<long long>(blockIdx.x) * (kTaskWarps / group_warps) + warp / group_warps;
         if (task < static_cast<long long>(p.n_units) * 2 * p.Hkv)
             block_task<kInter>(p, static_cast<int>(task / (2 * p.Hkv)), static_cast<int>(task % (2 * p.Hkv)), mem,
-                               warp % group_warps, group_warps, lane);
+                               warp % group_warps, group_warps, warp_rows, lane);
     } else {
         const long long task = static_cast<long long>(blockIdx.x - block_ctas) * kTaskWarps + warp;
         const int parts = (p.Hq + kPartHeads - 1) / kPartHeads;
@@ -922,8 +924,14 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
     if (!fp8) return launch_tokens<false>(p, a.interleaved != 0, sms, stream);
     if (a.qo_indptr == nullptr) return launch_tokens<true>(p, a.interleaved != 0, sms, stream);
     p.n_units = a.total_q / a.block_tokens + 2 * a.B;
-    const int group = a.block_tokens <= kRows ? 1 : (a.block_tokens <= 2 * kRows ? 2 : 4);
-    const long long block_ctas = (static_cast<long long>(p.n_units) * 2 * a.Hkv * group + kTaskWarps - 1) / kTaskWarps;
+    const long long tasks = static_cast<long long>(p.n_units) * 2 * a.Hkv;
+    int group = a.block_tokens <= kRows ? 1 : (a.block_tokens <= 2 * kRows ? 2 : 4);
+    // a block's rows over more warps while all of them run at once: 13 chunks, 1.7k
+    // tokens of 3 heads 8.1 -> 7.1 us with two (8.2 with four, which do not fit), one
+    // of 54 tokens 6.4 -> 4.5, 2 of 600 of 5 heads 10.1 -> 7.9
+    while (group < kTaskWarps && tasks * group * 2 <= static_cast<long long>(sms) * kTaskCtas * kTaskWarps) group *= 2;
+    const int warp_rows = std::min(kRows, (a.block_tokens / group + 3) / 4 * 4);
+    const long long block_ctas = (tasks * group + kTaskWarps - 1) / kTaskWarps;
     const long long queries =
         a.q != nullptr ? static_cast<long long>((a.total_q + kPartTokens - 1) / kPartTokens) * ((a.Hq + kPartHeads - 1) / kPartHeads) : 0;
     const long long grid = block_ctas + (queries + kTaskWarps - 1) / kTaskWarps;
@@ -939,7 +947,7 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
                                                        cudaSharedmemCarveoutMaxShared);
     });
     if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(grid), 32 * kTaskWarps, sizeof(TaskMemory), stream>>>(p, group, static_cast<int>(block_ctas));
+    kern<<<static_cast<unsigned>(grid), 32 * kTaskWarps, sizeof(TaskMemory), stream>>>(p, group, warp_rows, static_cast<int>(block_ctas));
     return cudaGetLastError();
 }
 
