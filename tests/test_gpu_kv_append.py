@@ -287,18 +287,19 @@ def test_append_fp8_block_steps(steps, hq, hkv, page, block, rot, inter, csr):
         old = [o + m for o, m in zip(old, new)]
 
 
-@pytest.mark.parametrize("inter", [False, True])
-def test_append_fp8_block_many_heads_positions_and_type(inter):
-    """300 + 2 x 100 heads, positions of their own, tensors of the float8 type."""
+@pytest.mark.parametrize("inter,page,block", [(False, 32, 16), (True, 64, 32), (False, 64, 64), (True, 256, 256)])
+def test_append_fp8_block_many_heads_positions_and_type(inter, page, block):
+    """240 + 2 x 120 heads (so many blocks that each takes as few warps as hold it), positions of their own, tensors of the
+    float8 type."""
     dev = gpu_or_skip()
     import causal_gqa_flashattention_attn_gb300 as attn
     rng = np.random.default_rng(31)
-    hq, hkv, page, block, new = 300, 100, 32, 16, [40, 25]
+    hq, hkv, new = 240, 120, [40, 25] if block < 256 else [200, 7]
     lists = bc.Lists(new, page, rng)
     pages, _ = lists.tensors(dev)
     batch = Batch([0, 0], new, hq, hkv, rng)
     table = bc.rope_table(900, 128)
-    pos = rng.permutation(65) * 13 % 900
+    pos = rng.permutation(sum(new)) * 13 % 900
     shape, blocks = (lists.num_pages, page, hkv, D), (lists.num_pages, page // block, hkv)
     dc = [torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2)]
     ds = [torch.zeros(blocks, device=dev) for _ in range(2)]
