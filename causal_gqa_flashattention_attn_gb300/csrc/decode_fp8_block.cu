@@ -17,18 +17,18 @@
 // rows; every warp of the grid takes one column and an equal share of the
 // 32-token tiles of all sequences, so a ragged batch is balanced whatever its
 // lengths, which only the device knows (a batch of short ones goes by whole
-// sequences).  A share that holds a whole sequence
-// writes its output; the pieces of a sequence that is cut between shares go to
-// the workspace, and a second kernel, which is launched along with the first
-// and waits for it on the device, joins them.  (The join by whichever CTA comes
-// last, inside the first kernel, was slower.)
+// sequences).  A share that holds a whole sequence writes its output; the pieces
+// of a sequence that is cut between shares go to the workspace, and a second
+// kernel, which is launched along with the first and waits for it on the device,
+// joins them.  (The join by whichever CTA comes last, inside the first kernel,
+// was slower.)
 //
 // Bound: one read of the codes from HBM.  64 ragged sequences of 512 to 32768
 // tokens, 32 heads over 8 (2.05 GB): 293 us, 7.0 TB/s; 16 of 16384 (537 MB): 88
 // us, 6.1 TB/s, 4 us of it the merge.  With 16 rows a column the loop is bound
 // by its own latency, 844 instructions a tile at two warps a scheduler (1.5 us
 // a tile): 24 sequences of up to 9000 tokens with 4 queries of 16 heads over 2
-// (57 MB) 35.7 us.  One sequence of 1000 tokens: 8.9 us for the two kernels,
+// (57 MB) 36 us.  One sequence of 1000 tokens: 9.3 us for the two kernels,
 // latency alone.  Tried: 12 warps with two stages each, 302 and 91 us for the
 // first two and 53 for the third (16 rows spill at 168 registers); a CTA that
 // widens a tile once into shared memory for its warps' groups of 16 rows, 43 us

@@ -12,8 +12,8 @@
 // block otherwise.
 //
 // Bound: the tensor cores.  8 sequences, 9.7k queries of 32 heads over 23.8k
-// tokens of 4 KV heads (360 GFLOP): 314.5 us, 1143 TFLOP/s, about 15 us of it
-// the copy before the prefill's first tile.  Three short prompts: 19.6 us, the
+// tokens of 4 KV heads (360 GFLOP): 311.5 us, 1155 TFLOP/s, about 15 us of it
+// the copy before the prefill's first tile.  Three short prompts: 17.5 us, the
 // latency of two launches and of five KV tiles one after another.
 #include <algorithm>
 

@@ -85,6 +85,8 @@ DECODE = [
     ([50, 1000, 0], 1, 40, 5, 1024, 512, False, "far"),
     ([500, 333], 2, 4, 4, 64, 16, True, "far"),
     ([4] * 300, 1, 2, 2, 16, 16, False, "pow2"),
+    ([0, 1, 96, 0, 33, 64, 0], 1, 8, 8, 64, 64, False, "pow2"),      # none long enough to be cut
+    ([0, 5, 96] * 200, 1, 12, 12, 16, 16, True, "any"),              # and several sequences a share
     ([65, 129, 40], 1, 300, 300, 16, 16, False, "any"),      # 300 KV heads: a column each, fewer shares
     ([40, 70], 16, 80, 80, 16, 16, False, "any"),
 ]
