@@ -693,16 +693,18 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) decode_fp8_block_merge_ke
     for (int i = 0; i < kMergeWarps; ++i) pre += sums[0][i], all += sums[1][i];
     const int n_tiles = tiles_of(length_of(p, b, false));
     const Cut cut(p.workers, all);
-    // the first kernel is done and its writes are here; CTAs without work wait
-    // too, so that this grid never ends before that one
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (n_tiles == 0 || bad || !cuts) return;
-    const int w0 = cut.share_of(pre), w1 = cut.share_of(pre + n_tiles - 1);
-    if (w0 == w1) return;   // one share held it all
+    int w0 = 0, w1 = 0;   // its first and last share
+    if (n_tiles != 0 && !bad && cuts) w0 = cut.share_of(pre), w1 = cut.share_of(pre + n_tiles - 1);
     const int r = (row / p.Hq) * p.G + row % p.G;
-    const int col = (r / rows_per_col) * p.Hkv + row % p.Hq / p.G;
+    int slot = ((r / rows_per_col) * p.Hkv + row % p.Hq / p.G) * rows_per_col + r % rows_per_col;
+    // the first kernel is done and its writes are here (what has been computed is
+    // computed before); CTAs without work wait too, so that this grid never ends
+    // before that one
+    asm volatile("griddepcontrol.wait;" : "+r"(w0), "+r"(w1), "+r"(slot)::"memory");
+    if (w0 == w1) return;   // one share held it all, or there is nothing
+    const int stride = p.cols * rows_per_col;
     auto at = [&](int w) -> size_t {   // the piece that starts the sequence is its share's second slot
-        return (static_cast<size_t>(2 * w + (w == w0 ? 1 : 0)) * p.cols + col) * rows_per_col + r % rows_per_col;
+        return static_cast<size_t>(2 * w + (w == w0 ? 1 : 0)) * stride + slot;
     };
     float top = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
