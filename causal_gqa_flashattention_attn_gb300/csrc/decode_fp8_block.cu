@@ -658,19 +658,19 @@ __global__ void __maxnreg__(NB == 1 ? 192 : 255) decode_fp8_block_kernel(const _
     }
 }
 
-// Joins the pieces of the sequences that were cut: `per_row` warps (1, 2, 4 or 8)
+// Joins the pieces of the sequences that were cut: 1 << per_shift warps (up to 8)
 // per output row, four elements a lane.  O = sum_s 2^(L_s - L) O_s / sum_s
 // 2^(L_s - L); each warp takes every per_row-th piece, kBatch at a time.
 __global__ void __launch_bounds__(32 * kMergeWarps, 4) decode_fp8_block_merge_kernel(const __grid_constant__ Params p,
-                                                                                  int rows_per_col, int per_row) {
+                                                                                  int rows_per_col, int per_shift) {
     __shared__ int sums[2][kMergeWarps];
     __shared__ float4 warp_acc[kMergeWarps][32];
     __shared__ float warp_top[kMergeWarps], warp_sum[kMergeWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = p.nq * p.Hq;
-    const int rows_per_cta = kMergeWarps / per_row;
+    const int per_row = 1 << per_shift, rows_per_cta = kMergeWarps >> per_shift;
     const int cta_per_seq = (rows + rows_per_cta - 1) / rows_per_cta;
-    const int b = blockIdx.x / cta_per_seq, row = blockIdx.x % cta_per_seq * rows_per_cta + warp / per_row;
+    const int b = blockIdx.x / cta_per_seq, row = blockIdx.x % cta_per_seq * rows_per_cta + (warp >> per_shift);
     // spans before the sequence, and of all of them
     int pre = 0, all = 0;
     bool cuts = false;
@@ -695,26 +695,28 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) decode_fp8_block_merge_ke
     const Cut cut(p.workers, all);
     int w0 = 0, w1 = 0;   // its first and last share
     if (n_tiles != 0 && !bad && cuts) w0 = cut.share_of(pre), w1 = cut.share_of(pre + n_tiles - 1);
-    const int r = (row / p.Hq) * p.G + row % p.G;
-    int slot = ((r / rows_per_col) * p.Hkv + row % p.Hq / p.G) * rows_per_col + r % rows_per_col;
-    // the first kernel is done and its writes are here (what has been computed is
-    // computed before); CTAs without work wait too, so that this grid never ends
-    // before that one
-    asm volatile("griddepcontrol.wait;" : "+r"(w0), "+r"(w1), "+r"(slot)::"memory");
+    // the warp's pieces: n rows of the workspace from `base` on, `step` apart (the
+    // piece that starts the sequence is its share's second slot, `first` rows on;
+    // fewer than 2^31 elements: two slots for each of the grid's warps)
+    const int r = (row / p.Hq) * p.G + row % p.G, skip = warp & (per_row - 1), slots = p.cols * rows_per_col;
+    int n = row < rows && w0 + skip <= w1 ? ((w1 - w0 - skip) >> per_shift) + 1 : 0;
+    int base = 2 * (w0 + skip) * slots + ((r / rows_per_col) * p.Hkv + row % p.Hq / p.G) * rows_per_col + r % rows_per_col;
+    int step = (2 << per_shift) * slots, first = skip == 0 ? slots : 0;
+    // the first kernel is done and its writes are here; CTAs without work wait
+    // too, so that this grid never ends before that one.  What has been computed
+    // is computed before.
+    asm volatile("griddepcontrol.wait;" : "+r"(w0), "+r"(w1), "+r"(n), "+r"(base), "+r"(step), "+r"(first)::"memory");
     if (w0 == w1) return;   // one share held it all, or there is nothing
-    const int stride = p.cols * rows_per_col;
-    auto at = [&](int w) -> size_t {   // the piece that starts the sequence is its share's second slot
-        return static_cast<size_t>(2 * w + (w == w0 ? 1 : 0)) * stride + slot;
-    };
     float top = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w = w0 + warp % per_row; row < rows && w <= w1; w += per_row * kBatch) {
-        const int m = min(kBatch, (w1 - w) / per_row + 1);
-        const float l = lane < m ? __ldcg(p.part_l + at(w + lane * per_row)) : -INFINITY;
+    for (; n > 0; n -= kBatch, base += kBatch * step, first = 0) {
+        const int m = min(kBatch, n);
+        const float l = lane < m ? __ldcg(p.part_l + base + lane * step + (lane == 0 ? first : 0)) : -INFINITY;
+        const float4* piece = reinterpret_cast<const float4*>(p.part_o) + base * (kD / 4) + lane;
         float4 v[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
-            if (i < m) v[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at(w + i * per_row) * kD) + lane);
+            if (i < m) v[i] = __ldcg(piece + (i * step + (i == 0 ? first : 0)) * (kD / 4));
         float high = l;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, off));
@@ -740,7 +742,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) decode_fp8_block_merge_ke
         warp_acc[warp][lane] = acc;
         if (lane == 0) warp_top[warp] = top, warp_sum[warp] = sum;
         __syncthreads();
-        if (warp % per_row != 0) return;
+        if (skip != 0) return;
         for (int i = 0; i < per_row; ++i) top = fmaxf(top, warp_top[warp + i]);
         sum = 0.f;
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -860,10 +862,11 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockArgs& a, cudaStream_t strea
     // more: as many warps to a row as there are pieces for, while the CTAs (four
     // fit on an SM) fit at once
     const long long all_rows = static_cast<long long>(a.B) * a.q_len * a.Hq;
-    int per_row = 1;
-    while (per_row < kMergeWarps && p.workers > 2LL * per_row * a.B && all_rows * 2 * per_row <= 4LL * sms * kMergeWarps)
-        per_row *= 2;
-    const int rows_per_cta = kMergeWarps / per_row;
+    int per_shift = 0;
+    while ((1 << per_shift) < kMergeWarps && p.workers > (2LL << per_shift) * a.B &&
+           all_rows << (per_shift + 1) <= 4LL * sms * kMergeWarps)
+        ++per_shift;
+    const int rows_per_cta = kMergeWarps >> per_shift;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -873,7 +876,7 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockArgs& a, cudaStream_t strea
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_fp8_block_merge_kernel, p, per, per_row);
+    return cudaLaunchKernelEx(&cfg, decode_fp8_block_merge_kernel, p, per, per_shift);
 }
 
 }  // namespace gb300
