@@ -72,6 +72,7 @@ struct Params {
     PageList list;
     const int32_t* seq_lens;
     Divisor page_div, block_div, cols_div, heads_div, group_div;
+    int page_blocks;     // blocks of a page
     bool tile_in_page;   // pages are multiples of a tile
     int B, Hq, Hkv, G, nq;
     int cols;       // KV heads x row groups
@@ -485,7 +486,7 @@ __device__ __forceinline__ void feed_tile(const Params& p, const int* before, Fe
         const size_t row_bytes = static_cast<size_t>(p.Hkv) * kD;
         const size_t off = (static_cast<size_t>(page) * p.list.page_size + o) * row_bytes + static_cast<size_t>(kvh) * kD;
         if ((lane & 15) == 0) {
-            const size_t at = (static_cast<size_t>(page) * (p.page_div.d / p.block_div.d) + p.block_div.div(o)) * p.Hkv + kvh;
+            const size_t at = (static_cast<size_t>(page) * p.page_blocks + p.block_div.div(o)) * p.Hkv + kvh;
             cp_async4(&info->k[lane >> 4], p.k_scale + at, there ? 4 : 0);
             cp_async4(&info->v[lane >> 4], p.v_scale + at, there ? 4 : 0);
         }
@@ -534,11 +535,11 @@ __global__ void __maxnreg__(NB == 1 ? 192 : 255) decode_fp8_block_kernel(const _
     __shared__ int warp_sum[kWarps];
     int* before = reinterpret_cast<int*>(smem + kWarps * kWarpBytes);
     int* lens = before + p.B + 1;
+    const bool cuts = count_tiles(p, before, lens, warp_sum, blockIdx.x == 0);
     if (too_many_tiles(p)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) flag_status(p.status, ATTN_DEV_SEQ_TOO_LONG);
         return;
     }
-    const bool cuts = count_tiles(p, before, lens, warp_sum, blockIdx.x == 0);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int total = before[p.B];
     const Cut cut(p.workers, total);
@@ -674,8 +675,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) decode_fp8_block_merge_ke
     // spans before the sequence, and of all of them
     int pre = 0, all = 0;
     bool cuts = false;
-    const bool bad = too_many_tiles(p);
-    for (int i = threadIdx.x; i < p.B && !bad; i += 32 * kMergeWarps) {
+    for (int i = threadIdx.x; i < p.B; i += 32 * kMergeWarps) {
         const int len = length_of(p, i, false), t = span_of(len);
         cuts |= tiles_of(len) > kWholeTiles;
         all += t;
@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) decode_fp8_block_merge_ke
     const int n_tiles = tiles_of(length_of(p, b, false));
     const Cut cut(p.workers, all);
     int w0 = 0, w1 = 0;   // its first and last share
-    if (n_tiles != 0 && !bad && cuts) w0 = cut.share_of(pre), w1 = cut.share_of(pre + n_tiles - 1);
+    if (n_tiles != 0 && cuts && !too_many_tiles(p)) w0 = cut.share_of(pre), w1 = cut.share_of(pre + n_tiles - 1);
     // the warp's pieces: n rows of the workspace from `base` on, `step` apart (the
     // piece that starts the sequence is its share's second slot, `first` rows on;
     // fewer than 2^31 elements: two slots for each of the grid's warps)
@@ -829,6 +829,7 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockArgs& a, cudaStream_t strea
     p.block_div = make_divisor(a.block_tokens);
     p.heads_div = make_divisor(a.Hkv);
     p.group_div = make_divisor(p.G);
+    p.page_blocks = a.page_size / a.block_tokens;
     p.tile_in_page = a.page_size % kTile == 0;
     const int per = rows_per_column(p, sms);
     p.cols_div = make_divisor(p.cols);

@@ -36,7 +36,7 @@ struct Params {
     const int32_t* seq_lens;
     const int32_t* qo_indptr;
     Divisor page_div, block_div;
-    int B, Hkv, max_rows;
+    int B, Hkv, max_rows, page_blocks;
     int q_block;      // query positions of a work item of the prefill
     int max_pairs, pair_bits;
     uint32_t* order;  // [max_pairs], work items' (sequence, query block) pairs, longest first
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) fp8_block_copy_kernel(const Params p
         const int n = page >= 0 ? min(kCopyRows, len - t0) : 0;
         const int o = t0 - entry * p.list.page_size;
         const size_t slot = static_cast<size_t>(page >= 0 ? page : 0) * p.list.page_size + o;
-        const size_t block = static_cast<size_t>(page >= 0 ? page : 0) * (p.page_div.d / p.block_div.d) + p.block_div.div(o);
+        const size_t block = static_cast<size_t>(page >= 0 ? page : 0) * p.page_blocks + p.block_div.div(o);
         for (uint32_t c = blockIdx.y; c < chunks; c += gridDim.y) {
             const int v0 = static_cast<int>(c) * 32, m = min(32, vecs - v0);   // vectors [v0, v0 + m) of each row
             const uint4* k_in = reinterpret_cast<const uint4*>(p.k_cache) + slot * vecs + v0 + lane;
@@ -304,6 +304,7 @@ cudaError_t launch_prefill_fp8_block(const PrefillBlockArgs& a, cudaStream_t str
     p.qo_indptr = a.qo_indptr;
     p.page_div = make_divisor(a.page_size);
     p.block_div = make_divisor(a.block_tokens);
+    p.page_blocks = a.page_size / a.block_tokens;
     p.q_block = 2 * (128 / (a.Hq / a.Hkv));
     p.max_rows = a.max_kv_rows;
     p.k_copy = reinterpret_cast<uint4*>(w);
