@@ -246,11 +246,11 @@ attn_status_t append_impl(const AppendArgs& a, int D, void* stream) {
     if (a.rot_dim > 0 && (a.cos_sin == nullptr || a.max_pos <= 0 || !aligned16(a.cos_sin))) return ATTN_ERR_INVALID_ARG;
     if (a.rot_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
     if (static_cast<long long>(a.Hq) + 2LL * a.Hkv >= (1LL << 24)) return ATTN_ERR_UNSUPPORTED;
-    // CTAs: at most one per token, per 8 tokens' 16 heads of queries, and per
-    // block's head of keys or values
-    const long long ctas = static_cast<long long>(a.total_q) + (a.total_q / 8 + 1LL) * (a.Hq / 16 + 1LL) +
-                           (a.total_q / 16 + 2LL * a.B) * 2 * a.Hkv;
-    if (ctas >= (1LL << 31)) return ATTN_ERR_UNSUPPORTED;
+    // warps are counted in int: at most two per token, one per 8 tokens' 4 heads of
+    // queries, and four per block's head of keys or values
+    const long long warps = 2LL * a.total_q + (a.total_q / 8 + 1LL) * (a.Hq / 4 + 1LL) +
+                            (a.total_q / 16 + 2LL * a.B) * 8 * a.Hkv;
+    if (warps >= (1LL << 31) - 64) return ATTN_ERR_UNSUPPORTED;
     if (a.total_q == 0) return ATTN_OK;
     return from_cuda(launch_kv_append(a, static_cast<cudaStream_t>(stream)));
 }

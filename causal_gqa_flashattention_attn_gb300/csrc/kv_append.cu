@@ -51,6 +51,7 @@ struct Params {
     int max_pos, rot, B, total_q, Hq, Hkv, block;
     bool wide;   // every row starts on 32 bytes
     Divisor page_div, block_div;
+    Divisor pair_div, part_div;   // 2 Hkv, and Hq over the heads of a query task
     int n_units;   // ragged batches into 8-bit blocks: blocks of tokens, and spare ones
     int32_t* status;
 };
@@ -722,7 +723,7 @@ __device__ __forceinline__ void query_task(const Params& p, int tile, int h0, ui
 template <bool kInter>
 __device__ __forceinline__ void block_task(const Params& p, int u, int pair, TaskMemory& mem, int w, int warps, int n_rows,
                                            int lane) {
-    const int l = lane & 7, warp = threadIdx.x >> 5, group = warp / warps;
+    const int l = lane & 7, warp = threadIdx.x >> 5, group = (warp - w) >> (warps >> 1);   // warps: 1, 2 or 4
     uint4* buf = mem.rows[warp];
     const int b = warp_rank(p.B, u, lane, [&](int x) { return p.block_div.div(p.qo_indptr[x]) + 2 * x; });
     const int i0 = p.qo_indptr[b], n = p.qo_indptr[b + 1] - i0;
@@ -866,20 +867,22 @@ __device__ __forceinline__ void block_task(const Params& p, int u, int pair, Tas
 // that, so no prefix sum is needed; the units left over do nothing.
 template <bool kInter>
 __global__ void __launch_bounds__(32 * kTaskWarps, kTaskCtas) kv_append_blocks_kernel(const __grid_constant__ Params p,
-                                                                             int group_warps, int warp_rows, int block_ctas) {
+                                                                             int group_shift, int warp_rows, int block_ctas) {
     extern __shared__ __align__(128) uint8_t smem[];
     TaskMemory& mem = *reinterpret_cast<TaskMemory*>(smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // (the host has checked that tasks are counted in int)
     if (static_cast<int>(blockIdx.x) < block_ctas) {
-        const long long task = static_cast<long long>(blockIdx.x) * (kTaskWarps / group_warps) + warp / group_warps;
-        if (task < static_cast<long long>(p.n_units) * 2 * p.Hkv)
-            block_task<kInter>(p, static_cast<int>(task / (2 * p.Hkv)), static_cast<int>(task % (2 * p.Hkv)), mem,
-                               warp % group_warps, group_warps, warp_rows, lane);
+        const int task = static_cast<int>(blockIdx.x) * (kTaskWarps >> group_shift) + (warp >> group_shift);
+        const int unit = p.pair_div.div(task), group_warps = 1 << group_shift;
+        if (unit < p.n_units)
+            block_task<kInter>(p, unit, task - unit * static_cast<int>(p.pair_div.d), mem, warp & (group_warps - 1), group_warps,
+                               warp_rows, lane);
     } else {
-        const long long task = static_cast<long long>(blockIdx.x - block_ctas) * kTaskWarps + warp;
-        const int parts = (p.Hq + kPartHeads - 1) / kPartHeads;
-        if (task < static_cast<long long>((p.total_q + kPartTokens - 1) / kPartTokens) * parts)
-            query_task<kInter>(p, static_cast<int>(task / parts), static_cast<int>(task % parts) * kPartHeads, mem.rows[warp], lane);
+        const int task = (static_cast<int>(blockIdx.x) - block_ctas) * kTaskWarps + warp;
+        const int tile = p.part_div.div(task);
+        if (tile * kPartTokens < p.total_q)
+            query_task<kInter>(p, tile, (task - tile * static_cast<int>(p.part_div.d)) * kPartHeads, mem.rows[warp], lane);
     }
 }
 
@@ -925,17 +928,19 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
     if (a.qo_indptr == nullptr) return launch_tokens<true>(p, a.interleaved != 0, sms, stream);
     p.n_units = a.total_q / a.block_tokens + 2 * a.B;
     const long long tasks = static_cast<long long>(p.n_units) * 2 * a.Hkv;
-    int group = a.block_tokens <= kRows ? 1 : (a.block_tokens <= 2 * kRows ? 2 : 4);
+    int shift = a.block_tokens <= kRows ? 0 : (a.block_tokens <= 2 * kRows ? 1 : 2);   // log2 of a group's warps
     // a block's rows over more warps while all of them run at once: 13 chunks, 1.7k
     // tokens of 3 heads 8.1 -> 7.1 us with two (8.2 with four, which do not fit), one
     // of 54 tokens 6.4 -> 4.5, 2 of 600 of 5 heads 10.1 -> 7.9
-    while (group < kTaskWarps && tasks * group * 2 <= static_cast<long long>(sms) * kTaskCtas * kTaskWarps) group *= 2;
-    const int warp_rows = std::min(kRows, (a.block_tokens / group + 3) / 4 * 4);
-    const long long block_ctas = (tasks * group + kTaskWarps - 1) / kTaskWarps;
-    const long long queries =
-        a.q != nullptr ? static_cast<long long>((a.total_q + kPartTokens - 1) / kPartTokens) * ((a.Hq + kPartHeads - 1) / kPartHeads) : 0;
+    while ((1 << shift) < kTaskWarps && tasks << (shift + 1) <= static_cast<long long>(sms) * kTaskCtas * kTaskWarps) ++shift;
+    const int warp_rows = std::min(kRows, ((a.block_tokens >> shift) + 3) / 4 * 4);
+    const long long block_ctas = ((tasks << shift) + kTaskWarps - 1) / kTaskWarps;
+    const int parts = (a.Hq + kPartHeads - 1) / kPartHeads;
+    const long long queries = a.q != nullptr ? static_cast<long long>((a.total_q + kPartTokens - 1) / kPartTokens) * parts : 0;
+    p.pair_div = make_divisor(2 * a.Hkv);
+    p.part_div = make_divisor(parts);
     const long long grid = block_ctas + (queries + kTaskWarps - 1) / kTaskWarps;
-    if (grid >= (1LL << 31)) return cudaErrorInvalidConfiguration;
+    if (grid * kTaskWarps >= (1LL << 31)) return cudaErrorInvalidConfiguration;
     auto kern = a.interleaved ? kv_append_blocks_kernel<true> : kv_append_blocks_kernel<false>;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = once_per_device(done, [] {
@@ -947,7 +952,7 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
                                                        cudaSharedmemCarveoutMaxShared);
     });
     if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(grid), 32 * kTaskWarps, sizeof(TaskMemory), stream>>>(p, group, warp_rows, static_cast<int>(block_ctas));
+    kern<<<static_cast<unsigned>(grid), 32 * kTaskWarps, sizeof(TaskMemory), stream>>>(p, shift, warp_rows, static_cast<int>(block_ctas));
     return cudaGetLastError();
 }
 
