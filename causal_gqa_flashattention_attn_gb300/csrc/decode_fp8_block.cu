@@ -24,15 +24,15 @@
 // was slower.)
 //
 // Bound: one read of the codes from HBM.  64 ragged sequences of 512 to 32768
-// tokens, 32 heads over 8 (2.05 GB): 293 us, 7.0 TB/s; 16 of 16384 (537 MB): 88
-// us, 6.1 TB/s, 4 us of it the merge.  With 16 rows a column the loop is bound
+// tokens, 32 heads over 8 (2.05 GB): 292 us, 7.0 TB/s; 16 of 16384 (537 MB): 87
+// us, 6.2 TB/s, 3 us of it the merge.  With 16 rows a column the loop is bound
 // by its own latency, 844 instructions a tile at two warps a scheduler (1.5 us
 // a tile): 24 sequences of up to 9000 tokens with 4 queries of 16 heads over 2
-// (57 MB) 36 us.  One sequence of 1000 tokens: 9.3 us for the two kernels,
-// latency alone.  Tried: 12 warps with two stages each, 302 and 91 us for the
+// (57 MB) 32.5 us.  One sequence of 1000 tokens: 8.2 us for the two kernels,
+// latency alone.  Tried, with an earlier merge: 12 warps with two stages each, 302 and 91 us for the
 // first two and 53 for the third (16 rows spill at 168 registers); a CTA that
 // widens a tile once into shared memory for its warps' groups of 16 rows, 43 us
-// for 24 sequences of 4500 tokens and 32 rows where the warps alone take 32, 57
+// for 24 sequences of 4500 tokens and 32 rows where the warps alone took 32, 59
 // for 57 at 64 rows and 85 for 98 only at 128.
 #include <algorithm>
 
@@ -860,11 +860,12 @@ cudaError_t launch_decode_fp8_block(const DecodeBlockArgs& a, cudaStream_t strea
     e = cudaGetLastError();
     if (e != cudaSuccess || p.workers == 1) return e;   // one share per column: no sequence is cut
     // a sequence has about workers / B pieces, one that is longer than the others
-    // more: as many warps to a row as there are pieces for, while the CTAs (four
-    // fit on an SM) fit at once
+    // more: as many warps to a row as there are kBatch pieces for, while the CTAs
+    // (four fit on an SM) fit at once (one for every two pieces took 0.9 % longer
+    // over 164 batches of all sizes)
     const long long all_rows = static_cast<long long>(a.B) * a.q_len * a.Hq;
     int per_shift = 0;
-    while ((1 << per_shift) < kMergeWarps && p.workers > (2LL << per_shift) * a.B &&
+    while ((1 << per_shift) < kMergeWarps && p.workers > (static_cast<long long>(kBatch) << per_shift) * a.B &&
            all_rows << (per_shift + 1) <= 4LL * sms * kMergeWarps)
         ++per_shift;
     const int rows_per_cta = kMergeWarps >> per_shift;

@@ -561,7 +561,7 @@ cudaError_t launch_tokens(const Params& p, bool interleaved, int sms, cudaStream
 
 // Ragged batches into 8-bit blocks.  Every warp copies up to kRows rows into shared
 // memory, all of them in flight at once, and works on them there, eight lanes a
-// row, four rows at a time.  17k tokens of 32 + 2 x 8 heads (378 MB): 71 us, 79 %
+// row, four rows at a time.  17k tokens of 32 + 2 x 8 heads (378 MB): 70.5 us, 80 %
 // of the copy rate; alone the queries take 47 us (their bytes 41) and the blocks
 // 40 (their bytes 15), bound by what a warp waits for at four warps a scheduler.
 // Tried: unrolled over rows in registers 120 us (a quarter of it waiting for
