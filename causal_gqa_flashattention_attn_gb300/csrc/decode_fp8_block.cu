@@ -26,7 +26,7 @@
 // Bound: one read of the codes from HBM.  64 ragged sequences of 512 to 32768
 // tokens, 32 heads over 8 (2.05 GB): 292 us, 7.0 TB/s; 16 of 16384 (537 MB): 87
 // us, 6.2 TB/s, 3 us of it the merge.  With 16 rows a column the loop is bound
-// by its own latency, 844 instructions a tile at two warps a scheduler (1.5 us
+// by its own latency, 832 instructions a tile at two warps a scheduler (1.5 us
 // a tile): 24 sequences of up to 9000 tokens with 4 queries of 16 heads over 2
 // (57 MB) 32.5 us.  One sequence of 1000 tokens: 8.2 us for the two kernels,
 // latency alone.  Tried, with an earlier merge: 12 warps with two stages each, 302 and 91 us for the
