@@ -255,6 +255,13 @@ attn_status_t append_impl(const AppendArgs& a, int D, void* stream) {
     return from_cuda(launch_kv_append(a, static_cast<cudaStream_t>(stream)));
 }
 
+// Sizes that the block-scaled readers take: rows of a decode, rows of the prefill's copy.
+bool decode_rows_ok(int q_len, int Hq) { return static_cast<long long>(Hq) * q_len < (1LL << 20); }
+bool copy_rows_ok(int B, int max_kv_rows, int Hkv) {
+    const long long rows = static_cast<long long>(max_kv_rows) + 128LL * B;   // each sequence's up to the next multiple of 128
+    return rows < (1LL << 31) && rows <= ((1LL << 33) - 1) / Hkv;
+}
+
 }  // namespace
 
 extern "C" {
@@ -610,6 +617,7 @@ attn_status_t attn_kv_append_fp8_block(const void* q, const void* k, const void*
 
 size_t attn_decode_fp8_block_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D) {
     if (B <= 0 || q_len <= 0 || q_len > 16 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D != 128) return 0;
+    if (!decode_rows_ok(q_len, Hq)) return 0;
     const int sms = device_sm_count();
     return sms > 0 ? decode_fp8_block_workspace(q_len, Hq, Hkv, sms) : 0;
 }
@@ -627,11 +635,11 @@ attn_status_t attn_decode_paged_fp8_block(const void* q, const void* k_cache, co
     if (st != ATTN_OK) return st;
     if (!std::isfinite(scale) || !aligned16(q) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
     if (q_len > 16 || B > decode_fp8_block_max_seqs()) return ATTN_ERR_UNSUPPORTED;
-    if (static_cast<long long>(Hq) * q_len >= (1LL << 20) || static_cast<long long>(Hq) * q_len * B >= (1LL << 31))
+    if (!decode_rows_ok(q_len, Hq) || static_cast<long long>(Hq) * q_len * B >= (1LL << 31))
         return ATTN_ERR_UNSUPPORTED;
     // tiles of 32 tokens, and two more for each sequence's end, are counted in int
     if (kv_indptr == nullptr &&
-        (static_cast<long long>(max_pages_per_seq) * page_size / 32 + 3) * B >= (1LL << 31))
+        static_cast<long long>(max_pages_per_seq) * page_size / 32 + 3 > ((1LL << 31) - 1) / B)
         return ATTN_ERR_UNSUPPORTED;
     if (workspace == nullptr || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
     const int sms = device_sm_count();
@@ -644,7 +652,7 @@ attn_status_t attn_decode_paged_fp8_block(const void* q, const void* k_cache, co
 }
 
 size_t attn_prefill_fp8_block_workspace_bytes(int B, int max_kv_rows, int Hkv, int D) {
-    if (B <= 0 || max_kv_rows <= 0 || Hkv <= 0 || D != 128) return 0;
+    if (B <= 0 || max_kv_rows <= 0 || Hkv <= 0 || D != 128 || !copy_rows_ok(B, max_kv_rows, Hkv)) return 0;
     return prefill_fp8_block_workspace(B, max_kv_rows, Hkv);
 }
 
@@ -666,10 +674,7 @@ attn_status_t attn_prefill_paged_fp8_block(const void* q, const void* k_cache, c
     if (Hq / Hkv > 128 || B > varlen_max_seqs() || scale <= 0.f) return ATTN_ERR_UNSUPPORTED;
     // as attn_prefill_paged_varlen: items and query blocks are counted in int and 21 bits
     if (total_q >= (1 << 22) || (static_cast<long long>(total_q) + B) * Hkv >= (1LL << 31)) return ATTN_ERR_UNSUPPORTED;
-    // rows of the copy, each sequence's up to the next multiple of 128, are counted in int
-    if (static_cast<long long>(max_kv_rows) + 128LL * B >= (1LL << 31) ||
-        (static_cast<long long>(max_kv_rows) + 128LL * B) * Hkv >= (1LL << 33))
-        return ATTN_ERR_UNSUPPORTED;
+    if (!copy_rows_ok(B, max_kv_rows, Hkv)) return ATTN_ERR_UNSUPPORTED;
     if (workspace == nullptr || !aligned16(workspace) ||
         workspace_bytes < prefill_fp8_block_workspace(B, max_kv_rows, Hkv))
         return ATTN_ERR_WORKSPACE;

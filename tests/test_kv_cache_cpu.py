@@ -99,6 +99,7 @@ def test_decode_validation(L):
     assert _decode(L, scale=float("nan")) == -1
     assert _decode(L, B=4097) == -2
     assert _decode(L, B=4096, mp=1 << 18) == -2              # tiles past int
+    assert _decode(L, B=4096, mp=(1 << 31) - 1, ps=(1 << 31) - 64, pages=1, block=64) == -2   # and past 64 bits
     assert _decode(L, Hq=1 << 20, Hkv=1 << 20) == -2
     assert _decode(L, ws=None) == -3
     assert _decode(L, ws=ODD) == -3
@@ -106,6 +107,9 @@ def test_decode_validation(L):
     assert attn.attn_decode_fp8_block_workspace_bytes(0, 1, 32, 8) == 0
     assert attn.attn_decode_fp8_block_workspace_bytes(2, 17, 32, 8) == 0
     assert attn.attn_decode_fp8_block_workspace_bytes(2, 1, 30, 8) == 0
+    # heads beyond what the entry takes, whose rows would pass 32 bits
+    assert attn.attn_decode_fp8_block_workspace_bytes(1, 16, 1 << 28, 1) == 0
+    assert attn.attn_decode_fp8_block_workspace_bytes(1, 1, (1 << 31) - 1, 1) == 0
     if torch.cuda.is_available():
         assert _decode(L) == -3                              # a workspace of no bytes
     else:
@@ -126,6 +130,8 @@ def test_prefill_validation(L):
     # 4096 words of order; 5 page words, rounded to 16 bytes
     assert need == 2 * 640 * 8 * 128 * 2 + 4096 * 4 + 32
     assert attn.attn_prefill_fp8_block_workspace_bytes(2, 0, 8) == 0
+    assert attn.attn_prefill_fp8_block_workspace_bytes(1, (1 << 31) - 1, 8) == 0     # beyond what the entry takes
+    assert attn.attn_prefill_fp8_block_workspace_bytes(1, 1 << 30, (1 << 31) - 1) == 0
     assert _prefill(L, bytes=need) == 0
     assert _prefill(L, bytes=need - 1) == -3
     assert _prefill(L, ws=None) == -3
