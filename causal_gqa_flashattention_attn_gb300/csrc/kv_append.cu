@@ -228,6 +228,9 @@ __device__ __forceinline__ float old_scale_of(float s) {
 // Values below this make fp32's products subnormal; a block whose largest one is
 // there has its rotated codes computed from scaled inputs.
 constexpr float kTiny = 7.8886090522101181e-31f;   // 2^-100
+// From here on a rotation may pass fp32's range, and cross_exact no longer takes
+// back what it rounds: such a block's rotated codes come from scaled inputs too.
+constexpr float kHuge = 3.0e38f;
 
 // 1 / s for s = 0 (0) or a power of two from 2^-126 to 2^126.
 __device__ __forceinline__ float inverse_of(float s) {
@@ -260,7 +263,7 @@ __device__ __forceinline__ float size_of(const Pairs& z) {
 __device__ __forceinline__ bool doubtful(float top, float own, bool rotated) {
     const int edge = static_cast<int>(__float_as_uint(top) & 0x7FFFFFu) - 0x600000;
     const bool lanes = rotated && __float_as_uint(own) + 8u >= __float_as_uint(top);
-    return (lanes && edge >= -4 && edge <= 4) || !(top < 3.0e38f);
+    return (lanes && edge >= -4 && edge <= 4) || !(top < kHuge);
 }
 
 // Whether fp32's value v of a rotated element (2 units off at most, scaled by
@@ -280,7 +283,7 @@ __device__ __forceinline__ float cross_exact(float a, float c, float b, float s)
     const float low = (fmaf(a, c, -p) - fmaf(b, s, -q)) + err;   // with the products' own
     const float h = r + low;
     const float rest = low - (h - r);
-    if (!(fabsf(h) < 3.0e38f)) return p - q;                     // infinities and NaN as they come
+    if (!(fabsf(h) < kHuge)) return p - q;                       // infinities and NaN as they come
     if (rest == 0.f) return h;
     const uint32_t u = __float_as_uint(h);
     // towards zero: one unit back where the rest points inwards
@@ -309,7 +312,7 @@ __device__ __noinline__ float size_again(const Params& p, const Source r, int l)
         load_angles(p, r.pos, l, t);
         auto turned = [&](float a, float c, float b, float s) {
             const float x = cross_exact(a, c, b, s);
-            return !(fabsf(x) < 3.0e38f) && fabsf(a) <= 3.4e38f && fabsf(b) <= 3.4e38f ? 3.402823466e38f : x;
+            return !(fabsf(x) < kHuge) && fabsf(a) <= 3.4e38f && fabsf(b) <= 3.4e38f ? 3.402823466e38f : x;
         };
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -848,7 +851,8 @@ __device__ __forceinline__ void block_task(const Params& p, int u, int pair, Tas
             if (!is_there(t0 + r, pos)) continue;
             uint2* row = reinterpret_cast<uint2*>(cells + (t0 + r - j0) * row_bytes);
             uint2 x = codes_of(buf[r * 16 + c0], inv), y = codes_of(buf[r * 16 + c1], inv);
-            if (turns && top < kTiny) {   // 16 bits rounded to odd do not hold such values' last bits
+            // 16 bits rounded to odd do not hold the last bits of tiny values, nor those past fp32's range
+            if (turns && (top < kTiny || !(top < kHuge))) {
                 const uint4 codes = codes_again<kInter>(p, Source{source(t0 + r), c0, c1, pos}, inv, l);
                 x = make_uint2(codes.x, codes.y);
                 y = make_uint2(codes.z, codes.w);

@@ -188,6 +188,48 @@ def test_append_fp8_block_rotated_far_from_one(size):
             assert np.array_equal(bc.E4M3[got], bc.E4M3[codes[w]]), (new, "kv"[w])
 
 
+@pytest.mark.parametrize("block", [32, 256])
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_fp8_block_rotated_past_fp32(inter, block):
+    """Keys whose rotation passes fp32's range, or comes near its end: the code of the exact value, whether a token comes alone
+    or within a prompt (blocks that stay in shared memory and ones that do not).  Infinities and NaN beside them."""
+    dev = gpu_or_skip()
+    import causal_gqa_flashattention_attn_gb300 as attn
+    rng = np.random.default_rng(41 + block)
+    table = bc.rope_table(300, D)
+    table[7] = np.float32(np.sqrt(0.5))                       # cosines and sines alike
+    cs = torch.from_numpy(table).to(dev)
+    for new, ragged in (([1, 1, 1], False), ([20, 3, 33], True), ([250, 130, 9], True)):
+        t = np.concatenate([np.arange(n) for n in new])
+        total = len(t)
+        k = bc.bf16(rng.uniform(0.7, 0.99, (total, 2, D)) * rng.choice([-1.0, 1.0], (total, 2, D)) * 2.0 ** 128)
+        k[0, 0], k[-1, 1] = 3.0e38, -3.0e38                   # 4.2e38 in every element of one half at position 7
+        k[1, 0, 3:9] = float("inf")
+        k[2, 1, 60:70] = float("nan")
+        pos = t.copy()
+        pos[[0, -1]] = 7
+        lists = bc.Lists([256] * 3, 256, rng)
+        pages, _ = lists.tensors(dev)
+        shape, blocks = (lists.num_pages, 256, 2, D), (lists.num_pages, 256 // block, 2)
+        codes, scales = np.zeros(shape, np.uint8), np.zeros(blocks, np.float32)
+        dc = [torch.zeros(shape, dtype=torch.uint8, device=dev) for _ in range(2)]
+        ds = [torch.zeros(blocks, device=dev) for _ in range(2)]
+        ptr = np.cumsum([0] + new)
+        attn.attn_kv_append_fp8_block(None, k.to(dev), k.to(dev), *dc, *ds, pages, torch.tensor(new, dtype=torch.int32, device=dev),
+                                      cos_sin=cs, positions=torch.tensor(pos, dtype=torch.int32, device=dev), interleaved=inter,
+                                      qo_indptr=torch.tensor(ptr, dtype=torch.int32, device=dev) if ragged else None)
+        torch.cuda.synchronize()
+        turned = bc.rotate(k.double().numpy(), table, pos, inter)
+        assert np.nanmax(np.abs(np.where(np.isinf(turned), 0, turned))) > 4.2e38
+        for b in range(3):
+            bc.append_blocks(codes, scales, lists, block, b, 0, turned[ptr[b]:ptr[b + 1]])
+        assert np.array_equal(ds[0].cpu().numpy(), scales)
+        got, want = bc.E4M3[dc[0].cpu().numpy()], bc.E4M3[codes]
+        assert np.array_equal(np.isnan(got), np.isnan(want)), new
+        off = np.argwhere(np.nan_to_num(got) != np.nan_to_num(want))
+        assert not len(off), (new, len(off), off[:3], got[tuple(off[0])], want[tuple(off[0])])
+
+
 def test_append_positions_in_place_padding_and_keys_only():
     """Positions of the caller's, q rotated in place, padded entries of length 0 and rows of no sequence left alone, no q."""
     dev = gpu_or_skip()
