@@ -639,7 +639,9 @@ def attn_prefill_paged_fp8_block(q, k_cache, v_cache, k_scale, v_scale, qo_indpt
     writes: ``q [total_q, Hq, D]`` bf16, rows ``qo_indptr[b]`` up to
     ``qo_indptr[b+1]`` being the last positions of sequence b's ``seq_lens[b]``
     cached tokens.  ``max_kv_rows``: at least the sum of ``seq_lens``, which
-    sizes the workspace (by default all that the page lists can hold).
+    sizes the workspace, 512 bytes per row and KV head (by default all that the
+    page lists can hold, padding included: a serving loop gives its own bound;
+    ``ValueError`` where that is more than a workspace may hold).
     ``scale`` (by default ``D ** -0.5``) is positive.
     ``workspace``: a uint8 tensor of attn_prefill_fp8_block_workspace_bytes()
     bytes.  Returns ``(o [total_q, Hq, D], lse [total_q, Hq], workspace)``.

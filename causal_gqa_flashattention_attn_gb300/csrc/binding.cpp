@@ -350,6 +350,10 @@ PyObject* prefill_fp8_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (!args.none(9)) {
             rows = PyLong_AsLongLong(args.a[9]);
             if (rows == -1 && PyErr_Occurred()) throw 0;
+        } else if (rows > 0x7FFFFFFF || (rows > 0 && s.count > 0 && c.hkv > 0 && c.d == 128 &&
+                                         attn_prefill_fp8_block_workspace_bytes(s.count, static_cast<int>(rows), c.hkv, c.d) == 0)) {
+            throw Refused("the page lists hold " + std::to_string(rows) +
+                          " tokens, more than a workspace may: max_kv_rows has to be given");
         }
         const int max_rows = small("max_kv_rows", std::max(rows, -1LL));
         at::Tensor ws, o, lse;

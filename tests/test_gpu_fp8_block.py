@@ -473,6 +473,30 @@ def test_prefill_many_sequences(n, new, hq):
         bc.check_attention(o[rows], lse[rows], bc.attend(q[rows].double().numpy(), *cache.values(b), weight_step=2.0 ** -8, small=0.0))
 
 
+def _wide_table(hkv, dev):
+    """An empty batch of 64 whose block table is 131071 pages of 256 tokens wide: 2^31 - 16384 tokens."""
+    codes = torch.zeros(2, 256, hkv, D, dtype=torch.uint8, device=dev)
+    scales = torch.ones(2, 4, hkv, device=dev)
+    return dict(q=torch.zeros(64, hkv, D, dtype=torch.bfloat16, device=dev), k_cache=codes, v_cache=codes, k_scale=scales,
+                v_scale=scales, qo_indptr=torch.arange(65, dtype=torch.int32, device=dev),
+                block_table=torch.zeros(64, 131071, dtype=torch.int32, device=dev),
+                seq_lens=torch.ones(64, dtype=torch.int32, device=dev))
+
+
+def test_prefill_default_rows_past_the_limit():
+    """Page lists that hold more than a workspace may: refused by name where max_kv_rows is left out, taken where it is given."""
+    dev = gpu_or_skip()
+    import causal_gqa_flashattention_attn_gb300 as attn
+    call = _wide_table(8, dev)
+    with pytest.raises(ValueError, match="max_kv_rows"):
+        attn.attn_prefill_paged_fp8_block(**call)
+    with pytest.raises(attn.AttnError, match="unsupported"):      # as the entry says of what the caller asks for
+        attn.attn_prefill_paged_fp8_block(**call, max_kv_rows=64 * 131071 * 256)
+    o, lse, _ = attn.attn_prefill_paged_fp8_block(**call, max_kv_rows=64)
+    torch.cuda.synchronize()
+    assert not o.any() and not lse.any()      # a token of zeros each
+
+
 def test_calls_on_two_streams_at_once():
     """Decodes and prefills of two batches on two streams, each with its own workspace, give what they give alone."""
     dev = gpu_or_skip()
