@@ -11,10 +11,12 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
 #include <cmath>
+#include <exception>
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
@@ -178,15 +180,16 @@ void check(const char* fn, attn_status_t status) {
     throw 0;   // the Python error is set
 }
 
-// Runs `body`; C++ exceptions become Python's.
+// Runs `body`; C++ exceptions become Python's, torch's their own (an allocation
+// that fails is an OutOfMemoryError here as anywhere).
 template <typename Body>
 PyObject* guarded(Body body) {
     try {
         return body();
     } catch (const Refused& e) {
         PyErr_SetString(PyExc_ValueError, e.what());
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (const std::exception&) {
+        torch::translate_exception_to_python(std::current_exception());
     } catch (int) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "call failed");
     } catch (...) {

@@ -497,6 +497,18 @@ def test_prefill_default_rows_past_the_limit():
     assert not o.any() and not lse.any()      # a token of zeros each
 
 
+def test_out_of_memory_is_torchs():
+    """A workspace that the GPU has no room for raises torch's own error, as an allocation in Python does."""
+    dev = gpu_or_skip()
+    import causal_gqa_flashattention_attn_gb300 as attn
+    call = _wide_table(1, dev)     # 1.1 TB
+    with pytest.raises(torch.OutOfMemoryError):
+        attn.attn_prefill_paged_fp8_block(**call)
+    o, _, _ = attn.attn_prefill_paged_fp8_block(**call, max_kv_rows=64)
+    torch.cuda.synchronize()
+    assert not o.any()
+
+
 def test_calls_on_two_streams_at_once():
     """Decodes and prefills of two batches on two streams, each with its own workspace, give what they give alone."""
     dev = gpu_or_skip()
