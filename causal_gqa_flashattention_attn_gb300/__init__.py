@@ -31,6 +31,7 @@ Entry points (names as in the C ABI):
 import ctypes
 import math
 import os
+import re
 
 import torch
 
@@ -562,6 +563,9 @@ def _native():
             from . import _binding
         except ImportError as e:
             raise RuntimeError("_binding.so is missing or does not load: build it with __graft_entry__.build()") from e
+        if re.match(r"[\d.]*\d", torch.__version__).group() != _binding.torch_version:   # without "+cu130" or "a0+git..."
+            raise RuntimeError(f"_binding.so was built for torch {_binding.torch_version}, not {torch.__version__}: "
+                               "build it with __graft_entry__.build()")
         _native_module = _binding
     return _native_module
 

@@ -7,9 +7,12 @@ point query, so the library loads on a machine without a GPU driver.
 
 csrc/binding.cpp, the compiled Python binding of the paged cache's entries, is
 built beside them with the host compiler, against the installed torch, and
-linked into ``_binding.so``; libattn.so itself knows nothing of torch.
+linked into ``_binding.so``; it is built again for another torch or Python than
+the ones noted beside it.  libattn.so itself knows nothing of torch.
 """
 
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -25,6 +28,8 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING_OBJ = os.path.join(BUILD_DIR, "binding.o")
 BINDING_PATH = os.path.join(HERE, "_binding.so")
+BINDING_NOTE = os.path.join(BUILD_DIR, "binding.txt")   # what it was built against
+API_HEADER = os.path.join(os.path.dirname(HERE), "include", "attn.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-DNDEBUG"] + ARCH
@@ -46,7 +51,7 @@ def sources():
 
 def headers():
     hs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    hs.append(os.path.join(os.path.dirname(HERE), "include", "attn.h"))
+    hs.append(API_HEADER)
     return hs
 
 
@@ -63,6 +68,23 @@ def _binding_commands():
     return ([cxx] + flags + [x for i in includes for x in ("-isystem", i)] + ["-c", BINDING_SRC, "-o", BINDING_OBJ],
             [cxx, "-shared", BINDING_OBJ, "-o", BINDING_PATH + ".tmp", "-L", HERE, "-l:" + LIB_NAME, "-L", lib, "-lc10",
              "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib])
+
+
+def _binding_against():
+    """The torch and the Python that the binding is built against, without importing torch."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:   # a torch that runs from its source tree
+        version = ""
+    return f"torch {version} {importlib.util.find_spec('torch').origin}\npython {sys.version}\n"
+
+
+def _noted():
+    try:
+        with open(BINDING_NOTE) as f:
+            return f.read()
+    except FileNotFoundError:
+        return None
 
 
 def _stale(target, deps):
@@ -84,7 +106,8 @@ def build(verbose=False, force=False, ptxas_verbose=False):
         if force or _stale(obj, [srcp] + hdrs):
             cmd = [exe] + NVCC_FLAGS + (["-Xptxas", "-v"] if ptxas_verbose else []) + ["-c", srcp, "-o", obj]
             jobs.append((src, cmd))
-    binding = force or _stale(BINDING_OBJ, [BINDING_SRC] + hdrs[-1:])
+    against = _binding_against()
+    binding = force or _stale(BINDING_OBJ, [BINDING_SRC, API_HEADER]) or _noted() != against
     if binding or _stale(BINDING_PATH, [BINDING_OBJ]):
         compile_binding, link_binding = _binding_commands()
     if binding:
@@ -118,6 +141,8 @@ def build(verbose=False, force=False, ptxas_verbose=False):
         if r.returncode != 0:
             raise RuntimeError("link of the binding failed:\n" + r.stdout + r.stderr)
         os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+        with open(BINDING_NOTE, "w") as f:
+            f.write(against)
     return LIB_PATH
 
 
