@@ -661,7 +661,10 @@ __global__ void __maxnreg__(NB == 1 ? 192 : 255) decode_fp8_block_kernel(const _
 
 // Joins the pieces of the sequences that were cut: 1 << per_shift warps (up to 8)
 // per output row, four elements a lane.  O = sum_s 2^(L_s - L) O_s / sum_s
-// 2^(L_s - L); each warp takes every per_row-th piece, kBatch at a time.
+// 2^(L_s - L); each warp takes every per_row-th piece, kBatch at a time.  Each CTA
+// counts the tiles of all sequences, also where its own was not cut: 32 heads over
+// 8, 64 sequences of 300 tokens take 15.7 us in all (their bytes 6.0), 1024 take
+// 123 (96), 4096 take 496 (386), and 4096 of 90 tokens 251 (123).
 __global__ void __launch_bounds__(32 * kMergeWarps, 4) decode_fp8_block_merge_kernel(const __grid_constant__ Params p,
                                                                                   int rows_per_col, int per_shift) {
     __shared__ int sums[2][kMergeWarps];
@@ -774,13 +777,19 @@ void set_columns(Params& p, int per, int sms) {
 // Rows of the workspace.
 size_t part_rows(const Params& p, int per) { return static_cast<size_t>(2) * p.workers * p.cols * per; }
 
-// Rows of a column: 16 where a KV head has more than 8, but 8 while the most
-// tokens that the lists can name make short shares of such columns.  A tile of
-// 8 rows costs a warp 0.7 of one of 16, all that runs once for a share less than
-// half, and its kernel leaves room for the merge's: 4 queries of 8 heads over 2,
-// 2400 tokens (1 tile a share) 11.6 us against 16.5; 8 sequences of 1000 and 64
-// rows (4) 15.7 against 17.6; 29 ragged ones of 12 rows, 32k tokens (13) 29.2
-// against 30.2; 24 of 4500 and 32 rows (22) 38.4 against 31.9.
+// Rows of a column: 16 where a KV head has more than 8, but 8 while the tokens
+// that the pool holds, or that a block table of its width can name, make short
+// shares of such columns.  A tile of 8 rows costs a warp 0.7 of one of 16, all
+// that runs once for a share less than half, and its kernel leaves room for the
+// merge's: 4 queries of 8 heads over 2, 2400 tokens (1 tile a share) 11.6 us
+// against 16.5; 8 sequences of 1000 and 64 rows (4) 15.7 against 17.6; 29 ragged
+// ones of 12 rows, 32k tokens (13) 29.2 against 30.2; 24 of 4500 and 32 rows (22)
+// 38.4 against 31.9.  The host does not know the lengths: in a pool far larger
+// than the batch a CSR list always takes 16, and a block table unless it is
+// narrow (in a pool of 64k pages the first two take 14.4 and 16.4 us by CSR list,
+// 10.1 and 15.7 by a table 32768 tokens wide, 10.3 and 15.0 in a pool of their
+// own).  Lists that share pages may name more tokens than the pool holds; the
+// rule is then off, the result is not.
 constexpr int kNarrowTiles = 12;
 int rows_per_column(Params& p, int sms) {
     set_columns(p, 8, sms);

@@ -518,6 +518,7 @@ attn_status_t attn_kv_append(const void* q, const void* k, const void* v,
  * between two codes falls on the side that exact arithmetic gives.  A NaN is
  * stored as NaN and an infinity as the largest code (NaN where the scale is 0);
  * neither counts for the scale.  A block whose first new token is its first token starts afresh.
+ * (Stored scales are at most 2^126; what this entry writes is at most 2^120.)
  *
  *   k_cache, v_cache  uint8 [num_pages, page_size, Hkv, D], e4m3 bytes (written)
  *   k_scale, v_scale  float32 [num_pages, page_size / block_tokens, Hkv]
@@ -544,7 +545,12 @@ attn_status_t attn_kv_append_fp8_block(const void* q, const void* k, const void*
  * nothing gets O = 0 and LSE = -inf.  The work is cut evenly over the GPU on
  * the device, whatever the lengths, so there is no split size to choose; the
  * pieces of a sequence are joined by LSE weight in a fixed order, so results
- * do not depend on timing.
+ * do not depend on timing.  (They do depend, within the roundings below, on
+ * how the work is cut: by the SM count, and by the pool's size where a KV head
+ * has more than 8 rows.)  Operands of the tensor cores are fp16: the codes
+ * exactly, a query row after a power of two that brings its largest element to
+ * [1, 2), and the weights times the values' scales, 2^-11 of each off; scores,
+ * maxima, sums and pieces are fp32.
  *
  *   q            [B, q_len, Hq, D] bfloat16: token-major, as attn_kv_append
  *                writes q_out for q_len new tokens per sequence       (read)
@@ -577,7 +583,8 @@ attn_status_t attn_decode_paged_fp8_block(const void* q, const void* k_cache, co
  * same cache: what attn_prefill_paged_varlen_ws computes, with K and V =
  * code * scale (rounded to bf16, which is exact for the power-of-two scales
  * that attn_kv_append_fp8_block writes) and the sequences' lengths given
- * directly.
+ * directly.  As there, the softmax weights are rounded to bf16 for the product
+ * with V (2^-8 of each at most); scores, maxima and sums are fp32.
  *
  *   q            [total_q, Hq, D] bfloat16; sequence b owns rows
  *                [qo_indptr[b], qo_indptr[b+1])                       (read)
