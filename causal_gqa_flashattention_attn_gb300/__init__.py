@@ -23,6 +23,9 @@ Entry points (names as in the C ABI):
   attn_kv_append_fp8_block  the same into an e4m3 cache with a scale per block of tokens and KV head
   attn_decode_paged_fp8_block   decode over that cache (1..16 queries per sequence), merge included
   attn_prefill_paged_fp8_block  ragged prefill over it
+  attn_qk_norm_rope         RMS norm of every query and key head with the rotation by position
+  attn_qk_norm_rope_bwd     its gradient
+  attn_varlen_fwd           attention of a ragged batch to contiguous keys: cross attention, or causal
   attn_lse_merge            LSE-weighted merge of split partials
   attn_lse_merge_bwd        its gradient
   attn_status_string
@@ -52,7 +55,9 @@ EXPORTED = ("attn_prefill_fwd", "attn_prefill_workspace_bytes", "attn_prefill_pl
             "attn_decode_paged_splitk_fp8", "attn_decode_paged_fused", "attn_decode_fused_workspace_bytes", "attn_decode_cooperative",
             "attn_decode_paged_splitk_static", "attn_kv_append", "attn_kv_append_fp8_block",
             "attn_decode_fp8_block_workspace_bytes", "attn_decode_paged_fp8_block",
-            "attn_prefill_fp8_block_workspace_bytes", "attn_prefill_paged_fp8_block", "attn_lse_merge", "attn_lse_merge_bwd", "attn_selftest_wait_timeout",
+            "attn_prefill_fp8_block_workspace_bytes", "attn_prefill_paged_fp8_block", "attn_qk_norm_rope",
+            "attn_qk_norm_rope_bwd_workspace_bytes", "attn_qk_norm_rope_bwd", "attn_varlen_fwd_workspace_bytes",
+            "attn_varlen_fwd", "attn_lse_merge", "attn_lse_merge_bwd", "attn_selftest_wait_timeout",
             "attn_status_string", "attn_abi_version")
 ATTN_DECODE_STATIC_SCRATCH_BYTES = 32 << 20
 
@@ -138,6 +143,18 @@ def lib():
     L.attn_prefill_paged_fp8_block.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32,
                                                i32, i32, i32, f32, vp, sz, vp, vp, vp, vp]
     L.attn_prefill_paged_fp8_block.restype = i32
+    norm = [vp, vp, i64, i64, vp, vp, i32, f32, vp, i32, i32, i32, vp, vp, vp, i64, i64]
+    L.attn_qk_norm_rope.argtypes = norm + [i32, i32, i32, i32, vp, vp]
+    L.attn_qk_norm_rope.restype = i32
+    L.attn_qk_norm_rope_bwd_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.attn_qk_norm_rope_bwd_workspace_bytes.restype = sz
+    L.attn_qk_norm_rope_bwd.argtypes = [vp, vp, i64, i64] + norm + [vp, vp, i32, i32, i32, i32, vp, sz, vp, vp]
+    L.attn_qk_norm_rope_bwd.restype = i32
+    L.attn_varlen_fwd_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
+    L.attn_varlen_fwd_workspace_bytes.restype = sz
+    L.attn_varlen_fwd.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, vp, sz, vp,
+                                  vp, vp, vp]
+    L.attn_varlen_fwd.restype = i32
     L.attn_lse_merge.argtypes = [vp, vp, i32, i32, i32, vp, vp, i32, vp]
     L.attn_lse_merge.restype = i32
     L.attn_lse_merge_bwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, vp]
@@ -652,6 +669,63 @@ def attn_prefill_paged_fp8_block(q, k_cache, v_cache, k_scale, v_scale, qo_indpt
     """
     return _run(stream, _native().prefill_fp8_block, q, k_cache, v_cache, k_scale, v_scale, qo_indptr, block_table, seq_lens,
                 kv_indptr, max_kv_rows, scale, workspace, o, lse, dev_status)
+
+
+def attn_qk_norm_rope(q, k, q_weight=None, k_weight=None, eps=1e-6, cos_sin=None, positions=None, interleaved=False,
+                      q_out=None, k_out=None, dev_status=None, stream=None):
+    """RMS norm of every head of ``q [T, Hq, D]`` and ``k [T, Hkv, D]`` (bf16, a
+    token's heads dense, tokens any multiple of 8 elements apart; either may be
+    None) by ``q_weight [D]`` and ``k_weight [D]`` (float32 or bfloat16, both
+    alike; None: that side is not normalised), then the rotation of
+    :func:`attn_kv_append` by ``cos_sin [max_pos, R]`` at ``positions [T]``
+    (None: the token's index).  Returns ``(q_out, k_out)``, None where absent;
+    an output given may be the input itself.
+    """
+    return _run(stream, _native().qk_norm_rope, q, k, q_weight, k_weight, eps, cos_sin, positions, interleaved, q_out, k_out,
+                dev_status)
+
+
+def attn_qk_norm_rope_bwd_workspace_bytes(T, Hq, Hkv, D=128):
+    """Bytes of workspace attn_qk_norm_rope_bwd takes on the current device."""
+    return int(lib().attn_qk_norm_rope_bwd_workspace_bytes(T, Hq, Hkv, D))
+
+
+def attn_qk_norm_rope_bwd(d_q_out, d_k_out, q, k, q_weight=None, k_weight=None, eps=1e-6, cos_sin=None, positions=None,
+                          interleaved=False, workspace=None, d_q=None, d_k=None, d_q_weight=None, d_k_weight=None,
+                          dev_status=None, stream=None):
+    """Gradient of :func:`attn_qk_norm_rope` from the outputs' gradients and the
+    forward call's inputs.  ``workspace``: a uint8 tensor of
+    attn_qk_norm_rope_bwd_workspace_bytes() bytes, scratch (None allocates one).
+    Returns ``(d_q, d_k, d_q_weight, d_k_weight, workspace)``: bf16 like q and k,
+    float32 ``[D]``, None where the input is absent.  ``d_q`` and ``d_k`` given
+    may have strides of their own (parts of the projection's gradient).
+    """
+    return _run(stream, _native().qk_norm_rope_bwd, d_q_out, d_k_out, q, k, q_weight, k_weight, eps, cos_sin, positions,
+                interleaved, workspace, d_q, d_k, d_q_weight, d_k_weight, dev_status)
+
+
+def attn_varlen_fwd_workspace_bytes(B, total_q, total_kv, Hq, Hkv, D=128):
+    """Bytes of workspace attn_varlen_fwd takes on the current device (often 0)."""
+    return int(lib().attn_varlen_fwd_workspace_bytes(B, total_q, total_kv, Hq, Hkv, D))
+
+
+def attn_varlen_fwd(q, k, v, qo_indptr, kv_indptr, kv_lens=None, causal=False, scale=None, workspace=None, o=None, lse=None,
+                    dev_status=None, stream=None):
+    """Attention of a ragged batch to contiguous keys: every key of a sequence
+    (cross attention to an encoder's states) or, with ``causal``, those up to
+    the diagonal that ends at the last key.
+
+    ``q [total_q, Hq, D]``, ``k, v [total_kv, Hkv, D]`` bf16, a token's heads
+    dense, tokens any multiple of 8 elements apart; D 64 or 128.  Sequence b
+    owns query rows ``qo_indptr[b]`` up to ``qo_indptr[b+1]`` and of the key rows
+    ``kv_indptr[b]`` up to ``kv_indptr[b+1]`` the first ``kv_lens[b]`` (None:
+    all), int32.  ``scale`` (by default ``D ** -0.5``) is positive.
+    ``workspace``: a uint8 tensor of attn_varlen_fwd_workspace_bytes() bytes,
+    scratch (None allocates one).  Returns ``(o [total_q, Hq, D], lse [total_q,
+    Hq], workspace)``.
+    """
+    return _run(stream, _native().varlen_fwd, q, k, v, qo_indptr, kv_indptr, kv_lens, causal, scale, workspace, o, lse,
+                dev_status)
 
 
 def decode_partials_view(workspace, B, Hq, max_kv_len, split_tokens, D):

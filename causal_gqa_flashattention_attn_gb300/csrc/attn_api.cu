@@ -255,6 +255,63 @@ attn_status_t append_impl(const AppendArgs& a, int D, void* stream) {
     return from_cuda(launch_kv_append(a, static_cast<cudaStream_t>(stream)));
 }
 
+// The checks of the norm with rotation and of its gradient (a.dy NULL: forward).
+attn_status_t qk_norm_check(const QkNormArgs& a, attn_dtype_t weight_dtype, bool backward) {
+    if (a.total < 0 || a.Hq < 0 || a.Hkv < 0 || a.Hq + static_cast<long long>(a.Hkv) == 0) return ATTN_ERR_INVALID_ARG;
+    const int heads[2] = {a.Hq, a.Hkv};
+    bool weights = false;
+    for (int i = 0; i < 2; ++i) {
+        if (heads[i] == 0) {
+            if (a.x[i] != nullptr || a.out[i] != nullptr || a.dy[i] != nullptr || a.weight[i] != nullptr || a.d_weight[i] != nullptr)
+                return ATTN_ERR_INVALID_ARG;
+            continue;
+        }
+        if (a.total > 0 && (a.x[i] == nullptr || a.out[i] == nullptr || (backward && a.dy[i] == nullptr)))
+            return ATTN_ERR_INVALID_ARG;
+        if (a.weight[i] == nullptr && a.d_weight[i] != nullptr) return ATTN_ERR_INVALID_ARG;
+        weights |= a.weight[i] != nullptr;
+        if (!aligned16(a.x[i]) || !aligned16(a.out[i]) || !aligned16(a.dy[i]) || !aligned16(a.weight[i]))
+            return ATTN_ERR_INVALID_ARG;
+        const long long row = static_cast<long long>(heads[i]) * a.D;
+        for (const long long stride : {a.x_stride[i], a.out_stride[i], backward ? a.dy_stride[i] : a.x_stride[i]})
+            if (stride % 8 != 0 || stride < row) return ATTN_ERR_INVALID_ARG;
+        if (a.x[i] != nullptr && a.out[i] == a.x[i] && a.out_stride[i] != a.x_stride[i]) return ATTN_ERR_INVALID_ARG;
+        if (a.dy[i] != nullptr && a.out[i] == a.dy[i] && a.out_stride[i] != a.dy_stride[i]) return ATTN_ERR_INVALID_ARG;
+    }
+    if (weights && (!std::isfinite(a.eps) || a.eps <= 0.f)) return ATTN_ERR_INVALID_ARG;
+    if (weights && weight_dtype != ATTN_F32 && weight_dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
+    if (a.D != 64 && a.D != 128) return ATTN_ERR_UNSUPPORTED;
+    if (a.rot_dim < 0 || a.rot_dim > a.D || (a.interleaved != 0 && a.interleaved != 1)) return ATTN_ERR_INVALID_ARG;
+    if (a.rot_dim > 0 && (a.cos_sin == nullptr || a.max_pos <= 0 || !aligned16(a.cos_sin))) return ATTN_ERR_INVALID_ARG;
+    if (a.rot_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+    if (static_cast<long long>(a.total) * (a.Hq + static_cast<long long>(a.Hkv)) >= (1LL << 31) - 64) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+// Sizes and pointers that attention over contiguous keys takes, forward and backward.
+attn_status_t varlen_check(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                           long long v_stride, const int32_t* qo_indptr, const int32_t* kv_indptr, int causal, int B,
+                           int total_q, int total_kv, int Hq, int Hkv, int D, float scale) {
+    if (B <= 0 || total_q < 0 || total_kv < 0 || Hq <= 0 || Hkv <= 0 || D <= 0) return ATTN_ERR_INVALID_ARG;
+    if (qo_indptr == nullptr || kv_indptr == nullptr || (total_q > 0 && q == nullptr) ||
+        (total_kv > 0 && (k == nullptr || v == nullptr)))
+        return ATTN_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0 || !std::isfinite(scale) || (causal != 0 && causal != 1)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v)) return ATTN_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+    if (q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 || q_stride < static_cast<long long>(Hq) * D ||
+        k_stride < static_cast<long long>(Hkv) * D || v_stride < static_cast<long long>(Hkv) * D)
+        return ATTN_ERR_INVALID_ARG;
+    if (Hq / Hkv > 128 || B > varlen_max_seqs() || scale <= 0.f) return ATTN_ERR_UNSUPPORTED;
+    // row strides of a TMA map are below 2^40 bytes
+    if (q_stride >= (1LL << 38) || k_stride >= (1LL << 38) || v_stride >= (1LL << 38)) return ATTN_ERR_UNSUPPORTED;
+    // query blocks are counted in 21 bits, rows and work items in int
+    if (total_q >= (1 << 22) || total_kv >= (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+    if ((static_cast<long long>(total_q) + B) * Hq >= (1LL << 31) || static_cast<long long>(total_kv) * Hkv >= (1LL << 31))
+        return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
 // Sizes that the block-scaled readers take: rows of a decode, rows of the prefill's copy.
 bool decode_rows_ok(int q_len, int Hq) { return static_cast<long long>(Hq) * q_len < (1LL << 20); }
 bool copy_rows_ok(int B, int max_kv_rows, int Hkv) {
@@ -683,6 +740,76 @@ attn_status_t attn_prefill_paged_fp8_block(const void* q, const void* k_cache, c
                              max_pages_per_seq, seq_lens, B, total_q, Hq, Hkv, num_pages, page_size, block_tokens,
                              max_kv_rows, scale, workspace, o, lse, dev_status};
     return from_cuda(launch_prefill_fp8_block(a, static_cast<cudaStream_t>(stream)));
+}
+
+attn_status_t attn_qk_norm_rope(const void* q, const void* k, long long q_stride, long long k_stride,
+                                const void* q_weight, const void* k_weight, attn_dtype_t weight_dtype, float eps,
+                                const float* cos_sin, int max_pos, int rot_dim, int interleaved,
+                                const int32_t* positions, void* q_out, void* k_out, long long q_out_stride,
+                                long long k_out_stride, int total, int Hq, int Hkv, int D, int32_t* dev_status,
+                                void* stream) {
+    const QkNormArgs a{{q, k},   {nullptr, nullptr}, {q_out, k_out},       {q_stride, k_stride}, {0, 0},
+                       {q_out_stride, k_out_stride}, {q_weight, k_weight}, weight_dtype == ATTN_BF16, eps, cos_sin,
+                       max_pos,  rot_dim, interleaved, positions, total, Hq, Hkv, D, {nullptr, nullptr}, nullptr, dev_status};
+    const attn_status_t st = qk_norm_check(a, weight_dtype, false);
+    if (st != ATTN_OK || total == 0) return st;
+    return from_cuda(launch_qk_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_qk_norm_rope_bwd_workspace_bytes(int total, int Hq, int Hkv, int D) {
+    if (total < 0 || Hq < 0 || Hkv < 0 || (D != 64 && D != 128)) return 0;
+    const int sms = device_sm_count();
+    return sms > 0 ? qk_norm_bwd_workspace(D, sms) : 0;
+}
+
+attn_status_t attn_qk_norm_rope_bwd(const void* d_q_out, const void* d_k_out, long long d_q_out_stride,
+                                    long long d_k_out_stride, const void* q, const void* k, long long q_stride,
+                                    long long k_stride, const void* q_weight, const void* k_weight,
+                                    attn_dtype_t weight_dtype, float eps, const float* cos_sin, int max_pos, int rot_dim,
+                                    int interleaved, const int32_t* positions, void* d_q, void* d_k,
+                                    long long d_q_stride, long long d_k_stride, float* d_q_weight, float* d_k_weight,
+                                    int total, int Hq, int Hkv, int D, void* workspace, size_t workspace_bytes,
+                                    int32_t* dev_status, void* stream) {
+    const QkNormArgs a{{q, k},   {d_q_out, d_k_out}, {d_q, d_k}, {q_stride, k_stride}, {d_q_out_stride, d_k_out_stride},
+                       {d_q_stride, d_k_stride}, {q_weight, k_weight}, weight_dtype == ATTN_BF16, eps, cos_sin,
+                       max_pos,  rot_dim, interleaved, positions, total, Hq, Hkv, D, {d_q_weight, d_k_weight}, workspace, dev_status};
+    const attn_status_t st = qk_norm_check(a, weight_dtype, true);
+    if (st != ATTN_OK) return st;
+    const bool sums = d_q_weight != nullptr || d_k_weight != nullptr;
+    if (sums) {
+        if (workspace == nullptr || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
+        const int sms = device_sm_count();
+        if (sms <= 0) return ATTN_ERR_CUDA;
+        if (workspace_bytes < qk_norm_bwd_workspace(D, sms)) return ATTN_ERR_WORKSPACE;
+    } else if (total == 0) {
+        return ATTN_OK;
+    }
+    return from_cuda(launch_qk_norm_bwd(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_varlen_fwd_workspace_bytes(int B, int total_q, int total_kv, int Hq, int Hkv, int D) {
+    if (B <= 0 || total_q <= 0 || total_kv < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128) return 0;
+    const int sms = device_sm_count();
+    return sms > 0 ? varlen_fwd_workspace(B, total_q, total_kv, Hq, Hkv, D, sms) : 0;
+}
+
+attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                              long long v_stride, const int32_t* qo_indptr, const int32_t* kv_indptr,
+                              const int32_t* kv_lens, int causal, int B, int total_q, int total_kv, int Hq, int Hkv,
+                              int D, float scale, void* workspace, size_t workspace_bytes, void* o, float* lse,
+                              int32_t* dev_status, void* stream) {
+    const attn_status_t st = varlen_check(q, k, v, q_stride, k_stride, v_stride, qo_indptr, kv_indptr, causal, B,
+                                          total_q, total_kv, Hq, Hkv, D, scale);
+    if (st != ATTN_OK) return st;
+    if ((total_q > 0 && o == nullptr) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
+    if (total_q == 0) return ATTN_OK;
+    const int sms = device_sm_count();
+    if (sms <= 0) return ATTN_ERR_CUDA;
+    const size_t need = varlen_fwd_workspace(B, total_q, total_kv, Hq, Hkv, D, sms);
+    if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
+    const VarlenFwdArgs a{q, k, v, q_stride, k_stride, v_stride, qo_indptr, kv_indptr, kv_lens, causal, B, total_q, total_kv,
+                          Hq, Hkv, D, scale, workspace, o, lse, dev_status};
+    return from_cuda(launch_varlen_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 attn_status_t attn_lse_merge(const float* o_part, const float* lse_part, int N, int S, int D, void* o, float* lse,

@@ -1,5 +1,6 @@
-// binding.cpp - the Python binding of the paged cache's writers and of the
-// block-scaled cache's readers, as a CPython module over the C ABI.
+// binding.cpp - the Python binding of the paged cache's writers, of the
+// block-scaled cache's readers and of the layer's operators around them (norms
+// with rotation), as a CPython module over the C ABI.
 //
 // It checks tensors, takes their pointers and sizes and the current CUDA
 // stream, allocates the outputs that are not given, and calls the C ABI.  A
@@ -382,7 +383,223 @@ PyObject* prefill_fp8_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// float argument or a default
+float number_or(const Args& args, int i, double otherwise) {
+    if (args.none(i)) return static_cast<float>(otherwise);
+    const double x = PyFloat_AsDouble(args.a[i]);
+    if (x == -1.0 && PyErr_Occurred()) throw 0;
+    return static_cast<float>(x);
+}
+
+PyObject* tuple_of(std::initializer_list<PyObject*> items) {
+    bool good = true;
+    for (PyObject* x : items) good = good && x != nullptr;
+    PyObject* t = good ? PyTuple_New(static_cast<Py_ssize_t>(items.size())) : nullptr;
+    Py_ssize_t i = 0;
+    for (PyObject* x : items) {
+        if (t != nullptr) PyTuple_SET_ITEM(t, i++, x);
+        else Py_XDECREF(x);
+    }
+    return t;
+}
+
+// An output: the caller's tensor at argument i, or a new one; None where `there` is not.
+PyObject* wrap_where(bool there, const Args& args, int i, const at::Tensor& t) {
+    if (!there) Py_RETURN_NONE;
+    return wrap_or(args, i, t);
+}
+
+// One side, queries (0) or keys (1), of a norm with rotation.
+struct NormSide {
+    void *x = nullptr, *dy = nullptr, *out = nullptr, *weight = nullptr;
+    float* d_weight = nullptr;
+    long long x_stride = 0, dy_stride = 0, out_stride = 0;
+    int64_t tokens = 0, heads = 0, d = 0;
+    bool there = false;
+    attn_dtype_t type = ATTN_F32;
+    at::Tensor made, d_made;
+};
+
+// Arguments: x, dy (or -1), weight, output, the weight's gradient (or -1).
+NormSide norm_side(const Args& args, const char* name, const char* dy_name, const char* w_name, const char* out_name,
+                   const char* dw_name, int x_at, int dy_at, int w_at, int out_at, int dw_at, at::Device device) {
+    NormSide s;
+    if (args.none(x_at)) {
+        for (const int i : {dy_at, w_at, out_at, dw_at})
+            if (i >= 0 && !args.none(i)) throw Refused(std::string(name) + " is absent, but not all that belongs to it");
+        return s;
+    }
+    s.there = true;
+    const at::Tensor& x = args.tensor(name, x_at);
+    s.x = token_rows(name, x, device, s.x_stride);
+    s.tokens = x.size(0), s.heads = x.size(1), s.d = x.size(2);
+    if (dy_at >= 0) {
+        const at::Tensor& dy = args.tensor(dy_name, dy_at);
+        s.dy = token_rows(dy_name, dy, device, s.dy_stride);
+        if (dy.sizes() != x.sizes()) throw Refused(std::string(dy_name) + " must have the shape of " + name);
+    }
+    if (args.none(out_at)) {
+        s.made = make_empty(x.sizes(), at::ScalarType::BFloat16, device);
+        s.out = token_rows(out_name, s.made, device, s.out_stride);
+    } else {
+        const at::Tensor& out = args.tensor(out_name, out_at);
+        s.out = token_rows(out_name, out, device, s.out_stride);
+        if (out.sizes() != x.sizes()) throw Refused(std::string(out_name) + " must have the shape of " + name);
+    }
+    if (!args.none(w_at)) {
+        const at::Tensor& w = args.tensor(w_name, w_at);
+        s.weight = expect(w_name, w, device, {s.d}, at::ScalarType::Float, at::ScalarType::BFloat16);
+        s.type = w.scalar_type() == at::ScalarType::Float ? ATTN_F32 : ATTN_BF16;
+        if (dw_at >= 0) {
+            if (args.none(dw_at)) s.d_made = make_empty({s.d}, at::ScalarType::Float, device);
+            s.d_weight = static_cast<float*>(expect(dw_name, args.none(dw_at) ? s.d_made : args.tensor(dw_name, dw_at), device,
+                                                    {s.d}, at::ScalarType::Float));
+        }
+    } else if (dw_at >= 0 && !args.none(dw_at)) {
+        throw Refused(std::string(dw_name) + " without " + w_name);
+    }
+    return s;
+}
+
+// What both calls share: sizes, the weights' type, the rotation's table.
+struct NormCall {
+    const float* cos_sin = nullptr;
+    const int32_t* positions = nullptr;
+    int max_pos = 0, rot = 0, total = 0, hq = 0, hkv = 0, d = 0;
+    attn_dtype_t type = ATTN_F32;
+};
+
+NormCall norm_call(const Args& args, const NormSide& q, const NormSide& k, int table_at, int positions_at, at::Device device) {
+    const NormSide& one = q.there ? q : k;
+    if (q.there && k.there && (q.tokens != k.tokens || q.d != k.d))
+        throw Refused("q and k must have the same tokens and head dimension");
+    if (q.weight != nullptr && k.weight != nullptr && q.type != k.type) throw Refused("q_weight and k_weight must have one type");
+    NormCall c;
+    c.total = small("q", one.tokens);
+    c.hq = small("q", q.heads);
+    c.hkv = small("k", k.heads);
+    c.d = small("q", one.d);
+    c.type = q.weight != nullptr ? q.type : k.type;
+    if (!args.none(table_at)) {
+        const at::Tensor& t = args.tensor("cos_sin", table_at);
+        c.cos_sin = static_cast<const float*>(expect("cos_sin", t, device, {-1, -1}, at::ScalarType::Float));
+        c.max_pos = small("cos_sin", t.size(0));
+        c.rot = small("cos_sin", t.size(1));
+    }
+    c.positions = optional_int(args, "positions", positions_at, one.tokens, device);
+    return c;
+}
+
+// qk_norm_rope(q, k, q_weight, k_weight, eps, cos_sin, positions, interleaved, q_out,
+// k_out, dev_status) -> (q_out, k_out)
+PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        const Args args{a, n};
+        const at::Device device = call_device(args.tensor("q or k", args.none(0) ? 1 : 0));
+        const NormSide q = norm_side(args, "q", "", "q_weight", "q_out", "", 0, -1, 2, 8, -1, device);
+        const NormSide k = norm_side(args, "k", "", "k_weight", "k_out", "", 1, -1, 3, 9, -1, device);
+        const NormCall c = norm_call(args, q, k, 5, 6, device);
+        check("attn_qk_norm_rope",
+              attn_qk_norm_rope(q.x, k.x, q.x_stride, k.x_stride, q.weight, k.weight, c.type, number_or(args, 4, 1e-6),
+                                c.cos_sin, c.max_pos, c.rot, args.truth(7), c.positions, q.out, k.out, q.out_stride,
+                                k.out_stride, c.total, c.hq, c.hkv, c.d, status_word(args, 10, device), stream_of(device)));
+        return tuple_of({wrap_where(q.there, args, 8, q.made), wrap_where(k.there, args, 9, k.made)});
+    });
+}
+
+// qk_norm_rope_bwd(d_q_out, d_k_out, q, k, q_weight, k_weight, eps, cos_sin, positions,
+// interleaved, workspace, d_q, d_k, d_q_weight, d_k_weight, dev_status)
+// -> (d_q, d_k, d_q_weight, d_k_weight, workspace)
+PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        const Args args{a, n};
+        const at::Device device = call_device(args.tensor("q or k", args.none(2) ? 3 : 2));
+        const NormSide q = norm_side(args, "q", "d_q_out", "q_weight", "d_q", "d_q_weight", 2, 0, 4, 11, 13, device);
+        const NormSide k = norm_side(args, "k", "d_k_out", "k_weight", "d_k", "d_k_weight", 3, 1, 5, 12, 14, device);
+        const NormCall c = norm_call(args, q, k, 7, 8, device);
+        at::Tensor ws;
+        if (args.none(10)) {
+            const size_t need = attn_qk_norm_rope_bwd_workspace_bytes(c.total, c.hq, c.hkv, c.d);
+            ws = make_empty({static_cast<int64_t>(std::max<size_t>(need, 16))}, at::ScalarType::Byte, device);
+        }
+        const at::Tensor& wt = args.none(10) ? ws : args.tensor("workspace", 10);
+        void* wp = expect("workspace", wt, device, {-1}, at::ScalarType::Byte);
+        check("attn_qk_norm_rope_bwd",
+              attn_qk_norm_rope_bwd(q.dy, k.dy, q.dy_stride, k.dy_stride, q.x, k.x, q.x_stride, k.x_stride, q.weight, k.weight,
+                                    c.type, number_or(args, 6, 1e-6), c.cos_sin, c.max_pos, c.rot, args.truth(9), c.positions,
+                                    q.out, k.out, q.out_stride, k.out_stride, q.d_weight, k.d_weight, c.total, c.hq, c.hkv,
+                                    c.d, wp, static_cast<size_t>(wt.numel()), status_word(args, 15, device),
+                                    stream_of(device)));
+        return tuple_of({wrap_where(q.there, args, 11, q.made), wrap_where(k.there, args, 12, k.made),
+                         wrap_where(q.d_weight != nullptr, args, 13, q.d_made),
+                         wrap_where(k.d_weight != nullptr, args, 14, k.d_made), wrap_or(args, 10, ws)});
+    });
+}
+
+// Queries, keys and values of a ragged batch over contiguous keys, arguments i .. i + 5.
+struct Ragged {
+    void *q, *k, *v;
+    long long q_stride, k_stride, v_stride;
+    const int32_t *qo, *kv, *lens;
+    int count, total_q, total_kv, hq, hkv, d;
+    at::IntArrayRef q_shape, k_shape;
+};
+
+Ragged ragged(const Args& args, int i, at::Device device) {
+    Ragged r{};
+    const at::Tensor &q = args.tensor("q", i), &k = args.tensor("k", i + 1), &v = args.tensor("v", i + 2);
+    r.q = token_rows("q", q, device, r.q_stride);
+    r.k = token_rows("k", k, device, r.k_stride);
+    r.v = token_rows("v", v, device, r.v_stride);
+    if (v.sizes() != k.sizes()) throw Refused("k and v must have the same shape");
+    if (q.size(2) != k.size(2)) throw Refused("q and k must have the same head dimension");
+    r.q_shape = q.sizes(), r.k_shape = k.sizes();
+    const at::Tensor& qo = args.tensor("qo_indptr", i + 3);
+    const int64_t count = qo.numel() - 1;
+    r.qo = static_cast<const int32_t*>(expect("qo_indptr", qo, device, {-1}, at::ScalarType::Int));
+    if (count < 1) throw Refused("qo_indptr must hold at least one sequence");
+    r.kv = static_cast<const int32_t*>(expect("kv_indptr", args.tensor("kv_indptr", i + 4), device, {count + 1}, at::ScalarType::Int));
+    r.lens = optional_int(args, "kv_lens", i + 5, count, device);
+    r.count = small("qo_indptr", count);
+    r.total_q = small("q", q.size(0));
+    r.total_kv = small("k", k.size(0));
+    r.hq = small("q", q.size(1));
+    r.hkv = small("k", k.size(1));
+    r.d = small("q", q.size(2));
+    return r;
+}
+
+// varlen_fwd(q, k, v, qo_indptr, kv_indptr, kv_lens, causal, scale, workspace, o, lse,
+// dev_status) -> (o, lse, workspace)
+PyObject* varlen_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        const Args args{a, n};
+        const at::Device device = call_device(args.tensor("q", 0));
+        const Ragged r = ragged(args, 0, device);
+        at::Tensor ws, o, lse;
+        if (args.none(8)) {
+            const size_t need = attn_varlen_fwd_workspace_bytes(r.count, r.total_q, r.total_kv, r.hq, r.hkv, r.d);
+            ws = make_empty({static_cast<int64_t>(std::max<size_t>(need, 16))}, at::ScalarType::Byte, device);
+        }
+        if (args.none(9)) o = make_empty(r.q_shape, at::ScalarType::BFloat16, device);
+        if (args.none(10)) lse = make_empty({r.total_q, r.hq}, at::ScalarType::Float, device);
+        const at::Tensor& wt = args.none(8) ? ws : args.tensor("workspace", 8);
+        void* wp = expect("workspace", wt, device, {-1}, at::ScalarType::Byte);
+        void* op = expect("o", args.none(9) ? o : args.tensor("o", 9), device, {r.total_q, r.hq, r.d}, at::ScalarType::BFloat16);
+        float* lp = static_cast<float*>(expect("lse", args.none(10) ? lse : args.tensor("lse", 10), device, {r.total_q, r.hq},
+                                               at::ScalarType::Float));
+        check("attn_varlen_fwd",
+              attn_varlen_fwd(r.q, r.k, r.v, r.q_stride, r.k_stride, r.v_stride, r.qo, r.kv, r.lens, args.truth(6), r.count,
+                              r.total_q, r.total_kv, r.hq, r.hkv, r.d, scale_or_default(args, 7, r.d), wp,
+                              static_cast<size_t>(wt.numel()), op, lp, status_word(args, 11, device), stream_of(device)));
+        return tuple_of({wrap_or(args, 9, o), wrap_or(args, 10, lse), wrap_or(args, 8, ws)});
+    });
+}
+
 PyMethodDef methods[] = {
+    {"varlen_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(varlen_fwd)), METH_FASTCALL, nullptr},
+    {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(qk_norm_rope)), METH_FASTCALL, nullptr},
+    {"qk_norm_rope_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(qk_norm_rope_bwd)), METH_FASTCALL, nullptr},
     {"kv_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(kv_append)), METH_FASTCALL, nullptr},
     {"decode_fp8_block", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(decode_fp8_block)), METH_FASTCALL, nullptr},
     {"prefill_fp8_block", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(prefill_fp8_block)), METH_FASTCALL, nullptr},

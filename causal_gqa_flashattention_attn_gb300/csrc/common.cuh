@@ -224,6 +224,47 @@ struct PrefillBlockArgs {
 size_t prefill_fp8_block_workspace(int B, int max_kv_rows, int Hkv);
 cudaError_t launch_prefill_fp8_block(const PrefillBlockArgs& a, cudaStream_t stream);
 
+// Norm and rotation of queries (0) and keys (1) by head (qk_norm.cu).
+struct QkNormArgs {
+    const void* x[2];       // [total, heads, D] bf16, rows x_stride elements apart
+    const void* dy[2];      // backward: gradients of the outputs
+    void* out[2];           // the outputs, or backward the gradients of x
+    long long x_stride[2], dy_stride[2], out_stride[2];
+    const void* weight[2];  // [D]; NULL: rotation alone
+    bool weight_bf16;       // else float32
+    float eps;
+    const float* cos_sin;   // [max_pos, rot_dim]
+    int max_pos, rot_dim, interleaved;
+    const int32_t* positions;   // [total], may be NULL
+    int total, Hq, Hkv, D;      // Hq or Hkv 0: absent
+    float* d_weight[2];     // backward: [D] or NULL
+    void* workspace;        // backward with a d_weight
+    int32_t* dev_status;
+};
+constexpr int kQkNormCtas = 4;   // CTAs per SM of the backward pass
+size_t qk_norm_bwd_workspace(int D, int sms);
+cudaError_t launch_qk_norm(const QkNormArgs& a, cudaStream_t stream);
+cudaError_t launch_qk_norm_bwd(const QkNormArgs& a, cudaStream_t stream);
+
+// Attention of a ragged batch over contiguous keys (prefill_tc.cu).
+struct VarlenFwdArgs {
+    const void* q;          // [total_q, Hq, D] bf16, rows q_stride elements apart
+    const void* k;          // [total_kv, Hkv, D]
+    const void* v;
+    long long q_stride, k_stride, v_stride;
+    const int32_t* qo_indptr;   // [B + 1]
+    const int32_t* kv_indptr;   // [B + 1]
+    const int32_t* kv_lens;     // [B], may be NULL
+    int causal, B, total_q, total_kv, Hq, Hkv, D;
+    float scale;
+    void* workspace;
+    void* o;                // [total_q, Hq, D], dense
+    float* lse;             // [total_q, Hq] or NULL
+    int32_t* dev_status;
+};
+size_t varlen_fwd_workspace(int B, int total_q, int total_kv, int Hq, int Hkv, int D, int sms);
+cudaError_t launch_varlen_fwd(const VarlenFwdArgs& a, cudaStream_t stream);
+
 int varlen_max_seqs();
 int varlen_max_pairs();
 int varlen_pair_bits();

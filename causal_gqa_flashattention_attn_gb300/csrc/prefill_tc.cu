@@ -105,6 +105,12 @@ struct Params {
     int gathered;   // K/V come by TMA from a contiguous copy in page-list order
     const uint32_t* order_in;   // the sorted pairs, *order_n of kMaxOrder words (NULL: every CTA sorts them)
     const int32_t* order_n;
+    // ragged batch over contiguous keys (kDirect): K/V rows [kv_indptr[b], kv_indptr[b + 1])
+    const int32_t* kv_lens;   // [B] of them that count (NULL: all)
+    int causal, total_q, total_kv;
+    int pieces;               // parts that each item's KV tiles are cut into
+    float* part_o;            // pieces > 1: [total_q * Hq][pieces][D]
+    float* part_lse;          // [total_q * Hq][pieces]
     // split schedule (dense only): the (item, KV tile) steps in item order
     // (batch, KV head, query block), cut into gridDim.x equal ranges
     long long sk_total;   // KV tile steps of all items
@@ -238,6 +244,45 @@ __device__ void split_find_start(const Params& p, long long L0, SplitWalk& w, in
     }
 }
 
+// kDirect: queries and keys of sequence b, offsets outside the tensors cut to them.
+struct DirectSeq {
+    int q_start, q_len, kv_start, kv_len;
+};
+__device__ __forceinline__ DirectSeq direct_seq(const Params& p, int b) {
+    DirectSeq s;
+    s.q_start = min(max(p.qo_indptr[b], 0), p.total_q);
+    s.q_len = min(max(p.qo_indptr[b + 1], s.q_start), p.total_q) - s.q_start;
+    s.kv_start = min(max(p.kv_indptr[b], 0), p.total_kv);
+    s.kv_len = min(max(p.kv_indptr[b + 1], s.kv_start), p.total_kv) - s.kv_start;
+    if (p.kv_lens != nullptr) s.kv_len = min(max(p.kv_lens[b], 0), s.kv_len);
+    return s;
+}
+// The last key that position `pos` sees; KV tiles that positions up to p_last see.
+__device__ __forceinline__ int direct_limit(const Params& p, int q_len, int kv_len, int pos) {
+    return p.causal ? min(kv_len - 1, pos + kv_len - q_len) : kv_len - 1;
+}
+__device__ __forceinline__ int direct_tiles(const Params& p, int q_len, int kv_len, int p_last) {
+    return max(0, direct_limit(p, q_len, kv_len, p_last) + kBN) / kBN;
+}
+// Its item: part `piece` of the KV tiles of query block qb and KV head kvh.
+__device__ __forceinline__ Item direct_item(const Params& p, int b, int qb, int kvh, int piece) {
+    const DirectSeq s = direct_seq(p, b);
+    Item it;
+    it.b = b;
+    it.kvh = kvh;
+    it.q_start = s.q_start;
+    it.q_len = s.q_len;
+    it.kv_base = s.kv_start;
+    it.kv_len = s.kv_len;
+    it.delta = s.kv_len - s.q_len;
+    it.p0 = qb * 2 * p.P;
+    const int n = direct_tiles(p, s.q_len, s.kv_len, min(it.p0 + 2 * p.P, s.q_len) - 1);
+    it.j0 = static_cast<int>(static_cast<long long>(n) * piece / p.pieces);
+    it.j1 = static_cast<int>(static_cast<long long>(n) * (piece + 1) / p.pieces);
+    it.n_kv = it.j1 - it.j0;
+    return it;
+}
+
 // Ragged batch: the item of sequence b, query block qb (2P positions) and KV
 // head kvh.
 __device__ __forceinline__ Item varlen_item(const Params& p, int b, int qb, int kvh) {
@@ -263,29 +308,39 @@ __device__ __forceinline__ Item varlen_item(const Params& p, int b, int qb, int 
 // Ragged batch, unsorted order: the pair word of item `idx` in
 // sequence-major order, within a sequence the furthest query block (longest
 // KV range) first.  `prefix[b]` counts the items of sequences before b.
+template <bool kDirect>
 __device__ __forceinline__ uint32_t pair_of_varlen(const Params& p, const int* prefix, int idx) {
     int lo = 0, hi = p.B;   // last b with prefix[b] <= idx
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (prefix[mid] <= idx) lo = mid; else hi = mid;
     }
-    const int q_len = p.qo_indptr[lo + 1] - p.qo_indptr[lo];
+    const int q_len = kDirect ? direct_seq(p, lo).q_len : p.qo_indptr[lo + 1] - p.qo_indptr[lo];
     const int n_qb = (q_len + 2 * p.P - 1) / (2 * p.P);
-    const int qb = n_qb - 1 - (idx - prefix[lo]) / p.Hkv;
+    const int qb = n_qb - 1 - (idx - prefix[lo]) / (kDirect ? p.Hkv * p.pieces : p.Hkv);
     return (static_cast<uint32_t>(lo) << kPairQbBits) | static_cast<uint32_t>(qb);
 }
 
 // Ragged batch: KV tiles of sequence b's query block qb, clamped to the
 // counting-sort range.
+template <bool kDirect>
 __device__ __forceinline__ int varlen_pair_key(const Params& p, int q_len, int kv_len, int qb) {
     const int p_last = min(qb * 2 * p.P + 2 * p.P, q_len) - 1;
+    if constexpr (kDirect) return min(direct_tiles(p, q_len, kv_len, p_last), kOrderBuckets - 1);
     const int kv_end = min(kv_len, p_last + kv_len - q_len + 1);
     const int n_kv = kv_end > 0 ? (kv_end + kBN - 1) / kBN : 0;
     return min(n_kv, kOrderBuckets - 1);
 }
 
 // Ragged batch: new-token and KV lengths of sequence b.
+template <bool kDirect>
 __device__ __forceinline__ void varlen_lens(const Params& p, int b, int& q_len, int& kv_len) {
+    if constexpr (kDirect) {
+        const DirectSeq s = direct_seq(p, b);
+        q_len = s.q_len;
+        kv_len = s.kv_len;
+        return;
+    }
     q_len = p.qo_indptr[b + 1] - p.qo_indptr[b];
     const int n_pages = p.kv_indptr[b + 1] - p.kv_indptr[b];
     const int last = (p.kv_last != nullptr) ? p.kv_last[b] : p.page_size;
@@ -294,6 +349,7 @@ __device__ __forceinline__ void varlen_lens(const Params& p, int b, int& q_len, 
 
 // Ragged batch (one warp): prefix[b] = work items of the sequences before b,
 // prefix[B] = all items.  One lane per sequence, 32 sequences per round.
+template <bool kDirect>
 __device__ void varlen_prefix(const Params& p, int* prefix, int lane) {
     int carry = 0;
 #pragma unroll 4
@@ -301,8 +357,8 @@ __device__ void varlen_prefix(const Params& p, int* prefix, int lane) {
         const int b = b0 + lane;
         int items = 0;
         if (b < p.B) {
-            const int ql = p.qo_indptr[b + 1] - p.qo_indptr[b];
-            items = ((ql + 2 * p.P - 1) / (2 * p.P)) * p.Hkv;
+            const int ql = kDirect ? direct_seq(p, b).q_len : p.qo_indptr[b + 1] - p.qo_indptr[b];
+            items = ((ql + 2 * p.P - 1) / (2 * p.P)) * (kDirect ? p.Hkv * p.pieces : p.Hkv);
         }
         int incl = items;
 #pragma unroll
@@ -322,15 +378,16 @@ __device__ void varlen_prefix(const Params& p, int* prefix, int lane) {
 // then a scatter in a fixed order (rounds of 32 sequences, one lane each;
 // within a round the furthest query blocks first, ties by lane) so that
 // every CTA writes the same list.
+template <bool kDirect>
 __device__ void varlen_sort_pairs(const Params& p, uint32_t* order, int* bucket, int lane) {
     for (int k = lane; k < kOrderBuckets; k += 32) bucket[k] = 0;
     __syncwarp();
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
         int q_len = 0, kv_len = 0;
-        if (b < p.B) varlen_lens(p, b, q_len, kv_len);
+        if (b < p.B) varlen_lens<kDirect>(p, b, q_len, kv_len);
         const int n_qb = (q_len + 2 * p.P - 1) / (2 * p.P);
-        for (int qb = 0; qb < n_qb; ++qb) atomicAdd(&bucket[varlen_pair_key(p, q_len, kv_len, qb)], 1);
+        for (int qb = 0; qb < n_qb; ++qb) atomicAdd(&bucket[varlen_pair_key<kDirect>(p, q_len, kv_len, qb)], 1);
     }
     __syncwarp();
     constexpr int per = kOrderBuckets / 32;   // lane 0 owns the largest keys
@@ -356,7 +413,7 @@ __device__ void varlen_sort_pairs(const Params& p, uint32_t* order, int* bucket,
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
         int q_len = 0, kv_len = 0;
-        if (b < p.B) varlen_lens(p, b, q_len, kv_len);
+        if (b < p.B) varlen_lens<kDirect>(p, b, q_len, kv_len);
         const int n_qb = (q_len + 2 * p.P - 1) / (2 * p.P);
         const int rounds = __reduce_max_sync(0xffffffffu, n_qb);
         for (int k = 0; k < rounds; ++k) {
@@ -366,7 +423,7 @@ __device__ void varlen_sort_pairs(const Params& p, uint32_t* order, int* bucket,
             int key = 0, pos = 0;
             uint32_t grp = 0;
             if (valid) {
-                key = varlen_pair_key(p, q_len, kv_len, qb);
+                key = varlen_pair_key<kDirect>(p, q_len, kv_len, qb);
                 grp = __match_any_sync(act, key);
                 pos = bucket[key] + __popc(grp & below);
             }
@@ -397,7 +454,10 @@ __device__ __forceinline__ int cta_item(int i) {
 // S = Q K^T takes that half's 4 K steps and P.V runs at N = 64 (an
 // instantiation of its own: the D = 128 kernels' MMA-issuing loop is left as
 // it is, which the tensor core's rate is sensitive to).
-template <bool kVarlen, bool kSplit, bool kD64 = false>
+// kDirect (ragged): K/V are the caller's own rows, by TMA from where they lie;
+// a sequence sees all of its keys or, causal, those up to its diagonal; an item
+// may be one of several parts of the KV tiles, which leaves fp32 partials.
+template <bool kVarlen, bool kSplit, bool kD64 = false, bool kDirect = false>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                       const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap o_map,
@@ -462,9 +522,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // here (any other is not held up)
         asm volatile("griddepcontrol.wait;" ::: "memory");
         if (warp == 0) {
-            varlen_prefix(p, prefix, lane);
+            varlen_prefix<kDirect>(p, prefix, lane);
             __syncwarp();
-            if (p.order_in == nullptr && prefix[p.B] / p.Hkv <= kMaxOrder) varlen_sort_pairs(p, order, bucket, lane);
+            if (p.order_in == nullptr && prefix[p.B] / (kDirect ? p.Hkv * p.pieces : p.Hkv) <= kMaxOrder)
+                varlen_sort_pairs<kDirect>(p, order, bucket, lane);
         } else if (p.order_in != nullptr) {
             // (the first words come without waiting for how many there are)
             const int n = *p.order_n;
@@ -491,10 +552,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
     if constexpr (kVarlen) n_items = prefix[p.B];
-    const bool sorted = kVarlen && n_items / p.Hkv <= kMaxOrder;
+    const int per_pair = kDirect ? p.Hkv * p.pieces : p.Hkv;   // items of a (sequence, query block)
+    const bool sorted = kVarlen && n_items / per_pair <= kMaxOrder;
     auto get_item = [&](int idx) -> Item {
-        if constexpr (kVarlen) {
-            const uint32_t pair = sorted ? order[idx / p.Hkv] : pair_of_varlen(p, prefix, idx);
+        if constexpr (kDirect) {
+            const uint32_t pair = sorted ? order[idx / per_pair] : pair_of_varlen<true>(p, prefix, idx);
+            const int in_pair = idx % per_pair;
+            return direct_item(p, static_cast<int>(pair >> kPairQbBits),
+                               static_cast<int>(pair & ((1u << kPairQbBits) - 1u)), in_pair / p.pieces,
+                               in_pair % p.pieces);
+        } else if constexpr (kVarlen) {
+            const uint32_t pair = sorted ? order[idx / p.Hkv] : pair_of_varlen<false>(p, prefix, idx);
             return varlen_item(p, static_cast<int>(pair >> kPairQbBits),
                                static_cast<int>(pair & ((1u << kPairQbBits) - 1u)), idx % p.Hkv);
         } else {
@@ -560,6 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // a row that sees no key: O = 0, LSE = -inf
         const int d_out = 64 * p.halves;   // D: the row stride of O
+        // a part's row: its partial is row_id * pieces + the part
+        auto part_row = [&](size_t row_id, int idx) { return row_id * p.pieces + idx % per_pair % p.pieces; };
         auto write_empty = [&](size_t row_id) {
             uint4* orow = reinterpret_cast<uint4*>(p.o + row_id * d_out);
             for (int c = 0; c < d_out / 8; ++c) orow[c] = make_uint4(0, 0, 0, 0);
@@ -583,11 +653,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             row_of(it, pos, row_id);
             const bool row_real = row_used && pos < it.q_len;
             if (it.n_kv == 0) {
-                if (row_real) write_empty(row_id);
+                if (kDirect && p.pieces > 1) {
+                    if (row_real) {   // nothing in this part: a weight of 0, whatever the partial's O holds
+                        const size_t at = part_row(row_id, cta_item(wk.i - 1));
+                        p.part_lse[at] = -INFINITY;
+                    }
+                } else if (row_real) {
+                    write_empty(row_id);
+                }
                 continue;
             }
             const int pos_min = it.p0 + t * p.P;     // smallest position of this tile
-            const int lim_row = pos + delta;         // last visible key of this row
+            // last visible key of this row, and of the tile's first row
+            const int lim_row = kDirect ? direct_limit(p, it.q_len, it.kv_len, pos) : pos + delta;
+            const int lim_first = kDirect ? direct_limit(p, it.q_len, it.kv_len, pos_min) : pos_min + delta;
             float m = -INFINITY, l = 0.f;
             bool o_live = false;   // O_t holds this piece's accumulation (after its first P.V)
             for (int j = it.j0; j < it.j1; ++j, ++kv_iter) {
@@ -599,13 +678,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_wait();
                 const int kv0 = j * kBN;
                 // causal mask only on tiles that cross this tile's diagonal
-                if (kv0 + kBN - 1 > pos_min + delta) {
+                if (kv0 + kBN - 1 > lim_first) {
                     const int lim = lim_row - kv0;
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (32 * c + e > lim) sr[c][e] = __float_as_uint(-INFINITY);
+                }
+                if constexpr (kDirect) {
+                    if (kv0 + kBN > it.kv_len) {
+                        // the rows behind the sequence's end hold anything, and a weight of 0
+                        // times NaN is NaN: both warpgroups zero them before their P is used
+                        const int vs = kv_iter % kStages;
+                        if (!(ok = wait(&v_full[vs], (kv_iter / kStages) & 1))) break;
+                        const int first = (it.kv_len - kv0) * 8;
+                        uint4* rows = reinterpret_cast<uint4*>(smem + kOffV + vs * kTile);
+                        for (int i = first + r; i < kHalf / 16; i += 128) {
+                            rows[i] = make_uint4(0u, 0u, 0u, 0u);
+                            if (!kD64) rows[kHalf / 16 + i] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();   // generic-proxy writes -> the tensor core's reads
+                    }
                 }
                 // row max: four independent chains of 3-input max
                 float mc[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -746,10 +840,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                         if (!ok) break;
-                    } else if (row_real) {
-                        uint4* orow = reinterpret_cast<uint4*>(p.o + row_id * kD);
+                    } else if (kDirect && p.pieces > 1) {
+                        if (row_real) {
+                            const size_t at = part_row(row_id, cta_item(wk.i - 1));
+                            float4* orow = reinterpret_cast<float4*>(p.part_o + at * (kD64 ? 64 : kD));
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
+                            for (int c = 0; c < (kD64 ? 2 : 4); ++c)
+#pragma unroll
+                                for (int e = 0; e < 32; e += 4)
+                                    orow[(32 * c + e) / 4] =
+                                        make_float4(__uint_as_float(ov[c][e]) * inv_l, __uint_as_float(ov[c][e + 1]) * inv_l,
+                                                    __uint_as_float(ov[c][e + 2]) * inv_l, __uint_as_float(ov[c][e + 3]) * inv_l);
+                            p.part_lse[at] = alive ? (m * kLn2 + logf(l)) : -INFINITY;
+                        }
+                        continue;
+                    } else if (row_real) {
+                        uint4* orow = reinterpret_cast<uint4*>(p.o + row_id * (kD64 ? 64 : kD));
+#pragma unroll
+                        for (int c = 0; c < (kD64 ? 2 : 4); ++c)
 #pragma unroll
                             for (int e = 0; e < 32; e += 8) orow[(32 * c + e) / 8] = pack8(c, e);
                     }
@@ -867,7 +975,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!kVarlen && r == 0) bulk_wait_all();   // O's TMA stores done before the CTA exits
     } else {
         regs_dec<kRegsControl>();
-        if (warp == kProducerWarp && kVarlen && p.gathered) {
+        if (warp == kProducerWarp && kDirect) {
+            // ------------------------- producer, ragged batch over contiguous keys
+            // Token t of sequence b is row kv_indptr[b] + t of K and V, viewed as
+            // [Hkv * D, rows]; rows behind its end are masked, and zeroed in V.
+            if (lane == 0) {
+                constexpr int kHalves = kD64 ? 1 : 2;
+                tma_prefetch_desc(&q_map);
+                tma_prefetch_desc(&k_map);
+                tma_prefetch_desc(&v_map);
+                uint32_t kv_iter = 0, item_iter = 0;
+                bool ok = true;
+                Walker wk = walk_begin();
+                for (Item it; ok && walk_next(wk, it);) {
+                    if (it.n_kv == 0) continue;
+                    if (item_iter > 0 && !(ok = wait(&q_empty, (item_iter - 1) & 1))) break;
+                    mbar_arrive_expect_tx(&q_full, 2 * p.P * p.G * 128 * kHalves);
+                    for (int t = 0; t < 2; ++t)
+                        for (int h = 0; h < kHalves; ++h)
+                            tma_load_3d(smem + kOffQ + t * kTile + h * kHalf, &q_map, &q_full, h * 64,
+                                        it.kvh * p.G, it.q_start + it.p0 + t * p.P);
+                    const int x = it.kvh * (64 * kHalves);
+                    for (int j = it.j0; j < it.j1; ++j, ++kv_iter) {
+                        const int s = kv_iter % kStages;
+                        const uint32_t par = ((kv_iter / kStages) - 1) & 1;
+                        const int row = it.kv_base + j * kBN;
+                        if (kv_iter >= kStages && !(ok = wait(&k_empty[s], par))) break;
+                        mbar_arrive_expect_tx(&k_full[s], kHalves * kHalf);
+                        for (int h = 0; h < kHalves; ++h)
+                            tma_load_2d(smem + kOffK + s * kTile + h * kHalf, &k_map, &k_full[s], x + 64 * h, row);
+                        if (kv_iter >= kStages && !(ok = wait(&v_empty[s], par))) break;
+                        mbar_arrive_expect_tx(&v_full[s], kHalves * kHalf);
+                        for (int h = 0; h < kHalves; ++h)
+                            tma_load_2d(smem + kOffV + s * kTile + h * kHalf, &v_map, &v_full[s], x + 64 * h, row);
+                    }
+                    ++item_iter;
+                }
+            }
+        } else if (warp == kProducerWarp && kVarlen && p.gathered) {
             // ------------------------- producer, ragged batch from the contiguous copy
             // Token t of sequence b is row kv_indptr[b] * page_size + t of the copy
             // [rows, Hkv, D]; the tile halves are 2D TMA boxes {64, 128}.  Rows past a sequence's end belong to the next sequence, or
@@ -1335,6 +1480,11 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, cudaStream_t stream) {
     p.gathered = 0;
     p.order_in = nullptr;
     p.order_n = nullptr;
+    p.kv_lens = nullptr;
+    p.causal = 1;
+    p.total_q = p.total_kv = 0;
+    p.pieces = 1;
+    p.part_o = p.part_lse = nullptr;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     p.sec_bh = section_pairs(a, p.n_qb, p.n_items < sms ? p.n_items : sms);
@@ -1412,6 +1562,12 @@ cudaError_t launch_prefill_varlen_tc(const VarlenArgs& a, cudaStream_t stream) {
     p.sk_zero_qb = 0;
     p.sk_count = nullptr;
     p.sk_o = p.sk_ml = nullptr;
+    p.kv_lens = nullptr;
+    p.causal = 1;
+    p.total_q = a.total_q;
+    p.total_kv = 0;
+    p.pieces = 1;
+    p.part_o = p.part_lse = nullptr;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     k_map = v_map = q_map;
@@ -1455,6 +1611,129 @@ cudaError_t launch_prefill_varlen_tc(const VarlenArgs& a, cudaStream_t stream) {
         return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<true, false>, q_map, k_map, v_map, q_map, p);
     }
     prefill_tc_kernel<true, false><<<sms, kThreads, smem, stream>>>(q_map, k_map, v_map, q_map, p);
+    return cudaGetLastError();
+}
+
+namespace {
+
+// Joins the parts of every row: O = sum_s e^(L_s - L) O_s / sum_s e^(L_s - L), one
+// warp a row, one lane a part's L.  Rows before the first sequence or behind the
+// last one are left alone.
+template <int kDim>
+__global__ void __launch_bounds__(256) varlen_merge_kernel(const Params p, int rows) {
+    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (row >= rows) return;
+    const int token = row / p.Hq;
+    if (token < p.qo_indptr[0] || token >= p.qo_indptr[p.B]) return;
+    const size_t at = static_cast<size_t>(row) * p.pieces;
+    const float l = lane < p.pieces ? __ldcg(p.part_lse + at + lane) : -INFINITY;
+    float top = l;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float w = l == -INFINITY ? 0.f : ex2((l - top) * kLog2e);
+    float sum = w;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    constexpr int kEach = kDim / 32;
+    float acc[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) acc[e] = 0.f;
+    for (int s = 0; s < p.pieces; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, w, s);
+        if (ws == 0.f) continue;   // an empty part's O is not written
+        const float* src = p.part_o + (at + s) * kDim + lane * kEach;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) acc[e] = fmaf(ws, __ldcg(src + e), acc[e]);
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + static_cast<size_t>(row) * kDim) + lane * (kEach / 2);
+#pragma unroll
+    for (int e = 0; e < kEach / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (p.lse != nullptr && lane == 0) p.lse[row] = sum > 0.f ? top + logf(sum) : -INFINITY;
+}
+
+// Parts of each item's KV tiles.  The host knows the totals, not the lengths:
+// with fewer items than half the SMs, as many parts as fill them, each of at
+// least kPartTiles tiles of the mean sequence.
+constexpr int kMaxPieces = 32;
+constexpr int kPartTiles = 3;
+int varlen_pieces(int B, int total_q, int total_kv, int Hq, int Hkv, int sms) {
+    const int P = kBM / (Hq / Hkv);
+    const long long blocks = std::max<long long>(B, (static_cast<long long>(total_q) + 2 * P - 1) / (2 * P));
+    const long long tiles = (static_cast<long long>(total_kv) / B + kBN - 1) / kBN;
+    const long long fill = sms / (blocks * Hkv);
+    return static_cast<int>(std::max<long long>(1, std::min<long long>({fill, tiles / kPartTiles, kMaxPieces})));
+}
+
+}  // namespace
+
+size_t varlen_fwd_workspace(int B, int total_q, int total_kv, int Hq, int Hkv, int D, int sms) {
+    const int pieces = varlen_pieces(B, total_q, total_kv, Hq, Hkv, sms);
+    return pieces == 1 ? 0 : static_cast<size_t>(total_q) * Hq * pieces * (D + 1) * sizeof(float);
+}
+
+cudaError_t launch_varlen_fwd(const VarlenFwdArgs& a, cudaStream_t stream) {
+    const int sms = device_sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const int G = a.Hq / a.Hkv;
+    const uint64_t D = static_cast<uint64_t>(a.D);
+    Params p{};
+    p.o = static_cast<__nv_bfloat16*>(a.o);
+    p.lse = a.lse;
+    p.status = a.dev_status;
+    p.B = a.B;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.G = G;
+    p.P = kBM / G;
+    p.halves = a.D / 64;
+    p.sec_bh = 1;
+    p.scale_log2 = a.scale * kLog2e;
+    p.qo_indptr = a.qo_indptr;
+    p.kv_indptr = a.kv_indptr;
+    p.kv_lens = a.kv_lens;
+    p.gathered = 1;   // K and V tiles come by TMA: one arrival each
+    p.page_size = 1;
+    p.causal = a.causal;
+    p.total_q = a.total_q;
+    p.total_kv = a.total_kv;
+    p.pieces = varlen_pieces(a.B, a.total_q, a.total_kv, a.Hq, a.Hkv, sms);
+    if (p.pieces > 1) {
+        p.part_o = static_cast<float*>(a.workspace);
+        p.part_lse = p.part_o + static_cast<size_t>(a.total_q) * a.Hq * p.pieces * a.D;
+    }
+    CUtensorMap q_map, k_map, v_map;
+    {
+        const uint64_t dims[3] = {D, static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.total_q)};
+        const uint64_t strides[2] = {D * 2, static_cast<uint64_t>(a.q_stride) * 2};
+        const uint32_t box[3] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(p.P)};
+        if (!encode_tiled_map(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, dims, strides, box,
+                              CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    }
+    k_map = v_map = q_map;   // without keys neither is used
+    if (a.total_kv > 0) {
+        const uint64_t dims[2] = {static_cast<uint64_t>(a.Hkv) * D, static_cast<uint64_t>(a.total_kv)};
+        const uint64_t k_strides[1] = {static_cast<uint64_t>(a.k_stride) * 2}, v_strides[1] = {static_cast<uint64_t>(a.v_stride) * 2};
+        const uint32_t box[2] = {64, kBN};
+        if (!encode_tiled_map(&k_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.k, dims, k_strides, box,
+                              CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_tiled_map(&v_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.v, dims, v_strides, box,
+                              CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    }
+    const size_t smem = kSmemBytes + 1024;
+    auto kern = a.D == 64 ? prefill_tc_kernel<true, false, true, true> : prefill_tc_kernel<true, false, false, true>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    // no more CTAs than there can be items
+    const long long items = (static_cast<long long>(a.total_q) / (2 * p.P) + a.B) * a.Hkv * p.pieces;
+    kern<<<static_cast<int>(std::min<long long>(items, sms)), kThreads, smem, stream>>>(q_map, k_map, v_map, q_map, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.pieces == 1) return e;
+    const int rows = a.total_q * a.Hq;
+    (a.D == 64 ? varlen_merge_kernel<64> : varlen_merge_kernel<128>)<<<(rows + 7) / 8, 256, 0, stream>>>(p, rows);
     return cudaGetLastError();
 }
 

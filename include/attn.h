@@ -611,6 +611,108 @@ attn_status_t attn_prefill_paged_fp8_block(const void* q, const void* k_cache, c
                                            void* o, float* lse, int32_t* dev_status, void* stream);
 
 /*
+ * attn_qk_norm_rope - RMS norm of every query and key head by a weight, then
+ * the rotation of its first rot_dim elements by its token's position, in one
+ * pass.  What a layer does to its queries and keys before the attention
+ * entries; cross attention gives its queries and its keys apart.
+ *
+ * Per head x [D]: r = (mean x^2 + eps)^(-1/2), y = R (x r w), with R the
+ * rotation of attn_kv_append.  In fp32 (squares above its range make r 0, as
+ * elements past 1.8e19 do), rounded once.
+ *
+ *   q, k         [total, Hq or Hkv, D] bfloat16, token rows *_stride elements
+ *                apart (read; NULL with Hq or Hkv 0: absent)
+ *   *_stride     multiples of 8, at least heads * D
+ *   q_weight, k_weight  [D] in weight_dtype, ATTN_F32 or ATTN_BF16 (read;
+ *                NULL: that side is rotated alone)
+ *   eps          > 0
+ *   cos_sin, max_pos, rot_dim, interleaved  as attn_kv_append
+ *   positions    int32 [total], the table row of each token (read; NULL: its
+ *                index).  A position outside [0, max_pos) sets
+ *                ATTN_DEV_POSITION_OUT_OF_RANGE and leaves its token unwritten.
+ *   q_out, k_out as q and k (written).  An output may be its input where the
+ *                strides agree; else they do not overlap.
+ *   D            64 or 128;  total * (Hq + Hkv) < 2^31.
+ */
+attn_status_t attn_qk_norm_rope(const void* q, const void* k, long long q_stride, long long k_stride,
+                                const void* q_weight, const void* k_weight, attn_dtype_t weight_dtype, float eps,
+                                const float* cos_sin, int max_pos, int rot_dim, int interleaved,
+                                const int32_t* positions, void* q_out, void* k_out, long long q_out_stride,
+                                long long k_out_stride, int total, int Hq, int Hkv, int D, int32_t* dev_status,
+                                void* stream);
+
+/*
+ * attn_qk_norm_rope_bwd - gradient of attn_qk_norm_rope.
+ *
+ * With n = x r and u = R^T dy: d_weight = sum over tokens and heads of u n,
+ * g = w u, dx = r (g - n mean(g n)); r is computed again from x.  Without a
+ * weight dx = u.  A token whose position is out of range has dx = 0 and adds
+ * nothing.  The sums are fp32 in a fixed order: results do not depend on timing
+ * (they do, within rounding, on the SM count).
+ *
+ *   d_q_out, d_k_out   gradients of the outputs, as those (read)
+ *   d_q, d_k           gradients of q and k, bfloat16, strides of their own
+ *                      (written; each may be its d_*_out or its input where the strides agree)
+ *   d_q_weight, d_k_weight  float32 [D] (written; NULL where the weight is NULL
+ *                      or the gradient is not wanted)
+ *   workspace          >= attn_qk_norm_rope_bwd_workspace_bytes() bytes,
+ *                      16-byte aligned: scratch (the size goes by the current
+ *                      device's SM count); not used without a d_*_weight.
+ *                      Calls that may run at the same time need separate ones.
+ * Other arguments and errors as attn_qk_norm_rope.
+ */
+size_t attn_qk_norm_rope_bwd_workspace_bytes(int total, int Hq, int Hkv, int D);
+attn_status_t attn_qk_norm_rope_bwd(const void* d_q_out, const void* d_k_out, long long d_q_out_stride,
+                                    long long d_k_out_stride, const void* q, const void* k, long long q_stride,
+                                    long long k_stride, const void* q_weight, const void* k_weight,
+                                    attn_dtype_t weight_dtype, float eps, const float* cos_sin, int max_pos, int rot_dim,
+                                    int interleaved, const int32_t* positions, void* d_q, void* d_k,
+                                    long long d_q_stride, long long d_k_stride, float* d_q_weight, float* d_k_weight,
+                                    int total, int Hq, int Hkv, int D, void* workspace, size_t workspace_bytes,
+                                    int32_t* dev_status, void* stream);
+
+/*
+ * attn_varlen_fwd - attention of a ragged batch of queries to keys and values
+ * of other lengths, contiguous in memory: every key (cross attention to an
+ * encoder's states) or causal.
+ *
+ * Per sequence O = softmax(scale * Q K^T + mask) V and the natural-log LSE; a
+ * query sees all of its sequence's keys, or with `causal` the first i + 1 +
+ * (keys - queries).  A row that sees nothing gets O = 0 and LSE = -inf.  The
+ * softmax weights are rounded to bf16 for the product with V (2^-8 of each at
+ * most); scores, maxima and sums are fp32.
+ *
+ *   q            [total_q, Hq, D] bfloat16, token rows q_stride elements apart (read)
+ *   k, v         [total_kv, Hkv, D] bfloat16, k_stride and v_stride apart (read)
+ *   *_stride     multiples of 8, at least heads * D (parts of a projection's
+ *                output as they are)
+ *   qo_indptr    int32 [B + 1]: sequence b owns query rows [qo_indptr[b], qo_indptr[b+1])
+ *   kv_indptr    int32 [B + 1]: and key rows [kv_indptr[b], kv_indptr[b+1])   (read)
+ *   kv_lens      int32 [B]: of which the first kv_lens[b] count (NULL: all), as
+ *                a padded batch has them.  Key rows that no query sees are not
+ *                used, whatever they hold, but for the causal diagonal: a NaN or
+ *                an infinity among the values shows in every query of its
+ *                sequence whose last visible key is in the same 128-key tile.
+ *   o            [total_q, Hq, D] dense; lse float32 [total_q, Hq] or NULL
+ *                (written; rows of no sequence are left alone)
+ *   scale        > 0
+ *   workspace    >= attn_varlen_fwd_workspace_bytes() bytes, 16-byte aligned:
+ *                scratch (NULL where that is 0).  Few and long sequences are cut
+ *                along their keys, and the parts joined in a fixed order: results
+ *                do not depend on timing.  (The size goes by the current
+ *                device's SM count.)  Calls that may run at the same time need
+ *                separate workspaces.
+ *   D 64 or 128, Hq / Hkv <= 128, B <= 2048, total_q < 2^22.
+ * Offsets outside the tensors are cut to them.
+ */
+size_t attn_varlen_fwd_workspace_bytes(int B, int total_q, int total_kv, int Hq, int Hkv, int D);
+attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                              long long v_stride, const int32_t* qo_indptr, const int32_t* kv_indptr,
+                              const int32_t* kv_lens, int causal, int B, int total_q, int total_kv, int Hq, int Hkv,
+                              int D, float scale, void* workspace, size_t workspace_bytes, void* o, float* lse,
+                              int32_t* dev_status, void* stream);
+
+/*
  * attn_lse_merge - LSE-weighted merge of split partials.
  *
  * Follows "splitk_kernels.py", _splitK_reduce: per row n,
