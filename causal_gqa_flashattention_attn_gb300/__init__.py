@@ -26,6 +26,7 @@ Entry points (names as in the C ABI):
   attn_qk_norm_rope         RMS norm of every query and key head with the rotation by position
   attn_qk_norm_rope_bwd     its gradient
   attn_varlen_fwd           attention of a ragged batch to contiguous keys: cross attention, or causal
+  attn_varlen_bwd           its gradient
   attn_lse_merge            LSE-weighted merge of split partials
   attn_lse_merge_bwd        its gradient
   attn_status_string
@@ -57,7 +58,7 @@ EXPORTED = ("attn_prefill_fwd", "attn_prefill_workspace_bytes", "attn_prefill_pl
             "attn_decode_fp8_block_workspace_bytes", "attn_decode_paged_fp8_block",
             "attn_prefill_fp8_block_workspace_bytes", "attn_prefill_paged_fp8_block", "attn_qk_norm_rope",
             "attn_qk_norm_rope_bwd_workspace_bytes", "attn_qk_norm_rope_bwd", "attn_varlen_fwd_workspace_bytes",
-            "attn_varlen_fwd", "attn_lse_merge", "attn_lse_merge_bwd", "attn_selftest_wait_timeout",
+            "attn_varlen_fwd", "attn_varlen_bwd_workspace_bytes", "attn_varlen_bwd", "attn_lse_merge", "attn_lse_merge_bwd", "attn_selftest_wait_timeout",
             "attn_status_string", "attn_abi_version")
 ATTN_DECODE_STATIC_SCRATCH_BYTES = 32 << 20
 
@@ -155,6 +156,10 @@ def lib():
     L.attn_varlen_fwd.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, vp, sz, vp,
                                   vp, vp, vp]
     L.attn_varlen_fwd.restype = i32
+    L.attn_varlen_bwd_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
+    L.attn_varlen_bwd_workspace_bytes.restype = sz
+    L.attn_varlen_bwd.argtypes = [vp] * 5 + [i64] * 5 + [vp] * 5 + [i32] * 7 + [f32, vp, sz, vp, vp, vp, i64, i64, i64, vp, vp]
+    L.attn_varlen_bwd.restype = i32
     L.attn_lse_merge.argtypes = [vp, vp, i32, i32, i32, vp, vp, i32, vp]
     L.attn_lse_merge.restype = i32
     L.attn_lse_merge_bwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, vp]
@@ -726,6 +731,25 @@ def attn_varlen_fwd(q, k, v, qo_indptr, kv_indptr, kv_lens=None, causal=False, s
     """
     return _run(stream, _native().varlen_fwd, q, k, v, qo_indptr, kv_indptr, kv_lens, causal, scale, workspace, o, lse,
                 dev_status)
+
+
+def attn_varlen_bwd_workspace_bytes(B, total_q, total_kv, Hq, Hkv, D=128):
+    """Bytes of workspace attn_varlen_bwd takes on the current device."""
+    return int(lib().attn_varlen_bwd_workspace_bytes(B, total_q, total_kv, Hq, Hkv, D))
+
+
+def attn_varlen_bwd(d_o, q, k, v, o, lse, qo_indptr, kv_indptr, kv_lens=None, causal=False, scale=None, d_lse=None,
+                    workspace=None, d_q=None, d_k=None, d_v=None, dev_status=None, stream=None):
+    """Gradient of :func:`attn_varlen_fwd` from ``d_o [total_q, Hq, D]`` (and
+    ``d_lse [total_q, Hq]``, None: zeros), the forward call's inputs and what it
+    returned, ``o`` and ``lse``.  ``workspace``: a uint8 tensor of
+    attn_varlen_bwd_workspace_bytes() bytes, scratch (None allocates one).
+    Returns ``(d_q, d_k, d_v, workspace)``, bf16 like q, k and v; key rows that
+    no query sees get zeros.  ``d_q, d_k, d_v`` given may have strides of their
+    own (parts of the projection's gradient).
+    """
+    return _run(stream, _native().varlen_bwd, d_o, q, k, v, o, lse, qo_indptr, kv_indptr, kv_lens, causal, scale, d_lse,
+                workspace, d_q, d_k, d_v, dev_status)
 
 
 def decode_partials_view(workspace, B, Hq, max_kv_len, split_tokens, D):

@@ -812,6 +812,45 @@ attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, long 
     return from_cuda(launch_varlen_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 
+size_t attn_varlen_bwd_workspace_bytes(int B, int total_q, int total_kv, int Hq, int Hkv, int D) {
+    if (B <= 0 || total_q < 0 || total_kv < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || D <= 0) return 0;
+    const int sms = device_sm_count();
+    return sms > 0 ? varlen_bwd_workspace(B, total_q, total_kv, Hq, Hkv, D, sms) : 0;
+}
+
+attn_status_t attn_varlen_bwd(const void* d_o, const void* q, const void* k, const void* v, const void* o,
+                              long long d_o_stride, long long q_stride, long long k_stride, long long v_stride,
+                              long long o_stride, const float* lse, const float* d_lse, const int32_t* qo_indptr,
+                              const int32_t* kv_indptr, const int32_t* kv_lens, int causal, int B, int total_q,
+                              int total_kv, int Hq, int Hkv, int D, float scale, void* workspace,
+                              size_t workspace_bytes, void* d_q, void* d_k, void* d_v, long long d_q_stride,
+                              long long d_k_stride, long long d_v_stride, int32_t* dev_status, void* stream) {
+    const attn_status_t st = varlen_check(q, k, v, q_stride, k_stride, v_stride, qo_indptr, kv_indptr, causal, B,
+                                          total_q, total_kv, Hq, Hkv, D, scale);
+    if (st != ATTN_OK) return st;
+    if (total_q > 0 && (d_o == nullptr || o == nullptr || lse == nullptr || d_q == nullptr)) return ATTN_ERR_INVALID_ARG;
+    if (total_kv > 0 && (d_k == nullptr || d_v == nullptr)) return ATTN_ERR_INVALID_ARG;
+    for (const void* x : {d_o, o, static_cast<const void*>(d_q), static_cast<const void*>(d_k), static_cast<const void*>(d_v)})
+        if (!aligned16(x)) return ATTN_ERR_INVALID_ARG;
+    const long long q_row = static_cast<long long>(Hq) * D, kv_row = static_cast<long long>(Hkv) * D;
+    for (const long long stride : {d_o_stride, o_stride, d_q_stride})
+        if (stride % 8 != 0 || stride < q_row) return ATTN_ERR_INVALID_ARG;
+    for (const long long stride : {d_k_stride, d_v_stride})
+        if (stride % 8 != 0 || stride < kv_row) return ATTN_ERR_INVALID_ARG;
+    if (d_o_stride >= (1LL << 38)) return ATTN_ERR_UNSUPPORTED;
+    if (total_q == 0 && total_kv == 0) return ATTN_OK;
+    const int sms = device_sm_count();
+    if (sms <= 0) return ATTN_ERR_CUDA;
+    if (!varlen_bwd_grid_ok(B, total_q, total_kv, Hq, Hkv, sms)) return ATTN_ERR_UNSUPPORTED;
+    if (workspace == nullptr || !aligned16(workspace) ||
+        workspace_bytes < varlen_bwd_workspace(B, total_q, total_kv, Hq, Hkv, D, sms))
+        return ATTN_ERR_WORKSPACE;
+    const VarlenBwdArgs a{d_o, q, k, v, o, d_o_stride, q_stride, k_stride, v_stride, o_stride, lse, d_lse, qo_indptr,
+                          kv_indptr, kv_lens, causal, B, total_q, total_kv, Hq, Hkv, D, scale, workspace, d_q, d_k, d_v,
+                          d_q_stride, d_k_stride, d_v_stride, dev_status};
+    return from_cuda(launch_varlen_bwd(a, static_cast<cudaStream_t>(stream)));
+}
+
 attn_status_t attn_lse_merge(const float* o_part, const float* lse_part, int N, int S, int D, void* o, float* lse,
                              attn_dtype_t o_dtype, void* stream) {
     if (o_part == nullptr || lse_part == nullptr || o == nullptr) return ATTN_ERR_INVALID_ARG;

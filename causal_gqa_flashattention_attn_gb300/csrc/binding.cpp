@@ -536,7 +536,8 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// Queries, keys and values of a ragged batch over contiguous keys, arguments i .. i + 5.
+// Queries, keys and values of a ragged batch over contiguous keys, arguments i, i + 1, i + 2;
+// its offsets and lengths, arguments at, at + 1, at + 2.
 struct Ragged {
     void *q, *k, *v;
     long long q_stride, k_stride, v_stride;
@@ -545,7 +546,7 @@ struct Ragged {
     at::IntArrayRef q_shape, k_shape;
 };
 
-Ragged ragged(const Args& args, int i, at::Device device) {
+Ragged ragged(const Args& args, int i, int at, at::Device device) {
     Ragged r{};
     const at::Tensor &q = args.tensor("q", i), &k = args.tensor("k", i + 1), &v = args.tensor("v", i + 2);
     r.q = token_rows("q", q, device, r.q_stride);
@@ -554,12 +555,12 @@ Ragged ragged(const Args& args, int i, at::Device device) {
     if (v.sizes() != k.sizes()) throw Refused("k and v must have the same shape");
     if (q.size(2) != k.size(2)) throw Refused("q and k must have the same head dimension");
     r.q_shape = q.sizes(), r.k_shape = k.sizes();
-    const at::Tensor& qo = args.tensor("qo_indptr", i + 3);
+    const at::Tensor& qo = args.tensor("qo_indptr", at);
     const int64_t count = qo.numel() - 1;
     r.qo = static_cast<const int32_t*>(expect("qo_indptr", qo, device, {-1}, at::ScalarType::Int));
     if (count < 1) throw Refused("qo_indptr must hold at least one sequence");
-    r.kv = static_cast<const int32_t*>(expect("kv_indptr", args.tensor("kv_indptr", i + 4), device, {count + 1}, at::ScalarType::Int));
-    r.lens = optional_int(args, "kv_lens", i + 5, count, device);
+    r.kv = static_cast<const int32_t*>(expect("kv_indptr", args.tensor("kv_indptr", at + 1), device, {count + 1}, at::ScalarType::Int));
+    r.lens = optional_int(args, "kv_lens", at + 2, count, device);
     r.count = small("qo_indptr", count);
     r.total_q = small("q", q.size(0));
     r.total_kv = small("k", k.size(0));
@@ -575,7 +576,7 @@ PyObject* varlen_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
         const Args args{a, n};
         const at::Device device = call_device(args.tensor("q", 0));
-        const Ragged r = ragged(args, 0, device);
+        const Ragged r = ragged(args, 0, 3, device);
         at::Tensor ws, o, lse;
         if (args.none(8)) {
             const size_t need = attn_varlen_fwd_workspace_bytes(r.count, r.total_q, r.total_kv, r.hq, r.hkv, r.d);
@@ -596,7 +597,58 @@ PyObject* varlen_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// A gradient: the caller's rows (argument i) or new ones, of the shape of what it belongs to.
+struct GradRows {
+    void* at;
+    long long stride;
+    at::Tensor made;
+};
+GradRows grad_rows(const Args& args, const char* name, int i, at::IntArrayRef shape, at::Device device) {
+    GradRows g;
+    if (args.none(i)) g.made = make_empty(shape, at::ScalarType::BFloat16, device);
+    const at::Tensor& t = args.none(i) ? g.made : args.tensor(name, i);
+    g.at = token_rows(name, t, device, g.stride);
+    if (t.sizes() != shape) throw Refused(std::string(name) + " must have the shape " + shape_text(shape) + ", not " + shape_text(t.sizes()));
+    return g;
+}
+
+// varlen_bwd(d_o, q, k, v, o, lse, qo_indptr, kv_indptr, kv_lens, causal, scale, d_lse,
+// workspace, d_q, d_k, d_v, dev_status) -> (d_q, d_k, d_v, workspace)
+PyObject* varlen_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        const Args args{a, n};
+        const at::Device device = call_device(args.tensor("q", 1));
+        const Ragged r = ragged(args, 1, 6, device);
+        long long do_stride = 0, o_stride = 0;
+        const at::Tensor &d_o = args.tensor("d_o", 0), &o = args.tensor("o", 4);
+        void* dop = token_rows("d_o", d_o, device, do_stride);
+        void* op = token_rows("o", o, device, o_stride);
+        if (d_o.sizes() != r.q_shape || o.sizes() != r.q_shape) throw Refused("d_o and o must have the shape of q");
+        const float* lse = static_cast<const float*>(expect("lse", args.tensor("lse", 5), device, {r.total_q, r.hq}, at::ScalarType::Float));
+        const float* d_lse = args.none(11) ? nullptr
+                                           : static_cast<const float*>(expect("d_lse", args.tensor("d_lse", 11), device,
+                                                                              {r.total_q, r.hq}, at::ScalarType::Float));
+        at::Tensor ws;
+        if (args.none(12)) {
+            const size_t need = attn_varlen_bwd_workspace_bytes(r.count, r.total_q, r.total_kv, r.hq, r.hkv, r.d);
+            ws = make_empty({static_cast<int64_t>(std::max<size_t>(need, 16))}, at::ScalarType::Byte, device);
+        }
+        const at::Tensor& wt = args.none(12) ? ws : args.tensor("workspace", 12);
+        void* wp = expect("workspace", wt, device, {-1}, at::ScalarType::Byte);
+        const GradRows dq = grad_rows(args, "d_q", 13, r.q_shape, device);
+        const GradRows dk = grad_rows(args, "d_k", 14, r.k_shape, device);
+        const GradRows dv = grad_rows(args, "d_v", 15, r.k_shape, device);
+        check("attn_varlen_bwd",
+              attn_varlen_bwd(dop, r.q, r.k, r.v, op, do_stride, r.q_stride, r.k_stride, r.v_stride, o_stride, lse, d_lse, r.qo,
+                              r.kv, r.lens, args.truth(9), r.count, r.total_q, r.total_kv, r.hq, r.hkv, r.d,
+                              scale_or_default(args, 10, r.d), wp, static_cast<size_t>(wt.numel()), dq.at, dk.at, dv.at,
+                              dq.stride, dk.stride, dv.stride, status_word(args, 16, device), stream_of(device)));
+        return tuple_of({wrap_or(args, 13, dq.made), wrap_or(args, 14, dk.made), wrap_or(args, 15, dv.made), wrap_or(args, 12, ws)});
+    });
+}
+
 PyMethodDef methods[] = {
+    {"varlen_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(varlen_bwd)), METH_FASTCALL, nullptr},
     {"varlen_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(varlen_fwd)), METH_FASTCALL, nullptr},
     {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(qk_norm_rope)), METH_FASTCALL, nullptr},
     {"qk_norm_rope_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(qk_norm_rope_bwd)), METH_FASTCALL, nullptr},

@@ -265,6 +265,32 @@ struct VarlenFwdArgs {
 size_t varlen_fwd_workspace(int B, int total_q, int total_kv, int Hq, int Hkv, int D, int sms);
 cudaError_t launch_varlen_fwd(const VarlenFwdArgs& a, cudaStream_t stream);
 
+// Its gradient (varlen_bwd.cu).
+struct VarlenBwdArgs {
+    const void* d_o;        // [total_q, Hq, D] bf16, as q, k, v and o: rows *_stride elements apart
+    const void* q;
+    const void* k;          // [total_kv, Hkv, D]
+    const void* v;
+    const void* o;
+    long long do_stride, q_stride, k_stride, v_stride, o_stride;
+    const float* lse;       // [total_q, Hq]
+    const float* d_lse;     // [total_q, Hq] or NULL
+    const int32_t* qo_indptr;
+    const int32_t* kv_indptr;
+    const int32_t* kv_lens;
+    int causal, B, total_q, total_kv, Hq, Hkv, D;
+    float scale;
+    void* workspace;
+    void* d_q;              // written, rows *_stride elements apart
+    void* d_k;
+    void* d_v;
+    long long dq_stride, dk_stride, dv_stride;
+    int32_t* dev_status;
+};
+size_t varlen_bwd_workspace(int B, int total_q, int total_kv, int Hq, int Hkv, int D, int sms);
+bool varlen_bwd_grid_ok(int B, int total_q, int total_kv, int Hq, int Hkv, int sms);
+cudaError_t launch_varlen_bwd(const VarlenBwdArgs& a, cudaStream_t stream);
+
 int varlen_max_seqs();
 int varlen_max_pairs();
 int varlen_pair_bits();

@@ -1,0 +1,804 @@
+// varlen_bwd.cu - gradient of attention over contiguous keys, on the
+// 5th-generation tensor cores.
+//
+// Mathematics, per sequence and head, with S = Q K^T and the forward pass's LSE:
+//   P = exp(scale S - LSE),  delta = sum_d dO O - dLSE,
+//   dV = P^T dO,  dP = dO V^T,  dS = P (dP - delta),
+//   dQ = scale dS K,  dK = scale dS^T Q,
+// dK and dV summed over the query heads of a KV head.  P is at most 1 and needs
+// no running maximum.  P and dS are rounded to bf16 for their products (2^-8 of
+// each at most); everything else is fp32.
+//
+// Two kernels, each its own pass over the tiles, so that every gradient is
+// accumulated in one place and in one order: five products would do with dQ
+// added up through global atomics, but then its rounding depends on timing.
+//   dK, dV: a CTA owns 128 keys of a KV head; the tiles of its queries stream by.
+//           S^T = K Q^T and dP^T = V dO^T are computed transposed, so that P^T
+//           and dS^T go back to TMEM as the A operands of dV += P^T dO and
+//           dK += dS^T Q and never touch shared memory;
+//   dQ:     a CTA owns a tile of queries; the key tiles stream by:
+//           S = Q K^T, dP = dO V^T, dQ += dS K.
+// As in the forward kernel a tile of queries holds P = floor(128 / G) positions
+// of all G heads of a KV head, position-major.
+//
+// Warps 0-7 turn scores into P and dS (a thread has a row of the tile and half
+// of its columns), warp 8 loads by TMA, warp 9 issues the MMAs, warp 10 brings
+// the queries' LSE and delta to the dK/dV kernel.  The S and dP products of the
+// next tile are issued while dS and P of this one are made: the tensor core
+// waits for neither in turn.  TMEM: S 128 columns, dP 128, dV 128, dK 128 (in
+// the dQ kernel a second S and dQ).
+//
+// A first kernel computes delta and lists the blocks of all sequences, those of
+// the longest first.  Few blocks are cut into parts along the streamed side,
+// whose fp32 sums a last kernel adds up in order.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace gb300 {
+namespace {
+
+constexpr int kBM = 128;        // rows and columns of a tile
+constexpr int kThreads = 384;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kStatWarp = 10;
+// Registers: launched at 168 per thread (384 x 168 = 64512); 2 x 128 x 216 + 128 x 72 = 64512.
+constexpr uint32_t kRegsSoftmax = 216, kRegsControl = 72;
+constexpr int kHalf = 128 * 128;   // bytes of one 64-column half of a 128-row tile
+constexpr int kTile = 2 * kHalf;
+constexpr int kStages = 2;
+constexpr int kStatSlots = 4;
+// shared memory (offsets from a 1024-aligned base): two resident tiles, then the
+// stages of the two streamed ones, then the queries' statistics
+constexpr int kOffR1 = 0, kOffR2 = kTile;
+constexpr int kOffY1 = 2 * kTile;
+constexpr int kOffY2 = kOffY1 + kStages * kTile;
+constexpr int kOffStat = kOffY2 + kStages * kTile;
+constexpr int kSmemBytes = kOffStat + kStatSlots * 2 * kBM * 4;
+// TMEM columns
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColDP = 128, kColAcc1 = 256, kColAcc2 = 384;   // dV, dK; or a second S, dQ
+
+struct Params {
+    const __nv_bfloat16* o;       // prepare
+    const __nv_bfloat16* d_o;
+    long long o_stride, do_stride;
+    const float* lse;
+    const float* d_lse;           // may be NULL
+    const int32_t *qo_indptr, *kv_indptr, *kv_lens;
+    int causal, B, total_q, total_kv, Hq, Hkv, G, P;
+    float scale, scale_log2;
+    float2* stats;                // [total_q * Hq] (-log2e LSE, delta)
+    int* counts;                  // blocks of keys, blocks of queries
+    int2* kv_blocks;              // (sequence, block), longest first
+    int2* q_blocks;
+    int max_kv_blocks, max_q_blocks, kv_pieces, q_pieces;
+    __nv_bfloat16 *dq, *dk, *dv;
+    long long dq_stride, dk_stride, dv_stride;
+    float *dq_part, *dk_part, *dv_part;   // [pieces][rows][heads][D]
+    int32_t* status;
+};
+
+struct Seq {
+    int q_start, q_len, kv_start, kv_room, kv_len;
+};
+// Offsets outside the tensors are cut to them.
+__device__ __forceinline__ Seq seq_of(const Params& p, int b) {
+    Seq s;
+    s.q_start = min(max(p.qo_indptr[b], 0), p.total_q);
+    s.q_len = min(max(p.qo_indptr[b + 1], s.q_start), p.total_q) - s.q_start;
+    s.kv_start = min(max(p.kv_indptr[b], 0), p.total_kv);
+    s.kv_room = min(max(p.kv_indptr[b + 1], s.kv_start), p.total_kv) - s.kv_start;
+    s.kv_len = p.kv_lens != nullptr ? min(max(p.kv_lens[b], 0), s.kv_room) : s.kv_room;
+    return s;
+}
+// The last key that position `pos` sees (-1 or less: none).
+__device__ __forceinline__ int limit_of(const Params& p, const Seq& s, int pos) {
+    return p.causal ? min(s.kv_len - 1, pos + s.kv_len - s.q_len) : s.kv_len - 1;
+}
+
+// --------------------------------------------------------------------- prepare
+
+constexpr int kPrepThreads = 512;
+constexpr int kMaxSeqs = 2048;
+
+// The blocks of one side of all sequences, sequences in `order`; `flip`: each
+// sequence's last block first.
+__device__ void list_blocks(const int* order, const int* len, int B, int per, bool flip, int* before, int* warp_sum,
+                            int2* out, int cap, int* count) {
+    // blocks before each place of the order
+    const int each = (B + kPrepThreads - 1) / kPrepThreads;
+    const int i0 = min(static_cast<int>(threadIdx.x) * each, B), i1 = min(i0 + each, B);
+    int sum = 0;
+    for (int i = i0; i < i1; ++i) sum += (len[order[i]] + per - 1) / per;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int base = incl - sum;
+    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    for (int i = i0; i < i1; ++i) {
+        before[i] = base;
+        base += (len[order[i]] + per - 1) / per;
+    }
+    if (threadIdx.x == kPrepThreads - 1) before[B] = base;
+    __syncthreads();
+    const int total = min(before[B], cap);   // (offsets that overlap could name more)
+    for (int x = threadIdx.x; x < total; x += kPrepThreads) {
+        int lo = 0, hi = B;   // last place with before <= x
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (before[mid] <= x) lo = mid; else hi = mid;
+        }
+        const int k = x - before[lo], n = (len[order[lo]] + per - 1) / per;
+        out[x] = make_int2(order[lo], flip ? n - 1 - k : k);
+    }
+    if (threadIdx.x == 0) *count = total;
+    __syncthreads();
+}
+
+// CTA 0 lists the blocks; the others compute delta, D / 8 lanes a row.
+template <int kD>
+__global__ void __launch_bounds__(kPrepThreads) varlen_bwd_prepare_kernel(const __grid_constant__ Params p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x == 0) {
+        __shared__ int q_len[kMaxSeqs], kv_len[kMaxSeqs], order[kMaxSeqs], before[kMaxSeqs + 1], warp_sum[kPrepThreads / 32];
+        for (int b = threadIdx.x; b < p.B; b += kPrepThreads) {
+            const Seq s = seq_of(p, b);
+            q_len[b] = s.q_len;
+            kv_len[b] = s.kv_room;
+        }
+        __syncthreads();
+        // keys' blocks cost their queries; with equal ones the lower sequence is first
+        for (int side = 0; side < 2; ++side) {
+            const int* cost = side == 0 ? q_len : kv_len;
+            for (int b = threadIdx.x; b < p.B; b += kPrepThreads) {
+                int rank = 0;
+                for (int i = 0; i < p.B; ++i) rank += cost[i] > cost[b] || (cost[i] == cost[b] && i < b);
+                order[rank] = b;
+            }
+            __syncthreads();
+            if (side == 0)
+                list_blocks(order, kv_len, p.B, kBM, false, before, warp_sum, p.kv_blocks, p.max_kv_blocks,
+                            p.counts);
+            else
+                list_blocks(order, q_len, p.B, p.P, true, before, warp_sum, p.q_blocks, p.max_q_blocks,
+                            p.counts + 1);
+        }
+        return;
+    }
+    constexpr int kLanes = kD / 8;
+    const int l = threadIdx.x % kLanes;
+    const long long rows = static_cast<long long>(p.total_q) * p.Hq;
+    const long long row = static_cast<long long>(blockIdx.x - 1) * (kPrepThreads / kLanes) + threadIdx.x / kLanes;
+    const bool live = row < rows;
+    const long long token = live ? row / p.Hq : 0;
+    const int head = live ? static_cast<int>(row - token * p.Hq) : 0;
+    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+    if (live) {
+        a = *reinterpret_cast<const uint4*>(p.o + token * p.o_stride + head * kD + 8 * l);
+        b = *reinterpret_cast<const uint4*>(p.d_o + token * p.do_stride + head * kD + 8 * l);
+    }
+    const uint32_t ua[4] = {a.x, a.y, a.z, a.w}, ub[4] = {b.x, b.y, b.z, b.w};
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        sum = fmaf(__uint_as_float(ua[i] << 16), __uint_as_float(ub[i] << 16), sum);
+        sum = fmaf(__uint_as_float(ua[i] & 0xFFFF0000u), __uint_as_float(ub[i] & 0xFFFF0000u), sum);
+    }
+#pragma unroll
+    for (int off = kLanes / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (live && l == 0) {
+        const float lse = p.lse[row];
+        // a row that saw nothing (LSE = -inf) has P = 0
+        p.stats[row] = lse == -INFINITY ? make_float2(-INFINITY, 0.f)
+                                        : make_float2(-lse * kLog2e, sum - (p.d_lse != nullptr ? p.d_lse[row] : 0.f));
+    }
+}
+
+// ---------------------------------------------------------------- the two passes
+
+// kDq: the pass over keys for dQ; else the pass over queries for dK and dV.
+// r1, r2: the resident tiles K, V (or Q, dO); y1, y2: the streamed ones Q, dO (or K, V).
+template <bool kDq, bool kD64>
+__global__ void __launch_bounds__(kThreads, 1)
+    varlen_bwd_kernel(const __grid_constant__ CUtensorMap r1_map, const __grid_constant__ CUtensorMap r2_map,
+                      const __grid_constant__ CUtensorMap y1_map, const __grid_constant__ CUtensorMap y2_map,
+                      const __grid_constant__ Params p) {
+    constexpr int kD = kD64 ? 64 : 128, kHalves = kD / 64;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align_1024(smem_raw);
+    __shared__ __align__(8) uint64_t r_full, y1_full[kStages], y2_full[kStages], y1_empty[kStages], y2_empty[kStages];
+    __shared__ __align__(8) uint64_t s_full[2], dp_full, p_ready, ds_ready, acc_full;
+    __shared__ __align__(8) uint64_t stat_full[kStatSlots], stat_empty[kStatSlots];
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ int abort_sh;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // the list of blocks and the statistics come from the kernel before
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int pieces = kDq ? p.q_pieces : p.kv_pieces;
+    const int per_block = p.Hkv * pieces;
+    const int entry = blockIdx.x / per_block;
+    if (entry >= __ldcg(p.counts + (kDq ? 1 : 0))) return;
+    const int2 blk = __ldcg((kDq ? p.q_blocks : p.kv_blocks) + entry);
+    const int kvh = (blockIdx.x % per_block) / pieces, piece = blockIdx.x % pieces;
+    const Seq sq = seq_of(p, blk.x);
+    const int delta = sq.kv_len - sq.q_len;
+    const int kv0_own = blk.y * kBM;   // dK, dV: the first key
+    const int p0_own = blk.y * p.P;    // dQ: the first position
+    // streamed tiles that this block meets, and this part of them
+    int first = 0, last = 0;
+    if constexpr (kDq) {
+        last = max(0, limit_of(p, sq, min(p0_own + p.P, sq.q_len) - 1) + kBM) / kBM;
+    } else if (kv0_own < sq.kv_len) {
+        last = (sq.q_len + p.P - 1) / p.P;
+        if (p.causal) first = min(max(0, kv0_own - delta) / p.P, last);
+    }
+    const int j0 = first + static_cast<int>(static_cast<long long>(last - first) * piece / pieces);
+    const int j1 = first + static_cast<int>(static_cast<long long>(last - first) * (piece + 1) / pieces);
+    const int n = j1 - j0;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&r_full, 1);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&y1_full[s], 1);
+            mbar_init(&y2_full[s], 1);
+            mbar_init(&y1_empty[s], 1);
+            mbar_init(&y2_empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) mbar_init(&s_full[s], 1);
+        mbar_init(&dp_full, 1);
+        mbar_init(&p_ready, 8);
+        mbar_init(&ds_ready, 8);
+        mbar_init(&acc_full, 1);
+        for (int s = 0; s < kStatSlots; ++s) {
+            mbar_init(&stat_full[s], 1);
+            mbar_init(&stat_empty[s], 8);
+        }
+        abort_sh = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&tmem_base_sh, kTmemCols);
+        tmem_relinquish();
+    }
+    const int rows_used = p.P * p.G;   // rows of a tile of queries
+    if (!kDq && rows_used < kBM) {
+        // the rows behind them are never loaded: zeros, which add nothing
+        constexpr int kVecs = kHalf / 16;
+        const int first_vec = rows_used * 8, per_half = kVecs - first_vec;
+        for (int i = threadIdx.x; i < 2 * kStages * kHalves * per_half; i += kThreads) {
+            const int h = i / per_half;   // halves of the stages, in the order of their places
+            const int at = kOffY1 + (h / kHalves) * kTile + (h % kHalves) * kHalf + (first_vec + i % per_half) * 16;
+            *reinterpret_cast<uint4*>(smem + at) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();   // generic-proxy writes -> the tensor core's reads
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_sh;
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        if (mbar_wait(bar, parity, &abort_sh)) return true;
+        flag_status(p.status, ATTN_DEV_WAIT_TIMEOUT);
+        atomicExch(&abort_sh, 1);
+        return false;
+    };
+
+    if (warp < 8) {
+        regs_inc<kRegsSoftmax>();
+        const int r = threadIdx.x & 127, h = warp >> 2;   // row of the tile, half of its columns
+        const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const float sl2 = p.scale_log2;
+        const float2 scl2 = make_float2(sl2, sl2);
+        // dQ: this row's position, limit and statistics
+        const int pos = p0_own + r / p.G;
+        const bool row_real = r < rows_used && pos < sq.q_len;
+        const size_t q_row = (static_cast<size_t>(sq.q_start) + pos) * p.Hq + kvh * p.G + r % p.G;
+        int lim = -1, lim_first = -1;
+        float2 own = make_float2(-INFINITY, 0.f);
+        if constexpr (kDq) {
+            lim = limit_of(p, sq, pos);
+            lim_first = limit_of(p, sq, p0_own);
+            if (row_real) own = __ldcg(p.stats + q_row);
+        }
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            const int y = j0 + j, st = j % kStages, slot = j % kStatSlots;
+            const float* nlse = reinterpret_cast<const float*>(smem + kOffStat) + slot * 2 * kBM + 64 * h;
+            const float* dlt = nlse + kBM;
+            // columns [c_lo, c_hi) of this row's half count
+            int c_lo = 0, c_hi = 64;
+            bool masked = false;
+            const uint32_t s_addr = tmem + lane_addr + ((kDq && (j & 1)) ? kColAcc1 : kColS) + 64 * h;
+            const uint32_t dp_addr = tmem + lane_addr + kColDP + 64 * h;
+            if (!(ok = wait(&s_full[kDq ? (j & 1) : 0], kDq ? ((j >> 1) & 1) : (j & 1)))) break;
+            tc_fence_after();
+            if constexpr (kDq) {
+                masked = y * kBM + kBM - 1 > lim_first;
+                c_hi = lim - y * kBM + 1 - 64 * h;
+                const int there = sq.kv_len - y * kBM;   // keys of the tile
+                if (there < kBM) {
+                    // dS is 0 there, but 0 times whatever lies behind the keys is not
+                    for (int i = there * 8 + threadIdx.x; i < kHalf / 16; i += 256) {
+                        uint4* rows = reinterpret_cast<uint4*>(smem + kOffY1 + st * kTile);
+                        rows[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (!kD64) rows[kHalf / 16 + i] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
+            } else {
+                if (!(ok = wait(&stat_full[slot], (j / kStatSlots) & 1))) break;
+                const int there = min(p.P, sq.q_len - y * p.P) * p.G;   // rows of the tile of queries
+                c_hi = there - 64 * h;
+                masked = there < rows_used;
+                if (p.causal && y * p.P + delta < kv0_own + kBM - 1) {
+                    masked = true;
+                    const long long from = static_cast<long long>(kv0_own + r - delta - y * p.P) * p.G;
+                    c_lo = static_cast<int>(min(max(from, 0LL), 128LL)) - 64 * h;
+                }
+                if (there < rows_used) {
+                    if (!(ok = wait(&y2_full[st], (j / kStages) & 1))) break;
+                    for (int i = there * 8 + threadIdx.x; i < kHalf / 16; i += 256) {
+                        uint4* rows = reinterpret_cast<uint4*>(smem + kOffY1 + st * kTile);
+                        constexpr int kNext = (kOffY2 - kOffY1) / 16;
+                        rows[i] = rows[kNext + i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (!kD64) rows[kHalf / 16 + i] = rows[kNext + kHalf / 16 + i] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
+            }
+            float2 pr[32];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t sr[32];
+                tmem_ld32(s_addr + 32 * c, sr);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    float4 nl = make_float4(own.x, own.x, own.x, own.x);
+                    if constexpr (!kDq) nl = *reinterpret_cast<const float4*>(nlse + 32 * c + e);
+                    const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), scl2,
+                                                 make_float2(nl.x, nl.y));
+                    const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3])), scl2,
+                                                 make_float2(nl.z, nl.w));
+                    pr[16 * c + e / 2] = make_float2(ex2(y0.x), ex2(y0.y));
+                    pr[16 * c + e / 2 + 1] = make_float2(ex2(y1.x), ex2(y1.y));
+                }
+            }
+            if (masked) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    if (2 * e < c_lo || 2 * e >= c_hi) pr[e].x = 0.f;
+                    if (2 * e + 1 < c_lo || 2 * e + 1 >= c_hi) pr[e].y = 0.f;
+                }
+            }
+            if constexpr (!kDq) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(pr[e].x, pr[e].y);
+                tmem_st32(s_addr, pk);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready);
+            }
+            if (!(ok = wait(&dp_full, j & 1))) break;
+            tc_fence_after();
+            uint32_t pk[32];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t dr[32];
+                tmem_ld32(dp_addr + 32 * c, dr);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    float4 dl = make_float4(own.y, own.y, own.y, own.y);
+                    if constexpr (!kDq) dl = *reinterpret_cast<const float4*>(dlt + 32 * c + e);
+                    const float2 p0 = pr[16 * c + e / 2], p1 = pr[16 * c + e / 2 + 1];
+                    float2 d0 = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(dr[e]), __uint_as_float(dr[e + 1])),
+                                                      make_float2(-dl.x, -dl.y)), p0);
+                    float2 d1 = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(dr[e + 2]), __uint_as_float(dr[e + 3])),
+                                                      make_float2(-dl.z, -dl.w)), p1);
+                    if (masked) {   // (what is not there may have a dP that is not finite)
+                        const int k = 32 * c + e;
+                        if (k < c_lo || k >= c_hi) d0.x = 0.f;
+                        if (k + 1 < c_lo || k + 1 >= c_hi) d0.y = 0.f;
+                        if (k + 2 < c_lo || k + 2 >= c_hi) d1.x = 0.f;
+                        if (k + 3 < c_lo || k + 3 >= c_hi) d1.y = 0.f;
+                    }
+                    pk[16 * c + e / 2] = pack_bf16x2(d0.x, d0.y);
+                    pk[16 * c + e / 2 + 1] = pack_bf16x2(d1.x, d1.y);
+                }
+            }
+            tmem_st32(dp_addr, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&ds_ready);
+                if (!kDq) mbar_arrive(&stat_empty[slot]);
+            }
+        }
+        // -------------------------------------------------------------- epilogue
+        if (ok && n > 0) ok = wait(&acc_full, 0);
+        if (ok) {
+            tc_fence_after();
+            // dQ: both halves of the threads share a row's columns; else the first four warps have dV, the others dK
+            constexpr int kCols = kDq ? kD / 2 : kD;
+            const uint32_t acc = tmem + lane_addr + (kDq ? kColAcc2 + kCols * h : (h == 0 ? kColAcc1 : kColAcc2));
+            const int key = kv0_own + r;
+            const bool store = kDq ? row_real : key < sq.kv_room;
+            const bool real = n > 0 && (kDq || key < sq.kv_len);
+            const float f = (kDq || h == 1) ? p.scale : 1.f;
+            const size_t row = kDq ? static_cast<size_t>(sq.q_start) + pos : static_cast<size_t>(sq.kv_start) + key;
+            const int head = kDq ? kvh * p.G + r % p.G : kvh;
+            const int heads = kDq ? p.Hq : p.Hkv, rows = kDq ? p.total_q : p.total_kv;
+            const int col0 = kDq ? kCols * h : 0;
+            __nv_bfloat16* out = kDq ? p.dq : (h == 0 ? p.dv : p.dk);
+            const long long stride = kDq ? p.dq_stride : (h == 0 ? p.dv_stride : p.dk_stride);
+            float* part = kDq ? p.dq_part : (h == 0 ? p.dv_part : p.dk_part);
+#pragma unroll
+            for (int c = 0; c < kCols / 32; ++c) {
+                uint32_t ar[32];
+                tmem_ld32(acc + 32 * c, ar);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) ar[e] = real ? __float_as_uint(__uint_as_float(ar[e]) * f) : 0u;
+                if (!store) continue;
+                if (pieces > 1) {
+                    float4* dst = reinterpret_cast<float4*>(
+                        part + ((static_cast<size_t>(piece) * rows + row) * heads + head) * kD + col0 + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dst[e] = make_float4(__uint_as_float(ar[4 * e]), __uint_as_float(ar[4 * e + 1]),
+                                             __uint_as_float(ar[4 * e + 2]), __uint_as_float(ar[4 * e + 3]));
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(out + row * stride + head * kD + col0 + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint4 v;
+                        v.x = pack_bf16x2(__uint_as_float(ar[8 * e]), __uint_as_float(ar[8 * e + 1]));
+                        v.y = pack_bf16x2(__uint_as_float(ar[8 * e + 2]), __uint_as_float(ar[8 * e + 3]));
+                        v.z = pack_bf16x2(__uint_as_float(ar[8 * e + 4]), __uint_as_float(ar[8 * e + 5]));
+                        v.w = pack_bf16x2(__uint_as_float(ar[8 * e + 6]), __uint_as_float(ar[8 * e + 7]));
+                        dst[e] = v;
+                    }
+                }
+            }
+        }
+    } else {
+        regs_dec<kRegsControl>();
+        if (warp == kProducerWarp && n > 0) {
+            if (lane == 0) {
+                const uint32_t q_bytes = static_cast<uint32_t>(rows_used) * 128 * kHalves;
+                constexpr uint32_t kKvBytes = kHalves * kHalf;
+                auto load_q = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int tile) {
+#pragma unroll
+                    for (int hh = 0; hh < kHalves; ++hh)
+                        tma_load_3d(dst + hh * kHalf, map, bar, 64 * hh, kvh * p.G, sq.q_start + tile * p.P);
+                };
+                auto load_kv = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int tile) {
+#pragma unroll
+                    for (int hh = 0; hh < kHalves; ++hh)
+                        tma_load_2d(dst + hh * kHalf, map, bar, kvh * kD + 64 * hh, sq.kv_start + tile * kBM);
+                };
+                auto load = [&](bool queries, uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int tile) {
+                    if (queries) load_q(dst, map, bar, tile);
+                    else load_kv(dst, map, bar, tile);
+                };
+                mbar_arrive_expect_tx(&r_full, 2 * (kDq ? q_bytes : kKvBytes));
+                load(kDq, smem + kOffR1, &r1_map, &r_full, blk.y);
+                load(kDq, smem + kOffR2, &r2_map, &r_full, blk.y);
+                for (int j = 0; j < n; ++j) {
+                    const int s = j % kStages;
+                    const uint32_t par = ((j / kStages) - 1) & 1, bytes = kDq ? kKvBytes : q_bytes;
+                    if (j >= kStages && !wait(&y1_empty[s], par)) break;
+                    mbar_arrive_expect_tx(&y1_full[s], bytes);
+                    load(!kDq, smem + kOffY1 + s * kTile, &y1_map, &y1_full[s], j0 + j);
+                    if (j >= kStages && !wait(&y2_empty[s], par)) break;
+                    mbar_arrive_expect_tx(&y2_full[s], bytes);
+                    load(!kDq, smem + kOffY2 + s * kTile, &y2_map, &y2_full[s], j0 + j);
+                }
+            }
+        } else if (warp == kStatWarp && !kDq) {
+            bool ok = true;
+            for (int j = 0; j < n; ++j) {
+                const int slot = j % kStatSlots;
+                const int p0 = (j0 + j) * p.P, there = min(p.P, sq.q_len - p0) * p.G;
+                float2 v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = lane + 32 * e, at = c / p.G;
+                    v[e] = make_float2(-INFINITY, 0.f);
+                    if (c < there)
+                        v[e] = __ldcg(p.stats + (static_cast<size_t>(sq.q_start) + p0 + at) * p.Hq + kvh * p.G + (c - at * p.G));
+                }
+                if (j >= kStatSlots) ok = wait(&stat_empty[slot], ((j / kStatSlots) - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                float* dst = reinterpret_cast<float*>(smem + kOffStat) + slot * 2 * kBM;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    dst[lane + 32 * e] = v[e].x;
+                    dst[kBM + lane + 32 * e] = v[e].y;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&stat_full[slot]);
+            }
+        } else if (warp == kMmaWarp && n > 0) {
+            if (lane == 0) {
+                constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, kBM, false);
+                constexpr uint32_t idesc_acc = idesc_bf16_f32(kBM, kD, true);
+                const uint32_t d_base = sw128_desc_lo(smem_u32(smem), 16);
+                auto scores = [&](uint32_t d, int a_off, int b_off) {   // D = A B^T over the head dimension
+                    const uint32_t a = d_base + (a_off >> 4), b = d_base + (b_off >> 4);
+                    umma_ss_lo<0>(d, a, b, idesc_s);
+#pragma unroll
+                    for (int kk = 1; kk < kD / 16; ++kk) {
+                        const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                        umma_ss_lo<1>(d, a + off, b + off, idesc_s);
+                    }
+                };
+                // D (+)= A B over the 128 streamed rows; A in TMEM, two halves of 64 columns packed to 32
+                auto gather = [&](uint32_t d, uint32_t a, int b_off, bool acc) {
+                    const uint32_t b = d_base + (b_off >> 4) + (((kHalf - 16) >> 4) << 16);
+                    umma_ts_lo(d, a, b, idesc_acc, acc ? 1u : 0u);
+#pragma unroll
+                    for (int kk = 1; kk < kBM / 16; ++kk)
+                        umma_ts_lo(d, a + (kk >> 2) * 64 + (kk & 3) * 8, b + ((kk * 16 * 128) >> 4), idesc_acc, 1u);
+                };
+                auto run = [&]() {
+                    if (!wait(&r_full, 0) || !wait(&y1_full[0], 0)) return;
+                    tc_fence_after();
+                    scores(tmem + kColS, kOffR1, kOffY1);
+                    umma_commit(&s_full[0]);
+                    if (!wait(&y2_full[0], 0)) return;
+                    tc_fence_after();
+                    scores(tmem + kColDP, kOffR2, kOffY2);
+                    umma_commit(&dp_full);
+                    if (kDq) umma_commit(&y2_empty[0]);
+                    for (int j = 0; j < n; ++j) {
+                        const int s = j % kStages, nx = (j + 1) % kStages;
+                        const uint32_t nx_par = ((j + 1) / kStages) & 1;
+                        const bool more = j + 1 < n;
+                        if constexpr (!kDq) {
+                            if (!wait(&p_ready, j & 1)) return;
+                            tc_fence_after();
+                            gather(tmem + kColAcc1, tmem + kColS, kOffY2 + s * kTile, j > 0);   // dV += P^T dO
+                            umma_commit(&y2_empty[s]);
+                        }
+                        if (more) {   // (for dK, dV it overwrites P, which the product before it has read)
+                            if (!wait(&y1_full[nx], nx_par)) return;
+                            tc_fence_after();
+                            scores(tmem + ((kDq && !(j & 1)) ? kColAcc1 : kColS), kOffR1, kOffY1 + nx * kTile);
+                            umma_commit(&s_full[kDq ? ((j + 1) & 1) : 0]);
+                        }
+                        if (!wait(&ds_ready, j & 1)) return;
+                        tc_fence_after();
+                        gather(tmem + kColAcc2, tmem + kColDP, kOffY1 + s * kTile, j > 0);   // dK += dS^T Q, or dQ += dS K
+                        umma_commit(&y1_empty[s]);
+                        if (more) {   // overwrites dS
+                            if (!wait(&y2_full[nx], nx_par)) return;
+                            tc_fence_after();
+                            scores(tmem + kColDP, kOffR2, kOffY2 + nx * kTile);
+                            umma_commit(&dp_full);
+                            if (kDq) umma_commit(&y2_empty[nx]);
+                        }
+                    }
+                    umma_commit(&acc_full);
+                };
+                run();
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// The parts of a gradient added up, in order: [pieces][rows][row_elems] fp32 to
+// bf16 rows `stride` apart, of the rows that belong to a sequence.
+__global__ void __launch_bounds__(256) varlen_bwd_sum_kernel(const float* part, int pieces, int rows, int row_elems,
+                                                             const int32_t* indptr, int B, __nv_bfloat16* out,
+                                                             long long stride) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int vecs = row_elems / 4;
+    const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    const long long row = i / vecs;
+    if (row >= rows || row < indptr[0] || row >= indptr[B]) return;
+    const float4* src = reinterpret_cast<const float4*>(part) + i;
+    float4 sum = __ldcg(src);
+    for (int s = 1; s < pieces; ++s) {
+        const float4 v = __ldcg(src + static_cast<long long>(s) * rows * vecs);
+        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+    }
+    *reinterpret_cast<uint2*>(out + row * stride + (i - row * vecs) * 4) =
+        make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+}
+
+// ------------------------------------------------------------------- host side
+
+// Parts of each block's streamed tiles, for the keys' and the queries' blocks:
+// the host knows the totals, not the lengths.  With fewer blocks than half the
+// SMs, as many parts as fill them, each of at least kPartTiles tiles of the mean
+// sequence.
+constexpr int kMaxPieces = 16;
+constexpr int kPartTiles = 2;
+struct Plan {
+    int kv_pieces, q_pieces;
+    long long kv_blocks, q_blocks;   // most that there can be
+};
+Plan plan_of(int B, int total_q, int total_kv, int Hq, int Hkv, int sms) {
+    const int P = kBM / (Hq / Hkv);
+    Plan x;
+    x.kv_blocks = total_kv / kBM + static_cast<long long>(B);
+    x.q_blocks = total_q / P + static_cast<long long>(B);
+    const long long kv_likely = std::max<long long>(B, (static_cast<long long>(total_kv) + kBM - 1) / kBM);
+    const long long q_likely = std::max<long long>(B, (static_cast<long long>(total_q) + P - 1) / P);
+    const long long q_tiles = std::max(1LL, q_likely / B), kv_tiles = std::max(1LL, kv_likely / B);
+    auto pieces = [&](long long blocks, long long tiles) {
+        return static_cast<int>(std::max<long long>(1, std::min<long long>({sms / (blocks * Hkv), tiles / kPartTiles, kMaxPieces})));
+    };
+    x.kv_pieces = pieces(kv_likely, q_tiles);
+    x.q_pieces = pieces(q_likely, kv_tiles);
+    return x;
+}
+
+size_t round16(size_t x) { return (x + 15) & ~static_cast<size_t>(15); }
+
+struct Layout {
+    size_t stats, counts, kv_blocks, q_blocks, dq, dk, dv, bytes;
+};
+Layout layout_of(const Plan& x, int total_q, int total_kv, int Hq, int Hkv, int D) {
+    Layout l;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t from = at;
+        at += round16(bytes);
+        return from;
+    };
+    l.stats = take(static_cast<size_t>(total_q) * Hq * sizeof(float2));
+    l.counts = take(2 * sizeof(int));
+    l.kv_blocks = take(static_cast<size_t>(x.kv_blocks) * sizeof(int2));
+    l.q_blocks = take(static_cast<size_t>(x.q_blocks) * sizeof(int2));
+    const size_t q_part = static_cast<size_t>(total_q) * Hq * D * sizeof(float), kv_part = static_cast<size_t>(total_kv) * Hkv * D * sizeof(float);
+    l.dq = take(x.q_pieces > 1 ? q_part * x.q_pieces : 0);
+    l.dk = take(x.kv_pieces > 1 ? kv_part * x.kv_pieces : 0);
+    l.dv = take(x.kv_pieces > 1 ? kv_part * x.kv_pieces : 0);
+    l.bytes = at;
+    return l;
+}
+
+template <bool kD64>
+cudaError_t launch(const VarlenBwdArgs& a, const Params& p, const Plan& x, const CUtensorMap& q, const CUtensorMap& d_o,
+                   const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
+    constexpr int kD = kD64 ? 64 : 128;
+    constexpr size_t kSmem = kSmemBytes + 1024;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = once_per_device(done, [] {
+        cudaError_t r = cudaFuncSetAttribute(varlen_bwd_kernel<false, kD64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(kSmem));
+        return r != cudaSuccess ? r
+                                : cudaFuncSetAttribute(varlen_bwd_kernel<true, kD64>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    });
+    if (e != cudaSuccess) return e;
+    const long long rows = static_cast<long long>(a.total_q) * a.Hq;
+    const long long per_cta = kPrepThreads / (kD / 8);
+    varlen_bwd_prepare_kernel<kD><<<static_cast<unsigned>(1 + (rows + per_cta - 1) / per_cta), kPrepThreads, 0, stream>>>(p);
+    e = cudaGetLastError();
+    if (e == cudaSuccess && a.total_kv > 0) {
+        varlen_bwd_kernel<false, kD64><<<static_cast<unsigned>(x.kv_blocks * a.Hkv * x.kv_pieces), kThreads, kSmem, stream>>>(k, v, q, d_o, p);
+        e = cudaGetLastError();
+    }
+    if (e == cudaSuccess && a.total_q > 0) {
+        varlen_bwd_kernel<true, kD64><<<static_cast<unsigned>(x.q_blocks * a.Hkv * x.q_pieces), kThreads, kSmem, stream>>>(q, d_o, k, v, p);
+        e = cudaGetLastError();
+    }
+    auto sum = [&](const float* part, int pieces, int n, int elems, const int32_t* indptr, __nv_bfloat16* out, long long stride) {
+        const long long vecs = static_cast<long long>(n) * (elems / 4);
+        varlen_bwd_sum_kernel<<<static_cast<unsigned>((vecs + 255) / 256), 256, 0, stream>>>(part, pieces, n, elems, indptr, a.B, out, stride);
+        return cudaGetLastError();
+    };
+    if (e == cudaSuccess && x.kv_pieces > 1 && a.total_kv > 0) {
+        e = sum(p.dk_part, x.kv_pieces, a.total_kv, a.Hkv * kD, a.kv_indptr, p.dk, p.dk_stride);
+        if (e == cudaSuccess) e = sum(p.dv_part, x.kv_pieces, a.total_kv, a.Hkv * kD, a.kv_indptr, p.dv, p.dv_stride);
+    }
+    if (e == cudaSuccess && x.q_pieces > 1 && a.total_q > 0)
+        e = sum(p.dq_part, x.q_pieces, a.total_q, a.Hq * kD, a.qo_indptr, p.dq, p.dq_stride);
+    return e;
+}
+
+}  // namespace
+
+size_t varlen_bwd_workspace(int B, int total_q, int total_kv, int Hq, int Hkv, int D, int sms) {
+    return layout_of(plan_of(B, total_q, total_kv, Hq, Hkv, sms), total_q, total_kv, Hq, Hkv, D).bytes;
+}
+
+// Whether the grids of both passes count in int.
+bool varlen_bwd_grid_ok(int B, int total_q, int total_kv, int Hq, int Hkv, int sms) {
+    const Plan x = plan_of(B, total_q, total_kv, Hq, Hkv, sms);
+    return x.kv_blocks * Hkv * x.kv_pieces < (1LL << 31) && x.q_blocks * Hkv * x.q_pieces < (1LL << 31);
+}
+
+cudaError_t launch_varlen_bwd(const VarlenBwdArgs& a, cudaStream_t stream) {
+    const int sms = device_sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const Plan x = plan_of(a.B, a.total_q, a.total_kv, a.Hq, a.Hkv, sms);
+    const Layout l = layout_of(x, a.total_q, a.total_kv, a.Hq, a.Hkv, a.D);
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    Params p{};
+    p.o = static_cast<const __nv_bfloat16*>(a.o);
+    p.d_o = static_cast<const __nv_bfloat16*>(a.d_o);
+    p.o_stride = a.o_stride;
+    p.do_stride = a.do_stride;
+    p.lse = a.lse;
+    p.d_lse = a.d_lse;
+    p.qo_indptr = a.qo_indptr;
+    p.kv_indptr = a.kv_indptr;
+    p.kv_lens = a.kv_lens;
+    p.causal = a.causal;
+    p.B = a.B;
+    p.total_q = a.total_q;
+    p.total_kv = a.total_kv;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.G = a.Hq / a.Hkv;
+    p.P = kBM / p.G;
+    p.scale = a.scale;
+    p.scale_log2 = a.scale * kLog2e;
+    p.stats = reinterpret_cast<float2*>(ws + l.stats);
+    p.counts = reinterpret_cast<int*>(ws + l.counts);
+    p.kv_blocks = reinterpret_cast<int2*>(ws + l.kv_blocks);
+    p.q_blocks = reinterpret_cast<int2*>(ws + l.q_blocks);
+    p.max_kv_blocks = static_cast<int>(x.kv_blocks);
+    p.max_q_blocks = static_cast<int>(x.q_blocks);
+    p.kv_pieces = x.kv_pieces;
+    p.q_pieces = x.q_pieces;
+    p.dq = static_cast<__nv_bfloat16*>(a.d_q);
+    p.dk = static_cast<__nv_bfloat16*>(a.d_k);
+    p.dv = static_cast<__nv_bfloat16*>(a.d_v);
+    p.dq_stride = a.dq_stride;
+    p.dk_stride = a.dk_stride;
+    p.dv_stride = a.dv_stride;
+    p.dq_part = reinterpret_cast<float*>(ws + l.dq);
+    p.dk_part = reinterpret_cast<float*>(ws + l.dk);
+    p.dv_part = reinterpret_cast<float*>(ws + l.dv);
+    p.status = a.dev_status;
+    const uint64_t D = static_cast<uint64_t>(a.D);
+    CUtensorMap q, d_o, k, v;
+    auto q_map = [&](CUtensorMap* m, const void* base, long long stride) {
+        const uint64_t dims[3] = {D, static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.total_q)};
+        const uint64_t strides[2] = {D * 2, static_cast<uint64_t>(stride) * 2};
+        const uint32_t box[3] = {64, static_cast<uint32_t>(p.G), static_cast<uint32_t>(p.P)};
+        return encode_tiled_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    auto kv_map = [&](CUtensorMap* m, const void* base, long long stride) {
+        const uint64_t dims[2] = {static_cast<uint64_t>(a.Hkv) * D, static_cast<uint64_t>(a.total_kv)};
+        const uint64_t strides[1] = {static_cast<uint64_t>(stride) * 2};
+        const uint32_t box[2] = {64, kBM};
+        return encode_tiled_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    // a side without rows has no tiles, and its maps are not used
+    bool good = true;
+    if (a.total_q > 0) good = q_map(&q, a.q, a.q_stride) && q_map(&d_o, a.d_o, a.do_stride);
+    if (good && a.total_kv > 0) good = kv_map(&k, a.k, a.k_stride) && kv_map(&v, a.v, a.v_stride);
+    if (!good) return cudaErrorInvalidValue;
+    if (a.total_q == 0) q = d_o = k;
+    if (a.total_kv == 0) k = v = q;
+    return a.D == 64 ? launch<true>(a, p, x, q, d_o, k, v, stream) : launch<false>(a, p, x, q, d_o, k, v, stream);
+}
+
+}  // namespace gb300

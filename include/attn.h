@@ -713,6 +713,39 @@ attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, long 
                               int32_t* dev_status, void* stream);
 
 /*
+ * attn_varlen_bwd - gradient of attn_varlen_fwd.
+ *
+ * With P = exp(scale Q K^T - lse) where a query sees a key and
+ * delta = sum_d d_o o - d_lse:  d_v = P^T d_o,  dS = P (d_o V^T - delta),
+ * d_q = scale dS K,  d_k = scale dS^T Q, the last two sums over the query heads
+ * of a KV head as well.  P and dS are rounded to bf16 for their products (2^-8
+ * of each at most), everything else is fp32.  No atomics: results do not depend
+ * on timing (within rounding they do on the SM count).
+ *
+ *   d_o, o       [total_q, Hq, D] bfloat16, token rows d_o_stride and o_stride
+ *                elements apart; o and lse are what the forward call left (read)
+ *   lse          float32 [total_q, Hq] (read)
+ *   d_lse        float32 [total_q, Hq], the gradient of lse (read; NULL: zeros)
+ *   d_q          [total_q, Hq, D] bfloat16, d_q_stride apart
+ *   d_k, d_v     [total_kv, Hkv, D], d_k_stride and d_v_stride apart
+ *                (written: rows of a sequence that no query sees, those behind
+ *                kv_lens[b] among them, get zeros; rows of no sequence are left
+ *                alone)
+ *   workspace    >= attn_varlen_bwd_workspace_bytes() bytes, 16-byte aligned:
+ *                scratch (the size goes by the current device's SM count).
+ *                Calls that may run at the same time need separate workspaces.
+ * Other arguments, limits and errors as attn_varlen_fwd.
+ */
+size_t attn_varlen_bwd_workspace_bytes(int B, int total_q, int total_kv, int Hq, int Hkv, int D);
+attn_status_t attn_varlen_bwd(const void* d_o, const void* q, const void* k, const void* v, const void* o,
+                              long long d_o_stride, long long q_stride, long long k_stride, long long v_stride,
+                              long long o_stride, const float* lse, const float* d_lse, const int32_t* qo_indptr,
+                              const int32_t* kv_indptr, const int32_t* kv_lens, int causal, int B, int total_q,
+                              int total_kv, int Hq, int Hkv, int D, float scale, void* workspace,
+                              size_t workspace_bytes, void* d_q, void* d_k, void* d_v, long long d_q_stride,
+                              long long d_k_stride, long long d_v_stride, int32_t* dev_status, void* stream);
+
+/*
  * attn_lse_merge - LSE-weighted merge of split partials.
  *
  * Follows "splitk_kernels.py", _splitK_reduce: per row n,
