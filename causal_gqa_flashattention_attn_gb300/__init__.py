@@ -2,9 +2,9 @@
 
 This module only marshals arguments: it takes torch tensors that already live
 on the GPU, passes their device pointers and sizes to the C ABI declared in
-``include/attn.h`` (through ctypes, or for the paged cache's writers and the
-block-scaled cache's readers through the compiled ``_binding``) and raises on a
-non-OK status.  Every step of the
+``include/attn.h`` (through ctypes, or for the paged cache's writers, the
+block-scaled cache's readers and the entries over contiguous keys through the
+compiled ``_binding``) and raises on a non-OK status.  Every step of the
 computation runs in the library's CUDA kernels; there is no fallback of any
 kind, and importing a function of this module fails loudly when the library
 has not been built.
@@ -27,6 +27,7 @@ Entry points (names as in the C ABI):
   attn_qk_norm_rope_bwd     its gradient
   attn_varlen_fwd           attention of a ragged batch to contiguous keys: cross attention, or causal
   attn_varlen_bwd           its gradient
+  attn_cross_decode         single tokens' attention to an encoder's states (1..16 queries per sequence)
   attn_lse_merge            LSE-weighted merge of split partials
   attn_lse_merge_bwd        its gradient
   attn_status_string
@@ -58,7 +59,8 @@ EXPORTED = ("attn_prefill_fwd", "attn_prefill_workspace_bytes", "attn_prefill_pl
             "attn_decode_fp8_block_workspace_bytes", "attn_decode_paged_fp8_block",
             "attn_prefill_fp8_block_workspace_bytes", "attn_prefill_paged_fp8_block", "attn_qk_norm_rope",
             "attn_qk_norm_rope_bwd_workspace_bytes", "attn_qk_norm_rope_bwd", "attn_varlen_fwd_workspace_bytes",
-            "attn_varlen_fwd", "attn_varlen_bwd_workspace_bytes", "attn_varlen_bwd", "attn_lse_merge", "attn_lse_merge_bwd", "attn_selftest_wait_timeout",
+            "attn_varlen_fwd", "attn_varlen_bwd_workspace_bytes", "attn_varlen_bwd",
+            "attn_cross_decode_workspace_bytes", "attn_cross_decode", "attn_lse_merge", "attn_lse_merge_bwd", "attn_selftest_wait_timeout",
             "attn_status_string", "attn_abi_version")
 ATTN_DECODE_STATIC_SCRATCH_BYTES = 32 << 20
 
@@ -160,6 +162,10 @@ def lib():
     L.attn_varlen_bwd_workspace_bytes.restype = sz
     L.attn_varlen_bwd.argtypes = [vp] * 5 + [i64] * 5 + [vp] * 5 + [i32] * 7 + [f32, vp, sz, vp, vp, vp, i64, i64, i64, vp, vp]
     L.attn_varlen_bwd.restype = i32
+    L.attn_cross_decode_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    L.attn_cross_decode_workspace_bytes.restype = sz
+    L.attn_cross_decode.argtypes = [vp, vp, vp, i64, i64, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, sz, vp, vp, vp, vp]
+    L.attn_cross_decode.restype = i32
     L.attn_lse_merge.argtypes = [vp, vp, i32, i32, i32, vp, vp, i32, vp]
     L.attn_lse_merge.restype = i32
     L.attn_lse_merge_bwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, vp]
@@ -750,6 +756,23 @@ def attn_varlen_bwd(d_o, q, k, v, o, lse, qo_indptr, kv_indptr, kv_lens=None, ca
     """
     return _run(stream, _native().varlen_bwd, d_o, q, k, v, o, lse, qo_indptr, kv_indptr, kv_lens, causal, scale, d_lse,
                 workspace, d_q, d_k, d_v, dev_status)
+
+
+def attn_cross_decode_workspace_bytes(B, q_len, Hq, Hkv, D=128):
+    """Bytes of workspace attn_cross_decode takes on the current device."""
+    return int(lib().attn_cross_decode_workspace_bytes(B, q_len, Hq, Hkv, D))
+
+
+def attn_cross_decode(q, k, v, kv_indptr, kv_lens=None, scale=None, workspace=None, o=None, lse=None, dev_status=None,
+                      stream=None):
+    """Single tokens' attention to an encoder's states: ``q [B, Hq, D]`` (one
+    query per sequence) or ``[B, q_len, Hq, D]`` (1..16, the beams of a search),
+    bf16, each of which sees every key of its sequence; ``k, v, kv_indptr,
+    kv_lens`` as :func:`attn_varlen_fwd`.  ``workspace``: a uint8 tensor of
+    attn_cross_decode_workspace_bytes() bytes, scratch (None allocates one).
+    Returns ``(o, lse, workspace)``, ``lse [B, Hq]`` or ``[B, q_len, Hq]``.
+    """
+    return _run(stream, _native().cross_decode, q, k, v, kv_indptr, kv_lens, scale, workspace, o, lse, dev_status)
 
 
 def decode_partials_view(workspace, B, Hq, max_kv_len, split_tokens, D):

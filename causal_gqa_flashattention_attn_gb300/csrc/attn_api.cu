@@ -851,6 +851,37 @@ attn_status_t attn_varlen_bwd(const void* d_o, const void* q, const void* k, con
     return from_cuda(launch_varlen_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 
+size_t attn_cross_decode_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D) {
+    if (B <= 0 || q_len <= 0 || q_len > 16 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
+    if (!decode_rows_ok(q_len, Hq)) return 0;
+    const int sms = device_sm_count();
+    return sms > 0 ? cross_decode_workspace(q_len, Hq, Hkv, D, sms) : 0;
+}
+
+attn_status_t attn_cross_decode(const void* q, const void* k, const void* v, long long k_stride, long long v_stride,
+                                const int32_t* kv_indptr, const int32_t* kv_lens, int B, int q_len, int total_kv,
+                                int Hq, int Hkv, int D, float scale, void* workspace, size_t workspace_bytes, void* o,
+                                float* lse, int32_t* dev_status, void* stream) {
+    if (q == nullptr || o == nullptr || kv_indptr == nullptr || (total_kv > 0 && (k == nullptr || v == nullptr)))
+        return ATTN_ERR_INVALID_ARG;
+    if (B <= 0 || q_len <= 0 || total_kv < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0 || !std::isfinite(scale))
+        return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+    if (k_stride % 8 != 0 || v_stride % 8 != 0 || k_stride < static_cast<long long>(Hkv) * D || v_stride < static_cast<long long>(Hkv) * D)
+        return ATTN_ERR_INVALID_ARG;
+    if (q_len > 16 || B > cross_decode_max_seqs() || k_stride >= (1LL << 38) || v_stride >= (1LL << 38)) return ATTN_ERR_UNSUPPORTED;
+    if (!decode_rows_ok(q_len, Hq) || static_cast<long long>(Hq) * q_len * B >= (1LL << 31) || total_kv >= (1 << 30))
+        return ATTN_ERR_UNSUPPORTED;
+    if (workspace == nullptr || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
+    const int sms = device_sm_count();
+    if (sms <= 0) return ATTN_ERR_CUDA;
+    if (workspace_bytes < cross_decode_workspace(q_len, Hq, Hkv, D, sms)) return ATTN_ERR_WORKSPACE;
+    const CrossDecodeArgs a{q, k, v, k_stride, v_stride, kv_indptr, kv_lens, B, q_len, total_kv, Hq, Hkv, D, scale, workspace,
+                            o, lse, dev_status};
+    return from_cuda(launch_cross_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
 attn_status_t attn_lse_merge(const float* o_part, const float* lse_part, int N, int S, int D, void* o, float* lse,
                              attn_dtype_t o_dtype, void* stream) {
     if (o_part == nullptr || lse_part == nullptr || o == nullptr) return ATTN_ERR_INVALID_ARG;

@@ -1,6 +1,6 @@
 // binding.cpp - the Python binding of the paged cache's writers, of the
-// block-scaled cache's readers and of the layer's operators around them (norms
-// with rotation), as a CPython module over the C ABI.
+// block-scaled cache's readers, of the norms with rotation and of the attention
+// over contiguous keys, as a CPython module over the C ABI.
 //
 // It checks tensors, takes their pointers and sizes and the current CUDA
 // stream, allocates the outputs that are not given, and calls the C ABI.  A
@@ -647,7 +647,51 @@ PyObject* varlen_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// cross_decode(q, k, v, kv_indptr, kv_lens, scale, workspace, o, lse, dev_status)
+// -> (o, lse, workspace)
+PyObject* cross_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        const Args args{a, n};
+        const at::Tensor& q = args.tensor("q", 0);
+        const at::Device device = call_device(q);
+        constexpr auto bf16 = at::ScalarType::BFloat16;
+        const bool single = q.dim() == 3;
+        if (!single && q.dim() != 4) throw Refused("q must be [B, Hq, D] or [B, q_len, Hq, D], not " + shape_text(q.sizes()));
+        const int64_t bsz = q.size(0), nq = single ? 1 : q.size(1), hq = q.size(-2), d = q.size(-1);
+        void* qp = single ? expect("q", q, device, {-1, -1, -1}, bf16) : expect("q", q, device, {-1, -1, -1, -1}, bf16);
+        const at::Tensor &k = args.tensor("k", 1), &v = args.tensor("v", 2);
+        long long ks = 0, vs = 0;
+        void* kp = token_rows("k", k, device, ks);
+        void* vp = token_rows("v", v, device, vs);
+        if (v.sizes() != k.sizes()) throw Refused("k and v must have the same shape");
+        if (k.size(2) != d) throw Refused("q and k must have the same head dimension");
+        const int32_t* kv = static_cast<const int32_t*>(expect("kv_indptr", args.tensor("kv_indptr", 3), device, {bsz + 1}, at::ScalarType::Int));
+        const int32_t* lens = optional_int(args, "kv_lens", 4, bsz, device);
+        const int b = small("q", bsz), i = small("q", nq), h = small("q", hq), hkv = small("k", k.size(1)), dd = small("q", d);
+        at::Tensor ws, o, lse;
+        if (args.none(6)) {
+            const size_t need = attn_cross_decode_workspace_bytes(b, i, h, hkv, dd);
+            ws = make_empty({static_cast<int64_t>(std::max<size_t>(need, 16))}, at::ScalarType::Byte, device);
+        }
+        if (args.none(7)) o = make_empty(q.sizes(), bf16, device);
+        if (args.none(8)) lse = make_empty(q.sizes().slice(0, q.dim() - 1), at::ScalarType::Float, device);
+        const at::Tensor& wt = args.none(6) ? ws : args.tensor("workspace", 6);
+        const at::Tensor& ot = args.none(7) ? o : args.tensor("o", 7);
+        const at::Tensor& lt = args.none(8) ? lse : args.tensor("lse", 8);
+        void* wp = expect("workspace", wt, device, {-1}, at::ScalarType::Byte);
+        void* op = single ? expect("o", ot, device, {bsz, hq, d}, bf16) : expect("o", ot, device, {bsz, nq, hq, d}, bf16);
+        float* lp = static_cast<float*>(single ? expect("lse", lt, device, {bsz, hq}, at::ScalarType::Float)
+                                               : expect("lse", lt, device, {bsz, nq, hq}, at::ScalarType::Float));
+        check("attn_cross_decode",
+              attn_cross_decode(qp, kp, vp, ks, vs, kv, lens, b, i, small("k", k.size(0)), h, hkv, dd,
+                                scale_or_default(args, 5, dd), wp, static_cast<size_t>(wt.numel()), op, lp,
+                                status_word(args, 9, device), stream_of(device)));
+        return tuple_of({wrap_or(args, 7, o), wrap_or(args, 8, lse), wrap_or(args, 6, ws)});
+    });
+}
+
 PyMethodDef methods[] = {
+    {"cross_decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(cross_decode)), METH_FASTCALL, nullptr},
     {"varlen_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(varlen_bwd)), METH_FASTCALL, nullptr},
     {"varlen_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(varlen_fwd)), METH_FASTCALL, nullptr},
     {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(qk_norm_rope)), METH_FASTCALL, nullptr},

@@ -291,6 +291,25 @@ size_t varlen_bwd_workspace(int B, int total_q, int total_kv, int Hq, int Hkv, i
 bool varlen_bwd_grid_ok(int B, int total_q, int total_kv, int Hq, int Hkv, int sms);
 cudaError_t launch_varlen_bwd(const VarlenBwdArgs& a, cudaStream_t stream);
 
+// Single tokens' attention to contiguous keys (cross_decode.cu).
+struct CrossDecodeArgs {
+    const void* q;          // [B, q_len, Hq, D] bf16
+    const void* k;          // [total_kv, Hkv, D], rows k_stride elements apart
+    const void* v;
+    long long k_stride, v_stride;
+    const int32_t* kv_indptr;   // [B + 1]
+    const int32_t* kv_lens;     // [B], may be NULL
+    int B, q_len, total_kv, Hq, Hkv, D;
+    float scale;
+    void* workspace;
+    void* o;                // as q
+    float* lse;             // [B, q_len, Hq] or NULL
+    int32_t* dev_status;
+};
+int cross_decode_max_seqs();
+size_t cross_decode_workspace(int q_len, int Hq, int Hkv, int D, int sms);
+cudaError_t launch_cross_decode(const CrossDecodeArgs& a, cudaStream_t stream);
+
 int varlen_max_seqs();
 int varlen_max_pairs();
 int varlen_pair_bits();

@@ -38,6 +38,7 @@
 
 #include "paged.cuh"
 #include "ptx.cuh"
+#include "shares.cuh"
 
 namespace gb300 {
 namespace {
@@ -100,13 +101,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Transpose of an 8x8 matrix of 16-bit elements held in fragment layout.
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
-    uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-
 // Sequence b's cached tokens: its length within what its page list holds.
 __device__ __forceinline__ int length_of(const Params& p, int b, bool flag) {
     const int len = p.seq_lens[b];
@@ -159,22 +153,6 @@ __device__ __forceinline__ bool count_tiles(const Params& p, int* before, int* l
     if (threadIdx.x == kThreads - 1) before[p.B] = base;   // the last run ends with the last sequence, or is empty
     return __syncthreads_or(most > kWholeTiles) != 0;
 }
-
-// The cut of `total` tiles (and ends) into shares: the first `extra` shares take each + 1
-// tiles, the others `each`.
-struct Cut {
-    int shares, each, extra;
-    __device__ __forceinline__ Cut(int workers, int total) {
-        shares = max(1, min(workers, total));
-        each = total / shares;
-        extra = total - each * shares;
-    }
-    __device__ __forceinline__ int start(int w) const { return w * each + min(w, extra); }
-    __device__ __forceinline__ int share_of(int x) const {
-        const int big = extra * (each + 1);
-        return x < big ? x / (each + 1) : extra + (x - big) / each;
-    }
-};
 
 // Per-warp state of the online softmax and the O^T accumulators of NB x 8 rows
 // (row 2t4 + j of block n): m for the sums, M for the values.

@@ -746,6 +746,31 @@ attn_status_t attn_varlen_bwd(const void* d_o, const void* q, const void* k, con
                               long long d_k_stride, long long d_v_stride, int32_t* dev_status, void* stream);
 
 /*
+ * attn_cross_decode - single tokens' attention to an encoder's states: 1 to 16
+ * queries per sequence (one token, the beams of a search), each of which sees
+ * every key of its sequence.
+ *
+ * What attn_varlen_fwd computes without `causal`, by one read of K and V: the
+ * work is cut evenly over the GPU on the device, whatever the lengths, and the
+ * pieces of a sequence are joined in a fixed order, so results do not depend on
+ * timing (within rounding they do on the SM count).  The softmax weights are
+ * rounded to bf16 for the product with V, as there.
+ *
+ *   q            [B, q_len, Hq, D] bfloat16, dense                     (read)
+ *   k, v, k_stride, v_stride, kv_indptr, kv_lens  as attn_varlen_fwd   (read)
+ *   workspace    >= attn_cross_decode_workspace_bytes() bytes, 16-byte aligned:
+ *                scratch (the size goes by the current device's SM count).
+ *                Calls that may run at the same time need separate workspaces.
+ *   o            as q; lse float32 [B, q_len, Hq] or NULL              (written)
+ *   D 64 or 128, q_len 1..16, any Hq % Hkv == 0, B <= 4096.
+ */
+size_t attn_cross_decode_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D);
+attn_status_t attn_cross_decode(const void* q, const void* k, const void* v, long long k_stride, long long v_stride,
+                                const int32_t* kv_indptr, const int32_t* kv_lens, int B, int q_len, int total_kv,
+                                int Hq, int Hkv, int D, float scale, void* workspace, size_t workspace_bytes, void* o,
+                                float* lse, int32_t* dev_status, void* stream);
+
+/*
  * attn_lse_merge - LSE-weighted merge of split partials.
  *
  * Follows "splitk_kernels.py", _splitK_reduce: per row n,
