@@ -34,6 +34,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -43,20 +44,44 @@ namespace {
 
 constexpr int kBM = 128;        // rows and columns of a tile
 constexpr int kThreads = 384;
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kStatWarp = 10;
-// Registers: launched at 168 per thread (384 x 168 = 64512); 2 x 128 x 216 + 128 x 72 = 64512.
-constexpr uint32_t kRegsSoftmax = 216, kRegsControl = 72;
+constexpr int kProducerWarp = 0, kMmaWarp = 1, kStatWarp = 2;
+constexpr int kScoreWarp = 4, kScoreThreads = 256;   // the first of eight
+// Registers: launched at 168 per thread (384 x 168 = 64512); 2 x 128 x 208 + 128 x 88 = 64512.
+constexpr uint32_t kRegsSoftmax = 208, kRegsControl = 88;
 constexpr int kHalf = 128 * 128;   // bytes of one 64-column half of a 128-row tile
 constexpr int kTile = 2 * kHalf;
-constexpr int kStages = 2;
-constexpr int kStatSlots = 4;
-// shared memory (offsets from a 1024-aligned base): two resident tiles, then the
-// stages of the two streamed ones, then the queries' statistics
-constexpr int kOffR1 = 0, kOffR2 = kTile;
-constexpr int kOffY1 = 2 * kTile;
-constexpr int kOffY2 = kOffY1 + kStages * kTile;
-constexpr int kOffStat = kOffY2 + kStages * kTile;
-constexpr int kSmemBytes = kOffStat + kStatSlots * 2 * kBM * 4;
+constexpr int kStatSlots = 2;
+// Stages of the streamed tiles: three of the first (Q, or K), two of the second
+// (dO, or V).  A stage is free when a product issued after its last reader is
+// done (MMAs complete in order), which is announced anyway:
+//   dK, dV: Q after dK, by dP of the next tile; dO after dV, by S of the next tile;
+//   dQ:     K after dQ, by dP of the next tile; V after its dP.
+// The first is wanted half a step later than it would be free with two stages,
+// less than a load takes: two stages of Q cost 550 to 1000 cycles a step of 3500.
+constexpr int kStages1 = 3, kStages2 = 2;
+// Shared memory, by addresses that are constants (the barriers and what the
+// system reserves lie below kOffR1): two resident tiles, then the stages of the
+// second streamed one and of the first, then (dK, dV) the queries' statistics.
+// With them, and TMEM taken whole (its columns start at 0), every operand of
+// every MMA is an immediate, and the issuing thread spends few instructions on
+// each: its issue slots are contended by the score warps of its SM quarter.
+constexpr int kOffR1 = 2048, kOffR2 = kOffR1 + kTile;
+constexpr int kOffY2 = kOffR2 + kTile;
+constexpr int kOffY1 = kOffY2 + kStages2 * kTile;
+constexpr int kOffStat = kOffY1 + kStages1 * kTile;
+constexpr int kEnd = kOffStat + kStatSlots * 2 * kBM * 4;
+// Barriers and words, where the dynamic part starts: behind the system's 1024
+// bytes (there is no static part).
+struct Control {
+    uint64_t r_full, y1_full[kStages1], y2_full[kStages2];
+    uint64_t s_full[2], dp_full[2];   // of even and odd tiles
+    uint64_t p_ready, ds_ready, acc_full;
+    uint64_t stat_full[kStatSlots], stat_empty[kStatSlots];
+    uint32_t tmem_base;
+    int abort;
+};
+constexpr int kSystem = 1024, kSmemBytes = kEnd - kSystem;
+static_assert(kSystem + sizeof(Control) <= kOffR1 && kSmemBytes <= 227 * 1024, "all of an SM's shared memory");
 // TMEM columns
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColDP = 128, kColAcc1 = 256, kColAcc2 = 384;   // dV, dK; or a second S, dQ
@@ -70,7 +95,7 @@ struct Params {
     const int32_t *qo_indptr, *kv_indptr, *kv_lens;
     int causal, B, total_q, total_kv, Hq, Hkv, G, P;
     float scale, scale_log2;
-    float2* stats;                // [total_q * Hq] (-log2e LSE, delta)
+    float2* stats;                // [total_q * Hq] (-log2e LSE, -delta)
     int* counts;                  // blocks of keys, blocks of queries
     int2* kv_blocks;              // (sequence, block), longest first
     int2* q_blocks;
@@ -199,7 +224,7 @@ __global__ void __launch_bounds__(kPrepThreads) varlen_bwd_prepare_kernel(const 
         const float lse = p.lse[row];
         // a row that saw nothing (LSE = -inf) has P = 0
         p.stats[row] = lse == -INFINITY ? make_float2(-INFINITY, 0.f)
-                                        : make_float2(-lse * kLog2e, sum - (p.d_lse != nullptr ? p.d_lse[row] : 0.f));
+                                        : make_float2(-lse * kLog2e, (p.d_lse != nullptr ? p.d_lse[row] : 0.f) - sum);
     }
 }
 
@@ -214,12 +239,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ Params p) {
     constexpr int kD = kD64 ? 64 : 128, kHalves = kD / 64;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = align_1024(smem_raw);
-    __shared__ __align__(8) uint64_t r_full, y1_full[kStages], y2_full[kStages], y1_empty[kStages], y2_empty[kStages];
-    __shared__ __align__(8) uint64_t s_full[2], dp_full, p_ready, ds_ready, acc_full;
-    __shared__ __align__(8) uint64_t stat_full[kStatSlots], stat_empty[kStatSlots];
-    __shared__ uint32_t tmem_base_sh;
-    __shared__ int abort_sh;
+    uint8_t* smem = smem_raw - kSystem;   // shared address 0
+    Control& sh = *reinterpret_cast<Control*>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // the list of blocks and the statistics come from the kernel before
@@ -247,27 +268,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = j1 - j0;
 
     if (threadIdx.x == 0) {
-        mbar_init(&r_full, 1);
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&y1_full[s], 1);
-            mbar_init(&y2_full[s], 1);
-            mbar_init(&y1_empty[s], 1);
-            mbar_init(&y2_empty[s], 1);
+        mbar_init(&sh.r_full, 1);
+        for (int s = 0; s < kStages1; ++s) mbar_init(&sh.y1_full[s], 1);
+        for (int s = 0; s < kStages2; ++s) mbar_init(&sh.y2_full[s], 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sh.s_full[s], 1);
+            mbar_init(&sh.dp_full[s], 1);
         }
-        for (int s = 0; s < 2; ++s) mbar_init(&s_full[s], 1);
-        mbar_init(&dp_full, 1);
-        mbar_init(&p_ready, 8);
-        mbar_init(&ds_ready, 8);
-        mbar_init(&acc_full, 1);
+        mbar_init(&sh.p_ready, 8);
+        mbar_init(&sh.ds_ready, 8);
+        mbar_init(&sh.acc_full, 1);
         for (int s = 0; s < kStatSlots; ++s) {
-            mbar_init(&stat_full[s], 1);
-            mbar_init(&stat_empty[s], 8);
+            mbar_init(&sh.stat_full[s], 1);
+            mbar_init(&sh.stat_empty[s], 8);
         }
-        abort_sh = 0;
+        sh.abort = 0;
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
-        tmem_alloc(&tmem_base_sh, kTmemCols);
+        tmem_alloc(&sh.tmem_base, kTmemCols);
         tmem_relinquish();
     }
     const int rows_used = p.P * p.G;   // rows of a tile of queries
@@ -275,9 +294,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the rows behind them are never loaded: zeros, which add nothing
         constexpr int kVecs = kHalf / 16;
         const int first_vec = rows_used * 8, per_half = kVecs - first_vec;
-        for (int i = threadIdx.x; i < 2 * kStages * kHalves * per_half; i += kThreads) {
+        for (int i = threadIdx.x; i < (kStages1 + kStages2) * kHalves * per_half; i += kThreads) {
             const int h = i / per_half;   // halves of the stages, in the order of their places
-            const int at = kOffY1 + (h / kHalves) * kTile + (h % kHalves) * kHalf + (first_vec + i % per_half) * 16;
+            const int at = kOffY2 + (h / kHalves) * kTile + (h % kHalves) * kHalf + (first_vec + i % per_half) * 16;
             *reinterpret_cast<uint4*>(smem + at) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();   // generic-proxy writes -> the tensor core's reads
@@ -285,17 +304,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_base_sh;
+    constexpr uint32_t tmem = 0;
+    // both hold by construction; without them nothing is done
+    const bool placed = sh.tmem_base == tmem && smem_u32(smem_raw) == kSystem;
+    if (!placed) flag_status(p.status, ATTN_DEV_WAIT_TIMEOUT);
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        if (mbar_wait(bar, parity, &abort_sh)) return true;
+        if (mbar_wait(bar, parity, &sh.abort)) return true;
         flag_status(p.status, ATTN_DEV_WAIT_TIMEOUT);
-        atomicExch(&abort_sh, 1);
+        atomicExch(&sh.abort, 1);
         return false;
     };
 
-    if (warp < 8) {
+    if (!placed) {
+    } else if (warp >= kScoreWarp) {
         regs_inc<kRegsSoftmax>();
-        const int r = threadIdx.x & 127, h = warp >> 2;   // row of the tile, half of its columns
+        const int r = threadIdx.x & 127, h = (warp - kScoreWarp) >> 2;   // row of the tile, half of its columns
+        const int i_score = threadIdx.x - 32 * kScoreWarp;
         const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const float sl2 = p.scale_log2;
         const float2 scl2 = make_float2(sl2, sl2);
@@ -312,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         bool ok = true;
         for (int j = 0; j < n; ++j) {
-            const int y = j0 + j, st = j % kStages, slot = j % kStatSlots;
+            const int y = j0 + j, st = j % kStages1, slot = j % kStatSlots;
             const float* nlse = reinterpret_cast<const float*>(smem + kOffStat) + slot * 2 * kBM + 64 * h;
             const float* dlt = nlse + kBM;
             // columns [c_lo, c_hi) of this row's half count
@@ -320,15 +344,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool masked = false;
             const uint32_t s_addr = tmem + lane_addr + ((kDq && (j & 1)) ? kColAcc1 : kColS) + 64 * h;
             const uint32_t dp_addr = tmem + lane_addr + kColDP + 64 * h;
-            if (!(ok = wait(&s_full[kDq ? (j & 1) : 0], kDq ? ((j >> 1) & 1) : (j & 1)))) break;
+            // the statistics are there before the scores
+            float4 nl[kDq ? 1 : 16];
+            if constexpr (!kDq) {
+                if (!(ok = wait(&sh.stat_full[slot], (j / kStatSlots) & 1))) break;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) nl[e] = reinterpret_cast<const float4*>(nlse)[e];
+            } else {
+                nl[0] = make_float4(own.x, own.x, own.x, own.x);
+            }
+            if (!(ok = wait(&sh.s_full[j & 1], (j >> 1) & 1))) break;
             tc_fence_after();
+            uint32_t sr[2][32];
+            tmem_ld32(s_addr, sr[0]);
+            tmem_ld32(s_addr + 32, sr[1]);
             if constexpr (kDq) {
                 masked = y * kBM + kBM - 1 > lim_first;
                 c_hi = lim - y * kBM + 1 - 64 * h;
                 const int there = sq.kv_len - y * kBM;   // keys of the tile
                 if (there < kBM) {
                     // dS is 0 there, but 0 times whatever lies behind the keys is not
-                    for (int i = there * 8 + threadIdx.x; i < kHalf / 16; i += 256) {
+                    for (int i = there * 8 + i_score; i < kHalf / 16; i += kScoreThreads) {
                         uint4* rows = reinterpret_cast<uint4*>(smem + kOffY1 + st * kTile);
                         rows[i] = make_uint4(0u, 0u, 0u, 0u);
                         if (!kD64) rows[kHalf / 16 + i] = make_uint4(0u, 0u, 0u, 0u);
@@ -336,7 +372,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                 }
             } else {
-                if (!(ok = wait(&stat_full[slot], (j / kStatSlots) & 1))) break;
                 const int there = min(p.P, sq.q_len - y * p.P) * p.G;   // rows of the tile of queries
                 c_hi = there - 64 * h;
                 masked = there < rows_used;
@@ -346,33 +381,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     c_lo = static_cast<int>(min(max(from, 0LL), 128LL)) - 64 * h;
                 }
                 if (there < rows_used) {
-                    if (!(ok = wait(&y2_full[st], (j / kStages) & 1))) break;
-                    for (int i = there * 8 + threadIdx.x; i < kHalf / 16; i += 256) {
+                    if (!(ok = wait(&sh.y2_full[j % kStages2], (j / kStages2) & 1))) break;
+                    for (int i = there * 8 + i_score; i < kHalf / 16; i += kScoreThreads) {
                         uint4* rows = reinterpret_cast<uint4*>(smem + kOffY1 + st * kTile);
-                        constexpr int kNext = (kOffY2 - kOffY1) / 16;
-                        rows[i] = rows[kNext + i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (!kD64) rows[kHalf / 16 + i] = rows[kNext + kHalf / 16 + i] = make_uint4(0u, 0u, 0u, 0u);
+                        uint4* rows2 = reinterpret_cast<uint4*>(smem + kOffY2 + (j % kStages2) * kTile);
+                        rows[i] = rows2[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (!kD64) rows[kHalf / 16 + i] = rows2[kHalf / 16 + i] = make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
                 }
             }
             float2 pr[32];
+            tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t sr[32];
-                tmem_ld32(s_addr + 32 * c, sr);
-                tmem_ld_wait();
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    float4 nl = make_float4(own.x, own.x, own.x, own.x);
-                    if constexpr (!kDq) nl = *reinterpret_cast<const float4*>(nlse + 32 * c + e);
-                    const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), scl2,
-                                                 make_float2(nl.x, nl.y));
-                    const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3])), scl2,
-                                                 make_float2(nl.z, nl.w));
-                    pr[16 * c + e / 2] = make_float2(ex2(y0.x), ex2(y0.y));
-                    pr[16 * c + e / 2 + 1] = make_float2(ex2(y1.x), ex2(y1.y));
-                }
+            for (int e = 0; e < 16; ++e) {
+                const float4 l = nl[kDq ? 0 : e];
+                const uint32_t* x = &sr[e >> 3][4 * (e & 7)];
+                const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), scl2, make_float2(l.x, l.y));
+                const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), scl2, make_float2(l.z, l.w));
+                pr[2 * e] = make_float2(ex2(y0.x), ex2(y0.y));
+                pr[2 * e + 1] = make_float2(ex2(y1.x), ex2(y1.y));
             }
             if (masked) {
 #pragma unroll
@@ -389,47 +417,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_ready);
+                if (lane == 0) mbar_arrive(&sh.p_ready);
             }
-            if (!(ok = wait(&dp_full, j & 1))) break;
+            if (!(ok = wait(&sh.dp_full[j & 1], (j >> 1) & 1))) break;
             tc_fence_after();
+            uint32_t dr[2][32];
+            tmem_ld32(dp_addr, dr[0]);
+            tmem_ld32(dp_addr + 32, dr[1]);
+            tmem_ld_wait();
             uint32_t pk[32];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t dr[32];
-                tmem_ld32(dp_addr + 32 * c, dr);
-                tmem_ld_wait();
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    float4 dl = make_float4(own.y, own.y, own.y, own.y);
-                    if constexpr (!kDq) dl = *reinterpret_cast<const float4*>(dlt + 32 * c + e);
-                    const float2 p0 = pr[16 * c + e / 2], p1 = pr[16 * c + e / 2 + 1];
-                    float2 d0 = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(dr[e]), __uint_as_float(dr[e + 1])),
-                                                      make_float2(-dl.x, -dl.y)), p0);
-                    float2 d1 = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(dr[e + 2]), __uint_as_float(dr[e + 3])),
-                                                      make_float2(-dl.z, -dl.w)), p1);
-                    if (masked) {   // (what is not there may have a dP that is not finite)
-                        const int k = 32 * c + e;
-                        if (k < c_lo || k >= c_hi) d0.x = 0.f;
-                        if (k + 1 < c_lo || k + 1 >= c_hi) d0.y = 0.f;
-                        if (k + 2 < c_lo || k + 2 >= c_hi) d1.x = 0.f;
-                        if (k + 3 < c_lo || k + 3 >= c_hi) d1.y = 0.f;
-                    }
-                    pk[16 * c + e / 2] = pack_bf16x2(d0.x, d0.y);
-                    pk[16 * c + e / 2 + 1] = pack_bf16x2(d1.x, d1.y);
+            for (int e = 0; e < 16; ++e) {
+                float4 dl = make_float4(own.y, own.y, own.y, own.y);
+                if constexpr (!kDq) dl = reinterpret_cast<const float4*>(dlt)[e];
+                const uint32_t* x = &dr[e >> 3][4 * (e & 7)];
+                float2 d0 = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(dl.x, dl.y)), pr[2 * e]);
+                float2 d1 = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), make_float2(dl.z, dl.w)), pr[2 * e + 1]);
+                if (masked) {   // (what is not there may have a dP that is not finite)
+                    const int k = 4 * e;
+                    if (k < c_lo || k >= c_hi) d0.x = 0.f;
+                    if (k + 1 < c_lo || k + 1 >= c_hi) d0.y = 0.f;
+                    if (k + 2 < c_lo || k + 2 >= c_hi) d1.x = 0.f;
+                    if (k + 3 < c_lo || k + 3 >= c_hi) d1.y = 0.f;
                 }
+                pk[2 * e] = pack_bf16x2(d0.x, d0.y);
+                pk[2 * e + 1] = pack_bf16x2(d1.x, d1.y);
             }
             tmem_st32(dp_addr, pk);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&ds_ready);
-                if (!kDq) mbar_arrive(&stat_empty[slot]);
+                mbar_arrive(&sh.ds_ready);
+                if (!kDq) mbar_arrive(&sh.stat_empty[slot]);
             }
         }
         // -------------------------------------------------------------- epilogue
-        if (ok && n > 0) ok = wait(&acc_full, 0);
+        if (ok && n > 0) ok = wait(&sh.acc_full, 0);
         if (ok) {
             tc_fence_after();
             // dQ: both halves of the threads share a row's columns; else the first four warps have dV, the others dK
@@ -495,18 +519,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (queries) load_q(dst, map, bar, tile);
                     else load_kv(dst, map, bar, tile);
                 };
-                mbar_arrive_expect_tx(&r_full, 2 * (kDq ? q_bytes : kKvBytes));
-                load(kDq, smem + kOffR1, &r1_map, &r_full, blk.y);
-                load(kDq, smem + kOffR2, &r2_map, &r_full, blk.y);
+                mbar_arrive_expect_tx(&sh.r_full, 2 * (kDq ? q_bytes : kKvBytes));
+                load(kDq, smem + kOffR1, &r1_map, &sh.r_full, blk.y);
+                load(kDq, smem + kOffR2, &r2_map, &sh.r_full, blk.y);
+                const uint32_t bytes = kDq ? kKvBytes : q_bytes;
+                auto load1 = [&](int j) {
+                    const int s = j % kStages1;
+                    mbar_arrive_expect_tx(&sh.y1_full[s], bytes);
+                    load(!kDq, smem + kOffY1 + s * kTile, &y1_map, &sh.y1_full[s], j0 + j);
+                };
+                auto load2 = [&](int j) {
+                    const int s = j % kStages2;
+                    mbar_arrive_expect_tx(&sh.y2_full[s], bytes);
+                    load(!kDq, smem + kOffY2 + s * kTile, &y2_map, &sh.y2_full[s], j0 + j);
+                };
+                // (a barrier waited for here cannot run a round ahead: its next
+                // phase is of a tile that is loaded only afterwards)
                 for (int j = 0; j < n; ++j) {
-                    const int s = j % kStages;
-                    const uint32_t par = ((j / kStages) - 1) & 1, bytes = kDq ? kKvBytes : q_bytes;
-                    if (j >= kStages && !wait(&y1_empty[s], par)) break;
-                    mbar_arrive_expect_tx(&y1_full[s], bytes);
-                    load(!kDq, smem + kOffY1 + s * kTile, &y1_map, &y1_full[s], j0 + j);
-                    if (j >= kStages && !wait(&y2_empty[s], par)) break;
-                    mbar_arrive_expect_tx(&y2_full[s], bytes);
-                    load(!kDq, smem + kOffY2 + s * kTile, &y2_map, &y2_full[s], j0 + j);
+                    if (j >= 2 && !wait(&sh.dp_full[j & 1], ((j - 2) >> 1) & 1)) break;   // dP of tile j - 2
+                    load1(j);
+                    if (!kDq && j >= 2 && !wait(&sh.s_full[(j - 1) & 1], ((j - 1) >> 1) & 1)) break;   // S of tile j - 1
+                    load2(j);
                 }
             }
         } else if (warp == kStatWarp && !kDq) {
@@ -522,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (c < there)
                         v[e] = __ldcg(p.stats + (static_cast<size_t>(sq.q_start) + p0 + at) * p.Hq + kvh * p.G + (c - at * p.G));
                 }
-                if (j >= kStatSlots) ok = wait(&stat_empty[slot], ((j / kStatSlots) - 1) & 1);
+                if (j >= kStatSlots) ok = wait(&sh.stat_empty[slot], ((j / kStatSlots) - 1) & 1);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 float* dst = reinterpret_cast<float*>(smem + kOffStat) + slot * 2 * kBM;
 #pragma unroll
@@ -531,69 +564,83 @@ __global__ void __launch_bounds__(kThreads, 1)
                     dst[kBM + lane + 32 * e] = v[e].y;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&stat_full[slot]);
+                if (lane == 0) mbar_arrive(&sh.stat_full[slot]);
             }
         } else if (warp == kMmaWarp && n > 0) {
             if (lane == 0) {
                 constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, kBM, false);
                 constexpr uint32_t idesc_acc = idesc_bf16_f32(kBM, kD, true);
-                const uint32_t d_base = sw128_desc_lo(smem_u32(smem), 16);
+                auto desc = [](int off, int lbo) constexpr -> uint32_t { return (off >> 4) | ((lbo >> 4) << 16); };
                 auto scores = [&](uint32_t d, int a_off, int b_off) {   // D = A B^T over the head dimension
-                    const uint32_t a = d_base + (a_off >> 4), b = d_base + (b_off >> 4);
-                    umma_ss_lo<0>(d, a, b, idesc_s);
+                    umma_ss_lo<0>(d, desc(a_off, 16), desc(b_off, 16), idesc_s);
 #pragma unroll
                     for (int kk = 1; kk < kD / 16; ++kk) {
-                        const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                        umma_ss_lo<1>(d, a + off, b + off, idesc_s);
+                        const int off = (kk >> 2) * kHalf + (kk & 3) * 32;
+                        umma_ss_lo<1>(d, desc(a_off + off, 16), desc(b_off + off, 16), idesc_s);
                     }
                 };
-                // D (+)= A B over the 128 streamed rows; A in TMEM, two halves of 64 columns packed to 32
-                auto gather = [&](uint32_t d, uint32_t a, int b_off, bool acc) {
-                    const uint32_t b = d_base + (b_off >> 4) + (((kHalf - 16) >> 4) << 16);
-                    umma_ts_lo(d, a, b, idesc_acc, acc ? 1u : 0u);
+                // D (+)= A B over the 128 streamed rows; A in TMEM, two halves of 64 columns packed
+                // to 32; `next`, what the product after it waits for, comes in the middle, where
+                // the tensor core has MMAs to go on with
+                auto gather = [&](uint32_t d, uint32_t a, int b_off, bool acc, auto next) -> bool {
+                    umma_ts_lo(d, a, desc(b_off, kHalf), idesc_acc, acc ? 1u : 0u);
+                    bool good = true;
 #pragma unroll
-                    for (int kk = 1; kk < kBM / 16; ++kk)
-                        umma_ts_lo(d, a + (kk >> 2) * 64 + (kk & 3) * 8, b + ((kk * 16 * 128) >> 4), idesc_acc, 1u);
+                    for (int kk = 1; kk < kBM / 16; ++kk) {
+                        if (kk == 5) good = next();
+                        umma_ts_lo(d, a + (kk >> 2) * 64 + (kk & 3) * 8, desc(b_off + kk * 16 * 128, kHalf), idesc_acc, 1u);
+                    }
+                    return good;
+                };
+                // One tile's step, even or odd.  False: a wait ran out.  (The three stages of y1
+                // are not unrolled: six copies of the step were 9 % slower.)
+                int s1 = 0, n1 = 1;   // this tile's stage of y1, the next one's
+                auto step = [&](int j, auto odd) -> bool {
+                    constexpr int kOdd = decltype(odd)::value, n2 = !kOdd;
+                    static_assert(kStages2 == 2, "even and odd tiles");
+                    const int k = j + 1;
+                    const bool more = k < n;
+                    auto next1 = [&] { return !more || wait(&sh.y1_full[n1], (k / kStages1) & 1); };
+                    auto next2 = [&] { return !more || wait(&sh.y2_full[n2], (k / kStages2) & 1); };
+                    if constexpr (!kDq) {
+                        if (!wait(&sh.p_ready, j & 1)) return false;
+                        tc_fence_after();
+                        if (!gather(tmem + kColAcc1, tmem + kColS, kOffY2 + kOdd * kTile, j > 0, next1)) return false;   // dV += P^T dO
+                    } else if (!next1()) {
+                        return false;
+                    }
+                    if (more) {   // (for dK, dV it overwrites P, which the product before it has read)
+                        tc_fence_after();
+                        scores(tmem + ((kDq && !kOdd) ? kColAcc1 : kColS), kOffR1, kOffY1 + n1 * kTile);
+                        umma_commit(&sh.s_full[!kOdd]);
+                    }
+                    if (!wait(&sh.ds_ready, j & 1)) return false;
+                    tc_fence_after();
+                    if (!gather(tmem + kColAcc2, tmem + kColDP, kOffY1 + s1 * kTile, j > 0, next2)) return false;   // dK += dS^T Q, or dQ += dS K
+                    if (more) {   // overwrites dS
+                        tc_fence_after();
+                        scores(tmem + kColDP, kOffR2, kOffY2 + n2 * kTile);
+                        umma_commit(&sh.dp_full[!kOdd]);
+                    }
+                    s1 = n1;
+                    n1 = n1 + 1 == kStages1 ? 0 : n1 + 1;
+                    return true;
                 };
                 auto run = [&]() {
-                    if (!wait(&r_full, 0) || !wait(&y1_full[0], 0)) return;
+                    if (!wait(&sh.r_full, 0) || !wait(&sh.y1_full[0], 0)) return;
                     tc_fence_after();
                     scores(tmem + kColS, kOffR1, kOffY1);
-                    umma_commit(&s_full[0]);
-                    if (!wait(&y2_full[0], 0)) return;
+                    umma_commit(&sh.s_full[0]);
+                    if (!wait(&sh.y2_full[0], 0)) return;
                     tc_fence_after();
                     scores(tmem + kColDP, kOffR2, kOffY2);
-                    umma_commit(&dp_full);
-                    if (kDq) umma_commit(&y2_empty[0]);
-                    for (int j = 0; j < n; ++j) {
-                        const int s = j % kStages, nx = (j + 1) % kStages;
-                        const uint32_t nx_par = ((j + 1) / kStages) & 1;
-                        const bool more = j + 1 < n;
-                        if constexpr (!kDq) {
-                            if (!wait(&p_ready, j & 1)) return;
-                            tc_fence_after();
-                            gather(tmem + kColAcc1, tmem + kColS, kOffY2 + s * kTile, j > 0);   // dV += P^T dO
-                            umma_commit(&y2_empty[s]);
-                        }
-                        if (more) {   // (for dK, dV it overwrites P, which the product before it has read)
-                            if (!wait(&y1_full[nx], nx_par)) return;
-                            tc_fence_after();
-                            scores(tmem + ((kDq && !(j & 1)) ? kColAcc1 : kColS), kOffR1, kOffY1 + nx * kTile);
-                            umma_commit(&s_full[kDq ? ((j + 1) & 1) : 0]);
-                        }
-                        if (!wait(&ds_ready, j & 1)) return;
-                        tc_fence_after();
-                        gather(tmem + kColAcc2, tmem + kColDP, kOffY1 + s * kTile, j > 0);   // dK += dS^T Q, or dQ += dS K
-                        umma_commit(&y1_empty[s]);
-                        if (more) {   // overwrites dS
-                            if (!wait(&y2_full[nx], nx_par)) return;
-                            tc_fence_after();
-                            scores(tmem + kColDP, kOffR2, kOffY2 + nx * kTile);
-                            umma_commit(&dp_full);
-                            if (kDq) umma_commit(&y2_empty[nx]);
-                        }
+                    umma_commit(&sh.dp_full[0]);
+                    for (int j = 0; j < n;) {
+                        bool good = step(j++, std::integral_constant<int, 0>{});
+                        if (good && j < n) good = step(j++, std::integral_constant<int, 1>{});
+                        if (!good) return;
                     }
-                    umma_commit(&acc_full);
+                    umma_commit(&sh.acc_full);
                 };
                 run();
             }
@@ -604,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (warp == kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc(sh.tmem_base, kTmemCols);
     }
 }
 
@@ -685,14 +732,13 @@ template <bool kD64>
 cudaError_t launch(const VarlenBwdArgs& a, const Params& p, const Plan& x, const CUtensorMap& q, const CUtensorMap& d_o,
                    const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
     constexpr int kD = kD64 ? 64 : 128;
-    constexpr size_t kSmem = kSmemBytes + 1024;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = once_per_device(done, [] {
         cudaError_t r = cudaFuncSetAttribute(varlen_bwd_kernel<false, kD64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(kSmem));
+                                             kSmemBytes);
         return r != cudaSuccess ? r
                                 : cudaFuncSetAttribute(varlen_bwd_kernel<true, kD64>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     });
     if (e != cudaSuccess) return e;
     const long long rows = static_cast<long long>(a.total_q) * a.Hq;
@@ -700,11 +746,11 @@ cudaError_t launch(const VarlenBwdArgs& a, const Params& p, const Plan& x, const
     varlen_bwd_prepare_kernel<kD><<<static_cast<unsigned>(1 + (rows + per_cta - 1) / per_cta), kPrepThreads, 0, stream>>>(p);
     e = cudaGetLastError();
     if (e == cudaSuccess && a.total_kv > 0) {
-        varlen_bwd_kernel<false, kD64><<<static_cast<unsigned>(x.kv_blocks * a.Hkv * x.kv_pieces), kThreads, kSmem, stream>>>(k, v, q, d_o, p);
+        varlen_bwd_kernel<false, kD64><<<static_cast<unsigned>(x.kv_blocks * a.Hkv * x.kv_pieces), kThreads, kSmemBytes, stream>>>(k, v, q, d_o, p);
         e = cudaGetLastError();
     }
     if (e == cudaSuccess && a.total_q > 0) {
-        varlen_bwd_kernel<true, kD64><<<static_cast<unsigned>(x.q_blocks * a.Hkv * x.q_pieces), kThreads, kSmem, stream>>>(q, d_o, k, v, p);
+        varlen_bwd_kernel<true, kD64><<<static_cast<unsigned>(x.q_blocks * a.Hkv * x.q_pieces), kThreads, kSmemBytes, stream>>>(q, d_o, k, v, p);
         e = cudaGetLastError();
     }
     auto sum = [&](const float* part, int pieces, int n, int elems, const int32_t* indptr, __nv_bfloat16* out, long long stride) {
