@@ -63,8 +63,7 @@ constexpr int kStages1 = 3, kStages2 = 2;
 // system reserves lie below kOffR1): two resident tiles, then the stages of the
 // second streamed one and of the first, then (dK, dV) the queries' statistics.
 // With them, and TMEM taken whole (its columns start at 0), every operand of
-// every MMA is an immediate, and the issuing thread spends few instructions on
-// each: its issue slots are contended by the score warps of its SM quarter.
+// every MMA but a stage is an immediate.
 constexpr int kOffR1 = 2048, kOffR2 = kOffR1 + kTile;
 constexpr int kOffY2 = kOffR2 + kTile;
 constexpr int kOffY1 = kOffY2 + kStages2 * kTile;
@@ -567,28 +566,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&sh.stat_full[slot]);
             }
         } else if (warp == kMmaWarp && n > 0) {
-            if (lane == 0) {
+            const uint32_t lead = elect_one();
+            {
                 constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, kBM, false);
                 constexpr uint32_t idesc_acc = idesc_bf16_f32(kBM, kD, true);
                 auto desc = [](int off, int lbo) constexpr -> uint32_t { return (off >> 4) | ((lbo >> 4) << 16); };
                 auto scores = [&](uint32_t d, int a_off, int b_off) {   // D = A B^T over the head dimension
-                    umma_ss_lo<0>(d, desc(a_off, 16), desc(b_off, 16), idesc_s);
+                    umma_ss_by<0>(lead, d, desc(a_off, 16), desc(b_off, 16), idesc_s);
 #pragma unroll
                     for (int kk = 1; kk < kD / 16; ++kk) {
                         const int off = (kk >> 2) * kHalf + (kk & 3) * 32;
-                        umma_ss_lo<1>(d, desc(a_off + off, 16), desc(b_off + off, 16), idesc_s);
+                        umma_ss_by<1>(lead, d, desc(a_off + off, 16), desc(b_off + off, 16), idesc_s);
                     }
                 };
                 // D (+)= A B over the 128 streamed rows; A in TMEM, two halves of 64 columns packed
                 // to 32; `next`, what the product after it waits for, comes in the middle, where
                 // the tensor core has MMAs to go on with
                 auto gather = [&](uint32_t d, uint32_t a, int b_off, bool acc, auto next) -> bool {
-                    umma_ts_lo(d, a, desc(b_off, kHalf), idesc_acc, acc ? 1u : 0u);
+                    umma_ts_by(lead, d, a, desc(b_off, kHalf), idesc_acc, acc ? 1u : 0u);
                     bool good = true;
 #pragma unroll
                     for (int kk = 1; kk < kBM / 16; ++kk) {
                         if (kk == 5) good = next();
-                        umma_ts_lo(d, a + (kk >> 2) * 64 + (kk & 3) * 8, desc(b_off + kk * 16 * 128, kHalf), idesc_acc, 1u);
+                        umma_ts_by(lead, d, a + (kk >> 2) * 64 + (kk & 3) * 8, desc(b_off + kk * 16 * 128, kHalf), idesc_acc, 1u);
                     }
                     return good;
                 };
@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (more) {   // (for dK, dV it overwrites P, which the product before it has read)
                         tc_fence_after();
                         scores(tmem + ((kDq && !kOdd) ? kColAcc1 : kColS), kOffR1, kOffY1 + n1 * kTile);
-                        umma_commit(&sh.s_full[!kOdd]);
+                        umma_commit_by(lead, &sh.s_full[!kOdd]);
                     }
                     if (!wait(&sh.ds_ready, j & 1)) return false;
                     tc_fence_after();
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (more) {   // overwrites dS
                         tc_fence_after();
                         scores(tmem + kColDP, kOffR2, kOffY2 + n2 * kTile);
-                        umma_commit(&sh.dp_full[!kOdd]);
+                        umma_commit_by(lead, &sh.dp_full[!kOdd]);
                     }
                     s1 = n1;
                     n1 = n1 + 1 == kStages1 ? 0 : n1 + 1;
@@ -630,17 +630,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!wait(&sh.r_full, 0) || !wait(&sh.y1_full[0], 0)) return;
                     tc_fence_after();
                     scores(tmem + kColS, kOffR1, kOffY1);
-                    umma_commit(&sh.s_full[0]);
+                    umma_commit_by(lead, &sh.s_full[0]);
                     if (!wait(&sh.y2_full[0], 0)) return;
                     tc_fence_after();
                     scores(tmem + kColDP, kOffR2, kOffY2);
-                    umma_commit(&sh.dp_full[0]);
+                    umma_commit_by(lead, &sh.dp_full[0]);
                     for (int j = 0; j < n;) {
                         bool good = step(j++, std::integral_constant<int, 0>{});
                         if (good && j < n) good = step(j++, std::integral_constant<int, 1>{});
                         if (!good) return;
                     }
-                    umma_commit(&sh.acc_full);
+                    umma_commit_by(lead, &sh.acc_full);
                 };
                 run();
             }
