@@ -1168,7 +1168,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == kMmaWarp) {
             // ------------------------------------------------------------- MMA issuer
-            if (lane == 0) {
+            const uint32_t lead = elect_one();
+            {
                 // tiles written by cp.async (the generic proxy) need a proxy fence
                 // before the tensor core reads them; TMA-written tiles do not
                 const bool cp_async_tiles = kVarlen && !p.gathered;
@@ -1184,20 +1185,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto issue_s = [&](int t, int stage) {  // S_t = Q_t K^T
                     const uint32_t dq = d_base + ((kOffQ + t * kTile) >> 4), dk = d_base + ((kOffK + stage * kTile) >> 4);
                     const uint32_t d = tmem + kColS + 128 * t;
-                    umma_ss_lo<0>(d, dq, dk, idesc_qk);
+                    umma_ss_by<0>(lead, d, dq, dk, idesc_qk);
     #pragma unroll
                     for (int kk = 1; kk < (kD64 ? 4 : kD / 16); ++kk) {
                         const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                        umma_ss_lo<1>(d, dq + off, dk + off, idesc_qk);
+                        umma_ss_by<1>(lead, d, dq + off, dk + off, idesc_qk);
                     }
                 };
                 auto issue_pv = [&](int t, int stage, bool acc) {  // O_t (+)= P_t V
                     // V: leading offset kHalf (the two 64-column halves) in bits 16-29
                     const uint32_t dv = d_base + ((kOffV + stage * kTile) >> 4) + (((kHalf - 16) >> 4) << 16);
                     const uint32_t d = tmem + kColO + 128 * t, a = tmem + kColS + 128 * t;
-                    umma_ts_lo(d, a, dv, idesc_pv, acc ? 1u : 0u);
+                    umma_ts_by(lead, d, a, dv, idesc_pv, acc ? 1u : 0u);
     #pragma unroll
-                    for (int kk = 1; kk < kBN / 16; ++kk) umma_ts_lo(d, a + kk * 8, dv + ((kk * 16 * 128) >> 4), idesc_pv, 1u);
+                    for (int kk = 1; kk < kBN / 16; ++kk) umma_ts_by(lead, d, a + kk * 8, dv + ((kk * 16 * 128) >> 4), idesc_pv, 1u);
                 };
                 uint32_t kv_iter = 0, item_iter = 0;
                 bool ok = true;
@@ -1209,11 +1210,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (cp_async_tiles) fence_proxy_async_smem();   // cp.async writes -> tensor-core reads
                     tc_fence_after();
                     issue_s(0, kv_iter % kStages);
-                    umma_commit(&s_full[0]);
+                    umma_commit_by(lead, &s_full[0]);
                     issue_s(1, kv_iter % kStages);
-                    umma_commit(&s_full[1]);
-                    umma_commit(&k_empty[kv_iter % kStages]);   // K_j no longer read
-                    if (it.j1 - it.j0 == 1) umma_commit(&q_empty);  // Q no longer read: the producer may refill it
+                    umma_commit_by(lead, &s_full[1]);
+                    umma_commit_by(lead, &k_empty[kv_iter % kStages]);   // K_j no longer read
+                    if (it.j1 - it.j0 == 1) umma_commit_by(lead, &q_empty);  // Q no longer read: the producer may refill it
                     for (int j = it.j0; j < it.j1 && ok; ++j, ++kv_iter) {
                         const int s = kv_iter % kStages;
                         const bool last = (j + 1 == it.j1);
@@ -1225,7 +1226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (j == it.j0 && item_iter > 0 && !(ok = wait(&o_empty[t], (item_iter - 1) & 1))) break;
                             tc_fence_after();
                             issue_pv(t, s, j > it.j0);                   // O_t (+)= P_t V_j
-                            if (t == 1) umma_commit(&v_empty[s]);     // V_j no longer read
+                            if (t == 1) umma_commit_by(lead, &v_empty[s]);     // V_j no longer read
                             if (!last) {
                                 if (t == 0) {
                                     if (!(ok = wait(&k_full[nxt % kStages], (nxt / kStages) & 1))) break;
@@ -1233,11 +1234,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     tc_fence_after();
                                 }
                                 issue_s(t, nxt % kStages);            // S_t = Q_t K_{j+1}^T (after P_t is read)
-                                umma_commit(&s_full[t]);
-                                if (t == 1) umma_commit(&k_empty[nxt % kStages]);   // K_{j+1} no longer read
-                                if (t == 1 && j + 2 == it.j1) umma_commit(&q_empty);  // last S read Q
+                                umma_commit_by(lead, &s_full[t]);
+                                if (t == 1) umma_commit_by(lead, &k_empty[nxt % kStages]);   // K_{j+1} no longer read
+                                if (t == 1 && j + 2 == it.j1) umma_commit_by(lead, &q_empty);  // last S read Q
                             } else {
-                                umma_commit(&o_full[t]);
+                                umma_commit_by(lead, &o_full[t]);
                             }
                         }
                     }
