@@ -85,6 +85,14 @@ static_assert(kSystem + sizeof(Control) <= kOffR1 && kSmemBytes <= 227 * 1024, "
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColDP = 128, kColAcc1 = 256, kColAcc2 = 384;   // dV, dK; or a second S, dQ
 
+struct Seq {
+    int q_start, q_len, kv_start, kv_len, kv_room;
+};
+struct alignas(16) Block {   // block `at` of a sequence
+    Seq s;
+    int at, pad[2];
+};
+
 struct Params {
     const __nv_bfloat16* o;       // prepare
     const __nv_bfloat16* d_o;
@@ -96,8 +104,8 @@ struct Params {
     float scale, scale_log2;
     float2* stats;                // [total_q * Hq] (-log2e LSE, -delta)
     int* counts;                  // blocks of keys, blocks of queries
-    int2* kv_blocks;              // (sequence, block), longest first
-    int2* q_blocks;
+    Block* kv_blocks;             // longest first
+    Block* q_blocks;
     int max_kv_blocks, max_q_blocks, kv_pieces, q_pieces;
     __nv_bfloat16 *dq, *dk, *dv;
     long long dq_stride, dk_stride, dv_stride;
@@ -105,9 +113,6 @@ struct Params {
     int32_t* status;
 };
 
-struct Seq {
-    int q_start, q_len, kv_start, kv_room, kv_len;
-};
 // Offsets outside the tensors are cut to them.
 __device__ __forceinline__ Seq seq_of(const Params& p, int b) {
     Seq s;
@@ -131,7 +136,7 @@ constexpr int kMaxSeqs = 2048;
 // The blocks of one side of all sequences, sequences in `order`; `flip`: each
 // sequence's last block first.
 __device__ void list_blocks(const int* order, const int* len, int B, int per, bool flip, int* before, int* warp_sum,
-                            int2* out, int cap, int* count) {
+                            Block* out, int cap, int* count, const Params& p) {
     // blocks before each place of the order
     const int each = (B + kPrepThreads - 1) / kPrepThreads;
     const int i0 = min(static_cast<int>(threadIdx.x) * each, B), i1 = min(i0 + each, B);
@@ -162,7 +167,7 @@ __device__ void list_blocks(const int* order, const int* len, int B, int per, bo
             if (before[mid] <= x) lo = mid; else hi = mid;
         }
         const int k = x - before[lo], n = (len[order[lo]] + per - 1) / per;
-        out[x] = make_int2(order[lo], flip ? n - 1 - k : k);
+        out[x] = Block{seq_of(p, order[lo]), flip ? n - 1 - k : k, {0, 0}};
     }
     if (threadIdx.x == 0) *count = total;
     __syncthreads();
@@ -191,10 +196,10 @@ __global__ void __launch_bounds__(kPrepThreads) varlen_bwd_prepare_kernel(const 
             __syncthreads();
             if (side == 0)
                 list_blocks(order, kv_len, p.B, kBM, false, before, warp_sum, p.kv_blocks, p.max_kv_blocks,
-                            p.counts);
+                            p.counts, p);
             else
                 list_blocks(order, q_len, p.B, p.P, true, before, warp_sum, p.q_blocks, p.max_q_blocks,
-                            p.counts + 1);
+                            p.counts + 1, p);
         }
         return;
     }
@@ -242,18 +247,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     Control& sh = *reinterpret_cast<Control*>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // the list of blocks and the statistics come from the kernel before
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // The list of blocks and the statistics come from the first kernel, for which
+    // dK/dV's CTAs wait.  Once the last of them is in, dQ's take the SMs that fall
+    // free: what they read is there then, so they wait for nothing but, in the
+    // grid's last CTA, for dK/dV's end, so that this grid does not end before.
+    if (!kDq || p.total_kv == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (kDq && blockIdx.x + 1 == gridDim.x) asm volatile("griddepcontrol.wait;" ::: "memory");
     const int pieces = kDq ? p.q_pieces : p.kv_pieces;
     const int per_block = p.Hkv * pieces;
     const int entry = blockIdx.x / per_block;
+    // (the list has room for the entry, whether or not it is there)
+    const int4* listed = reinterpret_cast<const int4*>((kDq ? p.q_blocks : p.kv_blocks) + entry);
+    const int4 lo = __ldcg(listed), hi = __ldcg(listed + 1);
     if (entry >= __ldcg(p.counts + (kDq ? 1 : 0))) return;
-    const int2 blk = __ldcg((kDq ? p.q_blocks : p.kv_blocks) + entry);
     const int kvh = (blockIdx.x % per_block) / pieces, piece = blockIdx.x % pieces;
-    const Seq sq = seq_of(p, blk.x);
+    const Seq sq{lo.x, lo.y, lo.z, lo.w, hi.x};
+    const int own = hi.y;
     const int delta = sq.kv_len - sq.q_len;
-    const int kv0_own = blk.y * kBM;   // dK, dV: the first key
-    const int p0_own = blk.y * p.P;    // dQ: the first position
+    const int kv0_own = own * kBM;   // dK, dV: the first key
+    const int p0_own = own * p.P;    // dQ: the first position
     // streamed tiles that this block meets, and this part of them
     int first = 0, last = 0;
     if constexpr (kDq) {
@@ -327,11 +340,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool row_real = r < rows_used && pos < sq.q_len;
         const size_t q_row = (static_cast<size_t>(sq.q_start) + pos) * p.Hq + kvh * p.G + r % p.G;
         int lim = -1, lim_first = -1;
-        float2 own = make_float2(-INFINITY, 0.f);
+        float2 stat = make_float2(-INFINITY, 0.f);
         if constexpr (kDq) {
             lim = limit_of(p, sq, pos);
             lim_first = limit_of(p, sq, p0_own);
-            if (row_real) own = __ldcg(p.stats + q_row);
+            if (row_real) stat = __ldcg(p.stats + q_row);
         }
         bool ok = true;
         for (int j = 0; j < n; ++j) {
@@ -350,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) nl[e] = reinterpret_cast<const float4*>(nlse)[e];
             } else {
-                nl[0] = make_float4(own.x, own.x, own.x, own.x);
+                nl[0] = make_float4(stat.x, stat.x, stat.x, stat.x);
             }
             if (!(ok = wait(&sh.s_full[j & 1], (j >> 1) & 1))) break;
             tc_fence_after();
@@ -427,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t pk[32];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                float4 dl = make_float4(own.y, own.y, own.y, own.y);
+                float4 dl = make_float4(stat.y, stat.y, stat.y, stat.y);
                 if constexpr (!kDq) dl = reinterpret_cast<const float4*>(dlt)[e];
                 const uint32_t* x = &dr[e >> 3][4 * (e & 7)];
                 float2 d0 = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(dl.x, dl.y)), pr[2 * e]);
@@ -469,6 +482,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             __nv_bfloat16* out = kDq ? p.dq : (h == 0 ? p.dv : p.dk);
             const long long stride = kDq ? p.dq_stride : (h == 0 ? p.dv_stride : p.dk_stride);
             float* part = kDq ? p.dq_part : (h == 0 ? p.dv_part : p.dk_part);
+            // bf16 rows leave through shared memory (the stages are done with), whole
+            // rows side by side: 32 rows a warp, 16 bytes apart from a power of two
+            constexpr int kPitch = kCols * 2 + 16, kLanes = kCols / 8;
+            uint8_t* rows_sh = smem + kOffY2 + (warp - kScoreWarp) * 32 * kPitch;
 #pragma unroll
             for (int c = 0; c < kCols / 32; ++c) {
                 uint32_t ar[32];
@@ -476,8 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 32; ++e) ar[e] = real ? __float_as_uint(__uint_as_float(ar[e]) * f) : 0u;
-                if (!store) continue;
                 if (pieces > 1) {
+                    if (!store) continue;
                     float4* dst = reinterpret_cast<float4*>(
                         part + ((static_cast<size_t>(piece) * rows + row) * heads + head) * kD + col0 + 32 * c);
 #pragma unroll
@@ -485,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         dst[e] = make_float4(__uint_as_float(ar[4 * e]), __uint_as_float(ar[4 * e + 1]),
                                              __uint_as_float(ar[4 * e + 2]), __uint_as_float(ar[4 * e + 3]));
                 } else {
-                    uint4* dst = reinterpret_cast<uint4*>(out + row * stride + head * kD + col0 + 32 * c);
+                    uint4* dst = reinterpret_cast<uint4*>(rows_sh + lane * kPitch + 64 * c);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         uint4 v;
@@ -495,6 +512,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         v.w = pack_bf16x2(__uint_as_float(ar[8 * e + 6]), __uint_as_float(ar[8 * e + 7]));
                         dst[e] = v;
                     }
+                }
+            }
+            if (pieces == 1) {
+                const long long at = store ? static_cast<long long>(row) * stride + head * kD + col0 : -1;
+                __syncwarp();
+#pragma unroll
+                for (int r0 = 0; r0 < 32; r0 += 32 / kLanes) {
+                    const int rr = r0 + lane / kLanes, c = lane % kLanes;
+                    const long long to = __shfl_sync(0xffffffffu, at, rr);
+                    const uint4 v = *reinterpret_cast<const uint4*>(rows_sh + rr * kPitch + 16 * c);
+                    if (to >= 0) *reinterpret_cast<uint4*>(out + to + 8 * c) = v;
                 }
             }
         }
@@ -519,8 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     else load_kv(dst, map, bar, tile);
                 };
                 mbar_arrive_expect_tx(&sh.r_full, 2 * (kDq ? q_bytes : kKvBytes));
-                load(kDq, smem + kOffR1, &r1_map, &sh.r_full, blk.y);
-                load(kDq, smem + kOffR2, &r2_map, &sh.r_full, blk.y);
+                load(kDq, smem + kOffR1, &r1_map, &sh.r_full, own);
+                load(kDq, smem + kOffR2, &r2_map, &sh.r_full, own);
                 const uint32_t bytes = kDq ? kKvBytes : q_bytes;
                 auto load1 = [&](int j) {
                     const int s = j % kStages1;
@@ -718,14 +746,31 @@ Layout layout_of(const Plan& x, int total_q, int total_kv, int Hq, int Hkv, int 
     };
     l.stats = take(static_cast<size_t>(total_q) * Hq * sizeof(float2));
     l.counts = take(2 * sizeof(int));
-    l.kv_blocks = take(static_cast<size_t>(x.kv_blocks) * sizeof(int2));
-    l.q_blocks = take(static_cast<size_t>(x.q_blocks) * sizeof(int2));
+    l.kv_blocks = take(static_cast<size_t>(x.kv_blocks) * sizeof(Block));
+    l.q_blocks = take(static_cast<size_t>(x.q_blocks) * sizeof(Block));
     const size_t q_part = static_cast<size_t>(total_q) * Hq * D * sizeof(float), kv_part = static_cast<size_t>(total_kv) * Hkv * D * sizeof(float);
     l.dq = take(x.q_pieces > 1 ? q_part * x.q_pieces : 0);
     l.dk = take(x.kv_pieces > 1 ? kv_part * x.kv_pieces : 0);
     l.dv = take(x.kv_pieces > 1 ? kv_part * x.kv_pieces : 0);
     l.bytes = at;
     return l;
+}
+
+// A launch whose CTAs may come in before the kernel before it has ended.
+template <typename... Args>
+cudaError_t launch_along(void (*kern)(Args...), unsigned grid, int threads, size_t smem, cudaStream_t stream,
+                         const typename std::common_type<Args>::type&... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <bool kD64>
@@ -745,14 +790,13 @@ cudaError_t launch(const VarlenBwdArgs& a, const Params& p, const Plan& x, const
     const long long per_cta = kPrepThreads / (kD / 8);
     varlen_bwd_prepare_kernel<kD><<<static_cast<unsigned>(1 + (rows + per_cta - 1) / per_cta), kPrepThreads, 0, stream>>>(p);
     e = cudaGetLastError();
-    if (e == cudaSuccess && a.total_kv > 0) {
+    if (e == cudaSuccess && a.total_kv > 0) {   // (not launched along: where its CTAs come in before the first kernel's end, causal batches take up to a quarter longer)
         varlen_bwd_kernel<false, kD64><<<static_cast<unsigned>(x.kv_blocks * a.Hkv * x.kv_pieces), kThreads, kSmemBytes, stream>>>(k, v, q, d_o, p);
         e = cudaGetLastError();
     }
-    if (e == cudaSuccess && a.total_q > 0) {
-        varlen_bwd_kernel<true, kD64><<<static_cast<unsigned>(x.q_blocks * a.Hkv * x.q_pieces), kThreads, kSmemBytes, stream>>>(q, d_o, k, v, p);
-        e = cudaGetLastError();
-    }
+    if (e == cudaSuccess && a.total_q > 0)
+        e = launch_along(varlen_bwd_kernel<true, kD64>, static_cast<unsigned>(x.q_blocks * a.Hkv * x.q_pieces), kThreads,
+                         kSmemBytes, stream, q, d_o, k, v, p);
     auto sum = [&](const float* part, int pieces, int n, int elems, const int32_t* indptr, __nv_bfloat16* out, long long stride) {
         const long long vecs = static_cast<long long>(n) * (elems / 4);
         varlen_bwd_sum_kernel<<<static_cast<unsigned>((vecs + 255) / 256), 256, 0, stream>>>(part, pieces, n, elems, indptr, a.B, out, stride);
@@ -807,8 +851,8 @@ cudaError_t launch_varlen_bwd(const VarlenBwdArgs& a, cudaStream_t stream) {
     p.scale_log2 = a.scale * kLog2e;
     p.stats = reinterpret_cast<float2*>(ws + l.stats);
     p.counts = reinterpret_cast<int*>(ws + l.counts);
-    p.kv_blocks = reinterpret_cast<int2*>(ws + l.kv_blocks);
-    p.q_blocks = reinterpret_cast<int2*>(ws + l.q_blocks);
+    p.kv_blocks = reinterpret_cast<Block*>(ws + l.kv_blocks);
+    p.q_blocks = reinterpret_cast<Block*>(ws + l.q_blocks);
     p.max_kv_blocks = static_cast<int>(x.kv_blocks);
     p.max_q_blocks = static_cast<int>(x.q_blocks);
     p.kv_pieces = x.kv_pieces;
