@@ -21,9 +21,9 @@
 // As in the forward kernel a tile of queries holds P = floor(128 / G) positions
 // of all G heads of a KV head, position-major.
 //
-// Warps 0-7 turn scores into P and dS (a thread has a row of the tile and half
-// of its columns), warp 8 loads by TMA, warp 9 issues the MMAs, warp 10 brings
-// the queries' LSE and delta to the dK/dV kernel.  The S and dP products of the
+// Warp 0 loads by TMA, warp 1 issues the MMAs, warp 2 brings the queries' LSE and
+// delta to the dK/dV kernel, warps 4-11 turn scores into P and dS (32 rows of the
+// tile and half of its columns each).  The S and dP products of the
 // next tile are issued while dS and P of this one are made: the tensor core
 // waits for neither in turn.  TMEM: S 128 columns, dP 128, dV 128, dK 128 (in
 // the dQ kernel a second S and dQ).
@@ -335,45 +335,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const float sl2 = p.scale_log2;
         const float2 scl2 = make_float2(sl2, sl2);
-        // dQ: this row's position, limit and statistics
-        const int pos = p0_own + r / p.G;
-        const bool row_real = r < rows_used && pos < sq.q_len;
-        const size_t q_row = (static_cast<size_t>(sq.q_start) + pos) * p.Hq + kvh * p.G + r % p.G;
-        int lim = -1, lim_first = -1;
-        float2 stat = make_float2(-INFINITY, 0.f);
+        // Scores come in the layout of an MMA's accumulators: element 4 i + 2 k + e of half
+        // u is row 16 u + 8 k + lane / 4 of the warp's 32, column 8 i + 2 (lane mod 4) + e
+        // of its 64.  A thread meets 16 columns and 4 rows, so that a column's statistics
+        // (dK, dV) are read by 8 lanes at once and not by each of 32.
+        const int row0 = 32 * (warp & 3) + (lane >> 2), col0 = 64 * h + 2 * (lane & 3);
+        int lim_first = -1;
+        float2 stat[4];   // dQ: the rows' statistics
         if constexpr (kDq) {
-            lim = limit_of(p, sq, pos);
             lim_first = limit_of(p, sq, p0_own);
-            if (row_real) stat = __ldcg(p.stats + q_row);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int rr = row0 + 8 * k, at = rr / p.G, pp = p0_own + at;
+                stat[k] = make_float2(-INFINITY, 0.f);
+                if (rr < rows_used && pp < sq.q_len)
+                    stat[k] = __ldcg(p.stats + (static_cast<size_t>(sq.q_start) + pp) * p.Hq + kvh * p.G + (rr - at * p.G));
+            }
         }
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             const int y = j0 + j, st = j % kStages1, slot = j % kStatSlots;
-            const float* nlse = reinterpret_cast<const float*>(smem + kOffStat) + slot * 2 * kBM + 64 * h;
-            const float* dlt = nlse + kBM;
-            // columns [c_lo, c_hi) of this row's half count
-            int c_lo = 0, c_hi = 64;
+            const float2* nlse = reinterpret_cast<const float2*>(smem + kOffStat + slot * 2 * kBM * 4) + (col0 >> 1);
+            const float2* dlt = nlse + kBM / 2;
             bool masked = false;
             const uint32_t s_addr = tmem + lane_addr + ((kDq && (j & 1)) ? kColAcc1 : kColS) + 64 * h;
             const uint32_t dp_addr = tmem + lane_addr + kColDP + 64 * h;
             // the statistics are there before the scores
-            float4 nl[kDq ? 1 : 16];
+            float2 nl[kDq ? 1 : 8];
             if constexpr (!kDq) {
                 if (!(ok = wait(&sh.stat_full[slot], (j / kStatSlots) & 1))) break;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) nl[e] = reinterpret_cast<const float4*>(nlse)[e];
-            } else {
-                nl[0] = make_float4(stat.x, stat.x, stat.x, stat.x);
+                for (int i = 0; i < 8; ++i) nl[i] = nlse[4 * i];
             }
             if (!(ok = wait(&sh.s_full[j & 1], (j >> 1) & 1))) break;
             tc_fence_after();
             uint32_t sr[2][32];
-            tmem_ld32(s_addr, sr[0]);
-            tmem_ld32(s_addr + 32, sr[1]);
+            tmem_ld_16x64(s_addr, sr[0]);
+            tmem_ld_16x64(s_addr + (16u << 16), sr[1]);
+            int there;   // rows (dQ: keys) of the streamed tile that are there
             if constexpr (kDq) {
                 masked = y * kBM + kBM - 1 > lim_first;
-                c_hi = lim - y * kBM + 1 - 64 * h;
-                const int there = sq.kv_len - y * kBM;   // keys of the tile
+                there = sq.kv_len - y * kBM;
                 if (there < kBM) {
                     // dS is 0 there, but 0 times whatever lies behind the keys is not
                     for (int i = there * 8 + i_score; i < kHalf / 16; i += kScoreThreads) {
@@ -384,14 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                 }
             } else {
-                const int there = min(p.P, sq.q_len - y * p.P) * p.G;   // rows of the tile of queries
-                c_hi = there - 64 * h;
-                masked = there < rows_used;
-                if (p.causal && y * p.P + delta < kv0_own + kBM - 1) {
-                    masked = true;
-                    const long long from = static_cast<long long>(kv0_own + r - delta - y * p.P) * p.G;
-                    c_lo = static_cast<int>(min(max(from, 0LL), 128LL)) - 64 * h;
-                }
+                there = min(p.P, sq.q_len - y * p.P) * p.G;
+                masked = there < rows_used || (p.causal && y * p.P + delta < kv0_own + kBM - 1);
                 if (there < rows_used) {
                     if (!(ok = wait(&sh.y2_full[j % kStages2], (j / kStages2) & 1))) break;
                     for (int i = there * 8 + i_score; i < kHalf / 16; i += kScoreThreads) {
@@ -403,59 +399,91 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                 }
             }
-            float2 pr[32];
+            // columns [lo, hi) of the tile count in row k of the thread
+            auto range = [&](int k, int& lo, int& hi) {
+                lo = 0;
+                if constexpr (kDq) {
+                    hi = limit_of(p, sq, p0_own + (row0 + 8 * k) / p.G) - y * kBM + 1;
+                } else {
+                    hi = there;
+                    if (p.causal) {
+                        const long long from = static_cast<long long>(kv0_own + row0 + 8 * k - delta - y * p.P) * p.G;
+                        lo = static_cast<int>(min(max(from, 0LL), 128LL));
+                    }
+                }
+            };
+            float2 pr[2][16];
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float4 l = nl[kDq ? 0 : e];
-                const uint32_t* x = &sr[e >> 3][4 * (e & 7)];
-                const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), scl2, make_float2(l.x, l.y));
-                const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), scl2, make_float2(l.z, l.w));
-                pr[2 * e] = make_float2(ex2(y0.x), ex2(y0.y));
-                pr[2 * e + 1] = make_float2(ex2(y1.x), ex2(y1.y));
-            }
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {   // e = 2 i + k
+                    const float2 l = kDq ? make_float2(stat[2 * u + (e & 1)].x, stat[2 * u + (e & 1)].x) : nl[kDq ? 0 : e >> 1];
+                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[u][2 * e]), __uint_as_float(sr[u][2 * e + 1])), scl2, l);
+                    pr[u][e] = make_float2(ex2(x.x), ex2(x.y));
+                }
             if (masked) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    if (2 * e < c_lo || 2 * e >= c_hi) pr[e].x = 0.f;
-                    if (2 * e + 1 < c_lo || 2 * e + 1 >= c_hi) pr[e].y = 0.f;
+                for (int k = 0; k < 4; ++k) {
+                    int lo, hi;
+                    range(k, lo, hi);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int c = col0 + 8 * i;
+                        float2& x = pr[k >> 1][2 * i + (k & 1)];
+                        if (c < lo || c >= hi) x.x = 0.f;
+                        if (c + 1 < lo || c + 1 >= hi) x.y = 0.f;
+                    }
                 }
             }
+            uint32_t pk[2][16];
             if constexpr (!kDq) {
-                uint32_t pk[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(pr[e].x, pr[e].y);
-                tmem_st32(s_addr, pk);
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) pk[u][e] = pack_bf16x2(pr[u][e].x, pr[u][e].y);
+                tmem_st_16x32(s_addr, pk[0]);
+                tmem_st_16x32(s_addr + (16u << 16), pk[1]);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.p_ready);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) nl[i] = dlt[4 * i];
             }
             if (!(ok = wait(&sh.dp_full[j & 1], (j >> 1) & 1))) break;
             tc_fence_after();
             uint32_t dr[2][32];
-            tmem_ld32(dp_addr, dr[0]);
-            tmem_ld32(dp_addr + 32, dr[1]);
+            tmem_ld_16x64(dp_addr, dr[0]);
+            tmem_ld_16x64(dp_addr + (16u << 16), dr[1]);
             tmem_ld_wait();
-            uint32_t pk[32];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                float4 dl = make_float4(stat.y, stat.y, stat.y, stat.y);
-                if constexpr (!kDq) dl = reinterpret_cast<const float4*>(dlt)[e];
-                const uint32_t* x = &dr[e >> 3][4 * (e & 7)];
-                float2 d0 = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(dl.x, dl.y)), pr[2 * e]);
-                float2 d1 = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), make_float2(dl.z, dl.w)), pr[2 * e + 1]);
-                if (masked) {   // (what is not there may have a dP that is not finite)
-                    const int k = 4 * e;
-                    if (k < c_lo || k >= c_hi) d0.x = 0.f;
-                    if (k + 1 < c_lo || k + 1 >= c_hi) d0.y = 0.f;
-                    if (k + 2 < c_lo || k + 2 >= c_hi) d1.x = 0.f;
-                    if (k + 3 < c_lo || k + 3 >= c_hi) d1.y = 0.f;
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float2 l = kDq ? make_float2(stat[2 * u + (e & 1)].y, stat[2 * u + (e & 1)].y) : nl[kDq ? 0 : e >> 1];
+                    pr[u][e] = __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(dr[u][2 * e]), __uint_as_float(dr[u][2 * e + 1])), l), pr[u][e]);
                 }
-                pk[2 * e] = pack_bf16x2(d0.x, d0.y);
-                pk[2 * e + 1] = pack_bf16x2(d1.x, d1.y);
+            if (masked) {   // again: what is not there may have a dP that is not finite
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    int lo, hi;
+                    range(k, lo, hi);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int c = col0 + 8 * i;
+                        float2& x = pr[k >> 1][2 * i + (k & 1)];
+                        if (c < lo || c >= hi) x.x = 0.f;
+                        if (c + 1 < lo || c + 1 >= hi) x.y = 0.f;
+                    }
+                }
             }
-            tmem_st32(dp_addr, pk);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) pk[u][e] = pack_bf16x2(pr[u][e].x, pr[u][e].y);
+            tmem_st_16x32(dp_addr, pk[0]);
+            tmem_st_16x32(dp_addr + (16u << 16), pk[1]);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -471,14 +499,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             // dQ: both halves of the threads share a row's columns; else the first four warps have dV, the others dK
             constexpr int kCols = kDq ? kD / 2 : kD;
             const uint32_t acc = tmem + lane_addr + (kDq ? kColAcc2 + kCols * h : (h == 0 ? kColAcc1 : kColAcc2));
-            const int key = kv0_own + r;
+            const int pos = p0_own + r / p.G, key = kv0_own + r;   // this thread's row now
+            const bool row_real = r < rows_used && pos < sq.q_len;
             const bool store = kDq ? row_real : key < sq.kv_room;
             const bool real = n > 0 && (kDq || key < sq.kv_len);
             const float f = (kDq || h == 1) ? p.scale : 1.f;
             const size_t row = kDq ? static_cast<size_t>(sq.q_start) + pos : static_cast<size_t>(sq.kv_start) + key;
             const int head = kDq ? kvh * p.G + r % p.G : kvh;
             const int heads = kDq ? p.Hq : p.Hkv, rows = kDq ? p.total_q : p.total_kv;
-            const int col0 = kDq ? kCols * h : 0;
+            const int out0 = kDq ? kCols * h : 0;   // its first column
             __nv_bfloat16* out = kDq ? p.dq : (h == 0 ? p.dv : p.dk);
             const long long stride = kDq ? p.dq_stride : (h == 0 ? p.dv_stride : p.dk_stride);
             float* part = kDq ? p.dq_part : (h == 0 ? p.dv_part : p.dk_part);
@@ -496,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (pieces > 1) {
                     if (!store) continue;
                     float4* dst = reinterpret_cast<float4*>(
-                        part + ((static_cast<size_t>(piece) * rows + row) * heads + head) * kD + col0 + 32 * c);
+                        part + ((static_cast<size_t>(piece) * rows + row) * heads + head) * kD + out0 + 32 * c);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         dst[e] = make_float4(__uint_as_float(ar[4 * e]), __uint_as_float(ar[4 * e + 1]),
@@ -515,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (pieces == 1) {
-                const long long at = store ? static_cast<long long>(row) * stride + head * kD + col0 : -1;
+                const long long at = store ? static_cast<long long>(row) * stride + head * kD + out0 : -1;
                 __syncwarp();
 #pragma unroll
                 for (int r0 = 0; r0 < 32; r0 += 32 / kLanes) {
