@@ -241,7 +241,7 @@ struct QkNormArgs {
     void* workspace;        // backward with a d_weight
     int32_t* dev_status;
 };
-constexpr int kQkNormCtas = 4;   // CTAs per SM of the backward pass
+constexpr int kQkNormCtas = 3, kQkNormBwdCtas = 2;   // CTAs per SM of the passes
 size_t qk_norm_bwd_workspace(int D, int sms);
 cudaError_t launch_qk_norm(const QkNormArgs& a, cudaStream_t stream);
 cudaError_t launch_qk_norm_bwd(const QkNormArgs& a, cudaStream_t stream);

@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "paged.cuh"
 #include "ptx.cuh"
 
 namespace gb300 {
@@ -42,14 +43,15 @@ struct Params {
     long long x_stride[2], dy_stride[2], out_stride[2];
     const void* w[2];             // NULL: not normalised
     int heads[2];                 // 0: absent
-    int units[2];                 // units of kPer rows per token
+    int units[2];                 // chunks of kPer rows
+    Divisor chunks[2];            // chunks per token
+    int q_ctas;                   // CTAs of the queries, which come first
     bool w_bf16;
     float eps;
     const float* cos_sin;
     int max_pos, rot;
     const int32_t* positions;     // NULL: the token's index
-    int n_units;
-    float* dw_part;               // [grid][2][D]
+    float* dw_part;               // [grid][D]
     int32_t* status;
 };
 
@@ -70,6 +72,17 @@ __device__ __forceinline__ Place place_of(int l, int rot) {
     Place a{8 * l, 8 * l + 4, 8 * l < rot};
     if (kHalves && a.turns) a.i0 = 4 * l, a.i1 = rot / 2 + 4 * l;
     return a;
+}
+
+// Loads that stay where they are written, ahead of the work that they overlap (of
+// plain ones the compiler moves those of read-only data down to their use).
+__device__ __forceinline__ int load_ahead(const int32_t* p) {
+    int v;
+    asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ void load_ahead(const float* p, float (&v)[4]) {
+    asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "l"(p));
 }
 
 // What a lane reads of a row: one 16-byte load where its elements are neighbours.
@@ -132,200 +145,215 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-// The rows of unit `u`: up to kPer heads of one token's queries or keys.
-struct Unit {
-    int token, which, head, n;
-};
+// Rows [head, head + n) of a token, one chunk of a group of lanes; n = 0: nothing
+// (a warp's groups go through their chunks together, their shuffles are by whole warps).
 template <int kPer>
-__device__ __forceinline__ Unit unit_of(const Params& p, int u) {
-    const int per_token = p.units[0] + p.units[1];
-    Unit x;
-    x.token = u / per_token;
-    const int i = u - x.token * per_token;
-    x.which = i >= p.units[0];
-    x.head = (x.which ? i - p.units[0] : i) * kPer;
-    x.n = min(kPer, (x.which ? p.heads[1] : p.heads[0]) - x.head);
-    return x;
-}
-__device__ __forceinline__ const __nv_bfloat16* row_of(const __nv_bfloat16* const (&base)[2], const long long (&stride)[2],
-                                                       const Unit& x, int d) {
-    return (x.which ? base[1] : base[0]) + x.token * (x.which ? stride[1] : stride[0]) + x.head * d;
-}
+struct Chunk {
+    int token, head, n;
+    uint2 x[kPer][2], dy[kPer][2];
+};
 
-// Cosines and sines of the lane; false: the token's position is not in the table.
-__device__ __forceinline__ bool angles(const Params& p, int token, int l, const Place& a, bool first, float (&c)[4],
-                                       float (&s)[4]) {
-    if (p.rot == 0) return true;
-    const int pos = p.positions != nullptr ? p.positions[token] : token;
-    const bool good = pos >= 0 && pos < p.max_pos;
-    if (!good && first) flag_status(p.status, ATTN_DEV_POSITION_OUT_OF_RANGE);
-    if (good && a.turns) {
-        const float* row = p.cos_sin + static_cast<size_t>(pos) * p.rot + 4 * l;
-        const float4 vc = *reinterpret_cast<const float4*>(row), vs = *reinterpret_cast<const float4*>(row + p.rot / 2);
-        c[0] = vc.x, c[1] = vc.y, c[2] = vc.z, c[3] = vc.w;
-        s[0] = vs.x, s[1] = vs.y, s[2] = vs.z, s[3] = vs.w;
-    }
-    return good;
-}
+// One side (queries or keys) of the call, as a CTA sees it.
+struct Side {
+    const __nv_bfloat16 *x, *dy;
+    __nv_bfloat16* out;
+    long long x_stride, dy_stride, out_stride;
+    int heads;
+};
 
-template <int kD, bool kHalves, int kPer>
-__global__ void __launch_bounds__(kThreads) qk_norm_kernel(const __grid_constant__ Params p) {
-    constexpr int kLanes = kD / 8;
-    const int l = threadIdx.x % kLanes;
-    const int u = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
-    const bool live = u < p.n_units;
-    const Place a = place_of<kHalves>(l, p.rot);
-    const Unit x = unit_of<kPer>(p, live ? u : 0);
-    const int n = live ? x.n : 0;
-    const __nv_bfloat16* src = row_of(p.x, p.x_stride, x, kD);
-    uint2 raw[kPer][2];
+// kBwd: the gradient.  The grid's first p.q_ctas CTAs take the queries, the others
+// the keys.  A group of D / 8 lanes takes chunks of kPer rows of one token, the next
+// one's rows (and its angles, whose position came one chunk before) on their way
+// while this one is worked on.  Neighbouring groups take neighbouring chunks: runs
+// of several chunks of a token, which would read its angles once, were slower by
+// half (a gradient of 16384 tokens of 40 heads 153 us against 94).
+template <int kD, bool kHalves, int kPer, bool kBwd>
+__global__ void __launch_bounds__(kThreads, (kBwd ? kQkNormBwdCtas : kQkNormCtas) + (kPer == 1)) qk_norm_kernel(const __grid_constant__ Params p) {
+    constexpr int kLanes = kD / 8, kGroups = kThreads / kLanes, kInWarp = 32 / kLanes;
+    if constexpr (kBwd) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int side = static_cast<int>(blockIdx.x) >= p.q_ctas;
+    const int cta = blockIdx.x - (side ? p.q_ctas : 0), ctas = side ? gridDim.x - p.q_ctas : p.q_ctas;
+    Side a;
+    a.x = side ? p.x[1] : p.x[0];
+    a.dy = side ? p.dy[1] : p.dy[0];
+    a.out = side ? p.out[1] : p.out[0];
+    a.x_stride = side ? p.x_stride[1] : p.x_stride[0];
+    a.dy_stride = side ? p.dy_stride[1] : p.dy_stride[0];
+    a.out_stride = side ? p.out_stride[1] : p.out_stride[0];
+    a.heads = side ? p.heads[1] : p.heads[0];
+    const Divisor chunks = side ? p.chunks[1] : p.chunks[0];
+    const int n_units = side ? p.units[1] : p.units[0];
+    const bool normed = (side ? p.w[1] : p.w[0]) != nullptr;
+    const int l = threadIdx.x % kLanes, grp = threadIdx.x / kLanes, in_warp = grp % kInWarp;
+    const Place at = place_of<kHalves>(l, p.rot);
+    float w[8];
+    load_weight(p, side, at, w);
+    float dw[8];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
-        if (i < n) load8<kHalves>(src + i * kD, a, raw[i]);
-    }
-    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f}, w[8];
-    const bool good = angles(p, x.token, l, a, live && x.head == 0 && l == 0, c, s);
-    load_weight(p, x.which, a, w);
-    const bool normed = (x.which ? p.w[1] : p.w[0]) != nullptr;
-    __nv_bfloat16* dst = (x.which ? p.out[1] : p.out[0]) + x.token * (x.which ? p.out_stride[1] : p.out_stride[0]) + x.head * kD;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        float y[8];
-        unpack4(raw[i][0], y);
-        unpack4(raw[i][1], y + 4);
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-        ss = group_sum<kLanes>(ss);
-        const float r = rsqrtf(ss * (1.f / kD) + p.eps);
-        if (normed) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] *= r * w[e];
-        }
-        if (a.turns) turn<kHalves>(y, c, s, 1.f);
-        if (i < n && good) store8<kHalves>(dst + i * kD, a, y);
-    }
-}
+    for (int e = 0; e < 8; ++e) dw[e] = 0.f;
 
-template <int kD, bool kHalves, int kPer>
-__global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(const __grid_constant__ Params p) {
-    constexpr int kLanes = kD / 8, kGroups = kThreads / kLanes;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int l = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
-    const Place a = place_of<kHalves>(l, p.rot);
-    float dw[2][8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.f;
-    // (a warp's groups leave the loop together: its shuffles are by whole warps)
-    const int warp_group = blockIdx.x * kGroups + (threadIdx.x & ~31) / kLanes, in_warp = grp - (threadIdx.x & ~31) / kLanes;
-    for (long long u0 = warp_group; u0 < p.n_units; u0 += gridDim.x * kGroups) {
-        const bool live = u0 + in_warp < p.n_units;
-        const Unit x = unit_of<kPer>(p, live ? static_cast<int>(u0) + in_warp : 0);
-        const int n = live ? x.n : 0;
-        const __nv_bfloat16* xs = row_of(p.x, p.x_stride, x, kD);
-        const __nv_bfloat16* ds = row_of(p.dy, p.dy_stride, x, kD);
-        uint2 xr[kPer][2], dr[kPer][2];
+    const int step = ctas * kGroups;
+    int base = cta * kGroups + grp - in_warp;   // the chunk of the warp's first group
+    auto position_of = [&](int u) -> int {
+        if (p.rot == 0 || u >= n_units) return 0;
+        return p.positions != nullptr ? load_ahead(p.positions + chunks.div(u)) : chunks.div(u);
+    };
+    auto fetch = [&](int u, Chunk<kPer>& c) {
+        c.n = 0;
+        if (u >= n_units) return;
+        c.token = chunks.div(u);
+        c.head = (u - c.token * static_cast<int>(chunks.d)) * kPer;
+        c.n = min(kPer, a.heads - c.head);
+        const __nv_bfloat16* xs = a.x + c.token * a.x_stride + c.head * kD;
+        const __nv_bfloat16* ds = kBwd ? a.dy + c.token * a.dy_stride + c.head * kD : nullptr;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            xr[i][0] = xr[i][1] = dr[i][0] = dr[i][1] = make_uint2(0u, 0u);
-            if (i < n) {
-                load8<kHalves>(xs + i * kD, a, xr[i]);
-                load8<kHalves>(ds + i * kD, a, dr[i]);
-            }
+            if (i >= c.n) continue;
+            load8<kHalves>(xs + i * kD, at, c.x[i]);
+            if constexpr (kBwd) load8<kHalves>(ds + i * kD, at, c.dy[i]);
         }
-        float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f}, w[8];
-        const bool good = angles(p, x.token, l, a, live && x.head == 0 && l == 0, c, s);
-        load_weight(p, x.which, a, w);
-        const bool normed = (x.which ? p.w[1] : p.w[0]) != nullptr;
-        __nv_bfloat16* dst = (x.which ? p.out[1] : p.out[0]) + x.token * (x.which ? p.out_stride[1] : p.out_stride[0]) + x.head * kD;
+    };
+    float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+    bool good = true;
+    // the angles of position pos; false: it is not in the table
+    auto angles = [&](int pos, bool flag, float (&c)[4], float (&s)[4]) -> bool {
+        if (p.rot == 0) return true;
+        if (pos < 0 || pos >= p.max_pos) {
+            if (flag) flag_status(p.status, ATTN_DEV_POSITION_OUT_OF_RANGE);
+            return false;
+        }
+        if (at.turns) {
+            const float* row = p.cos_sin + static_cast<size_t>(pos) * p.rot + 4 * l;
+            load_ahead(row, c);
+            load_ahead(row + p.rot / 2, s);
+        }
+        return true;
+    };
+    Chunk<kPer> now, next;
+    int pos_next = 0;
+    if (base < n_units) {
+        const int u = base + in_warp, pos = position_of(u);
+        pos_next = position_of(u + step);
+        fetch(u, now);
+        good = angles(pos, l == 0 && u < n_units && now.head == 0, cs, sn);
+    }
+    while (base < n_units) {
+        const int u_next = base + in_warp + step;
+        const bool more = base + step < n_units;
+        float cs_next[4] = {1.f, 1.f, 1.f, 1.f}, sn_next[4] = {0.f, 0.f, 0.f, 0.f};
+        bool good_next = true;
+        if (more) {
+            fetch(u_next, next);
+            good_next = angles(pos_next, l == 0 && u_next < n_units && next.head == 0, cs_next, sn_next);
+            pos_next = position_of(u_next + step);
+        }
+        __nv_bfloat16* dst = a.out + now.token * a.out_stride + now.head * kD;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
+            const bool live = i < now.n;
             float v[8], g[8];
-            unpack4(xr[i][0], v);
-            unpack4(xr[i][1], v + 4);
-            unpack4(dr[i][0], g);
-            unpack4(dr[i][1], g + 4);
-            if (a.turns) turn<kHalves>(g, c, s, -1.f);
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-            ss = group_sum<kLanes>(ss);
-            const float r = rsqrtf(ss * (1.f / kD) + p.eps);
-            const bool counts = i < n && good;
-            float along = 0.f, back[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[e] *= r;   // n
-                const float t = counts ? g[e] * v[e] : 0.f;
-                dw[0][e] += x.which ? 0.f : t;
-                dw[1][e] += x.which ? t : 0.f;
-                back[e] = g[e] * w[e];
-                along = fmaf(back[e], v[e], along);
+            unpack4(now.x[i][0], v);
+            unpack4(now.x[i][1], v + 4);
+            if constexpr (kBwd) {
+                unpack4(now.dy[i][0], g);
+                unpack4(now.dy[i][1], g + 4);
+                if (at.turns) turn<kHalves>(g, cs, sn, -1.f);
             }
-            along = group_sum<kLanes>(along) * (1.f / kD);
             if (normed) {
+                float ss = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) g[e] = r * fmaf(-v[e], along, back[e]);
-            }
-            if (!good) {   // the forward pass left the token out
+                for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+                ss = group_sum<kLanes>(ss);
+                const float r = rsqrtf(ss * (1.f / kD) + p.eps);
+                if constexpr (kBwd) {
+                    const bool counts = live && good;
+                    float along = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) g[e] = 0.f;
+                    for (int e = 0; e < 8; ++e) {
+                        v[e] *= r;   // n
+                        dw[e] += counts ? g[e] * v[e] : 0.f;
+                        g[e] *= w[e];
+                        along = fmaf(g[e], v[e], along);
+                    }
+                    along = group_sum<kLanes>(along) * (1.f / kD);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[e] = r * fmaf(-v[e], along, g[e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= r * w[e];
+                }
             }
-            if (i < n) store8<kHalves>(dst + i * kD, a, g);
+            if constexpr (kBwd) {
+                if (!good) {   // the forward pass left the token out
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[e] = 0.f;
+                }
+                if (live) store8<kHalves>(dst + i * kD, at, g);
+            } else {
+                if (at.turns) turn<kHalves>(v, cs, sn, 1.f);
+                if (live && good) store8<kHalves>(dst + i * kD, at, v);
+            }
         }
-    }
-    if (p.dw_part == nullptr) return;
-    __shared__ float acc[kGroups][kD];
+        if (!more) break;
+        base += step;
+        now = next;
+        good = good_next;
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        __syncthreads();
+        for (int e = 0; e < 4; ++e) cs[e] = cs_next[e], sn[e] = sn_next[e];
+    }
+    if constexpr (kBwd) {
+        if (p.dw_part == nullptr) return;
+        __shared__ float acc[kGroups][kD];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            acc[grp][a.i0 + e] = dw[which][e];
-            acc[grp][a.i1 + e] = dw[which][4 + e];
+            acc[grp][at.i0 + e] = dw[e];
+            acc[grp][at.i1 + e] = dw[4 + e];
         }
         __syncthreads();
         if (threadIdx.x < kD) {
             float sum = 0.f;
 #pragma unroll 8
             for (int i = 0; i < kGroups; ++i) sum += acc[i][threadIdx.x];
-            p.dw_part[(static_cast<size_t>(blockIdx.x) * 2 + which) * kD + threadIdx.x] = sum;
+            p.dw_part[static_cast<size_t>(blockIdx.x) * kD + threadIdx.x] = sum;
         }
     }
 }
 
-// The CTAs' sums, [n][2 d], joined: 32 columns a CTA, 32 slices of the sum each.
-__global__ void __launch_bounds__(kReduceCols* kReduceSlices) qk_norm_reduce_kernel(const float* part, int n, int d,
-                                                                                    float* dwq, float* dwk) {
+// The CTAs' sums, [q_ctas + k_ctas][d], joined for each side: 32 columns a CTA, 32
+// slices of the sum each.
+__global__ void __launch_bounds__(kReduceCols* kReduceSlices) qk_norm_reduce_kernel(const float* part, int q_ctas, int k_ctas,
+                                                                                    int d, float* dwq, float* dwk) {
     __shared__ float acc[kReduceSlices][kReduceCols];
     const int lane = threadIdx.x % kReduceCols, slice = threadIdx.x / kReduceCols;
-    const int col = blockIdx.x * kReduceCols + lane;
+    const int per_side = d / kReduceCols, side = static_cast<int>(blockIdx.x) >= per_side;
+    const int col = (blockIdx.x - side * per_side) * kReduceCols + lane;
+    const int first = side ? q_ctas : 0, n = side ? k_ctas : q_ctas;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float sum = 0.f;
 #pragma unroll 8
-    for (int i = slice; i < n; i += kReduceSlices) sum += __ldcg(part + static_cast<size_t>(i) * 2 * d + col);
+    for (int i = slice; i < n; i += kReduceSlices) sum += __ldcg(part + static_cast<size_t>(first + i) * d + col);
     acc[slice][lane] = sum;
     __syncthreads();
     if (slice != 0) return;
     sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kReduceSlices; ++i) sum += acc[i][lane];
-    float* out = col < d ? dwq : dwk;   // (a CTA's columns belong to one of them)
-    if (out != nullptr) out[col < d ? col : col - d] = sum;
+    float* out = side ? dwk : dwq;
+    if (out != nullptr) out[col] = sum;
 }
 
-// Heads of one unit: four rows share a token's angles and have their loads in
-// flight together; one row where four would leave SMs without work.
+// Rows of one chunk: four have their loads in flight together; one where four
+// would leave SMs without work.
 constexpr int kMany = 4;
-int rows_per_unit(const QkNormArgs& a, int sms) {
+int rows_per_chunk(const QkNormArgs& a, int sms) {
     const long long lanes = static_cast<long long>(a.total) * (a.Hq + a.Hkv) * (a.D / 8);
     return lanes >= static_cast<long long>(kMany) * sms * kThreads ? kMany : 1;
 }
-
-Params params_of(const QkNormArgs& a, int per) {
+// The call's parameters for chunks of `per` rows and up to most_ctas CTAs; the grid.
+Params params_of(const QkNormArgs& a, int per, int most_ctas, int& grid) {
     Params p{};
-    const int heads[2] = {a.Hq, a.Hkv};
+    const int heads[2] = {a.Hq, a.Hkv}, groups = kThreads / (a.D / 8);
+    int ctas[2];
     for (int i = 0; i < 2; ++i) {
         p.x[i] = static_cast<const __nv_bfloat16*>(a.x[i]);
         p.dy[i] = static_cast<const __nv_bfloat16*>(a.dy[i]);
@@ -335,15 +363,22 @@ Params params_of(const QkNormArgs& a, int per) {
         p.out_stride[i] = a.out_stride[i];
         p.w[i] = a.weight[i];
         p.heads[i] = heads[i];
-        p.units[i] = (heads[i] + per - 1) / per;
+        const int chunks = (heads[i] + per - 1) / per;
+        p.units[i] = a.total * chunks;
+        p.chunks[i] = make_divisor(std::max(chunks, 1));
+        const long long need = (static_cast<long long>(p.units[i]) + groups - 1) / groups;
+        // a side's part of the CTAs goes by its rows
+        const long long part = std::max<long long>(1, static_cast<long long>(most_ctas) * heads[i] / (a.Hq + a.Hkv));
+        ctas[i] = heads[i] == 0 ? 0 : static_cast<int>(std::max<long long>(1, std::min(need, part)));
     }
+    p.q_ctas = ctas[0];
+    grid = ctas[0] + ctas[1];
     p.w_bf16 = a.weight_bf16;
     p.eps = a.eps;
     p.cos_sin = a.cos_sin;
     p.max_pos = a.max_pos;
     p.rot = a.rot_dim;
     p.positions = a.positions;
-    p.n_units = a.total * (p.units[0] + p.units[1]);
     p.status = a.dev_status;
     return p;
 }
@@ -359,25 +394,23 @@ cudaError_t by_shape(const QkNormArgs& a, Call call) {
 }
 
 template <int kPer>
-cudaError_t forward(const QkNormArgs& a, cudaStream_t stream) {
-    const Params p = params_of(a, kPer);
-    const int groups = kThreads / (a.D / 8);
-    const int grid = (p.n_units + groups - 1) / groups;
+cudaError_t forward(const QkNormArgs& a, int sms, cudaStream_t stream) {
+    int grid;
+    const Params p = params_of(a, kPer, sms * kQkNormCtas, grid);
     return by_shape(a, [&](auto d, auto halves) {
-        qk_norm_kernel<decltype(d)::value, decltype(halves)::value, kPer><<<grid, kThreads, 0, stream>>>(p);
+        qk_norm_kernel<decltype(d)::value, decltype(halves)::value, kPer, false><<<grid, kThreads, 0, stream>>>(p);
         return cudaGetLastError();
     });
 }
 
 template <int kPer>
 cudaError_t backward(const QkNormArgs& a, int sms, cudaStream_t stream) {
-    Params p = params_of(a, kPer);
-    const int groups = kThreads / (a.D / 8);
-    const int grid = std::max(1, std::min((p.n_units + groups - 1) / groups, sms * kQkNormCtas));
+    int grid;
+    Params p = params_of(a, kPer, sms * kQkNormBwdCtas, grid);
     const bool sums = a.d_weight[0] != nullptr || a.d_weight[1] != nullptr;
     if (sums) p.dw_part = static_cast<float*>(a.workspace);
     const cudaError_t e = by_shape(a, [&](auto d, auto halves) {
-        qk_norm_bwd_kernel<decltype(d)::value, decltype(halves)::value, kPer><<<grid, kThreads, 0, stream>>>(p);
+        qk_norm_kernel<decltype(d)::value, decltype(halves)::value, kPer, true><<<grid, kThreads, 0, stream>>>(p);
         return cudaGetLastError();
     });
     if (e != cudaSuccess || !sums) return e;
@@ -390,24 +423,24 @@ cudaError_t backward(const QkNormArgs& a, int sms, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, qk_norm_reduce_kernel, static_cast<const float*>(p.dw_part), grid, a.D, a.d_weight[0],
-                              a.d_weight[1]);
+    return cudaLaunchKernelEx(&cfg, qk_norm_reduce_kernel, static_cast<const float*>(p.dw_part), p.q_ctas, grid - p.q_ctas, a.D,
+                              a.d_weight[0], a.d_weight[1]);
 }
 
 }  // namespace
 
-size_t qk_norm_bwd_workspace(int D, int sms) { return static_cast<size_t>(sms) * kQkNormCtas * 2 * D * sizeof(float); }
+size_t qk_norm_bwd_workspace(int D, int sms) { return (static_cast<size_t>(sms) * kQkNormBwdCtas + 1) * D * sizeof(float); }
 
 cudaError_t launch_qk_norm(const QkNormArgs& a, cudaStream_t stream) {
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    return rows_per_unit(a, sms) == 1 ? forward<1>(a, stream) : forward<kMany>(a, stream);
+    return rows_per_chunk(a, sms) == 1 ? forward<1>(a, sms, stream) : forward<kMany>(a, sms, stream);
 }
 
 cudaError_t launch_qk_norm_bwd(const QkNormArgs& a, cudaStream_t stream) {
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    return rows_per_unit(a, sms) == 1 ? backward<1>(a, sms, stream) : backward<kMany>(a, sms, stream);
+    return rows_per_chunk(a, sms) == 1 ? backward<1>(a, sms, stream) : backward<kMany>(a, sms, stream);
 }
 
 }  // namespace gb300
