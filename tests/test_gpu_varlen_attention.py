@@ -27,6 +27,9 @@ CASES = {
     "group of 128": ([9], [150], 128, 1, 64, {}),
     "group of 100, causal": ([9], [150], 100, 1, 128, dict(causal=True)),
     "many short": ([i % 9 for i in range(70)], [(i * 7) % 40 for i in range(70)], 4, 1, 128, {}),
+    # several items a CTA, of one tile and of two
+    "many items": ([37 * i % 400 for i in range(48)], [91 * i % 700 for i in range(48)], 16, 8, 64, {}),
+    "many items, causal": ([37 * i % 400 for i in range(40)], [37 * i % 400 for i in range(40)], 12, 12, 128, dict(causal=True)),
     "long keys, few queries": ([3, 20], [4000, 2500], 8, 2, 128, dict(room=[4000, 4000])),
     "long keys, few queries, causal": ([64], [3000], 4, 2, 64, dict(causal=True)),
     "long queries, few keys": ([3000], [70], 4, 2, 128, {}),
