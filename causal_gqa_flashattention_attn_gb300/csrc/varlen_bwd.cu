@@ -712,23 +712,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// The parts of a gradient added up, in order: [pieces][rows][row_elems] fp32 to
-// bf16 rows `stride` apart, of the rows that belong to a sequence.
-__global__ void __launch_bounds__(256) varlen_bwd_sum_kernel(const float* part, int pieces, int rows, int row_elems,
-                                                             const int32_t* indptr, int B, __nv_bfloat16* out,
-                                                             long long stride) {
+// The parts of gradients added up, in order: [pieces][rows][row_elems] fp32 to bf16
+// rows `stride` apart, of the rows that belong to a sequence; blockIdx.y is the gradient.
+struct Sum {
+    const float* part[2];
+    __nv_bfloat16* out[2];
+    long long stride[2];
+    const int32_t* indptr;
+    int pieces, rows, row_elems, B;
+};
+__global__ void __launch_bounds__(256) varlen_bwd_sum_kernel(const __grid_constant__ Sum a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int vecs = row_elems / 4;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int vecs = a.row_elems / 4;
     const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
     const long long row = i / vecs;
-    if (row >= rows || row < indptr[0] || row >= indptr[B]) return;
-    const float4* src = reinterpret_cast<const float4*>(part) + i;
+    if (row >= a.rows || row < a.indptr[0] || row >= a.indptr[a.B]) return;
+    const float4* src = reinterpret_cast<const float4*>(blockIdx.y ? a.part[1] : a.part[0]) + i;
     float4 sum = __ldcg(src);
-    for (int s = 1; s < pieces; ++s) {
-        const float4 v = __ldcg(src + static_cast<long long>(s) * rows * vecs);
+    for (int s = 1; s < a.pieces; ++s) {
+        const float4 v = __ldcg(src + static_cast<long long>(s) * a.rows * vecs);
         sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
     }
-    *reinterpret_cast<uint2*>(out + row * stride + (i - row * vecs) * 4) =
+    *reinterpret_cast<uint2*>((blockIdx.y ? a.out[1] : a.out[0]) + row * (blockIdx.y ? a.stride[1] : a.stride[0]) + (i - row * vecs) * 4) =
         make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
 }
 
@@ -787,13 +793,13 @@ Layout layout_of(const Plan& x, int total_q, int total_kv, int Hq, int Hkv, int 
 
 // A launch whose CTAs may come in before the kernel before it has ended.
 template <typename... Args>
-cudaError_t launch_along(void (*kern)(Args...), unsigned grid, int threads, size_t smem, cudaStream_t stream,
+cudaError_t launch_along(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
                          const typename std::common_type<Args>::type&... args) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -803,7 +809,7 @@ cudaError_t launch_along(void (*kern)(Args...), unsigned grid, int threads, size
 }
 
 template <bool kD64>
-cudaError_t launch(const VarlenBwdArgs& a, const Params& p, const Plan& x, const CUtensorMap& q, const CUtensorMap& d_o,
+cudaError_t launch(const VarlenBwdArgs& a, const Params& p, const Plan& x, int sms, const CUtensorMap& q, const CUtensorMap& d_o,
                    const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
     constexpr int kD = kD64 ? 64 : 128;
     static std::atomic<uint64_t> done{0};
@@ -817,26 +823,32 @@ cudaError_t launch(const VarlenBwdArgs& a, const Params& p, const Plan& x, const
     if (e != cudaSuccess) return e;
     const long long rows = static_cast<long long>(a.total_q) * a.Hq;
     const long long per_cta = kPrepThreads / (kD / 8);
-    varlen_bwd_prepare_kernel<kD><<<static_cast<unsigned>(1 + (rows + per_cta - 1) / per_cta), kPrepThreads, 0, stream>>>(p);
+    const long long prepare_ctas = 1 + (rows + per_cta - 1) / per_cta;
+    varlen_bwd_prepare_kernel<kD><<<static_cast<unsigned>(prepare_ctas), kPrepThreads, 0, stream>>>(p);
     e = cudaGetLastError();
-    if (e == cudaSuccess && a.total_kv > 0) {   // (not launched along: where its CTAs come in before the first kernel's end, causal batches take up to a quarter longer)
-        varlen_bwd_kernel<false, kD64><<<static_cast<unsigned>(x.kv_blocks * a.Hkv * x.kv_pieces), kThreads, kSmemBytes, stream>>>(k, v, q, d_o, p);
-        e = cudaGetLastError();
+    if (e == cudaSuccess && a.total_kv > 0) {
+        // along only behind a first kernel of a CTA or two an SM: 5 sequences of up to 300
+        // queries 33 -> 26 us, but coming in among many CTAs of it, causal batches take up
+        // to a quarter longer (4 of 1000 tokens 130 -> 157)
+        const long long grid = x.kv_blocks * a.Hkv * x.kv_pieces;
+        if (grid <= sms && prepare_ctas <= 2LL * sms) {
+            e = launch_along(varlen_bwd_kernel<false, kD64>, dim3(static_cast<unsigned>(grid)), kThreads, kSmemBytes, stream, k, v, q, d_o, p);
+        } else {
+            varlen_bwd_kernel<false, kD64><<<static_cast<unsigned>(grid), kThreads, kSmemBytes, stream>>>(k, v, q, d_o, p);
+            e = cudaGetLastError();
+        }
     }
     if (e == cudaSuccess && a.total_q > 0)
-        e = launch_along(varlen_bwd_kernel<true, kD64>, static_cast<unsigned>(x.q_blocks * a.Hkv * x.q_pieces), kThreads,
+        e = launch_along(varlen_bwd_kernel<true, kD64>, dim3(static_cast<unsigned>(x.q_blocks * a.Hkv * x.q_pieces)), kThreads,
                          kSmemBytes, stream, q, d_o, k, v, p);
-    auto sum = [&](const float* part, int pieces, int n, int elems, const int32_t* indptr, __nv_bfloat16* out, long long stride) {
-        const long long vecs = static_cast<long long>(n) * (elems / 4);
-        varlen_bwd_sum_kernel<<<static_cast<unsigned>((vecs + 255) / 256), 256, 0, stream>>>(part, pieces, n, elems, indptr, a.B, out, stride);
-        return cudaGetLastError();
+    auto sum = [&](const Sum& t, int gradients) {
+        const long long vecs = static_cast<long long>(t.rows) * (t.row_elems / 4);
+        return launch_along(varlen_bwd_sum_kernel, dim3(static_cast<unsigned>((vecs + 255) / 256), gradients), 256, 0, stream, t);
     };
-    if (e == cudaSuccess && x.kv_pieces > 1 && a.total_kv > 0) {
-        e = sum(p.dk_part, x.kv_pieces, a.total_kv, a.Hkv * kD, a.kv_indptr, p.dk, p.dk_stride);
-        if (e == cudaSuccess) e = sum(p.dv_part, x.kv_pieces, a.total_kv, a.Hkv * kD, a.kv_indptr, p.dv, p.dv_stride);
-    }
+    if (e == cudaSuccess && x.kv_pieces > 1 && a.total_kv > 0)
+        e = sum(Sum{{p.dk_part, p.dv_part}, {p.dk, p.dv}, {p.dk_stride, p.dv_stride}, a.kv_indptr, x.kv_pieces, a.total_kv, a.Hkv * kD, a.B}, 2);
     if (e == cudaSuccess && x.q_pieces > 1 && a.total_q > 0)
-        e = sum(p.dq_part, x.q_pieces, a.total_q, a.Hq * kD, a.qo_indptr, p.dq, p.dq_stride);
+        e = sum(Sum{{p.dq_part, nullptr}, {p.dq, nullptr}, {p.dq_stride, 0}, a.qo_indptr, x.q_pieces, a.total_q, a.Hq * kD, a.B}, 1);
     return e;
 }
 
@@ -917,7 +929,7 @@ cudaError_t launch_varlen_bwd(const VarlenBwdArgs& a, cudaStream_t stream) {
     if (!good) return cudaErrorInvalidValue;
     if (a.total_q == 0) q = d_o = k;
     if (a.total_kv == 0) k = v = q;
-    return a.D == 64 ? launch<true>(a, p, x, q, d_o, k, v, stream) : launch<false>(a, p, x, q, d_o, k, v, stream);
+    return a.D == 64 ? launch<true>(a, p, x, sms, q, d_o, k, v, stream) : launch<false>(a, p, x, sms, q, d_o, k, v, stream);
 }
 
 }  // namespace gb300

@@ -728,9 +728,9 @@ attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, long 
  *   d_lse        float32 [total_q, Hq], the gradient of lse (read; NULL: zeros)
  *   d_q          [total_q, Hq, D] bfloat16, d_q_stride apart
  *   d_k, d_v     [total_kv, Hkv, D], d_k_stride and d_v_stride apart
- *                (written: rows of a sequence that no query sees, those behind
- *                kv_lens[b] among them, get zeros; rows of no sequence are left
- *                alone)
+ *                (written; none of the three overlaps an input.  Rows of a
+ *                sequence that no query sees, those behind kv_lens[b] among
+ *                them, get zeros; rows of no sequence are left alone)
  *   workspace    >= attn_varlen_bwd_workspace_bytes() bytes, 16-byte aligned:
  *                scratch (the size goes by the current device's SM count).
  *                Calls that may run at the same time need separate workspaces.
