@@ -281,49 +281,18 @@ __device__ __forceinline__ uint32_t sw128_desc_lo(uint32_t smem_addr, uint32_t l
     return ((smem_addr & 0x3FFFFu) >> 4) | (((lbo_bytes >> 4) & 0x3FFFu) << 16);
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, kind::f16 (bf16/fp16 in, fp32 accumulate);
-// kAcc = 0 overwrites D.
-template <int kAcc>
-__device__ __forceinline__ void umma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
-        "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kSw128DescHi), "n"(kAcc)
-        : "memory");
-}
-// D[tmem] (+)= A[tmem] * B[smem], kind::f16.
-__device__ __forceinline__ void umma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
-                                           uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
-        "mov.b64 db, {%2, %4};\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(kSw128DescHi), "r"(accumulate)
-        : "memory");
-}
-
-// Arrive on an mbarrier once every tcgen05 op issued so far by this thread
-// has completed.
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     smem_u32(bar))
-                 : "memory");
-}
-
-// The same three for a warp that runs its issue loop as a whole, `lead` not 0 in
-// the one lane that issues (elect_one): control flow stays uniform, so the
+// MMAs and commits are issued by one lane of a warp that runs its issue loop as a
+// whole (lead = elect_one() is 1 in that lane): control flow stays uniform, so the
 // operands live in uniform registers.  A loop that one lane runs inside a branch
-// moves each operand there by an instruction with a long latency: with constant
-// operands a step of the attention gradient takes 2930 cycles this way and 3520
-// that way.
+// moves each operand there by an instruction with a long latency: the Llama-style
+// prefill took 80.2 us that way and takes 74 this way.
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t e;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
     return e;
 }
+// D[tmem] (+)= A[smem] * B[smem]^T, kind::f16 (bf16/fp16 in, fp32 accumulate);
+// kAcc = 0 overwrites D.
 template <int kAcc>
 __device__ __forceinline__ void umma_ss_by(uint32_t lead, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
     asm volatile(
@@ -334,6 +303,7 @@ __device__ __forceinline__ void umma_ss_by(uint32_t lead, uint32_t d_tmem, uint3
         "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kSw128DescHi), "n"(kAcc), "r"(lead)
         : "memory");
 }
+// D[tmem] (+)= A[tmem] * B[smem], kind::f16.
 __device__ __forceinline__ void umma_ts_by(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
                                            uint32_t accumulate) {
     asm volatile(
@@ -344,6 +314,8 @@ __device__ __forceinline__ void umma_ts_by(uint32_t lead, uint32_t d_tmem, uint3
         "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(kSw128DescHi), "r"(accumulate), "r"(lead)
         : "memory");
 }
+// Arrive on an mbarrier once every tcgen05 op issued so far by the leading lane
+// has completed.
 __device__ __forceinline__ void umma_commit_by(uint32_t lead, uint64_t* bar) {
     asm volatile(
         "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"

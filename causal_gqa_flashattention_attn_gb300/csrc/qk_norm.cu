@@ -15,12 +15,15 @@
 // 4l .. 4l+3 either way, one 16-byte load each for cosines and sines, used for
 // all the rows of a token that the lane takes.
 //
-// The gradient of a weight is a sum over all rows of all tokens: each lane
-// keeps its eight columns of both weights in registers over the rows it takes,
-// a CTA joins its lanes in order, and a second kernel the CTAs, in order: the
-// result does not depend on timing.
+// The gradient of a weight is a sum over all rows of all tokens: a CTA takes rows
+// of one side, each lane keeps its eight columns in registers over the rows it
+// takes, the CTA joins its lanes in order, and a second kernel the CTAs, in order:
+// the result does not depend on timing.
 //
-// Bound: the bytes of x (and dy) in and y (or dx) out.
+// Bound: the bytes of x (and dy) in and y (or dx) out.  16384 tokens of 32 + 4
+// heads of 128 (303 MB) 53.6 us, 5.65 TB/s; the gradient of 32 + 8 heads (505 MB)
+// 92.2 us, 5.48 TB/s, 0.83 and 0.81 of a copy's rate; one token 4 us, host
+// included.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -343,7 +346,9 @@ __global__ void __launch_bounds__(kReduceCols* kReduceSlices) qk_norm_reduce_ker
 }
 
 // Rows of one chunk: four have their loads in flight together; one where four
-// would leave SMs without work.
+// would leave SMs without work.  16384 tokens of 32 + 8 heads, forward / gradient:
+// four 60.1 / 92.5 us, two 61.5 / 96.1, one 93 / 140; one token: four 4.2 / 6.3,
+// one 3.9 / 4.9.
 constexpr int kMany = 4;
 int rows_per_chunk(const QkNormArgs& a, int sms) {
     const long long lanes = static_cast<long long>(a.total) * (a.Hq + a.Hkv) * (a.D / 8);

@@ -31,6 +31,18 @@
 // A first kernel computes delta and lists the blocks of all sequences, those of
 // the longest first.  Few blocks are cut into parts along the streamed side,
 // whose fp32 sums a last kernel adds up in order.
+//
+// Bound: the tensor cores.  Seven products, two more than atomics would need: 4
+// sequences of 2048 queries of 32 heads to 4096 keys (1.37e12 FLOP of five, 1.92e12
+// of seven) take 1138 us, 1245 in a long run (power), 1.7 PFLOP/s of the seven.  A
+// step of dK/dV is about 2500 cycles, 78 an MMA, of dQ 2020, 84 an MMA; a CTA
+// costs 9 and 5 us beside its steps (first loads, filling and draining, the rows
+// out), more of the whole where blocks are short: 8 causal documents of 256 to
+// 4096 tokens (1.04e12) 1105 us; 8 sequences of 20 queries to 1500 keys of 12
+// heads, D = 64, 70 us, where the bytes need 11.
+// Tried and slower: sixteen score warps (1570 -> 1641 us with an earlier MMA loop),
+// all stages of a dQ step unrolled (9 %), first loads issued before the CTA has met
+// (no change), a sequence's CTAs head by head (causal 4 %).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -743,9 +755,11 @@ __global__ void __launch_bounds__(256) varlen_bwd_sum_kernel(const __grid_consta
 // Parts of each block's streamed tiles, for the keys' and the queries' blocks:
 // the host knows the totals, not the lengths.  With fewer blocks than half the
 // SMs, as many parts as fill them, each of at least kPartTiles tiles of the mean
-// sequence.
+// sequence.  2048 queries of 16 heads to 100 keys 35 us, whole 175; 77 to 8192 keys
+// 73 and 117.  Parts of two tiles in place of four: 5 sequences of up to 300
+// queries 26.2 us against 23.9, 77 queries to 1500 keys 32.4 against 33.9.
 constexpr int kMaxPieces = 16;
-constexpr int kPartTiles = 2;
+constexpr int kPartTiles = 4;
 struct Plan {
     int kv_pieces, q_pieces;
     long long kv_blocks, q_blocks;   // most that there can be
