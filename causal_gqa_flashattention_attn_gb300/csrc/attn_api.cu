@@ -278,6 +278,8 @@ attn_status_t qk_norm_check(const QkNormArgs& a, attn_dtype_t weight_dtype, bool
         if (a.x[i] != nullptr && a.out[i] == a.x[i] && a.out_stride[i] != a.x_stride[i]) return ATTN_ERR_INVALID_ARG;
         if (a.dy[i] != nullptr && a.out[i] == a.dy[i] && a.out_stride[i] != a.dy_stride[i]) return ATTN_ERR_INVALID_ARG;
     }
+    // each side's sums are written, not added up: one buffer cannot take both
+    if (a.d_weight[0] != nullptr && a.d_weight[0] == a.d_weight[1]) return ATTN_ERR_INVALID_ARG;
     if (weights && (!std::isfinite(a.eps) || a.eps <= 0.f)) return ATTN_ERR_INVALID_ARG;
     if (weights && weight_dtype != ATTN_F32 && weight_dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
     if (a.D != 64 && a.D != 128) return ATTN_ERR_UNSUPPORTED;
@@ -788,7 +790,7 @@ attn_status_t attn_qk_norm_rope_bwd(const void* d_q_out, const void* d_k_out, lo
 }
 
 size_t attn_varlen_fwd_workspace_bytes(int B, int total_q, int total_kv, int Hq, int Hkv, int D) {
-    if (B <= 0 || total_q <= 0 || total_kv < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128) return 0;
+    if (B <= 0 || total_q <= 0 || total_kv < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || D <= 0) return 0;
     const int sms = device_sm_count();
     return sms > 0 ? varlen_fwd_workspace(B, total_q, total_kv, Hq, Hkv, D, sms) : 0;
 }

@@ -653,8 +653,9 @@ attn_status_t attn_qk_norm_rope(const void* q, const void* k, long long q_stride
  *   d_q_out, d_k_out   gradients of the outputs, as those (read)
  *   d_q, d_k           gradients of q and k, bfloat16, strides of their own
  *                      (written; each may be its d_*_out or its input where the strides agree)
- *   d_q_weight, d_k_weight  float32 [D] (written; NULL where the weight is NULL
- *                      or the gradient is not wanted)
+ *   d_q_weight, d_k_weight  float32 [D], a buffer each also where both sides share
+ *                      a weight (written; NULL where the weight is NULL or the
+ *                      gradient is not wanted)
  *   workspace          >= attn_qk_norm_rope_bwd_workspace_bytes() bytes,
  *                      16-byte aligned: scratch (the size goes by the current
  *                      device's SM count); not used without a d_*_weight.
@@ -694,7 +695,7 @@ attn_status_t attn_qk_norm_rope_bwd(const void* d_q_out, const void* d_k_out, lo
  *                an infinity among the values shows in every query of its
  *                sequence whose last visible key is in the same 128-key tile.
  *   o            [total_q, Hq, D] dense; lse float32 [total_q, Hq] or NULL
- *                (written; rows of no sequence are left alone)
+ *                (written; rows of no sequence are left alone; no overlap with an input)
  *   scale        > 0
  *   workspace    >= attn_varlen_fwd_workspace_bytes() bytes, 16-byte aligned:
  *                scratch (NULL where that is 0).  Few and long sequences are cut
@@ -761,7 +762,7 @@ attn_status_t attn_varlen_bwd(const void* d_o, const void* q, const void* k, con
  *   workspace    >= attn_cross_decode_workspace_bytes() bytes, 16-byte aligned:
  *                scratch (the size goes by the current device's SM count).
  *                Calls that may run at the same time need separate workspaces.
- *   o            as q; lse float32 [B, q_len, Hq] or NULL              (written)
+ *   o            as q, not q itself; lse float32 [B, q_len, Hq] or NULL (written)
  *   D 64 or 128, q_len 1..16, any Hq % Hkv == 0, B <= 4096.
  */
 size_t attn_cross_decode_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D);

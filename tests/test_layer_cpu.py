@@ -71,6 +71,8 @@ def test_norm_backward_workspace(L):
     assert _norm_bwd(L, dqw=FAKE, qw=None) == -1
     assert _norm_bwd(L, dqw=FAKE, ws=FAKE) == (-4 if NO_DEVICE else -3)
     assert attn.attn_qk_norm_rope_bwd_workspace_bytes(5, 4, 2, 96) == 0
+    # both sides' sums into one buffer
+    assert _norm_bwd(L, dqw=FAKE, dkw=FAKE, ws=FAKE, bytes=1 << 30) == -1
 
 
 def _varlen(L, **kw):
