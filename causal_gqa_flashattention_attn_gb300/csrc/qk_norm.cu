@@ -22,8 +22,11 @@
 //
 // Bound: the bytes of x (and dy) in and y (or dx) out.  16384 tokens of 32 + 4
 // heads of 128 (303 MB) 53.6 us, 5.65 TB/s; the gradient of 32 + 8 heads (505 MB)
-// 92.2 us, 5.48 TB/s, 0.83 and 0.81 of a copy's rate; one token 4 us, host
-// included.
+// 90.9 us, 5.55 TB/s, 0.83 and 0.82 of a copy's rate; one token 4 us, host
+// included.  Two thirds of the issue slots are taken, and how well the compiler
+// interleaves four rows decides: two elements at a time throughout (72 / 137 us), two
+// chunks in turn without moves (72 / 118) and the rows' sums side by side (spills,
+// 73 / 131) were slower than this order, 60.5 / 90.9 for 16384 tokens of 32 + 8 heads.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -269,12 +272,15 @@ __global__ void __launch_bounds__(kThreads, (kBwd ? kQkNormBwdCtas : kQkNormCtas
                 ss = group_sum<kLanes>(ss);
                 const float r = rsqrtf(ss * (1.f / kD) + p.eps);
                 if constexpr (kBwd) {
-                    const bool counts = live && good;
                     float along = 0.f;
 #pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= r;   // n
+                    if (live && good) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) dw[e] = fmaf(g[e], v[e], dw[e]);
+                    }
+#pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        v[e] *= r;   // n
-                        dw[e] += counts ? g[e] * v[e] : 0.f;
                         g[e] *= w[e];
                         along = fmaf(g[e], v[e], along);
                     }
@@ -347,7 +353,7 @@ __global__ void __launch_bounds__(kReduceCols* kReduceSlices) qk_norm_reduce_ker
 
 // Rows of one chunk: four have their loads in flight together; one where four
 // would leave SMs without work.  16384 tokens of 32 + 8 heads, forward / gradient:
-// four 60.1 / 92.5 us, two 61.5 / 96.1, one 93 / 140; one token: four 4.2 / 6.3,
+// four 60.1 / 92.5 us (90.9 since), two 61.5 / 96.1, one 93 / 140; one token: four 4.2 / 6.3,
 // one 3.9 / 4.9.
 constexpr int kMany = 4;
 int rows_per_chunk(const QkNormArgs& a, int sms) {
