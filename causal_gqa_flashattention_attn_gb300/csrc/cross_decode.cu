@@ -18,7 +18,7 @@
 // first and waits for it on the device, joins them in order.
 //
 // Bound: one read of the keys and values.  64 sequences of 512 to 6400 keys, four
-// beams, 32 heads over 8 (819 MB): 141 us, 5.8 TB/s.  One sequence of 1500 keys: 8.8 us
+// beams, 32 heads over 8 (819 MB): 138 us, 5.9 TB/s.  One sequence of 1500 keys: 8.6 us
 // in a graph (launches, one tile, the join), 10.3 in a stream.  Tried: shares of at
 // least two to six tiles, more registers (no gain); the join's CTAs over several
 // rows each (64 x 4 beams 1 % faster, one sequence a launch interval slower).
@@ -376,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the pieces of the sequences that were cut: 1 << per_shift warps (up to 8)
 // per output row.  O = sum_s 2^(L_s - L) O_s / sum_s 2^(L_s - L); each warp takes
-// every per_row-th piece, kBatch at a time, and the warps are joined in order.
+// every per_row-th piece, kBatch at a time (of which only those that are there are
+// loaded: 64 x 4 beams 140 -> 138 us), and the warps are joined in order.
 template <int kD>
 __global__ void __launch_bounds__(32 * kMergeWarps, 4) cross_decode_merge_kernel(const __grid_constant__ Params p,
                                                                                  int rows_per_col, int per_shift) {
@@ -432,10 +433,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) cross_decode_merge_kernel
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int at = w + (k << per_shift);
-            const float* src = p.part_o + slot(min(at, w1)) * kD + lane * kEach;
+            const float* src = p.part_o + slot(at) * kD + lane * kEach;
 #pragma unroll
             for (int e = 0; e < kEach; e += 2) {
-                const float2 u = __ldcg(reinterpret_cast<const float2*>(src + e));
+                const float2 u = at <= w1 ? __ldcg(reinterpret_cast<const float2*>(src + e)) : make_float2(0.f, 0.f);
                 v[k][e] = u.x, v[k][e + 1] = u.y;
             }
         }
