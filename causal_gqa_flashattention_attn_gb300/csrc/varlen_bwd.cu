@@ -26,7 +26,7 @@
 // tile and half of its columns each).  The S and dP products of the
 // next tile are issued while dS and P of this one are made: the tensor core
 // waits for neither in turn.  TMEM: S 128 columns, dP 128, dV 128, dK 128 (in
-// the dQ kernel a second S and dQ).
+// the dQ kernel a second S, or with D = 64 a second dP, and dQ).
 //
 // A first kernel computes delta and lists the blocks of all sequences, those of
 // the longest first.  Few blocks are cut into parts along the streamed side,
@@ -67,7 +67,8 @@ constexpr int kStatSlots = 2;
 // (dO, or V).  A stage is free when a product issued after its last reader is
 // done (MMAs complete in order), which is announced anyway:
 //   dK, dV: Q after dK, by dP of the next tile; dO after dV, by S of the next tile;
-//   dQ:     K after dQ, by dP of the next tile; V after its dP.
+//   dQ:     K after dQ, by dP of the next tile (D = 64: by dQ's own end); V after
+//           its dP.
 // The first is wanted half a step later than it would be free with two stages,
 // less than a load takes: two stages of Q cost 550 to 1000 cycles a step of 3500.
 constexpr int kStages1 = 3, kStages2 = 2;
@@ -86,7 +87,8 @@ constexpr int kEnd = kOffStat + kStatSlots * 2 * kBM * 4;
 struct Control {
     uint64_t r_full, y1_full[kStages1], y2_full[kStages2];
     uint64_t s_full[2], dp_full[2];   // of even and odd tiles
-    uint64_t p_ready, ds_ready, acc_full;
+    uint64_t p_ready, ds_ready, acc_full;   // (dQ with D = 64: p_ready is that S is read)
+    uint64_t sum_done[2];                   // dQ with D = 64: of even and odd tiles
     uint64_t stat_full[kStatSlots], stat_empty[kStatSlots];
     uint32_t tmem_base;
     int abort;
@@ -95,7 +97,7 @@ constexpr int kSystem = 1024, kSmemBytes = kEnd - kSystem;
 static_assert(kSystem + sizeof(Control) <= kOffR1 && kSmemBytes <= 227 * 1024, "all of an SM's shared memory");
 // TMEM columns
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColDP = 128, kColAcc1 = 256, kColAcc2 = 384;   // dV, dK; or a second S, dQ
+constexpr uint32_t kColS = 0, kColDP = 128, kColAcc1 = 256, kColAcc2 = 384;   // dV, dK; or a second S or dP, dQ
 
 struct Seq {
     int q_start, q_len, kv_start, kv_len, kv_room;
@@ -254,6 +256,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap y1_map, const __grid_constant__ CUtensorMap y2_map,
                       const __grid_constant__ Params p) {
     constexpr int kD = kD64 ? 64 : 128, kHalves = kD / 64;
+    // dQ: two buffers of S, so that the next S goes ahead of this tile's sum; or (early) two of
+    // dP, so that both go ahead and the score warps have a step's time for dS.  With D = 64
+    // their work is what a step takes: 8 causal documents of 16 heads 533 to 560 us by device,
+    // otherwise 552 to 572; with D = 128 the MMAs': 4 x 2048 queries to 4096 keys 1147, 1140.
+    constexpr bool kEarly = kDq && kD64;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw - kSystem;   // shared address 0
     Control& sh = *reinterpret_cast<Control*>(smem_raw);
@@ -302,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sh.p_ready, 8);
         mbar_init(&sh.ds_ready, 8);
         mbar_init(&sh.acc_full, 1);
+        for (int s = 0; s < 2; ++s) mbar_init(&sh.sum_done[s], 1);
         for (int s = 0; s < kStatSlots; ++s) {
             mbar_init(&sh.stat_full[s], 1);
             mbar_init(&sh.stat_empty[s], 8);
@@ -370,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2* nlse = reinterpret_cast<const float2*>(smem + kOffStat + slot * 2 * kBM * 4) + (col0 >> 1);
             const float2* dlt = nlse + kBM / 2;
             bool masked = false;
-            const uint32_t s_addr = tmem + lane_addr + ((kDq && (j & 1)) ? kColAcc1 : kColS) + 64 * h;
-            const uint32_t dp_addr = tmem + lane_addr + kColDP + 64 * h;
+            const uint32_t s_addr = tmem + lane_addr + ((kDq && !kEarly && (j & 1)) ? kColAcc1 : kColS) + 64 * h;
+            const uint32_t dp_addr = tmem + lane_addr + ((kEarly && (j & 1)) ? kColAcc1 : kColDP) + 64 * h;
             // the statistics are there before the scores
             float2 nl[kDq ? 1 : 8];
             if constexpr (!kDq) {
@@ -426,6 +434,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             float2 pr[2][16];
             tmem_ld_wait();
+            if constexpr (kEarly) {   // the next tile's S may come
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_ready);
+            }
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -604,8 +617,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (a barrier waited for here cannot run a round ahead: its next
                 // phase is of a tile that is loaded only afterwards)
                 for (int j = 0; j < n; ++j) {
-                    if (j >= 2 && !wait(&sh.dp_full[j & 1], ((j - 2) >> 1) & 1)) break;   // dP of tile j - 2
+                    if (kEarly && j >= 3 && !wait(&sh.sum_done[(j - 3) & 1], ((j - 3) >> 1) & 1)) break;   // dQ of tile j - 3
+                    if (!kEarly && j >= 2 && !wait(&sh.dp_full[j & 1], ((j - 2) >> 1) & 1)) break;   // dP of tile j - 2
                     load1(j);
+                    if (kEarly && j >= 2 && !wait(&sh.dp_full[j & 1], ((j - 2) >> 1) & 1)) break;
                     if (!kDq && j >= 2 && !wait(&sh.s_full[(j - 1) & 1], ((j - 1) >> 1) & 1)) break;   // S of tile j - 1
                     load2(j);
                 }
@@ -671,6 +686,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool more = k < n;
                     auto next1 = [&] { return !more || wait(&sh.y1_full[n1], (k / kStages1) & 1); };
                     auto next2 = [&] { return !more || wait(&sh.y2_full[n2], (k / kStages2) & 1); };
+                    if constexpr (kEarly) {
+                        if (more) {
+                            if (!next1() || !wait(&sh.p_ready, j & 1)) return false;
+                            tc_fence_after();
+                            scores(tmem + kColS, kOffR1, kOffY1 + n1 * kTile);
+                            umma_commit_by(lead, &sh.s_full[!kOdd]);
+                            if (!next2()) return false;
+                            tc_fence_after();
+                            scores(tmem + (kOdd ? kColDP : kColAcc1), kOffR2, kOffY2 + n2 * kTile);
+                            umma_commit_by(lead, &sh.dp_full[!kOdd]);
+                        }
+                        if (!wait(&sh.ds_ready, j & 1)) return false;
+                        tc_fence_after();
+                        if (!gather(tmem + kColAcc2, tmem + (kOdd ? kColAcc1 : kColDP), kOffY1 + s1 * kTile, j > 0, [] { return true; }))
+                            return false;   // dQ += dS K
+                        if (more) umma_commit_by(lead, &sh.sum_done[kOdd]);
+                        s1 = n1;
+                        n1 = n1 + 1 == kStages1 ? 0 : n1 + 1;
+                        return true;
+                    }
                     if constexpr (!kDq) {
                         if (!wait(&sh.p_ready, j & 1)) return false;
                         tc_fence_after();
