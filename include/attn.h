@@ -735,7 +735,10 @@ attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, long 
  *   workspace    >= attn_varlen_bwd_workspace_bytes() bytes, 16-byte aligned:
  *                scratch (the size goes by the current device's SM count).
  *                Calls that may run at the same time need separate workspaces.
- * Other arguments, limits and errors as attn_varlen_fwd.
+ * Other arguments, limits and errors as attn_varlen_fwd.  (What lies in rows that
+ * do not count, or in other sequences, reaches no gradient.  With `causal` a NaN or
+ * an infinity in a row of q, k, v or d_o may, beside the rows that it concerns,
+ * show in those of its sequence that share a tile of 128 with it on the diagonal.)
  */
 size_t attn_varlen_bwd_workspace_bytes(int B, int total_q, int total_kv, int Hq, int Hkv, int D);
 attn_status_t attn_varlen_bwd(const void* d_o, const void* q, const void* k, const void* v, const void* o,

@@ -229,6 +229,44 @@ def test_rows_past_32_bits():
         ragged.check(label, got, w, t)
 
 
+@pytest.mark.parametrize("d, group, causal", [(128, 4, False), (64, 3, True), (128, 5, True)])
+def test_a_sequence_of_nan_stays_alone(d, group, causal):
+    """Tiles hold rows of the sequences beside their own: what lies there reaches no output and no gradient."""
+    dev = gpu_or_skip()
+    import causal_gqa_flashattention_attn_gb300 as attn
+    q, kv = [70, 45, 150, 3], [70, 130, 90, 33]
+    x, y = (ragged.Batch(dev, q, kv, 2 * group, 2, d, causal=causal, lead=4, tail=30, seed=21) for _ in range(2))
+    of_q, of_kv = x.sequence_rows()
+    of_q[x.q_at[1]:x.q_at[2]] = False
+    of_kv[x.kv_at[1]:x.kv_at[2]] = False
+    for t, rows in ((x.q, of_q), (x.do, of_q), (x.k, of_kv), (x.v, of_kv)):
+        t[~rows] = float("nan")
+    o, lse = _forward(attn, x)
+    want_o, want_l, tol_o, tol_l = ragged.forward(y)
+    ragged.check("o", o, want_o, tol_o, of_q)
+    ragged.check("lse", lse, want_l, tol_l, of_q)
+    out = attn.attn_varlen_bwd(x.do, x.q, x.k, x.v, o, lse, **x.args())
+    o = torch.where(of_q[:, None, None], o, want_o.to(o.dtype))
+    lse = torch.where(of_q[:, None], lse, want_l.to(lse.dtype))
+    want, tol = ragged.backward(y, o, lse)
+    for label, got, w, t, rows in zip(("dq", "dk", "dv"), out, want, tol, (of_q, of_kv, of_kv)):
+        ragged.check(label, got, w, t, rows)
+
+
+def test_the_most_sequences():
+    dev = gpu_or_skip()
+    import causal_gqa_flashattention_attn_gb300 as attn
+    q, kv = [i % 4 for i in range(2048)], [i * 5 % 7 for i in range(2048)]
+    x = ragged.Batch(dev, q, kv, 2, 1, 64, seed=22)
+    o, lse = _forward(attn, x)
+    want_o, want_l, tol_o, tol_l = ragged.forward(x)
+    ragged.check("o", o, want_o, tol_o)
+    ragged.check("lse", lse, want_l, tol_l)
+    want, tol = ragged.backward(x, o, lse)
+    for label, got, w, t in zip(("dq", "dk", "dv"), attn.attn_varlen_bwd(x.do, x.q, x.k, x.v, o, lse, **x.args()), want, tol):
+        ragged.check(label, got, w, t)
+
+
 def test_offsets_outside_the_tensors_are_cut():
     dev = gpu_or_skip()
     import causal_gqa_flashattention_attn_gb300 as attn
