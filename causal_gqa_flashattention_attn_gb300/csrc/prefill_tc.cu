@@ -824,7 +824,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&o_empty[t]);
                 ++item_iter;
                 if (np == 1) {
-                    const bool alive = l > 0.f;
+                    // (kDirect: a sum that is NaN, from a NaN or an infinite score, is not an
+                    // empty row's: it shows in O and LSE, and through LSE in the gradient)
+                    const bool alive = kDirect ? l != 0.f : l > 0.f;
                     const float inv_l = alive ? 1.f / l : 0.f;
                     auto pack8 = [&](int c, int e) {   // columns 32 c + e .. + 7 of this row, as bf16
                         uint4 v;
@@ -1677,16 +1679,16 @@ __global__ void __launch_bounds__(256) varlen_merge_kernel(const Params p, int r
     for (int e = 0; e < kEach; ++e) acc[e] = 0.f;
     for (int s = 0; s < p.pieces; ++s) {
         const float ws = __shfl_sync(0xffffffffu, w, s);
-        if (ws == 0.f) continue;   // an empty part's O is not written
+        if (ws == 0.f) continue;   // an empty part's O is not written (a part of NaN has a weight of NaN)
         const float* src = p.part_o + (at + s) * kDim + lane * kEach;
 #pragma unroll
         for (int e = 0; e < kEach; ++e) acc[e] = fmaf(ws, __ldcg(src + e), acc[e]);
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + static_cast<size_t>(row) * kDim) + lane * (kEach / 2);
 #pragma unroll
     for (int e = 0; e < kEach / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    if (p.lse != nullptr && lane == 0) p.lse[row] = sum > 0.f ? top + logf(sum) : -INFINITY;
+    if (p.lse != nullptr && lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
 }
 
 // Parts of each item's KV tiles.  The host knows the totals, not the lengths:

@@ -679,7 +679,8 @@ attn_status_t attn_qk_norm_rope_bwd(const void* d_q_out, const void* d_k_out, lo
  *
  * Per sequence O = softmax(scale * Q K^T + mask) V and the natural-log LSE; a
  * query sees all of its sequence's keys, or with `causal` the first i + 1 +
- * (keys - queries).  A row that sees nothing gets O = 0 and LSE = -inf.  The
+ * (keys - queries).  A row that sees nothing gets O = 0 and LSE = -inf; one whose
+ * query or visible keys give a score of NaN or +inf gets NaN in both.  The
  * softmax weights are rounded to bf16 for the product with V (2^-8 of each at
  * most); scores, maxima and sums are fp32.
  *
