@@ -828,6 +828,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // empty row's: it shows in O and LSE, and through LSE in the gradient)
                     const bool alive = kDirect ? l != 0.f : l > 0.f;
                     const float inv_l = alive ? 1.f / l : 0.f;
+                    if constexpr (kDirect) {
+                        // O_t may hold no product at all, or weights of 0 times anything
+                        if (!alive) {
+#pragma unroll
+                            for (int c = 0; c < (kD64 ? 2 : 4); ++c)
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) ov[c][e] = 0u;
+                        }
+                    }
                     auto pack8 = [&](int c, int e) {   // columns 32 c + e .. + 7 of this row, as bf16
                         uint4 v;
                         v.x = pack_bf16x2(__uint_as_float(ov[c][e]) * inv_l, __uint_as_float(ov[c][e + 1]) * inv_l);
@@ -1237,6 +1246,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     issue_s(0, kv_iter % kStages);
                     umma_commit_by(lead, &s_full[0]);
                     const int tiles = one_tile(it) ? 1 : 2;
+                    // The KV tiles behind this one's end are the second query tile's alone: the
+                    // first has weights of 0 there, and 0 times a NaN among the values is NaN.
+                    const int end0 = kDirect ? direct_tiles(p, it.q_len, it.kv_len, min(it.p0 + p.P, it.q_len) - 1) : it.n_kv;
                     if (!kShort || tiles == 2) {
                         issue_s(1, kv_iter % kStages);
                         umma_commit_by(lead, &s_full[1]);
@@ -1256,7 +1268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (!(ok = wait(&p_full[t], t_iter & 1))) break;
                             if (j == it.j0 && t_items > 0 && !(ok = wait(&o_empty[t], (t_items - 1) & 1))) break;
                             tc_fence_after();
-                            issue_pv(t, s, j > it.j0);                   // O_t (+)= P_t V_j
+                            if (!kDirect || t == 1 || j < end0) issue_pv(t, s, j > it.j0);   // O_t (+)= P_t V_j
                             if (t + 1 == (kShort ? tiles : 2)) umma_commit_by(lead, &v_empty[s]);     // V_j no longer read
                             if (!last) {
                                 if (t == 0) {

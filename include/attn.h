@@ -597,8 +597,9 @@ attn_status_t attn_decode_paged_fp8_block(const void* q, const void* k_cache, co
  *   scale        > 0
  * Cache and page-list arguments as attn_decode_paged_fp8_block; limits as
  * attn_prefill_paged_varlen.  A token on a bad page is read as zeros.  A NaN
- * among a sequence's values shows in every query of that sequence whose last
- * visible token is in the same 128-token tile or later.
+ * among a sequence's values shows in every query of that sequence whose block
+ * of 2 floor(128 / (Hq / Hkv)) queries holds one that sees a token of the same
+ * 128-token tile.
  */
 size_t attn_prefill_fp8_block_workspace_bytes(int B, int max_kv_rows, int Hkv, int D);
 attn_status_t attn_prefill_paged_fp8_block(const void* q, const void* k_cache, const void* v_cache,
@@ -691,10 +692,13 @@ attn_status_t attn_qk_norm_rope_bwd(const void* d_q_out, const void* d_k_out, lo
  *   qo_indptr    int32 [B + 1]: sequence b owns query rows [qo_indptr[b], qo_indptr[b+1])
  *   kv_indptr    int32 [B + 1]: and key rows [kv_indptr[b], kv_indptr[b+1])   (read)
  *   kv_lens      int32 [B]: of which the first kv_lens[b] count (NULL: all), as
- *                a padded batch has them.  Key rows that no query sees are not
- *                used, whatever they hold, but for the causal diagonal: a NaN or
- *                an infinity among the values shows in every query of its
- *                sequence whose last visible key is in the same 128-key tile.
+ *                a padded batch has them.  Rows that do not count are not used,
+ *                whatever they hold.  With `causal`, blocks of floor(128 / (Hq /
+ *                Hkv)) queries meet tiles of 128 keys, both counted from their
+ *                sequence's first: a block meets a tile where one of its queries
+ *                sees one of the tile's keys, and a NaN or an infinity among the
+ *                tile's values then shows in all of the block's queries that see
+ *                a key at all.  (A masked key row shows nowhere.)
  *   o            [total_q, Hq, D] dense; lse float32 [total_q, Hq] or NULL
  *                (written; rows of no sequence are left alone; no overlap with an input)
  *   scale        > 0
@@ -738,8 +742,9 @@ attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, long 
  *                Calls that may run at the same time need separate workspaces.
  * Other arguments, limits and errors as attn_varlen_fwd.  (What lies in rows that
  * do not count, or in other sequences, reaches no gradient.  With `causal` a NaN or
- * an infinity in a row of q, k, v or d_o may, beside the rows that it concerns,
- * show in those of its sequence that share a tile of 128 with it on the diagonal.)
+ * an infinity in a row of q or d_o shows at most in d_k and d_v of the tiles that
+ * its block meets, one in a row of k or v at most in d_q of the blocks that its
+ * tile meets, beside its own row's gradients.)
  */
 size_t attn_varlen_bwd_workspace_bytes(int B, int total_q, int total_kv, int Hq, int Hkv, int D);
 attn_status_t attn_varlen_bwd(const void* d_o, const void* q, const void* k, const void* v, const void* o,
