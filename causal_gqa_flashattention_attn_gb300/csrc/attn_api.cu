@@ -286,7 +286,8 @@ attn_status_t qk_norm_check(const QkNormArgs& a, attn_dtype_t weight_dtype, bool
     if (a.rot_dim < 0 || a.rot_dim > a.D || (a.interleaved != 0 && a.interleaved != 1)) return ATTN_ERR_INVALID_ARG;
     if (a.rot_dim > 0 && (a.cos_sin == nullptr || a.max_pos <= 0 || !aligned16(a.cos_sin))) return ATTN_ERR_INVALID_ARG;
     if (a.rot_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
-    if (static_cast<long long>(a.total) * (a.Hq + static_cast<long long>(a.Hkv)) >= (1LL << 31) - 64) return ATTN_ERR_UNSUPPORTED;
+    // rows are counted in int, up to three steps of the grid ahead (fewer than 2^15 rows each)
+    if (std::max(a.total, 1) * (a.Hq + static_cast<long long>(a.Hkv)) > (1LL << 31) - (1LL << 20)) return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }
 

@@ -210,8 +210,9 @@ __global__ void __launch_bounds__(kThreads, (kBwd ? kQkNormBwdCtas : kQkNormCtas
         c.token = chunks.div(u);
         c.head = (u - c.token * static_cast<int>(chunks.d)) * kPer;
         c.n = min(kPer, a.heads - c.head);
-        const __nv_bfloat16* xs = a.x + c.token * a.x_stride + c.head * kD;
-        const __nv_bfloat16* ds = kBwd ? a.dy + c.token * a.dy_stride + c.head * kD : nullptr;
+        const long long in_row = static_cast<long long>(c.head) * kD;   // (heads are not bounded: it passes 32 bits)
+        const __nv_bfloat16* xs = a.x + c.token * a.x_stride + in_row;
+        const __nv_bfloat16* ds = kBwd ? a.dy + c.token * a.dy_stride + in_row : nullptr;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             if (i >= c.n) continue;
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, (kBwd ? kQkNormBwdCtas : kQkNormCtas
             good_next = angles(pos_next, l == 0 && u_next < n_units && next.head == 0, cs_next, sn_next);
             pos_next = position_of(u_next + step);
         }
-        __nv_bfloat16* dst = a.out + now.token * a.out_stride + now.head * kD;
+        __nv_bfloat16* dst = a.out + now.token * a.out_stride + static_cast<long long>(now.head) * kD;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const bool live = i < now.n;

@@ -633,7 +633,7 @@ attn_status_t attn_prefill_paged_fp8_block(const void* q, const void* k_cache, c
  *                ATTN_DEV_POSITION_OUT_OF_RANGE and leaves its token unwritten.
  *   q_out, k_out as q and k (written).  An output may be its input where the
  *                strides agree; else they do not overlap.
- *   D            64 or 128;  total * (Hq + Hkv) < 2^31.
+ *   D            64 or 128;  total * (Hq + Hkv) <= 2^31 - 2^20.
  */
 attn_status_t attn_qk_norm_rope(const void* q, const void* k, long long q_stride, long long k_stride,
                                 const void* q_weight, const void* k_weight, attn_dtype_t weight_dtype, float eps,
