@@ -310,8 +310,11 @@ attn_status_t varlen_check(const void* q, const void* k, const void* v, long lon
     if (q_stride >= (1LL << 38) || k_stride >= (1LL << 38) || v_stride >= (1LL << 38)) return ATTN_ERR_UNSUPPORTED;
     // query blocks are counted in 21 bits, rows and work items in int
     if (total_q >= (1 << 22) || total_kv >= (1 << 30)) return ATTN_ERR_UNSUPPORTED;
-    if ((static_cast<long long>(total_q) + B) * Hq >= (1LL << 31) || static_cast<long long>(total_kv) * Hkv >= (1LL << 31))
+    // (work items a step of the grid ahead of the last one, too)
+    if ((static_cast<long long>(total_q) + B) * Hq > (1LL << 31) - (1LL << 20) || static_cast<long long>(total_kv) * Hkv >= (1LL << 31))
         return ATTN_ERR_UNSUPPORTED;
+    // an element's place in its token's row, a TMA coordinate among others, is an int
+    if (static_cast<long long>(Hq) * D >= (1LL << 31)) return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }
 

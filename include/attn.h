@@ -708,7 +708,8 @@ attn_status_t attn_qk_norm_rope_bwd(const void* d_q_out, const void* d_k_out, lo
  *                do not depend on timing.  (The size goes by the current
  *                device's SM count.)  Calls that may run at the same time need
  *                separate workspaces.
- *   D 64 or 128, Hq / Hkv <= 128, B <= 2048, total_q < 2^22.
+ *   D 64 or 128, Hq / Hkv <= 128, Hq * D < 2^31, B <= 2048, total_q < 2^22,
+ *   (total_q + B) * Hq <= 2^31 - 2^20.
  * Offsets outside the tensors are cut to them.
  */
 size_t attn_varlen_fwd_workspace_bytes(int B, int total_q, int total_kv, int Hq, int Hkv, int D);
