@@ -464,7 +464,10 @@ __device__ __forceinline__ int cta_item(int i) {
 // it is, which the tensor core's rate is sensitive to).
 // kDirect (ragged): K/V are the caller's own rows, by TMA from where they lie;
 // a sequence sees all of its keys or, causal, those up to its diagonal; an item
-// may be one of several parts of the KV tiles, which leaves fp32 partials.
+// may be one of several parts of the KV tiles, which leaves fp32 partials.  Both
+// query tiles walk the KV tiles of the second one.  (To leave the first one's P.V
+// out behind its own end, so that no NaN among the values there reaches it, costs
+// the MMA loop a test: 4 x 2048 queries of D = 64 284 -> 297 us, D = 128 360 -> 356.)
 // kShort (kDirect): items whose positions fit in the first tile leave the second
 // out.
 template <bool kVarlen, bool kSplit, bool kD64 = false, bool kDirect = false, bool kShort = false>
@@ -829,8 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool alive = kDirect ? l != 0.f : l > 0.f;
                     const float inv_l = alive ? 1.f / l : 0.f;
                     if constexpr (kDirect) {
-                        // O_t may hold no product at all, or weights of 0 times anything
-                        if (!alive) {
+                        if (!alive) {   // weights of 0 times anything
 #pragma unroll
                             for (int c = 0; c < (kD64 ? 2 : 4); ++c)
 #pragma unroll
@@ -1246,9 +1248,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     issue_s(0, kv_iter % kStages);
                     umma_commit_by(lead, &s_full[0]);
                     const int tiles = one_tile(it) ? 1 : 2;
-                    // The KV tiles behind this one's end are the second query tile's alone: the
-                    // first has weights of 0 there, and 0 times a NaN among the values is NaN.
-                    const int end0 = kDirect ? direct_tiles(p, it.q_len, it.kv_len, min(it.p0 + p.P, it.q_len) - 1) : it.n_kv;
                     if (!kShort || tiles == 2) {
                         issue_s(1, kv_iter % kStages);
                         umma_commit_by(lead, &s_full[1]);
@@ -1268,7 +1267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (!(ok = wait(&p_full[t], t_iter & 1))) break;
                             if (j == it.j0 && t_items > 0 && !(ok = wait(&o_empty[t], (t_items - 1) & 1))) break;
                             tc_fence_after();
-                            if (!kDirect || t == 1 || j < end0) issue_pv(t, s, j > it.j0);   // O_t (+)= P_t V_j
+                            issue_pv(t, s, j > it.j0);                   // O_t (+)= P_t V_j
                             if (t + 1 == (kShort ? tiles : 2)) umma_commit_by(lead, &v_empty[s]);     // V_j no longer read
                             if (!last) {
                                 if (t == 0) {

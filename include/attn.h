@@ -693,12 +693,12 @@ attn_status_t attn_qk_norm_rope_bwd(const void* d_q_out, const void* d_k_out, lo
  *   kv_indptr    int32 [B + 1]: and key rows [kv_indptr[b], kv_indptr[b+1])   (read)
  *   kv_lens      int32 [B]: of which the first kv_lens[b] count (NULL: all), as
  *                a padded batch has them.  Rows that do not count are not used,
- *                whatever they hold.  With `causal`, blocks of floor(128 / (Hq /
- *                Hkv)) queries meet tiles of 128 keys, both counted from their
- *                sequence's first: a block meets a tile where one of its queries
- *                sees one of the tile's keys, and a NaN or an infinity among the
- *                tile's values then shows in all of the block's queries that see
- *                a key at all.  (A masked key row shows nowhere.)
+ *                whatever they hold.  With `causal` a NaN or an infinity among a
+ *                sequence's values shows, beside in the queries that see it, at
+ *                most in those that share a block of 2 floor(128 / (Hq / Hkv))
+ *                positions (counted from the sequence's first query) with one
+ *                that sees a key of the same tile of 128 (counted from its first
+ *                key); never in one that sees no key.  A masked key row shows nowhere.
  *   o            [total_q, Hq, D] dense; lse float32 [total_q, Hq] or NULL
  *                (written; rows of no sequence are left alone; no overlap with an input)
  *   scale        > 0
@@ -742,10 +742,12 @@ attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, long 
  *                scratch (the size goes by the current device's SM count).
  *                Calls that may run at the same time need separate workspaces.
  * Other arguments, limits and errors as attn_varlen_fwd.  (What lies in rows that
- * do not count, or in other sequences, reaches no gradient.  With `causal` a NaN or
- * an infinity in a row of q or d_o shows at most in d_k and d_v of the tiles that
- * its block meets, one in a row of k or v at most in d_q of the blocks that its
- * tile meets, beside its own row's gradients.)
+ * do not count, or in other sequences, reaches no gradient.  With `causal`, call a
+ * block of floor(128 / (Hq / Hkv)) positions and a tile of 128 keys joined where
+ * one of the block's queries sees one of the tile's keys: a NaN or an infinity in
+ * a row of q or d_o shows, beside in that row's d_q, at most in d_k and d_v of the
+ * tiles joined to its block, one in a row of k or v, beside in that row's d_k and
+ * d_v, at most in d_q of the blocks joined to its tile.)
  */
 size_t attn_varlen_bwd_workspace_bytes(int B, int total_q, int total_kv, int Hq, int Hkv, int D);
 attn_status_t attn_varlen_bwd(const void* d_o, const void* q, const void* k, const void* v, const void* o,

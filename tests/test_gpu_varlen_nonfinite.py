@@ -115,10 +115,10 @@ CAUSAL = [([256], [256], 2, 2, 128), ([300, 70], [300, 200], 3, 3, 64), ([200], 
           ([400], [150], 4, 4, 128), ([40], [3000], 4, 2, 128), ([64], [1000], 2, 1, 64), ([500], [170], 8, 2, 64)]
 
 
-def _reach(x, b):
-    """For sequence b: whether a block of floor(128 / group) positions holds a query that sees a key of a tile of 128, as
-    [queries, keys]; and whether a query sees a key."""
-    n, m, per = x.q_len[b], x.kv_len[b], 128 // (x.hq // x.hkv)
+def _reach(x, b, tiles):
+    """For sequence b: whether a block of tiles * floor(128 / group) positions holds a query that sees a key of a tile of 128,
+    as [queries, keys]; and whether a query sees a key."""
+    n, m, per = x.q_len[b], x.kv_len[b], tiles * (128 // (x.hq // x.hkv))
     i, j = torch.arange(n, device=x.q.device)[:, None], torch.arange(m, device=x.q.device)
     last = torch.clamp(i // per * per + per, max=n) - 1
     return last + m - n >= j // 128 * 128, i + m - n >= j
@@ -131,7 +131,7 @@ def test_reach_of_a_nan_value_under_the_causal_mask(case):
     x, y = (ragged.Batch(dev, q, kv, hq, hkv, d, causal=True, seed=41) for _ in range(2))
     clean_o, clean_l = _forward(y)
     b, group, n, m = len(q) - 1, hq // hkv, q[-1], kv[-1]
-    meets, sees = _reach(x, b)
+    meets, sees = _reach(x, b, 2)
     for key in sorted({0, m // 3, m // 2, m * 3 // 4, m - 70, m - 1}):
         x.v.copy_(y.v)
         x.v[x.kv_at[b] + key, hkv - 1] = NAN
@@ -154,7 +154,7 @@ def test_reach_of_a_nan_in_the_gradient_under_the_causal_mask(case, what):
     o, lse = _forward(y)
     clean = _backward(y, o, lse)
     b, group, n, m = len(q) - 1, hq // hkv, q[-1], kv[-1]
-    meets, sees = _reach(x, b)
+    joined, sees = _reach(x, b, 1)
     of_q, of_k = slice(x.q_at[b], x.q_at[b] + n), slice(x.kv_at[b], x.kv_at[b] + m)
     size = n if what in ("q", "do") else m
     for at in sorted({0, size // 3, size // 2, size * 3 // 4, size - 1}):
@@ -164,13 +164,13 @@ def test_reach_of_a_nan_in_the_gradient_under_the_causal_mask(case, what):
             getattr(x, what).copy_(getattr(y, what))
             getattr(x, what)[x.q_at[b] + at, hq - 1] = NAN
             for which in (1, 2):
-                may[which][of_k, hkv - 1] = meets[at]
+                may[which][of_k, hkv - 1] = joined[at]
                 has[which][of_k, hkv - 1] = sees[at]
             may[0][x.q_at[b] + at, hq - 1] = has[0][x.q_at[b] + at, hq - 1] = bool(sees[at].any())
         else:
             getattr(x, what).copy_(getattr(y, what))
             getattr(x, what)[x.kv_at[b] + at, hkv - 1] = NAN
-            may[0][of_q, hq - group:] = meets[:, at, None]
+            may[0][of_q, hq - group:] = joined[:, at, None]
             has[0][of_q, hq - group:] = sees[:, at, None]
             seen = bool(sees[:, at].any())
             for which in (1, 2) if what == "k" else (1,):
