@@ -57,6 +57,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 #include <vector>
 
 #include "common.cuh"
@@ -485,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
-    __shared__ SplitWalk walk_sh[kThreads / 32];          // split schedule: each warp's position
+    __shared__ SplitWalk walk_sh[kThreads / 32][2];       // split schedule: each warp's position, this round's and the next
     __shared__ __align__(8) uint64_t sk_bar[2];           // split epilogue: a tile's 128 threads meet
     __shared__ __align__(8) uint64_t epi_bar[2];          // O staging: a tile's 128 threads meet
     __shared__ int sk_word[2];                            // split epilogue: arrival order / go flag
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 w.L = L0;
                 w.L1 = static_cast<long long>(blockIdx.x + 1) * p.sk_total / gridDim.x;
-                for (int k = 0; k < kThreads / 32; ++k) walk_sh[k] = w;
+                for (int k = 0; k < kThreads / 32; ++k) walk_sh[k][0] = w;
             }
         }
     }
@@ -585,22 +586,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             return item_of(p, idx);
         }
     };
-    // every role walks the same sequence of items (or, split, of item
-    // pieces); the split position lives in shared memory, one per warp, so
-    // that it holds no registers across the KV loops
+    // Every role walks the same sequence of items (or, split, of item pieces).  The
+    // threads of a warp come out of their waits each for itself, so none may move on
+    // a split position for the others.  The producer and the MMA warp keep theirs in
+    // each thread.  A softmax warp's lives in shared memory, where it holds no
+    // registers across the KV loops (in each thread a chunk of 512 queries to 65,536
+    // keys takes 346 us, so 329): every thread reads this round's and writes the next
+    // one beside it, all the same, and the rounds' tcgen05.ld, which take the whole
+    // warp, keep them less than a round apart.
     struct Walker {
         int i;
+        SplitWalk own;   // split schedule, producer and MMA warp
     };
-    auto walk_begin = [&]() -> Walker { return Walker{0}; };
-    auto walk_next = [&](Walker& k, Item& it) -> bool {
-        if constexpr (kSplit) {
-            const unsigned act = __activemask();
-            SplitWalk w = walk_sh[warp];
+    auto walk_begin = [&]() -> Walker {
+        Walker k;
+        k.i = 0;
+        if constexpr (kSplit) k.own = walk_sh[warp][0];
+        return k;
+    };
+    auto walk_next = [&](Walker& k, Item& it, auto in_shared) -> bool {
+        if constexpr (kSplit && decltype(in_shared)::value) {
+            SplitWalk w = walk_sh[warp][k.i & 1];
             const bool got = split_next(p, w, it);
-            __syncwarp(act);
-            if (lane == __ffs(act) - 1) walk_sh[warp] = w;
-            __syncwarp(act);
+            walk_sh[warp][++k.i & 1] = w;
             return got;
+        } else if constexpr (kSplit) {
+            return split_next(p, k.own, it);
         } else {
             const int idx = cta_item(k.i++);
             if (idx >= n_items) return false;
@@ -665,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         Walker wk = walk_begin();
-        for (Item it; ok && walk_next(wk, it);) {
+        for (Item it; ok && walk_next(wk, it, std::true_type{});) {
             const int delta = it.delta;
             int pos;
             size_t row_id;
@@ -797,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return wait(&sk_bar[t], phase);
             };
             if constexpr (kSplit) {
-                const SplitWalk w = walk_sh[warp];   // still the item of this piece
+                const SplitWalk w = walk_sh[warp][wk.i & 1];   // still the item of this piece
                 const long long item_end = w.start + dense_qb_tiles(p.q_len, p.kv_len, p.P, w.qb);
                 c0 = split_cta_of(p, w.start);
                 np = split_cta_of(p, item_end - 1) - c0 + 1;
@@ -1021,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t kv_iter = 0, item_iter = 0;
                 bool ok = true;
                 Walker wk = walk_begin();
-                for (Item it; ok && walk_next(wk, it);) {
+                for (Item it; ok && walk_next(wk, it, std::false_type{});) {
                     if (it.n_kv == 0) continue;
                     if (item_iter > 0 && !(ok = wait(&q_empty, (item_iter - 1) & 1))) break;
                     const int tiles = one_tile(it) ? 1 : 2;
@@ -1059,7 +1070,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t kv_iter = 0, item_iter = 0;
                 bool ok = true;
                 Walker wk = walk_begin();
-                for (Item it; ok && walk_next(wk, it);) {
+                for (Item it; ok && walk_next(wk, it, std::false_type{});) {
                     if (it.n_kv == 0) continue;
                     if (item_iter > 0 && !(ok = wait(&q_empty, (item_iter - 1) & 1))) break;
                     mbar_arrive_expect_tx(&q_full, 2 * p.P * p.G * 256);
@@ -1102,7 +1113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t kv_iter = 0, item_iter = 0;
             bool ok = true;
             Walker wk = walk_begin();
-            for (Item it; ok && walk_next(wk, it);) {
+            for (Item it; ok && walk_next(wk, it, std::false_type{});) {
                 if (it.n_kv == 0) continue;
                 if (lane == 0) {
                     if (item_iter > 0) ok = wait(&q_empty, (item_iter - 1) & 1);
@@ -1174,7 +1185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t kv_iter = 0, item_iter = 0;
                 bool ok = true;
                 Walker wk = walk_begin();
-                for (Item it; ok && walk_next(wk, it);) {
+                for (Item it; ok && walk_next(wk, it, std::false_type{});) {
                     if (it.n_kv == 0) continue;
                     if (item_iter > 0 && !(ok = wait(&q_empty, (item_iter - 1) & 1))) break;
                     mbar_arrive_expect_tx(&q_full, 2 * p.P * p.G * 128 * p.halves);
@@ -1239,7 +1250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t skipped = 0, skipped_items = 0;   // by the second tile
                 bool ok = true;
                 Walker wk = walk_begin();
-                for (Item it; ok && walk_next(wk, it);) {
+                for (Item it; ok && walk_next(wk, it, std::false_type{});) {
                     if (it.n_kv == 0) continue;
                     if (!(ok = wait(&q_full, item_iter & 1))) break;
                     if (!(ok = wait(&k_full[kv_iter % kStages], (kv_iter / kStages) & 1))) break;
