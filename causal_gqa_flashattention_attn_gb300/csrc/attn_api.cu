@@ -854,7 +854,8 @@ attn_status_t attn_varlen_bwd(const void* d_o, const void* q, const void* k, con
     const VarlenBwdArgs a{d_o, q, k, v, o, d_o_stride, q_stride, k_stride, v_stride, o_stride, lse, d_lse, qo_indptr,
                           kv_indptr, kv_lens, causal, B, total_q, total_kv, Hq, Hkv, D, scale, workspace, d_q, d_k, d_v,
                           d_q_stride, d_k_stride, d_v_stride, dev_status};
-    return from_cuda(launch_varlen_bwd(a, static_cast<cudaStream_t>(stream)));
+    const cudaError_t e = launch_varlen_bwd(a, static_cast<cudaStream_t>(stream));
+    return e == cudaErrorNotSupported ? ATTN_ERR_UNSUPPORTED : from_cuda(e);   // (its layout of shared memory)
 }
 
 size_t attn_cross_decode_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D) {

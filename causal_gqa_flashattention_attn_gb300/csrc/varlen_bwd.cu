@@ -337,7 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     constexpr uint32_t tmem = 0;
-    // both hold by construction; without them nothing is done
+    // both hold by construction (the host has asked how much the system keeps);
+    // without them nothing is done
     const bool placed = sh.tmem_base == tmem && smem_u32(smem_raw) == kSystem;
     if (!placed) flag_status(p.status, ATTN_DEV_WAIT_TIMEOUT);
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -863,8 +864,13 @@ cudaError_t launch(const VarlenBwdArgs& a, const Params& p, const Plan& x, int s
     constexpr int kD = kD64 ? 64 : 128;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = once_per_device(done, [] {
-        cudaError_t r = cudaFuncSetAttribute(varlen_bwd_kernel<false, kD64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kSmemBytes);
+        // the addresses of shared memory are constants behind what the system keeps of it
+        int dev = 0, kept = 0;
+        cudaError_t r = cudaGetDevice(&dev);
+        if (r == cudaSuccess) r = cudaDeviceGetAttribute(&kept, cudaDevAttrReservedSharedMemoryPerBlock, dev);
+        if (r != cudaSuccess) return r;
+        if (kept != kSystem) return cudaErrorNotSupported;
+        r = cudaFuncSetAttribute(varlen_bwd_kernel<false, kD64>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         return r != cudaSuccess ? r
                                 : cudaFuncSetAttribute(varlen_bwd_kernel<true, kD64>,
                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);

@@ -741,7 +741,9 @@ attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, long 
  *   workspace    >= attn_varlen_bwd_workspace_bytes() bytes, 16-byte aligned:
  *                scratch (the size goes by the current device's SM count).
  *                Calls that may run at the same time need separate workspaces.
- * Other arguments, limits and errors as attn_varlen_fwd.  (What lies in rows that
+ * Other arguments, limits and errors as attn_varlen_fwd; ATTN_ERR_UNSUPPORTED too
+ * on a device that keeps other than 1024 bytes of a block's shared memory for
+ * itself.  (What lies in rows that
  * do not count, or in other sequences, reaches no gradient.  With `causal`, call a
  * block of floor(128 / (Hq / Hkv)) positions and a tile of 128 keys joined where
  * one of the block's queries sees one of the tile's keys: a NaN or an infinity in
