@@ -690,7 +690,9 @@ def attn_qk_norm_rope(q, k, q_weight=None, k_weight=None, eps=1e-6, cos_sin=None
     alike; None: that side is not normalised), then the rotation of
     :func:`attn_kv_append` by ``cos_sin [max_pos, R]`` at ``positions [T]``
     (None: the token's index).  Returns ``(q_out, k_out)``, None where absent;
-    an output given may be the input itself.
+    an output given may be the input itself.  It is not recorded for torch's
+    differentiation: inputs that require a gradient are refused while gradients
+    are on.
     """
     return _run(stream, _native().qk_norm_rope, q, k, q_weight, k_weight, eps, cos_sin, positions, interleaved, q_out, k_out,
                 dev_status)
@@ -733,7 +735,8 @@ def attn_varlen_fwd(q, k, v, qo_indptr, kv_indptr, kv_lens=None, causal=False, s
     all), int32.  ``scale`` (by default ``D ** -0.5``) is positive.
     ``workspace``: a uint8 tensor of attn_varlen_fwd_workspace_bytes() bytes,
     scratch (None allocates one).  Returns ``(o [total_q, Hq, D], lse [total_q,
-    Hq], workspace)``.
+    Hq], workspace)``.  Not recorded for torch's differentiation: inputs that
+    require a gradient are refused while gradients are on.
     """
     return _run(stream, _native().varlen_fwd, q, k, v, qo_indptr, kv_indptr, kv_lens, causal, scale, workspace, o, lse,
                 dev_status)
@@ -771,6 +774,7 @@ def attn_cross_decode(q, k, v, kv_indptr, kv_lens=None, scale=None, workspace=No
     kv_lens`` as :func:`attn_varlen_fwd`.  ``workspace``: a uint8 tensor of
     attn_cross_decode_workspace_bytes() bytes, scratch (None allocates one).
     Returns ``(o, lse, workspace)``, ``lse [B, Hq]`` or ``[B, q_len, Hq]``.
+    Inputs that require a gradient are refused while gradients are on: it has none.
     """
     return _run(stream, _native().cross_decode, q, k, v, kv_indptr, kv_lens, scale, workspace, o, lse, dev_status)
 

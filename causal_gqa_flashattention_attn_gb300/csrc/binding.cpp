@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -22,6 +23,7 @@
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
+#include <utility>
 
 #include "../../include/attn.h"
 
@@ -58,6 +60,16 @@ at::Device call_device(const at::Tensor& t) {
     if (!t.is_cuda() || t.get_device() != c10::cuda::current_device())
         throw Refused("tensors must be on the current CUDA device");
     return t.device();
+}
+
+// Forward calls record nothing for torch's differentiation: where it would expect
+// them to (an input wants a gradient, gradients are on), they are refused, so that
+// no weight goes without its gradient unnoticed.
+void expect_unrecorded(const Args& args, std::initializer_list<std::pair<const char*, int>> inputs, const char* advice) {
+    if (!c10::GradMode::is_enabled()) return;
+    for (const auto& [name, i] : inputs)
+        if (!args.none(i) && THPVariable_Check(args.a[i]) && THPVariable_Unpack(args.a[i]).requires_grad())
+            throw Refused(std::string(name) + " requires a gradient, which this call does not record: call it under torch.no_grad()" + advice);
 }
 
 // A dense tensor's pointer, after checks of its device, type and shape (-1: any size).
@@ -495,6 +507,8 @@ NormCall norm_call(const Args& args, const NormSide& q, const NormSide& k, int t
 PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
         const Args args{a, n};
+        expect_unrecorded(args, {{"q", 0}, {"k", 1}, {"q_weight", 2}, {"k_weight", 3}},
+                          " or in a torch.autograd.Function, with attn_qk_norm_rope_bwd for the gradient");
         const at::Device device = call_device(args.tensor("q or k", args.none(0) ? 1 : 0));
         const NormSide q = norm_side(args, "q", "", "q_weight", "q_out", "", 0, -1, 2, 8, -1, device);
         const NormSide k = norm_side(args, "k", "", "k_weight", "k_out", "", 1, -1, 3, 9, -1, device);
@@ -575,6 +589,8 @@ Ragged ragged(const Args& args, int i, int at, at::Device device) {
 PyObject* varlen_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
         const Args args{a, n};
+        expect_unrecorded(args, {{"q", 0}, {"k", 1}, {"v", 2}},
+                          " or in a torch.autograd.Function, with attn_varlen_bwd for the gradient");
         const at::Device device = call_device(args.tensor("q", 0));
         const Ragged r = ragged(args, 0, 3, device);
         at::Tensor ws, o, lse;
@@ -652,6 +668,7 @@ PyObject* varlen_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* cross_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
         const Args args{a, n};
+        expect_unrecorded(args, {{"q", 0}, {"k", 1}, {"v", 2}}, "");
         const at::Tensor& q = args.tensor("q", 0);
         const at::Device device = call_device(q);
         constexpr auto bf16 = at::ScalarType::BFloat16;
