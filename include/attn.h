@@ -633,7 +633,8 @@ attn_status_t attn_prefill_paged_fp8_block(const void* q, const void* k_cache, c
  *                ATTN_DEV_POSITION_OUT_OF_RANGE and leaves its token unwritten.
  *   q_out, k_out as q and k (written).  An output may be its input where the
  *                strides agree; else they do not overlap.
- *   D            64 or 128;  total * (Hq + Hkv) <= 2^31 - 2^20.
+ *   D            64 or 128;  rot_dim a multiple of 16;  total * (Hq + Hkv) <=
+ *                2^31 - 2^20 (ATTN_ERR_UNSUPPORTED otherwise)
  */
 attn_status_t attn_qk_norm_rope(const void* q, const void* k, long long q_stride, long long k_stride,
                                 const void* q_weight, const void* k_weight, attn_dtype_t weight_dtype, float eps,
@@ -709,7 +710,8 @@ attn_status_t attn_qk_norm_rope_bwd(const void* d_q_out, const void* d_k_out, lo
  *                device's SM count.)  Calls that may run at the same time need
  *                separate workspaces.
  *   D 64 or 128, Hq / Hkv <= 128, Hq * D < 2^31, B <= 2048, total_q < 2^22,
- *   (total_q + B) * Hq <= 2^31 - 2^20.
+ *   total_kv < 2^30, (total_q + B) * Hq <= 2^31 - 2^20, total_kv * Hkv < 2^31,
+ *   strides of q, k and v < 2^38 (ATTN_ERR_UNSUPPORTED otherwise).
  * Offsets outside the tensors are cut to them.
  */
 size_t attn_varlen_fwd_workspace_bytes(int B, int total_q, int total_kv, int Hq, int Hkv, int D);
@@ -741,9 +743,10 @@ attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, long 
  *   workspace    >= attn_varlen_bwd_workspace_bytes() bytes, 16-byte aligned:
  *                scratch (the size goes by the current device's SM count).
  *                Calls that may run at the same time need separate workspaces.
- * Other arguments, limits and errors as attn_varlen_fwd; ATTN_ERR_UNSUPPORTED too
- * on a device that keeps other than 1024 bytes of a block's shared memory for
- * itself.  (What lies in rows that
+ * Other arguments, limits and errors as attn_varlen_fwd (d_o_stride < 2^38 too);
+ * ATTN_ERR_UNSUPPORTED also for 2^31 and more CTAs (a block of 128 keys, or of
+ * floor(128 / (Hq / Hkv)) queries, of a KV head takes one) and on a device that
+ * keeps other than 1024 bytes of a block's shared memory for itself.  (What lies in rows that
  * do not count, or in other sequences, reaches no gradient.  With `causal`, call a
  * block of floor(128 / (Hq / Hkv)) positions and a tile of 128 keys joined where
  * one of the block's queries sees one of the tile's keys: a NaN or an infinity in
@@ -777,7 +780,10 @@ attn_status_t attn_varlen_bwd(const void* d_o, const void* q, const void* k, con
  *                scratch (the size goes by the current device's SM count).
  *                Calls that may run at the same time need separate workspaces.
  *   o            as q, not q itself; lse float32 [B, q_len, Hq] or NULL (written)
- *   D 64 or 128, q_len 1..16, any Hq % Hkv == 0, B <= 4096.
+ *   scale        any finite number
+ *   D 64 or 128, q_len 1..16, any Hq % Hkv == 0, B <= 4096, Hq * q_len < 2^20,
+ *   B * q_len * Hq < 2^31, total_kv < 2^30, strides < 2^38
+ *   (ATTN_ERR_UNSUPPORTED otherwise).
  */
 size_t attn_cross_decode_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D);
 attn_status_t attn_cross_decode(const void* q, const void* k, const void* v, long long k_stride, long long v_stride,
