@@ -255,6 +255,11 @@ attn_status_t append_impl(const AppendArgs& a, int D, void* stream) {
     return from_cuda(launch_kv_append(a, static_cast<cudaStream_t>(stream)));
 }
 
+// Rows are counted in int, up to three steps of the grid ahead (fewer than 2^15 rows each).
+bool qk_norm_rows_ok(int total, int Hq, int Hkv) {
+    return std::max(total, 1) * (Hq + static_cast<long long>(Hkv)) <= (1LL << 31) - (1LL << 20);
+}
+
 // The checks of the norm with rotation and of its gradient (a.dy NULL: forward).
 attn_status_t qk_norm_check(const QkNormArgs& a, attn_dtype_t weight_dtype, bool backward) {
     if (a.total < 0 || a.Hq < 0 || a.Hkv < 0 || a.Hq + static_cast<long long>(a.Hkv) == 0) return ATTN_ERR_INVALID_ARG;
@@ -286,9 +291,20 @@ attn_status_t qk_norm_check(const QkNormArgs& a, attn_dtype_t weight_dtype, bool
     if (a.rot_dim < 0 || a.rot_dim > a.D || (a.interleaved != 0 && a.interleaved != 1)) return ATTN_ERR_INVALID_ARG;
     if (a.rot_dim > 0 && (a.cos_sin == nullptr || a.max_pos <= 0 || !aligned16(a.cos_sin))) return ATTN_ERR_INVALID_ARG;
     if (a.rot_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
-    // rows are counted in int, up to three steps of the grid ahead (fewer than 2^15 rows each)
-    if (std::max(a.total, 1) * (a.Hq + static_cast<long long>(a.Hkv)) > (1LL << 31) - (1LL << 20)) return ATTN_ERR_UNSUPPORTED;
-    return ATTN_OK;
+    return qk_norm_rows_ok(a.total, a.Hq, a.Hkv) ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
+}
+
+// Sizes that attention over contiguous keys takes, of those that can be one's at all.
+bool varlen_sizes_ok(int B, int total_q, int total_kv, int Hq, int Hkv, int D) {
+    if (D != 64 && D != 128) return false;
+    if (Hq / Hkv > 128 || B > varlen_max_seqs()) return false;
+    // query blocks are counted in 21 bits, rows and work items in int (work items a step of
+    // the grid ahead of the last one, too)
+    if (total_q >= (1 << 22) || total_kv >= (1 << 30)) return false;
+    if ((static_cast<long long>(total_q) + B) * Hq > (1LL << 31) - (1LL << 20) || static_cast<long long>(total_kv) * Hkv >= (1LL << 31))
+        return false;
+    // an element's place in its token's row, a TMA coordinate among others, is an int
+    return static_cast<long long>(Hq) * D < (1LL << 31);
 }
 
 // Sizes and pointers that attention over contiguous keys takes, forward and backward.
@@ -305,21 +321,17 @@ attn_status_t varlen_check(const void* q, const void* k, const void* v, long lon
     if (q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 || q_stride < static_cast<long long>(Hq) * D ||
         k_stride < static_cast<long long>(Hkv) * D || v_stride < static_cast<long long>(Hkv) * D)
         return ATTN_ERR_INVALID_ARG;
-    if (Hq / Hkv > 128 || B > varlen_max_seqs() || scale <= 0.f) return ATTN_ERR_UNSUPPORTED;
+    if (scale <= 0.f || !varlen_sizes_ok(B, total_q, total_kv, Hq, Hkv, D)) return ATTN_ERR_UNSUPPORTED;
     // row strides of a TMA map are below 2^40 bytes
     if (q_stride >= (1LL << 38) || k_stride >= (1LL << 38) || v_stride >= (1LL << 38)) return ATTN_ERR_UNSUPPORTED;
-    // query blocks are counted in 21 bits, rows and work items in int
-    if (total_q >= (1 << 22) || total_kv >= (1 << 30)) return ATTN_ERR_UNSUPPORTED;
-    // (work items a step of the grid ahead of the last one, too)
-    if ((static_cast<long long>(total_q) + B) * Hq > (1LL << 31) - (1LL << 20) || static_cast<long long>(total_kv) * Hkv >= (1LL << 31))
-        return ATTN_ERR_UNSUPPORTED;
-    // an element's place in its token's row, a TMA coordinate among others, is an int
-    if (static_cast<long long>(Hq) * D >= (1LL << 31)) return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }
 
 // Sizes that the block-scaled readers take: rows of a decode, rows of the prefill's copy.
 bool decode_rows_ok(int q_len, int Hq) { return static_cast<long long>(Hq) * q_len < (1LL << 20); }
+bool cross_decode_sizes_ok(int B, int q_len, int Hq) {
+    return B <= cross_decode_max_seqs() && decode_rows_ok(q_len, Hq) && static_cast<long long>(Hq) * q_len * B < (1LL << 31);
+}
 bool copy_rows_ok(int B, int max_kv_rows, int Hkv) {
     const long long rows = static_cast<long long>(max_kv_rows) + 128LL * B;   // each sequence's up to the next multiple of 128
     return rows < (1LL << 31) && rows <= ((1LL << 33) - 1) / Hkv;
@@ -763,7 +775,7 @@ attn_status_t attn_qk_norm_rope(const void* q, const void* k, long long q_stride
 }
 
 size_t attn_qk_norm_rope_bwd_workspace_bytes(int total, int Hq, int Hkv, int D) {
-    if (total < 0 || Hq < 0 || Hkv < 0 || (D != 64 && D != 128)) return 0;
+    if (total < 0 || Hq < 0 || Hkv < 0 || (Hq == 0 && Hkv == 0) || (D != 64 && D != 128) || !qk_norm_rows_ok(total, Hq, Hkv)) return 0;
     const int sms = device_sm_count();
     return sms > 0 ? qk_norm_bwd_workspace(D, sms) : 0;
 }
@@ -794,7 +806,8 @@ attn_status_t attn_qk_norm_rope_bwd(const void* d_q_out, const void* d_k_out, lo
 }
 
 size_t attn_varlen_fwd_workspace_bytes(int B, int total_q, int total_kv, int Hq, int Hkv, int D) {
-    if (B <= 0 || total_q <= 0 || total_kv < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || D <= 0) return 0;
+    if (B <= 0 || total_q <= 0 || total_kv < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
+    if (!varlen_sizes_ok(B, total_q, total_kv, Hq, Hkv, D)) return 0;
     const int sms = device_sm_count();
     return sms > 0 ? varlen_fwd_workspace(B, total_q, total_kv, Hq, Hkv, D, sms) : 0;
 }
@@ -819,9 +832,11 @@ attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, long 
 }
 
 size_t attn_varlen_bwd_workspace_bytes(int B, int total_q, int total_kv, int Hq, int Hkv, int D) {
-    if (B <= 0 || total_q < 0 || total_kv < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || D <= 0) return 0;
+    if (B <= 0 || total_q < 0 || total_kv < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
+    if (!varlen_sizes_ok(B, total_q, total_kv, Hq, Hkv, D)) return 0;
     const int sms = device_sm_count();
-    return sms > 0 ? varlen_bwd_workspace(B, total_q, total_kv, Hq, Hkv, D, sms) : 0;
+    if (sms <= 0 || !varlen_bwd_grid_ok(B, total_q, total_kv, Hq, Hkv, sms)) return 0;
+    return varlen_bwd_workspace(B, total_q, total_kv, Hq, Hkv, D, sms);
 }
 
 attn_status_t attn_varlen_bwd(const void* d_o, const void* q, const void* k, const void* v, const void* o,
@@ -860,7 +875,7 @@ attn_status_t attn_varlen_bwd(const void* d_o, const void* q, const void* k, con
 
 size_t attn_cross_decode_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D) {
     if (B <= 0 || q_len <= 0 || q_len > 16 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
-    if (!decode_rows_ok(q_len, Hq)) return 0;
+    if (!cross_decode_sizes_ok(B, q_len, Hq)) return 0;
     const int sms = device_sm_count();
     return sms > 0 ? cross_decode_workspace(q_len, Hq, Hkv, D, sms) : 0;
 }
@@ -877,9 +892,8 @@ attn_status_t attn_cross_decode(const void* q, const void* k, const void* v, lon
     if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
     if (k_stride % 8 != 0 || v_stride % 8 != 0 || k_stride < static_cast<long long>(Hkv) * D || v_stride < static_cast<long long>(Hkv) * D)
         return ATTN_ERR_INVALID_ARG;
-    if (q_len > 16 || B > cross_decode_max_seqs() || k_stride >= (1LL << 38) || v_stride >= (1LL << 38)) return ATTN_ERR_UNSUPPORTED;
-    if (!decode_rows_ok(q_len, Hq) || static_cast<long long>(Hq) * q_len * B >= (1LL << 31) || total_kv >= (1 << 30))
-        return ATTN_ERR_UNSUPPORTED;
+    if (q_len > 16 || !cross_decode_sizes_ok(B, q_len, Hq) || total_kv >= (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+    if (k_stride >= (1LL << 38) || v_stride >= (1LL << 38)) return ATTN_ERR_UNSUPPORTED;
     if (workspace == nullptr || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
     const int sms = device_sm_count();
     if (sms <= 0) return ATTN_ERR_CUDA;

@@ -707,7 +707,8 @@ attn_status_t attn_qk_norm_rope_bwd(const void* d_q_out, const void* d_k_out, lo
  *                scratch (NULL where that is 0).  Few and long sequences are cut
  *                along their keys, and the parts joined in a fixed order: results
  *                do not depend on timing.  (The size goes by the current
- *                device's SM count.)  Calls that may run at the same time need
+ *                device's SM count; it is 0, here and below, for sizes that the
+ *                entry refuses.)  Calls that may run at the same time need
  *                separate workspaces.
  *   D 64 or 128, Hq / Hkv <= 128, Hq * D < 2^31, B <= 2048, total_q < 2^22,
  *   total_kv < 2^30, (total_q + B) * Hq <= 2^31 - 2^20, total_kv * Hkv < 2^31,
