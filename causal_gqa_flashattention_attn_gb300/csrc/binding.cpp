@@ -72,6 +72,13 @@ void expect_unrecorded(const Args& args, std::initializer_list<std::pair<const c
             throw Refused(std::string(name) + " requires a gradient, which this call does not record: call it under torch.no_grad()" + advice);
 }
 
+// An output that is read or written as something else of the same call, too.  (Parts of
+// one buffer whose rows lie between each other's are fine.)
+void expect_apart(const char* name, const void* out, std::initializer_list<std::pair<const char*, const void*>> others) {
+    for (const auto& [other, at] : others)
+        if (out != nullptr && out == at) throw Refused(std::string(name) + " must not be the same memory as " + other);
+}
+
 // A dense tensor's pointer, after checks of its device, type and shape (-1: any size).
 void* expect(const char* name, const at::Tensor& t, at::Device device, std::initializer_list<int64_t> shape,
              at::ScalarType type, at::ScalarType other = at::ScalarType::Undefined) {
@@ -512,6 +519,8 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Device device = call_device(args.tensor("q or k", args.none(0) ? 1 : 0));
         const NormSide q = norm_side(args, "q", "", "q_weight", "q_out", "", 0, -1, 2, 8, -1, device);
         const NormSide k = norm_side(args, "k", "", "k_weight", "k_out", "", 1, -1, 3, 9, -1, device);
+        expect_apart("q_out", q.out, {{"k", k.x}, {"k_out", k.out}});
+        expect_apart("k_out", k.out, {{"q", q.x}});
         const NormCall c = norm_call(args, q, k, 5, 6, device);
         check("attn_qk_norm_rope",
               attn_qk_norm_rope(q.x, k.x, q.x_stride, k.x_stride, q.weight, k.weight, c.type, number_or(args, 4, 1e-6),
@@ -530,6 +539,8 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Device device = call_device(args.tensor("q or k", args.none(2) ? 3 : 2));
         const NormSide q = norm_side(args, "q", "d_q_out", "q_weight", "d_q", "d_q_weight", 2, 0, 4, 11, 13, device);
         const NormSide k = norm_side(args, "k", "d_k_out", "k_weight", "d_k", "d_k_weight", 3, 1, 5, 12, 14, device);
+        expect_apart("d_q", q.out, {{"k", k.x}, {"d_k_out", k.dy}, {"d_k", k.out}});
+        expect_apart("d_k", k.out, {{"q", q.x}, {"d_q_out", q.dy}});
         const NormCall c = norm_call(args, q, k, 7, 8, device);
         at::Tensor ws;
         if (args.none(10)) {
@@ -605,6 +616,7 @@ PyObject* varlen_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         void* op = expect("o", args.none(9) ? o : args.tensor("o", 9), device, {r.total_q, r.hq, r.d}, at::ScalarType::BFloat16);
         float* lp = static_cast<float*>(expect("lse", args.none(10) ? lse : args.tensor("lse", 10), device, {r.total_q, r.hq},
                                                at::ScalarType::Float));
+        expect_apart("o", op, {{"q", r.q}, {"k", r.k}, {"v", r.v}});
         check("attn_varlen_fwd",
               attn_varlen_fwd(r.q, r.k, r.v, r.q_stride, r.k_stride, r.v_stride, r.qo, r.kv, r.lens, args.truth(6), r.count,
                               r.total_q, r.total_kv, r.hq, r.hkv, r.d, scale_or_default(args, 7, r.d), wp,
@@ -654,6 +666,9 @@ PyObject* varlen_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const GradRows dq = grad_rows(args, "d_q", 13, r.q_shape, device);
         const GradRows dk = grad_rows(args, "d_k", 14, r.k_shape, device);
         const GradRows dv = grad_rows(args, "d_v", 15, r.k_shape, device);
+        expect_apart("d_q", dq.at, {{"d_o", dop}, {"q", r.q}, {"k", r.k}, {"v", r.v}, {"o", op}, {"d_k", dk.at}, {"d_v", dv.at}});
+        expect_apart("d_k", dk.at, {{"d_o", dop}, {"q", r.q}, {"k", r.k}, {"v", r.v}, {"o", op}, {"d_v", dv.at}});
+        expect_apart("d_v", dv.at, {{"d_o", dop}, {"q", r.q}, {"k", r.k}, {"v", r.v}, {"o", op}});
         check("attn_varlen_bwd",
               attn_varlen_bwd(dop, r.q, r.k, r.v, op, do_stride, r.q_stride, r.k_stride, r.v_stride, o_stride, lse, d_lse, r.qo,
                               r.kv, r.lens, args.truth(9), r.count, r.total_q, r.total_kv, r.hq, r.hkv, r.d,
@@ -699,6 +714,7 @@ PyObject* cross_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         void* op = single ? expect("o", ot, device, {bsz, hq, d}, bf16) : expect("o", ot, device, {bsz, nq, hq, d}, bf16);
         float* lp = static_cast<float*>(single ? expect("lse", lt, device, {bsz, hq}, at::ScalarType::Float)
                                                : expect("lse", lt, device, {bsz, nq, hq}, at::ScalarType::Float));
+        expect_apart("o", op, {{"q", qp}, {"k", kp}, {"v", vp}});
         check("attn_cross_decode",
               attn_cross_decode(qp, kp, vp, ks, vs, kv, lens, b, i, small("k", k.size(0)), h, hkv, dd,
                                 scale_or_default(args, 5, dd), wp, static_cast<size_t>(wt.numel()), op, lp,
