@@ -20,6 +20,12 @@ __device__ __forceinline__ void flag_status(int32_t* status, int32_t bit) {
     if (status != nullptr) atomicOr(status, bit);
 }
 
+// a + b of counts that are not negative, at most INT_MAX: sums over sequences, whose
+// rows overlap where offsets fall, so that no tensor's size bounds them.
+__device__ __forceinline__ int add_capped(int a, int b) {
+    return static_cast<int>(min(static_cast<unsigned>(a) + static_cast<unsigned>(b), 0x7FFFFFFFu));
+}
+
 __device__ __forceinline__ uint8_t* align_1024(uint8_t* p) {
     return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }

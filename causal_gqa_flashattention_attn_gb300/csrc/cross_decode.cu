@@ -44,6 +44,9 @@ constexpr int kEnd = 2;
 // Where no sequence has more tiles, none is cut: 16 sequences of 60 keys 7.6 us,
 // cut 7.9; 32 of 200 keys whole 13.5 us, cut 8.5.
 constexpr int kWholeTiles = 6;
+// More spans than this (rising offsets have fewer than 2^26 + 3 kMaxSeqs) are not worked
+// on: offsets that fall can name the same keys for every sequence.
+constexpr int kMostSpans = 1 << 28;
 constexpr int kMergeWarps = 8;
 constexpr int kBatch = 8;       // pieces a merging warp has in flight
 
@@ -105,15 +108,16 @@ __device__ __forceinline__ bool count_tiles(const Params& p, int* before, int* l
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += v;
+        if (lane >= off) incl = add_capped(incl, v);
     }
+    int base = __shfl_up_sync(0xffffffffu, incl, 1);
+    if (lane == 0) base = 0;
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    int base = incl - sum;
-    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    for (int w = 0; w < warp; ++w) base = add_capped(base, warp_sum[w]);
     for (int b = b0; b < b1; ++b) {
         before[b] = base;
-        base += span_of(lens[b]);
+        base = add_capped(base, span_of(lens[b]));
     }
     if (threadIdx.x == kThreads - 1) before[p.B] = base;   // the last run ends with the last sequence, or is empty
     return __syncthreads_or(most > kWholeTiles) != 0;
@@ -164,6 +168,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x < kWarps * kStages) mbar_init(&full_all[0][0] + threadIdx.x, 1);
     fence_mbar_init();
     const bool cuts = count_tiles(p, before, lens, warp_sum);   // (ends with a barrier of the CTA)
+    if (before[p.B] > kMostSpans) {
+        if (threadIdx.x == 0) flag_status(p.status, ATTN_DEV_SEQ_TOO_LONG);
+        return;
+    }
     const Cut cut(p.workers, before[p.B]);
     const int whole_shares = min(p.workers, p.B);   // of whole sequences
     const int n_rows = p.G * p.nq;
@@ -396,23 +404,23 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) cross_decode_merge_kernel
     for (int i = threadIdx.x; i < p.B; i += 32 * kMergeWarps) {
         const int len = length_of(p, i), t = span_of(len);
         cuts |= tiles_of(len) > kWholeTiles;
-        all += t;
-        if (i < b) pre += t;
+        all = add_capped(all, t);
+        if (i < b) pre = add_capped(pre, t);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
-        pre += __shfl_xor_sync(0xffffffffu, pre, off);
-        all += __shfl_xor_sync(0xffffffffu, all, off);
+        pre = add_capped(pre, __shfl_xor_sync(0xffffffffu, pre, off));
+        all = add_capped(all, __shfl_xor_sync(0xffffffffu, all, off));
     }
     if (lane == 0) sums[0][warp] = pre, sums[1][warp] = all;
     cuts = __syncthreads_or(cuts) != 0;
     pre = all = 0;
 #pragma unroll
-    for (int i = 0; i < kMergeWarps; ++i) pre += sums[0][i], all += sums[1][i];
+    for (int i = 0; i < kMergeWarps; ++i) pre = add_capped(pre, sums[0][i]), all = add_capped(all, sums[1][i]);
     const int n_tiles = tiles_of(length_of(p, b));
     const Cut cut(p.workers, all);
     int w0 = 0, w1 = 0;   // its first and last share
-    if (n_tiles != 0 && cuts) w0 = cut.share_of(pre), w1 = cut.share_of(pre + n_tiles - 1);
+    if (n_tiles != 0 && cuts && all <= kMostSpans) w0 = cut.share_of(pre), w1 = cut.share_of(pre + n_tiles - 1);
     // the first kernel is done and its writes are here; CTAs without work wait
     // too, so that this grid never ends before that one
     asm volatile("griddepcontrol.wait;" : "+r"(w0), "+r"(w1)::"memory");

@@ -370,13 +370,24 @@ __device__ void varlen_prefix(const Params& p, int* prefix, int lane) {
             items = ((ql + 2 * p.P - 1) / (2 * p.P)) * (kDirect ? p.Hkv * p.pieces : p.Hkv);
         }
         int incl = items;
+        if constexpr (kDirect) {
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += v;
+            for (int off = 1; off < 32; off <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl = add_capped(incl, v);
+            }
+            const int before = __shfl_up_sync(0xffffffffu, incl, 1);
+            if (b < p.B) prefix[b] = lane > 0 ? add_capped(carry, before) : carry;
+            carry = add_capped(carry, __shfl_sync(0xffffffffu, incl, 31));
+        } else {
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += v;
+            }
+            if (b < p.B) prefix[b] = carry + incl - items;
+            carry += __shfl_sync(0xffffffffu, incl, 31);
         }
-        if (b < p.B) prefix[b] = carry + incl - items;
-        carry += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) prefix[p.B] = carry;
 }
@@ -571,6 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (kVarlen) n_items = prefix[p.B];
     const int per_pair = kDirect ? p.Hkv * p.pieces : p.Hkv;   // items of a (sequence, query block)
     const bool sorted = kVarlen && n_items / per_pair <= kMaxOrder && !(kDirect && n_items <= static_cast<int>(gridDim.x));
+    if constexpr (kDirect) n_items = min(n_items, p.n_items);   // (offsets that overlap could name more)
     auto get_item = [&](int idx) -> Item {
         if constexpr (kDirect) {
             const uint32_t pair = sorted ? order[idx / per_pair] : pair_of_varlen<true>(p, prefix, idx);
@@ -1785,6 +1797,9 @@ cudaError_t launch_varlen_fwd(const VarlenFwdArgs& a, cudaStream_t stream) {
                               CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
     }
+    // no more CTAs than there can be items
+    const long long items = (static_cast<long long>(a.total_q) / (2 * p.P) + a.B) * a.Hkv * p.pieces;
+    p.n_items = static_cast<int>(items);   // (below 2^31 with the sizes that are taken)
     const size_t smem = kSmemBytes + 1024;
     // sequences of at most one tile's positions in the mean: 64 of 16 queries to 577 keys 55.3 us,
     // with empty second tiles 57.3; where tiles are full the check costs, 2048 queries each 389 and 364
@@ -1793,8 +1808,6 @@ cudaError_t launch_varlen_fwd(const VarlenFwdArgs& a, cudaStream_t stream) {
                           : (few ? prefill_tc_kernel<true, false, false, true, true> : prefill_tc_kernel<true, false, false, true>);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    // no more CTAs than there can be items
-    const long long items = (static_cast<long long>(a.total_q) / (2 * p.P) + a.B) * a.Hkv * p.pieces;
     kern<<<static_cast<int>(std::min<long long>(items, sms)), kThreads, smem, stream>>>(q_map, k_map, v_map, q_map, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.pieces == 1) return e;

@@ -163,13 +163,13 @@ __device__ void list_blocks(const int* order, const int* len, int B, int per, bo
         const int v = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += v;
     }
-    if (lane == 31) warp_sum[warp] = incl;
+    if (lane == 31) warp_sum[warp] = incl;   // (below 2^31: 2^23 blocks a sequence at most, 128 sequences)
     __syncthreads();
     int base = incl - sum;
-    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    for (int w = 0; w < warp; ++w) base = add_capped(base, warp_sum[w]);
     for (int i = i0; i < i1; ++i) {
         before[i] = base;
-        base += (len[order[i]] + per - 1) / per;
+        base = add_capped(base, (len[order[i]] + per - 1) / per);
     }
     if (threadIdx.x == kPrepThreads - 1) before[B] = base;
     __syncthreads();

@@ -713,7 +713,9 @@ attn_status_t attn_qk_norm_rope_bwd(const void* d_q_out, const void* d_k_out, lo
  *   D 64 or 128, Hq / Hkv <= 128, Hq * D < 2^31, B <= 2048, total_q < 2^22,
  *   total_kv < 2^30, (total_q + B) * Hq <= 2^31 - 2^20, total_kv * Hkv < 2^31,
  *   strides of q, k and v < 2^38 (ATTN_ERR_UNSUPPORTED otherwise).
- * Offsets outside the tensors are cut to them.
+ * Offsets outside the tensors are cut to them.  Where offsets fall, sequences
+ * share rows, and no more of their query rows are worked on than a batch of
+ * rising offsets could have: the results of such rows are not defined.
  */
 size_t attn_varlen_fwd_workspace_bytes(int B, int total_q, int total_kv, int Hq, int Hkv, int D);
 attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
@@ -776,7 +778,10 @@ attn_status_t attn_varlen_bwd(const void* d_o, const void* q, const void* k, con
  * rounded to bf16 for the product with V, as there.
  *
  *   q            [B, q_len, Hq, D] bfloat16, dense                     (read)
- *   k, v, k_stride, v_stride, kv_indptr, kv_lens  as attn_varlen_fwd   (read)
+ *   k, v, k_stride, v_stride, kv_indptr, kv_lens  as attn_varlen_fwd (read).
+ *                Offsets that fall let sequences share keys; where they name
+ *                more than 2^32 for all sequences together (in tiles of 16),
+ *                ATTN_DEV_SEQ_TOO_LONG is set and nothing is written.
  *   workspace    >= attn_cross_decode_workspace_bytes() bytes, 16-byte aligned:
  *                scratch (the size goes by the current device's SM count).
  *                Calls that may run at the same time need separate workspaces.
