@@ -22,8 +22,8 @@
 //
 // Bound: the bytes of x (and dy) in and y (or dx) out.  16384 tokens of 32 + 4
 // heads of 128 (303 MB) 53.6 us, 5.65 TB/s; the gradient of 32 + 8 heads (505 MB)
-// 90.9 us, 5.55 TB/s, 0.83 and 0.82 of a copy's rate; one token 4 us, host
-// included.  Two thirds of the issue slots are taken, and how well the compiler
+// 90.9 us, 5.55 TB/s, 0.83 and 0.82 of a copy's rate; one token 4.6 to 5.1 us,
+// host included.  Two thirds of the issue slots are taken, and how well the compiler
 // interleaves four rows decides: two elements at a time throughout (72 / 137 us), two
 // chunks in turn without moves (72 / 118) and the rows' sums side by side (spills,
 // 73 / 131) were slower than this order, 60.5 / 90.9 for 16384 tokens of 32 + 8 heads.

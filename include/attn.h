@@ -771,10 +771,11 @@ attn_status_t attn_varlen_bwd(const void* d_o, const void* q, const void* k, con
  * queries per sequence (one token, the beams of a search), each of which sees
  * every key of its sequence.
  *
- * What attn_varlen_fwd computes without `causal`, by one read of K and V: the
- * work is cut evenly over the GPU on the device, whatever the lengths, and the
- * pieces of a sequence are joined in a fixed order, so results do not depend on
- * timing (within rounding they do on the SM count).  The softmax weights are
+ * What attn_varlen_fwd computes without `causal`.  K and V are read once for every
+ * 16 rows (queries times heads, q_len * Hq / Hkv) of a KV head.  The work is cut
+ * evenly over the GPU on the device, whatever the lengths, and the pieces of a
+ * sequence are joined in a fixed order, so results do not depend on timing
+ * (within rounding they do on the SM count).  The softmax weights are
  * rounded to bf16 for the product with V, as there.
  *
  *   q            [B, q_len, Hq, D] bfloat16, dense                     (read)
