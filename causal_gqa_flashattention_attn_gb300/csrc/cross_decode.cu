@@ -19,11 +19,12 @@
 //
 // Bound: one read of the keys and values for every 16 rows of a KV head (more rows
 // take columns of their own, which read them again: 16 sequences of 4096 keys, 16
-// queries of 64 heads over 8, 180 us where one read takes 40).  64 sequences of 512 to 6400 keys, four
-// beams, 32 heads over 8 (819 MB): 138 us, 5.9 TB/s.  One sequence of 1500 keys: 8.6 us
-// in a graph (launches, one tile, the join), 10.3 in a stream.  Tried: shares of at
-// least two to six tiles, more registers (no gain); the join's CTAs over several
-// rows each (64 x 4 beams 1 % faster, one sequence a launch interval slower).
+// queries of 64 heads over 8, 180 us where one read takes 40).  64 sequences of 512
+// to 6400 keys, four beams, 32 heads over 8 (819 MB): 138 us, 5.9 TB/s.  One sequence
+// of 1500 keys: 8.6 us in a graph (launches, one tile, the join), 10.3 in a stream.
+// Tried: shares of at least two to six tiles, more registers (no gain); the join's
+// CTAs over several rows each (64 x 4 beams 1 % faster, one sequence a launch interval
+// slower).
 #include <cuda_bf16.h>
 
 #include <algorithm>
